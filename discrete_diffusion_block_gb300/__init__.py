@@ -117,6 +117,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _U64 = ctypes.c_uint64
+_I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _SIGS = {
@@ -165,6 +166,14 @@ _SIGS = {
     "dg_op_sampler_update": (_I, [_P, _I, _I, _I, ctypes.POINTER(dg_sampler_config), _P, _P, _P,
                                   _P, _P, _P, _P, _P, _P]),
     "dg_op_kv_append": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "dg_op_qk_norm_rope": (_I, [_P, _P, _I, _I64, _I64, _P, _I, _I, _I, _I, _I, _F, _P, _P, _F, _P, _I64, _P,
+                                _I64, _P]),
+    "dg_op_rope_kv_append": (_I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _F, _P, _P,
+                                  _I, _I, _P]),
+    "dg_op_tree_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dg_op_tree_attention": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                                  _I64, _P, _SZ, _P]),
+    "dg_op_token_logprobs": (_I, [_P, _I, _I64, _I, _I, _F, _P, _I, _P, _P, _P, _I, _P, _P, _P]),
 }
 
 
@@ -575,3 +584,167 @@ def dg_op_kv_append(k_new, v_new, k_pool, v_pool, page_table, n_layers, n_pages,
     _check(load().dg_op_kv_append(_ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool),
                                   _ptr(page_table), n_layers, n_pages, pos0, n_new, Hkv, hd,
                                   page_size, _stream(stream)))
+
+
+# ---- serving drafted tokens (torch CUDA tensors on the current device) --------
+
+def _einval(msg):
+    raise DgError(DG_EINVAL, msg)
+
+
+def _on_device(*tensors):
+    """All on the current CUDA device (None is skipped)."""
+    import torch
+    cur = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            _einval("a tensor is not on a CUDA device")
+        cur = torch.cuda.current_device() if cur is None else cur
+        if t.get_device() != cur:
+            _einval("a tensor is not on the current CUDA device")
+
+
+def _head_rows(t, what, kinds):
+    """A [rows][heads][hd] tensor whose rows may be strided: its row stride."""
+    if t.dim() != 3 or str(t.dtype) not in kinds:
+        _einval(f"{what} must be [rows][heads][head_dim] of {' or '.join(kinds)}")
+    T, H, hd = t.shape
+    if t.numel() and ((hd > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != hd)):
+        _einval(f"{what}: the heads of a row must be adjacent")
+    return t.stride(0) if T > 1 else H * hd
+
+
+def _dense(t, what, kind, shape):
+    """A contiguous tensor of that type and shape (None entries: any extent)."""
+    if str(t.dtype) != kind or t.dim() != len(shape) or not t.is_contiguous() or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        _einval(f"{what} must be a contiguous {kind} tensor of shape {tuple('*' if n is None else n for n in shape)}")
+
+
+_BF16, _F32, _I32T, _I64T = "torch.bfloat16", "torch.float32", "torch.int32", "torch.int64"
+
+
+def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, eps=1e-6, rope_base=10000.0,
+                       rope_dim=None, stream=None):
+    """q, k: [T][heads][hd] bf16 or fp32 (rows may be strided); q_out, k_out
+    bf16 of the same shapes; positions int32 [T]; gains fp32 [hd] or None (no
+    norm).  k and k_out (or q and q_out) may be None."""
+    some = q if q is not None else k
+    if some is None:
+        _einval("q and k are both None")
+    _on_device(q, k, positions, q_out, k_out, q_gain, k_gain)
+    side = []
+    for x, o, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if (x is None) != (o is None):
+            _einval(f"{what} and {what}_out go together")
+        if x is None:
+            side.append((0, 0, 0))
+            continue
+        side.append((x.shape[1] if x.dim() == 3 else 0, _head_rows(x, what, (_BF16, _F32)),
+                     _head_rows(o, what + "_out", (_BF16,))))
+        if x.dtype != some.dtype or x.shape[0] != some.shape[0] or x.shape[2] != some.shape[2] or o.shape != x.shape:
+            _einval("q, k and their outputs must agree in rows, head_dim and (inputs) type")
+    T, _, hd = some.shape
+    if positions is not None:
+        _dense(positions, "positions", _I32T, (T,))
+    for gain in (q_gain, k_gain):
+        if gain is not None:
+            _dense(gain, "a gain", _F32, (hd,))
+    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    (hq, qs, qos), (hkv, ks, kos) = side
+    _check(load().dg_op_qk_norm_rope(addr(q), addr(k), int(str(some.dtype) == _F32), qs, ks, addr(positions), T, hq,
+                                     hkv, hd, hd if rope_dim is None else rope_dim, rope_base, addr(q_gain),
+                                     addr(k_gain), eps, addr(q_out), qos, addr(k_out), kos, _stream(stream)))
+
+
+def _batch_args(k_pool, v_pool, page_tables, prefix_lens, offsets):
+    """Checked (n_pages, Hkv, page_size, hd, n_seqs, max_pages) of a batch over the pools."""
+    _dense(k_pool, "k_pool", _BF16, (None,) * 4)
+    _dense(v_pool, "v_pool", _BF16, k_pool.shape)
+    _dense(prefix_lens, "prefix_lens", _I32T, (None,))
+    B = prefix_lens.shape[0]
+    _dense(offsets, "offsets", _I32T, (B + 1,))
+    _dense(page_tables, "page_tables", _I32T, (B, None))
+    return (*k_pool.shape, B, page_tables.shape[1])
+
+
+def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets, positions=None, k_gain=None,
+                         eps=1e-6, rope_base=10000.0, rope_dim=None, stream=None):
+    """k, v: [T][Hkv][hd] bf16 (rows may be strided); pools
+    [n_pages][Hkv][page_size][hd]; page_tables int32 [B][max_pages];
+    prefix_lens int32 [B]; offsets int32 [B + 1]."""
+    _on_device(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets, positions, k_gain)
+    n_pages, hkv, pg, hd, B, max_pages = _batch_args(k_pool, v_pool, page_tables, prefix_lens, offsets)
+    ks, vs = _head_rows(k, "k", (_BF16,)), _head_rows(v, "v", (_BF16,))
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != hkv or k.shape[2] != hd:
+        _einval("k and v must be [rows][heads][head_dim] of the pools' heads")
+    if positions is not None:
+        _dense(positions, "positions", _I32T, (T,))
+    if k_gain is not None:
+        _dense(k_gain, "k_gain", _F32, (hd,))
+    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _check(load().dg_op_rope_kv_append(addr(k), addr(v), ks, vs, addr(positions), addr(prefix_lens), addr(offsets),
+                                       addr(page_tables), max_pages, B, T, hkv, hd,
+                                       hd if rope_dim is None else rope_dim, rope_base, addr(k_gain), eps,
+                                       addr(k_pool), addr(v_pool), n_pages, pg, _stream(stream)))
+
+
+def dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd):
+    return load().dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd)
+
+
+def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, tree_mask, out, workspace, scale=None,
+                         stream=None):
+    """q, out: [T][Hq][hd] bf16 (rows may be strided); tree_mask int64
+    [T][words] (bit d: the row sees drafted token d of its sequence) or None
+    (causal); scale None: 1 / sqrt(hd)."""
+    _on_device(q, k_pool, v_pool, page_tables, prefix_lens, offsets, tree_mask, out, workspace)
+    n_pages, hkv, pg, hd, B, max_pages = _batch_args(k_pool, v_pool, page_tables, prefix_lens, offsets)
+    qs, os_ = _head_rows(q, "q", (_BF16,)), _head_rows(out, "out", (_BF16,))
+    T, hq, _ = q.shape
+    if out.shape != q.shape or q.shape[2] != hd:
+        _einval("q and out must be [rows][heads][head_dim] of the pools' head_dim")
+    words = 0
+    if tree_mask is not None:
+        _dense(tree_mask, "tree_mask", _I64T, (T, None))
+        words = tree_mask.shape[1]
+    if workspace is not None and not workspace.is_contiguous():
+        _einval("the workspace must be contiguous")
+    _check(load().dg_op_tree_attention(q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), page_tables.data_ptr(),
+                                       max_pages, prefix_lens.data_ptr(), offsets.data_ptr(),
+                                       tree_mask.data_ptr() if words else None, words, B, T, hq, hkv, hd, pg, n_pages,
+                                       hd ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                                       None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
+                                       _stream(stream)))
+
+
+def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_ids=None, top_logprobs=None,
+                         inv_tau=1.0, stream=None):
+    """logits: [T][V] fp32 or bf16 (rows may be strided); tokens int32
+    [T][given] and logprobs fp32 [T][given] (None: none given); entropy, lse
+    fp32 [T]; top_ids int32 [T][k], top_logprobs fp32 [T][k]."""
+    _on_device(logits, tokens, logprobs, entropy, lse, top_ids, top_logprobs)
+    kind = str(logits.dtype)
+    if logits.dim() != 2 or kind not in (_BF16, _F32) or (logits.numel() and logits.shape[1] > 1 and logits.stride(1) != 1):
+        _einval("logits must be [rows][vocab] of fp32 or bf16 with adjacent entries")
+    T, V = logits.shape
+    if (tokens is None) != (logprobs is None) or (top_ids is None and top_logprobs is not None):
+        _einval("tokens go with logprobs, top_logprobs with top_ids")
+    given = k = 0
+    if tokens is not None:
+        _dense(tokens, "tokens", _I32T, (T, None))
+        given = tokens.shape[1]
+        _dense(logprobs, "logprobs", _F32, (T, given))
+    if top_ids is not None:
+        _dense(top_ids, "top_ids", _I32T, (T, None))
+        k = top_ids.shape[1]
+    for t, what, shape in ((entropy, "entropy", (T,)), (lse, "lse", (T,)), (top_logprobs, "top_logprobs", (T, k))):
+        if t is not None:
+            _dense(t, what, _F32, shape)
+    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _check(load().dg_op_token_logprobs(logits.data_ptr(), int(kind == _BF16), logits.stride(0) if T > 1 else V, T, V,
+                                       inv_tau, addr(tokens), given, addr(logprobs), addr(entropy), addr(lse), k,
+                                       addr(top_ids), addr(top_logprobs), _stream(stream)))

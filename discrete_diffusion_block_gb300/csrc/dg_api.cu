@@ -18,6 +18,7 @@
 // uniformly, and the KV-append forward overwrites those slots with the
 // clean canvas's K/V.
 #include <chrono>
+#include <cmath>
 #include <cstdarg>
 #include <map>
 #include <mutex>
@@ -1408,6 +1409,9 @@ int dg_op_status(void *stream) {
   if (v[0] == 0 && v[1] == 0) return DG_OK;
   CK(cudaMemset(st, 0, sizeof(v)));
   if (v[0]) return device_fail(v[0]);
+  if (v[1] == dg::kBadSequence)
+    return fail(DG_EINVAL, "a sequence's rows or slots were outside the call's arrays (it was skipped)");
+  if (v[1] == dg::kBadToken) return fail(DG_EINVAL, "a token id was outside the vocabulary");
   return fail(DG_EINVAL, "a page table entry was outside the pools (its keys were skipped)");
 }
 
@@ -1616,6 +1620,153 @@ int dg_op_kv_append(const uint16_t *k_new, const uint16_t *v_new, uint16_t *k_po
   CK(dg::kv_append((const bf16 *)k_new, (const bf16 *)v_new, (bf16 *)k_pool, (bf16 *)v_pool,
                    page_table, n_layers, n_pages, pos0, n_new, n_kv_heads, head_dim, page_size,
                    (cudaStream_t)stream));
+  return DG_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// Rows of `heads` heads: present, 16-byte aligned, far enough apart.
+int check_rows(const char *what, const void *p, int64_t stride, int32_t n_tok, int32_t heads, int32_t head_dim,
+               int elems16) {
+  if (n_tok == 0 || heads == 0) return DG_OK;
+  if (!p) return fail(DG_EINVAL, "null %s", what);
+  if (!aligned16(p)) return fail(DG_EINVAL, "%s is not 16-byte aligned", what);
+  if (n_tok > 1 && (stride < (int64_t)heads * head_dim || stride % elems16))
+    return fail(DG_EINVAL, "%s: row stride %lld (needs a multiple of %d, at least %lld)", what, (long long)stride,
+                elems16, (long long)heads * head_dim);
+  return DG_OK;
+}
+
+int check_rope(int32_t n_tok, int32_t head_dim, int32_t rope_dim, float rope_base, bool normed, float eps) {
+  if (n_tok < 0) return fail(DG_EINVAL, "negative row count");
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return fail(DG_EINVAL, "head_dim must be 64, 128 or 256");
+  if (rope_dim < 0 || rope_dim > head_dim || rope_dim % 16)
+    return fail(DG_EINVAL, "rope_dim must be a multiple of 16 in [0, head_dim]");
+  if (rope_dim && !(rope_base >= 1.0f && rope_base < INFINITY)) return fail(DG_EINVAL, "rope_base must be finite and >= 1");
+  if (normed && !(eps > 0.0f && eps < INFINITY)) return fail(DG_EINVAL, "eps must be finite and > 0");
+  return DG_OK;
+}
+
+int check_batch(const int32_t *prefix_lens, const int32_t *offsets, const int32_t *page_tables, int32_t max_pages,
+                int32_t n_seqs, const void *k_pool, const void *v_pool, int32_t n_pages) {
+  if (n_seqs < 0 || max_pages < 0) return fail(DG_EINVAL, "negative sequence or page count");
+  if (!offsets || (n_seqs && (!prefix_lens || (max_pages && !page_tables)))) return fail(DG_EINVAL, "null pointer");
+  if (!k_pool || !v_pool) return fail(DG_EINVAL, "null pool");
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(DG_EINVAL, "a pool is not 16-byte aligned");
+  if (n_pages < 1) return fail(DG_EINVAL, "n_pages must be at least 1");
+  return DG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dg_op_qk_norm_rope(const void *q, const void *k, int32_t in_f32, int64_t q_stride, int64_t k_stride,
+                       const int32_t *positions, int32_t n_tok, int32_t n_q_heads, int32_t n_kv_heads,
+                       int32_t head_dim, int32_t rope_dim, float rope_base, const float *q_gain,
+                       const float *k_gain, float eps, uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out,
+                       int64_t k_out_stride, void *stream) {
+  if (n_q_heads < 0 || n_kv_heads < 0) return fail(DG_EINVAL, "negative head count");
+  CKR(check_rope(n_tok, head_dim, rope_dim, rope_base, q_gain || k_gain, eps));
+  const int e16 = in_f32 ? 4 : 8;
+  CKR(check_rows("q", q, q_stride, n_tok, n_q_heads, head_dim, e16));
+  CKR(check_rows("k", k, k_stride, n_tok, n_kv_heads, head_dim, e16));
+  CKR(check_rows("q_out", q_out, q_out_stride, n_tok, n_q_heads, head_dim, 8));
+  CKR(check_rows("k_out", k_out, k_out_stride, n_tok, n_kv_heads, head_dim, 8));
+  if (n_tok == 0 || n_q_heads + n_kv_heads == 0) return DG_OK;
+  if (rope_dim && !positions) return fail(DG_EINVAL, "null positions");
+  if (!aligned16(q_gain) || !aligned16(k_gain)) return fail(DG_EINVAL, "a gain is not 16-byte aligned");
+  if ((n_q_heads && q == q_out && (in_f32 || (n_tok > 1 && q_stride != q_out_stride))) ||
+      (n_kv_heads && k == k_out && (in_f32 || (n_tok > 1 && k_stride != k_out_stride))))
+    return fail(DG_EINVAL, "in place needs bf16 rows of one stride");
+  dg::QkNormRope a{q, k, in_f32 ? 1 : 0, q_stride, k_stride, positions, n_tok, n_q_heads, n_kv_heads, head_dim,
+                   rope_dim, rope_base, q_gain, k_gain, eps, (bf16 *)q_out, q_out_stride, (bf16 *)k_out,
+                   k_out_stride};
+  CK(dg::qk_norm_rope(a, (cudaStream_t)stream));
+  return DG_OK;
+}
+
+int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
+                         const int32_t *positions, const int32_t *prefix_lens, const int32_t *offsets,
+                         const int32_t *page_tables, int32_t max_pages, int32_t n_seqs, int32_t n_tok,
+                         int32_t n_kv_heads, int32_t head_dim, int32_t rope_dim, float rope_base,
+                         const float *k_gain, float eps, uint16_t *k_pool, uint16_t *v_pool, int32_t n_pages,
+                         int32_t page_size, void *stream) {
+  CKR(check_rope(n_tok, head_dim, rope_dim, rope_base, k_gain != nullptr, eps));
+  if (n_kv_heads < 1 || page_size < 1) return fail(DG_EINVAL, "n_kv_heads and page_size must be at least 1");
+  CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, v_pool, n_pages));
+  CKR(check_rows("k", k, k_stride, n_tok, n_kv_heads, head_dim, 8));
+  CKR(check_rows("v", v, v_stride, n_tok, n_kv_heads, head_dim, 8));
+  if (!aligned16(k_gain)) return fail(DG_EINVAL, "the gain is not 16-byte aligned");
+  if (n_tok == 0 || n_seqs == 0) return DG_OK;
+  int *status = nullptr;
+  CKR(op_status_ptr(&status));
+  dg::RopeKvAppend a{(const bf16 *)k, (const bf16 *)v, k_stride, v_stride, positions, prefix_lens, offsets,
+                     page_tables, max_pages, n_seqs, n_tok, n_kv_heads, head_dim, rope_dim, rope_base, k_gain, eps,
+                     (bf16 *)k_pool, (bf16 *)v_pool, n_pages, page_size};
+  CK(dg::rope_kv_append(a, status, (cudaStream_t)stream));
+  return DG_OK;
+}
+
+size_t dg_op_tree_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                            int32_t head_dim) {
+  if (n_tok < 0 || n_seqs < 0 || n_kv_heads < 1 || n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return dg::tree_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);
+}
+
+int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool, const uint16_t *v_pool,
+                         const int32_t *page_tables, int32_t max_pages, const int32_t *prefix_lens,
+                         const int32_t *offsets, const uint64_t *tree_mask, int32_t mask_words, int32_t n_seqs,
+                         int32_t n_tok, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t page_size,
+                         int32_t n_pages, float scale, uint16_t *out, int64_t out_stride, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  if (n_tok < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 128)
+    return fail(DG_EINVAL, "unsupported head counts or row count");
+  if (head_dim != 64 && head_dim != 128) return fail(DG_EINVAL, "head_dim must be 64 or 128");
+  if (page_size < 64 || page_size % 64) return fail(DG_EINVAL, "page_size must be a positive multiple of 64");
+  if (!(scale > 0.0f && scale < INFINITY)) return fail(DG_EINVAL, "scale must be finite and > 0");
+  if (tree_mask ? mask_words < 1 : mask_words != 0)
+    return fail(DG_EINVAL, "mask_words must be at least 1 with a mask, 0 without");
+  CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, v_pool, n_pages));
+  CKR(check_rows("q", q, q_stride, n_tok, n_q_heads, head_dim, 8));
+  CKR(check_rows("out", out, out_stride, n_tok, n_q_heads, head_dim, 8));
+  if (n_tok == 0 || n_seqs == 0) return DG_OK;
+  if (q == out) return fail(DG_EINVAL, "out must not be q");
+  const size_t need = dg::tree_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);
+  if (workspace_bytes < need || (need && !workspace))
+    return fail(DG_EINVAL, "workspace too small (%zu bytes, needs %zu)", workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(DG_EINVAL, "the workspace is not 16-byte aligned");
+  int *status = nullptr;
+  CKR(op_status_ptr(&status));
+  dg::TreeAttention a{(const bf16 *)q, q_stride, (const bf16 *)k_pool, (const bf16 *)v_pool, page_tables, max_pages,
+                      prefix_lens, offsets, (const unsigned long long *)tree_mask, mask_words, n_seqs, n_tok,
+                      n_q_heads, n_kv_heads, head_dim, page_size, n_pages, scale, (bf16 *)out, out_stride};
+  CK(dg::tree_attention(a, workspace, status, (cudaStream_t)stream));
+  return DG_OK;
+}
+
+int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_stride, int32_t rows, int32_t V,
+                         float inv_tau, const int32_t *tokens, int32_t n_given, float *logprobs, float *entropy,
+                         float *lse, int32_t top_k, int32_t *top_ids, float *top_logprobs, void *stream) {
+  if (rows < 0 || V < 1 || n_given < 0) return fail(DG_EINVAL, "rows, n_given >= 0 and V >= 1 required");
+  if (top_k < 0 || top_k > 32 || top_k > V) return fail(DG_EINVAL, "top_k must be in [0, min(32, V)]");
+  if (!(inv_tau > 0.0f && inv_tau < INFINITY)) return fail(DG_EINVAL, "inv_tau must be finite and > 0");
+  if (rows == 0) return DG_OK;
+  if (!logits) return fail(DG_EINVAL, "null logits");
+  if ((uintptr_t)logits % (logits_bf16 ? 2 : 4)) return fail(DG_EINVAL, "logits are not aligned to their elements");
+  if (rows > 1 && row_stride < V) return fail(DG_EINVAL, "row_stride is smaller than V");
+  if (n_given && (!tokens || !logprobs)) return fail(DG_EINVAL, "null tokens or logprobs");
+  if (top_k && !top_ids) return fail(DG_EINVAL, "null top_ids");
+  int *status = nullptr;
+  CKR(op_status_ptr(&status));
+  dg::TokenLogprobs a{logits, logits_bf16 ? 1 : 0, row_stride, rows, V, inv_tau, tokens, n_given, logprobs, entropy,
+                      lse, top_k, top_ids, top_logprobs};
+  CK(dg::token_logprobs(a, status, (cudaStream_t)stream));
   return DG_OK;
 }
 

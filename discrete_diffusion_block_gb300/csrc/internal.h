@@ -231,4 +231,74 @@ cudaError_t attention(const bf16 *q, const bf16 *k_pool, const bf16 *v_pool, con
                       const AttnShape &s, bf16 *out, void *ws, size_t ws_bytes, cudaStream_t st,
                       int *err = nullptr, bool out_tiles = false);
 
+// ---- draft serving (kernels_rope.cu, kernels_tree.cu, kernels_logprobs.cu) --
+// Record codes of the status word's second int (reported by dg_op_status).
+constexpr int kBadPage = 39;      // a page table entry outside the pools
+constexpr int kBadSequence = 41;  // sequence offsets or cached lengths outside the call's arrays
+constexpr int kBadToken = 42;     // a token id outside the vocabulary
+
+// q, k: bf16 (fp32 when in_f32) rows of heads, `stride` elements apart.
+struct QkNormRope {
+  const void *q, *k;
+  int in_f32;
+  long long q_stride, k_stride;
+  const int *positions;
+  int n_tok, Hq, Hkv, hd, rope_dim;
+  float rope_base;
+  const float *q_gain, *k_gain;
+  float eps;
+  bf16 *q_out;
+  long long q_out_stride;
+  bf16 *k_out;
+  long long k_out_stride;
+};
+cudaError_t qk_norm_rope(const QkNormRope &a, cudaStream_t st);
+
+// Packed rows of n_seqs sequences: rows [offsets[b], offsets[b + 1]) are
+// sequence b's, the first of them at logical slot prefix_lens[b], its pages at
+// page_tables[b * max_pages ...].
+struct RopeKvAppend {
+  const bf16 *k, *v;
+  long long k_stride, v_stride;
+  const int *positions, *prefix_lens, *offsets, *page_tables;
+  int max_pages, n_seqs, n_tok, Hkv, hd, rope_dim;
+  float rope_base;
+  const float *k_gain;
+  float eps;
+  bf16 *k_pool, *v_pool;
+  int n_pages, pg;
+};
+cudaError_t rope_kv_append(const RopeKvAppend &a, int *err, cudaStream_t st);
+
+struct TreeAttention {
+  const bf16 *q;
+  long long q_stride;
+  const bf16 *k_pool, *v_pool;
+  const int *page_tables;
+  int max_pages;
+  const int *prefix_lens, *offsets;
+  const unsigned long long *mask;  // [n_tok][mask_words], null: causal
+  int mask_words, n_seqs, n_tok, Hq, Hkv, hd, pg, n_pages;
+  float scale;
+  bf16 *out;
+  long long out_stride;
+};
+size_t tree_attention_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int hd);
+cudaError_t tree_attention(const TreeAttention &a, void *ws, int *err, cudaStream_t st);
+
+struct TokenLogprobs {
+  const void *logits;
+  int is_bf16;
+  long long row_stride;
+  int rows, V;
+  float inv_tau;
+  const int *tokens;
+  int n_given;
+  float *logprobs, *entropy, *lse;
+  int top_k;
+  int *top_ids;
+  float *top_logprobs;
+};
+cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st);
+
 }  // namespace dg

@@ -377,7 +377,8 @@ int dg_op_fill_weights(uint16_t *dst, uint64_t n, uint64_t seed, uint32_t tensor
  * synchronises `stream`, returns DG_ETIMEOUT (a wait gave up), DG_ECUDA (a
  * kernel found itself launched without the thread-block cluster shape it
  * exchanges partial results in, and returned before touching anything) or
- * DG_EINVAL (a bad page index) when a kernel-level call since the last
+ * DG_EINVAL (a bad page index, sequence bound or token id, as the call that
+ * reads them says) when a kernel-level call since the last
  * dg_op_status recorded one, and clears the record; DG_OK otherwise.  The record is
  * shared by every kernel-level call on the device, and while it is set later
  * kernel-level kernels skip their waits (their outputs are not valid). */
@@ -548,6 +549,124 @@ int dg_op_kv_append(const uint16_t *k_new, const uint16_t *v_new, uint16_t *k_po
                     uint16_t *v_pool, const int32_t *page_table, int32_t n_layers,
                     int32_t n_pages, int32_t pos0, int32_t n_new, int32_t n_kv_heads,
                     int32_t head_dim, int32_t page_size, void *stream);
+
+/* ---- serving drafted tokens ------------------------------------------------
+ * The four calls below run one after the other when a decoder checks drafted
+ * tokens (or decodes token by token) for a batch of uneven sequences over the
+ * paged cache: queries and keys of the new tokens normed and rotated, keys and
+ * values appended, the new tokens' attention over prefix and draft tree, and
+ * the drafted tokens' log probabilities.  No counterpart in the report, whose
+ * drafts are whole canvases; page and pool layouts are those of
+ * dg_op_canvas_attention, the rotation that of the decoder's own keys.
+ *
+ * Packed rows of a batch: n_tok rows of which rows offsets[b] ..
+ * offsets[b + 1] - 1 belong to sequence b (offsets: device int32
+ * [n_seqs + 1], ascending from 0 or later); the first of them takes the
+ * sequence's logical slot prefix_lens[b] (device int32 [n_seqs]: its cached
+ * tokens).  Rows behind offsets[n_seqs] (a batch padded for a captured step)
+ * are neither read nor written.  Sequence b's logical page j is
+ * page_tables[b * max_pages + j] (device int32 [n_seqs][max_pages]).  Lengths
+ * live on the device, so a captured call can be replayed with other ones.
+ * Rows of heads are `stride` elements apart (a multiple of 8, >= heads *
+ * head_dim: slices of the packed QKV rows will do), heads of a row adjacent;
+ * row addresses are 16-byte aligned.  All calls are asynchronous on `stream`
+ * and can be captured into a CUDA graph. */
+
+/* Per-head RMS norms of queries and keys with the position rotation in the
+ * same pass: for every token t and head row x of q and k
+ *   y = x * rsqrt(mean(x^2) + eps) * gain,
+ *   (y_j, y_{j + r/2}) <- (y_j cos a - y_{j + r/2} sin a, y_{j + r/2} cos a + y_j sin a),
+ *   a = positions[t] * rope_base^(-2 j / r),  j < r / 2,  r = rope_dim,
+ * in fp32 (angles reduced exactly at any position), rounded once to bf16.
+ *   q, k       device rows [n_tok][heads][head_dim], bf16, or fp32 with
+ *              in_f32 != 0 (then strides are multiples of 4); k may be NULL
+ *              with n_kv_heads == 0, q with n_q_heads == 0
+ *   positions  device int32 [n_tok] (may be NULL when rope_dim == 0)
+ *   q_gain,
+ *   k_gain     device fp32 [head_dim], 16-byte aligned; NULL: no norm for
+ *              that side (eps is then unused)
+ *   q_out,
+ *   k_out      device bf16 rows; may be q and k themselves (bf16, the same
+ *              stride), must not overlap them otherwise
+ * head_dim in {64, 128, 256}; rope_dim a multiple of 16 in [0, head_dim];
+ * rope_base >= 1; eps > 0 when a gain is given. */
+int dg_op_qk_norm_rope(const void *q, const void *k, int32_t in_f32, int64_t q_stride,
+                       int64_t k_stride, const int32_t *positions, int32_t n_tok,
+                       int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t rope_dim,
+                       float rope_base, const float *q_gain, const float *k_gain, float eps,
+                       uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out,
+                       int64_t k_out_stride, void *stream);
+
+/* Append new keys and values to the paged cache, the keys normed (k_gain not
+ * NULL) and rotated on the way as in dg_op_qk_norm_rope: row t of sequence b
+ * goes to logical slot prefix_lens[b] + t - offsets[b].
+ *   k, v        device bf16 rows [n_tok][n_kv_heads][head_dim]
+ *   positions   device int32 [n_tok]: the rotation's positions; NULL: each
+ *               row's logical slot (drafted trees have positions of their own:
+ *               prefix_lens[b] + depth)
+ *   k_pool,
+ *   v_pool      device bf16 pools of one layer, layout of
+ *               dg_op_canvas_attention, 16-byte aligned
+ * A row whose slot lies outside the page table (or whose page outside the
+ * pools) is not written and is reported by dg_op_status.  Shapes as
+ * dg_op_qk_norm_rope; page_size >= 1. */
+int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
+                         const int32_t *positions, const int32_t *prefix_lens,
+                         const int32_t *offsets, const int32_t *page_tables, int32_t max_pages,
+                         int32_t n_seqs, int32_t n_tok, int32_t n_kv_heads, int32_t head_dim,
+                         int32_t rope_dim, float rope_base, const float *k_gain, float eps,
+                         uint16_t *k_pool, uint16_t *v_pool, int32_t n_pages, int32_t page_size,
+                         void *stream);
+
+/* Attention of drafted tokens over the paged cache, their own keys and values
+ * already appended: row offsets[b] + t, query head h (KV head h / (Hq / Hkv))
+ *   out = sum_j p_j v_j,  p = softmax_j(scale q . k_j)
+ * over the sequence's prefix_lens[b] cached keys and those of its drafted keys
+ * d (slot prefix_lens[b] + d) that the row sees: bit d % 64 of word
+ * tree_mask[row * mask_words + d / 64] (device uint64; bits past mask_words *
+ * 64 read as 0), or d <= t where tree_mask is NULL (one new token per
+ * sequence: the plain decoding step).  A row that sees no key is zero.
+ *   q, out       device bf16 rows [n_tok][n_q_heads][head_dim]
+ * Keys and values of the sequence's own slots must be finite; the pages' other
+ * slots may hold anything.  A sequence whose rows lie outside [0, n_tok) or
+ * whose slots outside the page table is skipped (its rows are left alone),
+ * keys of a page outside the pools are skipped; both are reported by
+ * dg_op_status.
+ * scale > 0; head_dim in {64, 128}; n_q_heads / n_kv_heads <= 128; page_size a
+ * multiple of 64.  workspace: device scratch of
+ * dg_op_tree_attention_workspace_bytes() bytes, 16-byte aligned, contents
+ * arbitrary; calls that overlap on the GPU need one each. */
+size_t dg_op_tree_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
+                                            int32_t n_kv_heads, int32_t head_dim);
+int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool,
+                         const uint16_t *v_pool, const int32_t *page_tables, int32_t max_pages,
+                         const int32_t *prefix_lens, const int32_t *offsets,
+                         const uint64_t *tree_mask, int32_t mask_words, int32_t n_seqs,
+                         int32_t n_tok, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                         int32_t page_size, int32_t n_pages, float scale, uint16_t *out,
+                         int64_t out_stride, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Log probabilities of given tokens under rows of logits, with the entropy and
+ * the most likely tokens of each row.  With y = fp32(logit * inv_tau)
+ * (inv_tau = 1 / temperature) and lse = log sum_v e^{y_v}:
+ *   logprobs [rows][n_given]     y[tokens[r][j]] - lse; 0 where the id is -1
+ *                                (no token), NaN where it lies outside [0, V)
+ *                                otherwise, reported by dg_op_status
+ *   entropy  [rows]              -sum_v p_v log p_v in nats (may be NULL)
+ *   lse      [rows]              (may be NULL)
+ *   top_ids, top_logprobs [rows][top_k]  the largest logits in descending
+ *                                order, equal ones by ascending index
+ *                                (top_logprobs may be NULL)
+ * logits: device fp32 (bf16 when logits_bf16 != 0) rows, row_stride >= V
+ * elements apart, of the elements' natural alignment.  Entries of -inf have
+ * probability 0 (a row of nothing else: lse -inf, entropy 0, log
+ * probabilities -inf).  A row that holds a NaN, or whose y reaches +inf, gives
+ * NaN throughout (NaN entries order as -inf).  tokens device int32
+ * [rows][n_given]; n_given >= 0; top_k in [0, min(32, V)]; inv_tau > 0. */
+int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_stride, int32_t rows,
+                         int32_t V, float inv_tau, const int32_t *tokens, int32_t n_given,
+                         float *logprobs, float *entropy, float *lse, int32_t top_k,
+                         int32_t *top_ids, float *top_logprobs, void *stream);
 
 #ifdef __cplusplus
 }
