@@ -1727,6 +1727,7 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
                          size_t workspace_bytes, void *stream) {
   if (n_tok < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 128)
     return fail(DG_EINVAL, "unsupported head counts or row count");
+  if ((int64_t)n_tok * n_q_heads > INT32_MAX - 128) return fail(DG_EINVAL, "too many rows of heads");
   if (head_dim != 64 && head_dim != 128) return fail(DG_EINVAL, "head_dim must be 64 or 128");
   if (page_size < 64 || page_size % 64) return fail(DG_EINVAL, "page_size must be a positive multiple of 64");
   if (!(scale > 0.0f && scale < INFINITY)) return fail(DG_EINVAL, "scale must be finite and > 0");

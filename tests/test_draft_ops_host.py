@@ -61,6 +61,7 @@ AT = dict(q=A, qs=2048, k_pool=A, v_pool=A, tables=A, max_pages=4, prefix=A, off
     dict(prefix=None), dict(offsets=None), dict(words=0), dict(mask=None), dict(n_seqs=-1), dict(n_tok=-1), dict(hq=15), dict(hq=0),
     dict(hkv=0), dict(hq=1032), dict(hd=256), dict(pg=32), dict(pg=100), dict(n_pages=0), dict(scale=0.0), dict(scale=-1.0),
     dict(scale=INF), dict(scale=float("nan")), dict(max_pages=-1),
+    dict(n_tok=1 << 28),
 ])
 def test_tree_attention_refuses(L, change):
     assert call(L.dg_op_tree_attention, AT, **change) == dgp.DG_EINVAL
