@@ -12,6 +12,7 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
@@ -587,43 +588,48 @@ def dg_op_kv_append(k_new, v_new, k_pool, v_pool, page_table, n_layers, n_pages,
 
 
 # ---- serving drafted tokens (torch CUDA tensors on the current device) --------
+# The small calls of a decoding step take a few microseconds on the GPU, so the
+# checks here read each tensor attribute once and build no temporaries.
+
+_BF16, _F32, _I32T, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
 
 def _einval(msg):
     raise DgError(DG_EINVAL, msg)
 
 
-def _on_device(*tensors):
-    """All on the current CUDA device (None is skipped)."""
-    import torch
-    cur = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            _einval("a tensor is not on a CUDA device")
-        cur = torch.cuda.current_device() if cur is None else cur
-        if t.get_device() != cur:
-            _einval("a tensor is not on the current CUDA device")
+def _device(t):
+    """The current CUDA device, which t lies on."""
+    if not t.is_cuda:
+        _einval("a tensor is not on a CUDA device")
+    cur = torch.cuda.current_device()
+    if t.get_device() != cur:
+        _einval("a tensor is not on the current CUDA device")
+    return cur
 
 
-def _head_rows(t, what, kinds):
-    """A [rows][heads][hd] tensor whose rows may be strided: its row stride."""
-    if t.dim() != 3 or str(t.dtype) not in kinds:
-        _einval(f"{what} must be [rows][heads][head_dim] of {' or '.join(kinds)}")
-    T, H, hd = t.shape
-    if t.numel() and ((hd > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != hd)):
+def _dense(t, what, kind, shape, dev):
+    """Address of a contiguous tensor of that type, shape and device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not kind or t.shape != shape or not t.is_contiguous():
+        _einval(f"{what} must be a contiguous {kind} tensor of shape {tuple(shape)}")
+    if t.get_device() != dev:
+        _einval(f"{what} is not on the current CUDA device")
+    return t.data_ptr()
+
+
+def _rows(t, what, kind, shape, dev):
+    """(address, row stride) of a [rows][heads][hd] tensor whose rows may be strided."""
+    if t.dtype is not kind or t.shape != shape:
+        _einval(f"{what} must be a {kind} tensor of shape {tuple(shape)}")
+    if t.get_device() != dev:
+        _einval(f"{what} is not on the current CUDA device")
+    row, head, one = t.stride()
+    hd = shape[2]
+    if (one != 1 or (head != hd and shape[1] > 1)) and t.numel():
         _einval(f"{what}: the heads of a row must be adjacent")
-    return t.stride(0) if T > 1 else H * hd
-
-
-def _dense(t, what, kind, shape):
-    """A contiguous tensor of that type and shape (None entries: any extent)."""
-    if str(t.dtype) != kind or t.dim() != len(shape) or not t.is_contiguous() or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)):
-        _einval(f"{what} must be a contiguous {kind} tensor of shape {tuple('*' if n is None else n for n in shape)}")
-
-
-_BF16, _F32, _I32T, _I64T = "torch.bfloat16", "torch.float32", "torch.int32", "torch.int64"
+    return t.data_ptr(), row if shape[0] > 1 else shape[1] * hd
 
 
 def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, eps=1e-6, rope_base=10000.0,
@@ -632,42 +638,31 @@ def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, 
     bf16 of the same shapes; positions int32 [T]; gains fp32 [hd] or None (no
     norm).  k and k_out (or q and q_out) may be None."""
     some = q if q is not None else k
-    if some is None:
-        _einval("q and k are both None")
-    _on_device(q, k, positions, q_out, k_out, q_gain, k_gain)
-    side = []
-    for x, o, what in ((q, q_out, "q"), (k, k_out, "k")):
-        if (x is None) != (o is None):
-            _einval(f"{what} and {what}_out go together")
-        if x is None:
-            side.append((0, 0, 0))
-            continue
-        side.append((x.shape[1] if x.dim() == 3 else 0, _head_rows(x, what, (_BF16, _F32)),
-                     _head_rows(o, what + "_out", (_BF16,))))
-        if x.dtype != some.dtype or x.shape[0] != some.shape[0] or x.shape[2] != some.shape[2] or o.shape != x.shape:
-            _einval("q, k and their outputs must agree in rows, head_dim and (inputs) type")
+    if some is None or some.dim() != 3 or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        _einval("q and q_out, k and k_out go together, [rows][heads][head_dim] each, and one pair is needed")
+    dev = _device(some)
+    kind = some.dtype
+    if kind is not _BF16 and kind is not _F32:
+        _einval("q and k must be bf16 or fp32")
     T, _, hd = some.shape
-    if positions is not None:
-        _dense(positions, "positions", _I32T, (T,))
-    for gain in (q_gain, k_gain):
-        if gain is not None:
-            _dense(gain, "a gain", _F32, (hd,))
-    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    (hq, qs, qos), (hkv, ks, kos) = side
-    _check(load().dg_op_qk_norm_rope(addr(q), addr(k), int(str(some.dtype) == _F32), qs, ks, addr(positions), T, hq,
-                                     hkv, hd, hd if rope_dim is None else rope_dim, rope_base, addr(q_gain),
-                                     addr(k_gain), eps, addr(q_out), qos, addr(k_out), kos, _stream(stream)))
-
-
-def _batch_args(k_pool, v_pool, page_tables, prefix_lens, offsets):
-    """Checked (n_pages, Hkv, page_size, hd, n_seqs, max_pages) of a batch over the pools."""
-    _dense(k_pool, "k_pool", _BF16, (None,) * 4)
-    _dense(v_pool, "v_pool", _BF16, k_pool.shape)
-    _dense(prefix_lens, "prefix_lens", _I32T, (None,))
-    B = prefix_lens.shape[0]
-    _dense(offsets, "offsets", _I32T, (B + 1,))
-    _dense(page_tables, "page_tables", _I32T, (B, None))
-    return (*k_pool.shape, B, page_tables.shape[1])
+    hq = hkv = 0
+    qp = qs = qo = qos = kp = ks = ko = kos = None
+    if q is not None:
+        shape = q.shape
+        hq = shape[1]
+        qp, qs = _rows(q, "q", kind, shape, dev)
+        qo, qos = _rows(q_out, "q_out", _BF16, shape, dev)
+    if k is not None:
+        shape = k.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != hd:
+            _einval("q and k must agree in rows and head_dim")
+        hkv = shape[1]
+        kp, ks = _rows(k, "k", kind, shape, dev)
+        ko, kos = _rows(k_out, "k_out", _BF16, shape, dev)
+    _check(load().dg_op_qk_norm_rope(
+        qp, kp, 1 if kind is _F32 else 0, qs or 0, ks or 0, _dense(positions, "positions", _I32T, (T,), dev), T, hq,
+        hkv, hd, hd if rope_dim is None else rope_dim, rope_base, _dense(q_gain, "q_gain", _F32, (hd,), dev),
+        _dense(k_gain, "k_gain", _F32, (hd,), dev), eps, qo, qos or 0, ko, kos or 0, _stream(stream)))
 
 
 def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets, positions=None, k_gain=None,
@@ -675,21 +670,23 @@ def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets
     """k, v: [T][Hkv][hd] bf16 (rows may be strided); pools
     [n_pages][Hkv][page_size][hd]; page_tables int32 [B][max_pages];
     prefix_lens int32 [B]; offsets int32 [B + 1]."""
-    _on_device(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets, positions, k_gain)
-    n_pages, hkv, pg, hd, B, max_pages = _batch_args(k_pool, v_pool, page_tables, prefix_lens, offsets)
-    ks, vs = _head_rows(k, "k", (_BF16,)), _head_rows(v, "v", (_BF16,))
+    dev = _device(k_pool)
+    pool, table = k_pool.shape, page_tables.shape
+    if len(pool) != 4 or len(table) != 2 or k.dim() != 3:
+        _einval("pools are [n_pages][heads][page_size][head_dim], page_tables [sequences][pages], k and v [rows][heads][head_dim]")
+    n_pages, hkv, pg, hd = pool
+    B, max_pages = table
     T = k.shape[0]
-    if k.shape != v.shape or k.shape[1] != hkv or k.shape[2] != hd:
-        _einval("k and v must be [rows][heads][head_dim] of the pools' heads")
-    if positions is not None:
-        _dense(positions, "positions", _I32T, (T,))
-    if k_gain is not None:
-        _dense(k_gain, "k_gain", _F32, (hd,))
-    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _check(load().dg_op_rope_kv_append(addr(k), addr(v), ks, vs, addr(positions), addr(prefix_lens), addr(offsets),
-                                       addr(page_tables), max_pages, B, T, hkv, hd,
-                                       hd if rope_dim is None else rope_dim, rope_base, addr(k_gain), eps,
-                                       addr(k_pool), addr(v_pool), n_pages, pg, _stream(stream)))
+    shape = (T, hkv, hd)
+    kp, ks = _rows(k, "k", _BF16, shape, dev)
+    vp, vs = _rows(v, "v", _BF16, shape, dev)
+    _check(load().dg_op_rope_kv_append(
+        kp, vp, ks, vs, _dense(positions, "positions", _I32T, (T,), dev),
+        _dense(prefix_lens, "prefix_lens", _I32T, (B,), dev), _dense(offsets, "offsets", _I32T, (B + 1,), dev),
+        _dense(page_tables, "page_tables", _I32T, table, dev), max_pages, B, T, hkv, hd,
+        hd if rope_dim is None else rope_dim, rope_base, _dense(k_gain, "k_gain", _F32, (hd,), dev), eps,
+        _dense(k_pool, "k_pool", _BF16, pool, dev), _dense(v_pool, "v_pool", _BF16, pool, dev), n_pages, pg,
+        _stream(stream)))
 
 
 def dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd):
@@ -700,25 +697,31 @@ def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, t
                          stream=None):
     """q, out: [T][Hq][hd] bf16 (rows may be strided); tree_mask int64
     [T][words] (bit d: the row sees drafted token d of its sequence) or None
-    (causal); scale None: 1 / sqrt(hd)."""
-    _on_device(q, k_pool, v_pool, page_tables, prefix_lens, offsets, tree_mask, out, workspace)
-    n_pages, hkv, pg, hd, B, max_pages = _batch_args(k_pool, v_pool, page_tables, prefix_lens, offsets)
-    qs, os_ = _head_rows(q, "q", (_BF16,)), _head_rows(out, "out", (_BF16,))
-    T, hq, _ = q.shape
-    if out.shape != q.shape or q.shape[2] != hd:
-        _einval("q and out must be [rows][heads][head_dim] of the pools' head_dim")
-    words = 0
-    if tree_mask is not None:
-        _dense(tree_mask, "tree_mask", _I64T, (T, None))
-        words = tree_mask.shape[1]
-    if workspace is not None and not workspace.is_contiguous():
-        _einval("the workspace must be contiguous")
-    _check(load().dg_op_tree_attention(q.data_ptr(), qs, k_pool.data_ptr(), v_pool.data_ptr(), page_tables.data_ptr(),
-                                       max_pages, prefix_lens.data_ptr(), offsets.data_ptr(),
-                                       tree_mask.data_ptr() if words else None, words, B, T, hq, hkv, hd, pg, n_pages,
-                                       hd ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                                       None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
-                                       _stream(stream)))
+    (causal); workspace: a contiguous tensor or None; scale None: 1 / sqrt(hd)."""
+    dev = _device(k_pool)
+    pool, table, shape = k_pool.shape, page_tables.shape, q.shape
+    if len(pool) != 4 or len(table) != 2 or len(shape) != 3 or shape[2] != pool[3]:
+        _einval("pools are [n_pages][heads][page_size][head_dim], page_tables [sequences][pages], q [rows][heads][head_dim]")
+    n_pages, hkv, pg, hd = pool
+    B, max_pages = table
+    T = shape[0]
+    qp, qs = _rows(q, "q", _BF16, shape, dev)
+    op, os_ = _rows(out, "out", _BF16, shape, dev)
+    mp, words = None, 0
+    if tree_mask is not None and T:
+        words = tree_mask.shape[-1]
+        mp = _dense(tree_mask, "tree_mask", _I64T, (T, words), dev)
+    wp, wn = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            _einval("the workspace must be contiguous, on the current CUDA device")
+        wp, wn = workspace.data_ptr(), workspace.nbytes
+    _check(load().dg_op_tree_attention(
+        qp, qs, _dense(k_pool, "k_pool", _BF16, pool, dev), _dense(v_pool, "v_pool", _BF16, pool, dev),
+        _dense(page_tables, "page_tables", _I32T, table, dev), max_pages,
+        _dense(prefix_lens, "prefix_lens", _I32T, (B,), dev), _dense(offsets, "offsets", _I32T, (B + 1,), dev), mp,
+        words, B, T, shape[1], hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, wp, wn,
+        _stream(stream)))
 
 
 def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_ids=None, top_logprobs=None,
@@ -726,25 +729,22 @@ def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_i
     """logits: [T][V] fp32 or bf16 (rows may be strided); tokens int32
     [T][given] and logprobs fp32 [T][given] (None: none given); entropy, lse
     fp32 [T]; top_ids int32 [T][k], top_logprobs fp32 [T][k]."""
-    _on_device(logits, tokens, logprobs, entropy, lse, top_ids, top_logprobs)
-    kind = str(logits.dtype)
-    if logits.dim() != 2 or kind not in (_BF16, _F32) or (logits.numel() and logits.shape[1] > 1 and logits.stride(1) != 1):
-        _einval("logits must be [rows][vocab] of fp32 or bf16 with adjacent entries")
+    dev = _device(logits)
+    kind = logits.dtype
+    if logits.dim() != 2 or (kind is not _BF16 and kind is not _F32):
+        _einval("logits must be [rows][vocab] of fp32 or bf16")
     T, V = logits.shape
+    row, one = logits.stride()
+    if one != 1 and V > 1:
+        _einval("logits: the entries of a row must be adjacent")
     if (tokens is None) != (logprobs is None) or (top_ids is None and top_logprobs is not None):
         _einval("tokens go with logprobs, top_logprobs with top_ids")
-    given = k = 0
-    if tokens is not None:
-        _dense(tokens, "tokens", _I32T, (T, None))
-        given = tokens.shape[1]
-        _dense(logprobs, "logprobs", _F32, (T, given))
-    if top_ids is not None:
-        _dense(top_ids, "top_ids", _I32T, (T, None))
-        k = top_ids.shape[1]
-    for t, what, shape in ((entropy, "entropy", (T,)), (lse, "lse", (T,)), (top_logprobs, "top_logprobs", (T, k))):
-        if t is not None:
-            _dense(t, what, _F32, shape)
-    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _check(load().dg_op_token_logprobs(logits.data_ptr(), int(kind == _BF16), logits.stride(0) if T > 1 else V, T, V,
-                                       inv_tau, addr(tokens), given, addr(logprobs), addr(entropy), addr(lse), k,
-                                       addr(top_ids), addr(top_logprobs), _stream(stream)))
+    given = 0 if tokens is None else tokens.shape[-1]
+    k = 0 if top_ids is None else top_ids.shape[-1]
+    rows, pairs, tops = (T,), (T, given), (T, k)
+    _check(load().dg_op_token_logprobs(
+        logits.data_ptr(), 1 if kind is _BF16 else 0, row if T > 1 else V, T, V, inv_tau,
+        _dense(tokens, "tokens", _I32T, pairs, dev), given, _dense(logprobs, "logprobs", _F32, pairs, dev),
+        _dense(entropy, "entropy", _F32, rows, dev), _dense(lse, "lse", _F32, rows, dev), k,
+        _dense(top_ids, "top_ids", _I32T, tops, dev), _dense(top_logprobs, "top_logprobs", _F32, tops, dev),
+        _stream(stream)))

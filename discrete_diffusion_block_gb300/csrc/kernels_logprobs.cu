@@ -3,146 +3,383 @@
 // S = sum e^(y - m), A = sum e^(y - m) (y - m):
 //   log p(v) = (y_v - m) - log S,  lse = m + log S,  entropy = log S - A / S.
 //
-// One block per row; the row is read once.  Each thread keeps a running
-// (m, S, A) of its entries and each warp a list of its 32 best entries, one a
-// lane, in descending order: an entry enters it when it beats the list's last.
-// Entries are ordered by a 64-bit key (order-preserving bits of the value,
-// then the complement of the index), so equal values go to the lower index.
+// Bound by the logits' bytes, each read once.  A row is split over the blocks
+// of a cluster when there are fewer rows than blocks fit the machine, and
+// their states joined through distributed shared memory (one launch, no
+// workspace).  A thread takes a batch of kVecs 16-byte vectors at a time, the
+// next batch already in flight, and moves its running maximum once per batch;
+// sums are kept in units of log2, fp32.
+//
+// The most likely tokens: each warp keeps a list of its 32 best entries, one a
+// lane, in descending order of a 64-bit key (order-preserving bits of the
+// value, then the complement of the index: equal values go to the lower
+// index).  A list starts empty, so nearly every entry of a warp's first
+// batches would enter it; the k-th largest of the block's thread maxima of the
+// first batch is a lower bound of the block's k-th best entry, and entries
+// below it are dropped at one compare per batch: of a row of 262144 random
+// logits about k * 262144 / 8192 reach a list, however many warps share it.
+#include "gemm_tc.cuh"
 #include "internal.h"
 
 namespace dg {
 
 namespace {
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
+constexpr int kVecs = 4;            // 16-byte vectors of a thread's batch
+constexpr int kMaxLpCluster = 16;   // blocks of a row (a non-portable cluster size)
+constexpr float kLn2f = 0.693147180559945309f;
 
+// m: largest raw logit; s = sum 2^d, a = sum 2^d d with d = (x - m) c.
 struct RowSum {
   float m, s, a;
 };
 
-__device__ __forceinline__ RowSum merge(const RowSum &x, const RowSum &y) {
-  RowSum o;
-  o.m = fmaxf(x.m, y.m);
-  if (o.m == -INFINITY) return RowSum{-INFINITY, 0.0f, 0.0f};
-  const float dx = x.m - o.m, dy = y.m - o.m;
-  const float ex = x.m == -INFINITY ? 0.0f : expf(dx), ey = y.m == -INFINITY ? 0.0f : expf(dy);
-  o.s = x.s * ex + y.s * ey;
-  o.a = (ex > 0.0f ? ex * (x.a + dx * x.s) : 0.0f) + (ey > 0.0f ? ey * (y.a + dy * y.s) : 0.0f);
-  return o;
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__device__ __forceinline__ unsigned long long order_key(float v, int i) {
-  uint32_t b = __float_as_uint(v + 0.0f);  // -0 counts as 0
-  if (v != v) b = 0xff800000u;              // NaN orders as -inf
-  b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return ((unsigned long long)b << 32) | (uint32_t)~i;
+// (s, a) moved to a reference maximum that is larger by -d / c.
+__device__ __forceinline__ void rebase(RowSum &r, float m, float c) {
+  if (r.m > -INFINITY) {
+    const float d = (r.m - m) * c, f = ex2_approx(d);
+    r.a = f > 0.0f ? f * (r.a + d * r.s) : 0.0f;
+    r.s *= f;
+  }
+  r.m = m;
 }
-__device__ __forceinline__ float key_value(unsigned long long k) {
-  const uint32_t b = (uint32_t)(k >> 32);
+
+__device__ __forceinline__ RowSum merge(RowSum x, RowSum y, float c) {
+  const float m = fmaxf(x.m, y.m);
+  rebase(x, m, c);
+  rebase(y, m, c);
+  return RowSum{m, x.s + y.s, x.a + y.a};
+}
+
+// Order-preserving bits of a value; NaN counts as -inf, -0 as 0.  0 is below all.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = v != v ? 0xff800000u : __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t b) {
   return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
 }
 
-// The 32 best of two descending lists, one entry a lane, descending.
-__device__ __forceinline__ unsigned long long merge_lists(unsigned long long x, unsigned long long y) {
+template <typename K>
+__device__ __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
+template <typename K>
+__device__ __forceinline__ K smaller(K a, K b) { return a < b ? a : b; }
+
+// The 32 largest of two descending lists, one entry a lane, descending.
+template <typename K>
+__device__ __forceinline__ K merge_lists(K x, K y) {
   const int lane = threadIdx.x & 31;
-  const unsigned long long r = __shfl_sync(0xffffffffu, y, 31 - lane);
-  x = x > r ? x : r;  // bitonic: the 32 best
+  x = larger(x, __shfl_sync(0xffffffffu, y, 31 - lane));  // bitonic
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    const unsigned long long z = __shfl_xor_sync(0xffffffffu, x, o);
-    x = (lane & o) ? (x < z ? x : z) : (x > z ? x : z);
+    const K z = __shfl_xor_sync(0xffffffffu, x, o);
+    x = (lane & o) ? smaller(x, z) : larger(x, z);
   }
   return x;
 }
 
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const bf16 *p) { return __bfloat162float(*p); }
+// 32 entries, one a lane, into descending order.
+template <typename K>
+__device__ __forceinline__ K sort_lanes(K x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+    for (int o = n >> 1; o; o >>= 1) {
+      const K z = __shfl_xor_sync(0xffffffffu, x, o);
+      const bool first = !(lane & o), down = !(lane & n);
+      x = (first == down) ? larger(x, z) : smaller(x, z);
+    }
+  return x;
+}
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const TokenLogprobs p, int *err) {
-  __shared__ RowSum s_sum[kLpThreads / 32];
-  __shared__ unsigned long long s_top[kLpThreads / 32][32];
-  __shared__ int s_bad;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x;
-  const T *x = (const T *)p.logits + row * p.row_stride;
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  RowSum r{-INFINITY, 0.0f, 0.0f};
-  unsigned long long best = 0;
-  bool bad = false;
-  for (int base = warp * 32; base < p.V; base += kLpThreads) {
-    const int v = base + lane;
-    const bool in = v < p.V;
-    const float raw = in ? load1(x + v) : -INFINITY;
-    const float y = raw * p.inv_tau;
-    bad |= !(y < INFINITY);
-    if (y > -INFINITY) r = merge(r, RowSum{y, 1.0f, 0.0f});
-    if (p.top_k) {
-      unsigned long long k = in ? order_key(raw, v) : 0;
-      unsigned todo = __ballot_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, best, 31));
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const unsigned long long n = __shfl_sync(0xffffffffu, k, src);
-        const int at = __popc(__ballot_sync(0xffffffffu, best > n));  // entries before it
-        const unsigned long long up = __shfl_up_sync(0xffffffffu, best, 1);
-        if (lane == at) best = n;
-        else if (lane > at) best = up;
-      }
+// The block's warps' lists (one per warp, kLpWarps of them) joined in shared
+// memory, pairwise; list[0] holds the result after the call.
+template <typename K>
+__device__ __forceinline__ void join_lists(K (*list)[32], K mine) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  list[warp][lane] = mine;
+#pragma unroll
+  for (int n = kLpWarps / 2; n; n >>= 1) {
+    __syncthreads();
+    if (warp < n) {
+      mine = merge_lists(mine, list[warp + n][lane]);
+      list[warp][lane] = mine;
     }
   }
-  if (bad) s_bad = 1;
+  __syncthreads();
+}
+
+// Elements of a thread's batch, held as loaded.
+template <typename T>
+struct Batch;
+template <>
+struct Batch<float> {
+  static constexpr int E = 4;  // elements of a vector
+  uint4 r[kVecs];
+  __device__ __forceinline__ float at(int j) const { return __uint_as_float((&r[j >> 2].x)[j & 3]); }
+  __device__ __forceinline__ float max() const {
+    float m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = at(j);
+#pragma unroll
+    for (int j = 4; j < 4 * kVecs; ++j) m[j & 3] = fmaxf(m[j & 3], at(j));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  }
+  static __device__ __forceinline__ uint32_t absent() { return 0xff800000u; }
+};
+template <>
+struct Batch<bf16> {
+  static constexpr int E = 8;
+  uint4 r[kVecs];
+  __device__ __forceinline__ float at(int j) const {
+    const uint32_t w = (&r[j >> 3].x)[(j >> 1) & 3];
+    return __uint_as_float((j & 1) ? w & 0xffff0000u : w << 16);
+  }
+  __device__ __forceinline__ float max() const {
+    __nv_bfloat162 m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = *(const __nv_bfloat162 *)(&r[0].x + j);
+#pragma unroll
+    for (int j = 4; j < 4 * kVecs; ++j) m[j & 3] = __hmax2(m[j & 3], *(const __nv_bfloat162 *)(&r[j >> 2].x + (j & 3)));
+    const __nv_bfloat162 a = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+    return fmaxf(__low2float(a), __high2float(a));
+  }
+  static __device__ __forceinline__ uint32_t absent() { return 0xff80ff80u; }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t elem_bits(const T *p);
+template <>
+__device__ __forceinline__ uint32_t elem_bits<float>(const float *p) { return __float_as_uint(*p); }
+template <>
+__device__ __forceinline__ uint32_t elem_bits<bf16>(const bf16 *p) { return *(const uint16_t *)p; }
+
+struct LpArgs {
+  TokenLogprobs a;
+  float c;       // log2(e) / tau
+  int cluster;   // blocks per row
+  int *err;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __grid_constant__ LpArgs p) {
+  constexpr int E = Batch<T>::E, N = E * kVecs;
+  __shared__ unsigned long long s_top[kLpWarps][32];
+  __shared__ uint32_t s_bound[kLpWarps][32];
+  __shared__ RowSum s_sum[kLpWarps];
+  // every block of the launch sees the same cluster size
+  if (p.cluster > 1 && cluster_ctas() != (uint32_t)p.cluster) {
+    if (threadIdx.x == 0 && p.err) atomicExch(p.err, kShapeErrorBase + 4);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x / p.cluster, rank = blockIdx.x - row * p.cluster;
+  const int V = p.a.V, k = p.a.top_k;
+  const T *x = (const T *)p.a.logits + (size_t)row * p.a.row_stride;
+  // 16-byte vectors from the boundary at or before the row on; vector j holds
+  // the entries j E - lead ..; entries outside the row are not read
+  const int lead = (int)(((uintptr_t)x & 15) / sizeof(T));
+  const long long n_vec = ((long long)V + lead + E - 1) / E;
+  const long long per = (n_vec + p.cluster - 1) / p.cluster;
+  const long long v_begin = per * rank, v_end = min(n_vec, v_begin + per);
+  auto load = [&](Batch<T> &b, long long v0) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const long long v = v0 + u * kLpThreads + threadIdx.x, i0 = v * E - lead;
+      if (v < v_end && i0 >= 0 && i0 + E <= V) {
+        b.r[u] = __ldcs((const uint4 *)(x + i0));
+      } else {
+        uint32_t w[4] = {Batch<T>::absent(), Batch<T>::absent(), Batch<T>::absent(), Batch<T>::absent()};
+        if (v < v_end) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (i0 + e >= 0 && i0 + e < V) {
+              const uint32_t bits = elem_bits(x + i0 + e);
+              if (sizeof(T) == 4) w[e & 3] = bits;
+              else w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | (bits << 16) : (w[e >> 1] & 0xffff0000u) | bits;
+            }
+        }
+        b.r[u] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  };
+
+  RowSum r{-INFINITY, 0.0f, 0.0f};
+  unsigned long long best = 0, kth = 0;  // the warp's list; its k-th entry
+  uint32_t bound = 0;                    // entries below it are not among the block's k best
+  Batch<T> cur, nxt;
+  constexpr long long kStep = (long long)kLpThreads * kVecs;
+  load(cur, v_begin);
+  for (long long v0 = v_begin; v0 < v_end; v0 += kStep) {
+    if (v0 + kStep < v_end) load(nxt, v0 + kStep);
+    const float mb = cur.max();
+    if (mb > r.m) rebase(r, mb, p.c);
+    const float m = r.m > -INFINITY ? r.m : 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float d = (cur.at(j) - m) * p.c, e = ex2_approx(d);
+      r.s += e;  // NaN here marks the row
+      r.a += e * fmaxf(d, -1000.0f);
+    }
+    if (k) {
+      const uint32_t ob = order_bits(mb);
+      if (v0 == v_begin) {  // the block's bound; a thread without entries has none
+        const long long first = v0 + threadIdx.x;
+        join_lists(s_bound, sort_lanes(first < v_end && (first + 1) * E > lead ? ob : 0u));
+        bound = s_bound[0][k - 1];
+      }
+      // later batches hold higher indices, so an equal value does not enter a full list
+      if (__any_sync(0xffffffffu, ob >= bound && (ob > (uint32_t)(kth >> 32) || kth == 0))) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const long long i = (v0 + (j / E) * kLpThreads + threadIdx.x) * E - lead + j % E;
+          const uint32_t o = order_bits(cur.at(j));
+          const unsigned long long key = ((unsigned long long)o << 32) | (uint32_t)~(uint32_t)i;
+          const bool in = v0 + (j / E) * kLpThreads + threadIdx.x < v_end && i >= 0 && i < V;
+          unsigned todo = __ballot_sync(0xffffffffu, in && o >= bound && key > kth);
+          while (todo) {
+            const unsigned long long n = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
+            const int at = __popc(__ballot_sync(0xffffffffu, best > n));  // entries before it
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, best, 1);
+            if (lane == at) best = n;
+            else if (lane > at) best = up;
+            kth = __shfl_sync(0xffffffffu, best, k - 1);
+            todo &= todo - 1;
+            todo &= __ballot_sync(0xffffffffu, key > kth);
+          }
+        }
+      }
+    }
+    cur = nxt;
+  }
+
+  // ---- the block's state, then the row's ------------------------------------------
   for (int o = 16; o; o >>= 1) {
     RowSum q;
     q.m = __shfl_xor_sync(0xffffffffu, r.m, o);
     q.s = __shfl_xor_sync(0xffffffffu, r.s, o);
     q.a = __shfl_xor_sync(0xffffffffu, r.a, o);
-    r = merge(r, q);
+    r = merge(r, q, p.c);
   }
   if (lane == 0) s_sum[warp] = r;
-  s_top[warp][lane] = best;
-  __syncthreads();
-  if (warp != 0) return;
-  r = s_sum[0];
-  for (int w = 1; w < kLpThreads / 32; ++w) {
-    r = merge(r, s_sum[w]);
-    best = merge_lists(best, s_top[w][lane]);
+  if (k) join_lists(s_top, best);
+  else __syncthreads();
+  if (warp == 0) {
+    r = s_sum[0];
+    for (int w = 1; w < kLpWarps; ++w) r = merge(r, s_sum[w], p.c);
   }
+  if (p.cluster > 1) {
+    __syncthreads();
+    if (threadIdx.x == 0) s_sum[0] = r;
+    __syncwarp();
+    tc::cluster_sync();
+    if (rank == 0) {  // warp w takes block w's state
+      RowSum q{-INFINITY, 0.0f, 0.0f};
+      unsigned long long l = 0;
+      if (warp < p.cluster) {
+        const uint32_t at = tc::cluster_addr(tc::smem_u32(&s_sum[0]), (uint32_t)warp);
+        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(q.m) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(q.s) : "r"(at + 4) : "memory");
+        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(q.a) : "r"(at + 8) : "memory");
+        asm volatile("ld.shared::cluster.u64 %0, [%1];\n"
+                     : "=l"(l)
+                     : "r"(tc::cluster_addr(tc::smem_u32(&s_top[0][lane]), (uint32_t)warp))
+                     : "memory");
+      }
+      __syncthreads();  // this block's own state is read before it is overwritten
+      if (lane == 0) s_sum[warp] = q;
+      if (k) join_lists(s_top, l);
+      else __syncthreads();
+      if (warp == 0) {
+        r = s_sum[0];
+        for (int w = 1; w < p.cluster; ++w) r = merge(r, s_sum[w], p.c);
+      }
+    }
+    __syncwarp();
+    tc::cluster_sync();  // the peers' states have been read
+  }
+  if (rank != 0 || warp != 0) return;
   const float nan = __int_as_float(0x7fc00000);
-  const float logs = s_bad ? nan : (r.s > 0.0f ? logf(r.s) : 0.0f);
+  const float top = r.m * p.a.inv_tau;
+  const bool bad = !(r.s >= 0.0f) || top == INFINITY;  // a NaN entry, or +inf
+  const float logs = bad ? nan : (r.s > 0.0f ? logf(r.s) : 0.0f);
   auto logprob = [&](float raw) {
-    if (s_bad) return nan;
-    return raw == -INFINITY ? raw : (raw * p.inv_tau - r.m) - logs;
+    if (bad) return nan;
+    return raw == -INFINITY ? raw : (raw * p.a.inv_tau - top) - logs;
   };
   if (lane == 0) {
-    if (p.lse) p.lse[row] = r.m + logs;
-    if (p.entropy) p.entropy[row] = s_bad ? nan : (r.s > 0.0f ? logs - r.a / r.s : 0.0f);
+    if (p.a.lse) p.a.lse[row] = top + logs;
+    if (p.a.entropy) p.a.entropy[row] = bad ? nan : (r.s > 0.0f ? logs - kLn2f * (r.a / r.s) : 0.0f);
   }
-  if (lane < p.top_k) {
-    p.top_ids[(long long)row * p.top_k + lane] = (int)~(uint32_t)best;
-    if (p.top_logprobs) p.top_logprobs[(long long)row * p.top_k + lane] = logprob(key_value(best));
+  if (lane < k) {
+    const unsigned long long key = s_top[0][lane];
+    p.a.top_ids[(size_t)row * k + lane] = (int)~(uint32_t)key;
+    if (p.a.top_logprobs) p.a.top_logprobs[(size_t)row * k + lane] = logprob(order_value((uint32_t)(key >> 32)));
   }
-  for (int j = lane; j < p.n_given; j += 32) {
-    const long long at = (long long)row * p.n_given + j;
-    const int id = p.tokens[at];
+  for (int j = lane; j < p.a.n_given; j += 32) {
+    const size_t at = (size_t)row * p.a.n_given + j;
+    const int id = p.a.tokens[at];
     float lp = 0.0f;  // -1: no token here
-    if (id >= 0 && id < p.V) {
-      lp = logprob(load1(x + id));
+    if (id >= 0 && id < V) {
+      const uint32_t b = elem_bits(x + id);
+      lp = logprob(__uint_as_float(sizeof(T) == 4 ? b : b << 16));
     } else if (id != -1) {
       lp = nan;
-      if (err) atomicExch(err + 1, kBadToken);
+      if (p.err) atomicExch(p.err + 1, kBadToken);
     }
-    p.logprobs[at] = lp;
+    p.a.logprobs[at] = lp;
   }
+}
+
+template <typename T>
+cudaError_t launch(const LpArgs &p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.a.rows * p.cluster);
+  cfg.blockDim = dim3(kLpThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  if (p.cluster > 1) {
+    if (p.cluster > 8) {
+      static unsigned long long attr_set = 0;
+      int dev = 0;
+      cudaError_t e = cudaGetDevice(&dev);
+      if (e != cudaSuccess) return e;
+      if (dev >= 64 || !((attr_set >> dev) & 1ull)) {
+        e = cudaFuncSetAttribute(token_logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set |= 1ull << dev;
+      }
+    }
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, p);
 }
 
 }  // namespace
 
 cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
-  if (a.is_bf16) token_logprobs_kernel<bf16><<<a.rows, kLpThreads, 0, st>>>(a, err);
-  else token_logprobs_kernel<float><<<a.rows, kLpThreads, 0, st>>>(a, err);
-  return cudaGetLastError();
+  LpArgs p;
+  p.a = a;
+  p.c = (float)(1.4426950408889634 * (double)a.inv_tau);
+  p.err = err;
+  // blocks per row: two for every SM in all, no fewer than 8192 entries each
+  int c = 1;
+  while (c < kMaxLpCluster && (long long)a.rows * c * 2 <= 2 * 152 && a.V / (2 * c) >= 8192) c *= 2;
+  p.cluster = c;
+  return a.is_bf16 ? launch<bf16>(p, st) : launch<float>(p, st);
 }
 
 }  // namespace dg
