@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   uint32_t bound = 0;                    // entries below it are not among the block's k best
   Batch<T> cur, nxt;
   constexpr long long kStep = (long long)kLpThreads * kVecs;
+  long long refresh = v_begin + kStep;  // the batch after which the bound is renewed
   load(cur, v_begin);
   for (long long v0 = v_begin; v0 < v_end; v0 += kStep) {
     if (v0 + kStep < v_end) load(nxt, v0 + kStep);
@@ -232,19 +233,28 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
     if (k) {
       const uint32_t ob = order_bits(mb);
       if (v0 == v_begin) {  // the block's bound; a thread without entries has none
-        const long long first = v0 + threadIdx.x;
-        join_lists(s_bound, sort_lanes(first < v_end && (first + 1) * E > lead ? ob : 0u));
+        join_lists(s_bound, sort_lanes(v0 + threadIdx.x < v_end ? ob : 0u));
         bound = s_bound[0][k - 1];
       }
       // later batches hold higher indices, so an equal value does not enter a full list
       if (__any_sync(0xffffffffu, ob >= bound && (ob > (uint32_t)(kth >> 32) || kth == 0))) {
+        // the lane's candidates (NaN among them: the exact test drops it)
+        const uint32_t low = larger(bound, (uint32_t)(kth >> 32));
+        const float lim = low ? order_value(low) : -INFINITY;
+        uint32_t mask = 0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const long long i = (v0 + (j / E) * kLpThreads + threadIdx.x) * E - lead + j % E;
-          const uint32_t o = order_bits(cur.at(j));
+        for (int j = 0; j < N; ++j) mask |= cur.at(j) < lim ? 0u : 1u << j;
+        while (__any_sync(0xffffffffu, mask != 0)) {
+          const int j = __ffs(mask) - 1;
+          float v = 0.0f;
+#pragma unroll
+          for (int q = 0; q < N; ++q)
+            if (q == j) v = cur.at(q);
+          const long long at_v = v0 + (j / E) * kLpThreads + threadIdx.x, i = at_v * E - lead + j % E;
+          const uint32_t o = order_bits(v);
           const unsigned long long key = ((unsigned long long)o << 32) | (uint32_t)~(uint32_t)i;
-          const bool in = v0 + (j / E) * kLpThreads + threadIdx.x < v_end && i >= 0 && i < V;
-          unsigned todo = __ballot_sync(0xffffffffu, in && o >= bound && key > kth);
+          unsigned todo = __ballot_sync(0xffffffffu, mask && at_v < v_end && i >= 0 && i < V && o >= bound && key > kth);
+          mask &= mask - 1;
           while (todo) {
             const unsigned long long n = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
             const int at = __popc(__ballot_sync(0xffffffffu, best > n));  // entries before it
@@ -255,6 +265,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
             todo &= todo - 1;
             todo &= __ballot_sync(0xffffffffu, key > kth);
           }
+        }
+      }
+      // after 2, 4, 8 ... batches: the k-th entry of all the block's lists so far
+      if (v0 == refresh) {
+        refresh = v_begin + 2 * (refresh + kStep - v_begin) - kStep;
+        if (v0 + kStep < v_end) {
+          join_lists(s_bound, (uint32_t)(best >> 32));
+          bound = larger(bound, s_bound[0][k - 1]);
         }
       }
     }
