@@ -1671,6 +1671,7 @@ int dg_op_qk_norm_rope(const void *q, const void *k, int32_t in_f32, int64_t q_s
                        const float *k_gain, float eps, uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out,
                        int64_t k_out_stride, void *stream) {
   if (n_q_heads < 0 || n_kv_heads < 0) return fail(DG_EINVAL, "negative head count");
+  if ((int64_t)n_tok * ((int64_t)n_q_heads + n_kv_heads) >= 1 << 30) return fail(DG_EINVAL, "too many rows of heads");
   CKR(check_rope(n_tok, head_dim, rope_dim, rope_base, q_gain || k_gain, eps));
   const int e16 = in_f32 ? 4 : 8;
   CKR(check_rows("q", q, q_stride, n_tok, n_q_heads, head_dim, e16));
@@ -1698,6 +1699,7 @@ int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride,
                          int32_t page_size, void *stream) {
   CKR(check_rope(n_tok, head_dim, rope_dim, rope_base, k_gain != nullptr, eps));
   if (n_kv_heads < 1 || page_size < 1) return fail(DG_EINVAL, "n_kv_heads and page_size must be at least 1");
+  if ((int64_t)n_tok * n_kv_heads >= 1 << 30) return fail(DG_EINVAL, "too many rows of heads");
   CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, v_pool, n_pages));
   CKR(check_rows("k", k, k_stride, n_tok, n_kv_heads, head_dim, 8));
   CKR(check_rows("v", v, v_stride, n_tok, n_kv_heads, head_dim, 8));

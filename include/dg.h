@@ -564,7 +564,7 @@ int dg_op_kv_append(const uint16_t *k_new, const uint16_t *v_new, uint16_t *k_po
  * [n_seqs + 1], ascending from 0 or later); the first of them takes the
  * sequence's logical slot prefix_lens[b] (device int32 [n_seqs]: its cached
  * tokens).  Rows behind offsets[n_seqs] (a batch padded for a captured step)
- * are neither read nor written.  Sequence b's logical page j is
+ * take no part: what they hold does not matter, and they are left as they are.  Sequence b's logical page j is
  * page_tables[b * max_pages + j] (device int32 [n_seqs][max_pages]).  Lengths
  * live on the device, so a captured call can be replayed with other ones.
  * Rows of heads are `stride` elements apart (a multiple of 8, >= heads *
