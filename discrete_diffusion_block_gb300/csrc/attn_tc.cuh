@@ -22,6 +22,12 @@ __device__ __forceinline__ void attn_arrive(uint64_t *b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(tc::smem_u32(b)) : "memory");
 }
 
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // Shared-memory descriptor of the N-contiguous V tile: 8-key groups 1024 B
 // apart along K (SBO), 64-wide hd blocks 16 KB apart along N (LBO), 128-byte
 // swizzle.

@@ -24,6 +24,7 @@
 // head of a token takes them.
 #include <math.h>
 
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace dg {
@@ -52,29 +53,6 @@ __device__ __forceinline__ void load_chunks(Chunks<T> &x, const T *head, int c0,
     x.a[i] = ((const uint4 *)(head + 8 * c0))[i];
     x.b[i] = ((const uint4 *)(head + 8 * c1))[i];
   }
-}
-
-// Two fp32 values in a register pair, for the two-wide fp32 instructions.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair(float a, float b) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 split(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // Eight values of a chunk as four pairs.

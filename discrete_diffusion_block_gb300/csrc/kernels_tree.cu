@@ -10,13 +10,15 @@
 // up to ~275 rows per KV head the cache's bytes are the floor.  The rows of a
 // (sequence, KV head) are packed into tiles of 128 (the MMA's M); one tile and
 // its sequence's keys, in tiles of 128, are a unit.  Lengths live on the
-// device: every block adds up the units' key tiles, all blocks take equal
+// device: every block adds up the units' key tiles, and all blocks take equal
 // ranges of that sum (a range may end inside a unit, and hold several small
-// ones), and the memory pipes of all SMs stay equally busy however uneven the
-// batch is.  A unit that lies in one range is written out by its block; the
-// fp32 partial sums and softmax states of a unit that spans several go to the
-// workspace, and tree_merge_kernel joins them in the order of the keys (the
-// sums do not depend on which block ends first, so results repeat bit for bit).
+// ones), so that the memory pipes of all SMs stay equally busy however uneven
+// the batch is.  A unit that lies in one range is written out by its block.  Of
+// one that spans several, each block leaves fp32 partial sums and softmax
+// states in the workspace and raises a flag; after its own work, each joins a
+// share of the unit's rows, once all the unit's flags are up.  The blocks wait
+// for one another (for a bounded time), so the launch is cooperative.  Pieces
+// are added in the order of the keys: results repeat bit for bit.
 //
 // Roles of a block (384 threads, as in the canvas attention): warps 0 and 6
 // stream K and V tiles through rings of bulk copies out of the pre-swizzled
@@ -26,10 +28,14 @@
 // stage the next unit's rows as soon as the last S of a unit is done.  Quarters
 // without rows (a few drafted tokens fill one) skip the arithmetic.
 //
-// Roundings: P is rounded to bf16 for the second product, the row sum adds the
-// rounded values, so that a row whose weight is on one key returns that value
-// unchanged; scores, sums, accumulators and partial sums are fp32.
+// Roundings: P is rounded to bf16 for the second product (the row sum adds the
+// unrounded values); scores, sums, accumulators and partial sums are fp32.
+#include <atomic>
+#include <chrono>
+#include <mutex>
+
 #include "attn_tc.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 
 namespace dg {
@@ -38,23 +44,18 @@ namespace {
 
 constexpr int kTreeThreads = 384;
 constexpr int kTreePvWarp = 11;
-constexpr int kTreeCtas = 152;      // one block per SM
+constexpr int kTreeCtas = 152;      // most blocks: one per SM
 constexpr int kTreeFlags = 8;       // K tiles whose bad-page flags are kept: more than are ever in flight
-
-// What block c's first unit needs from tree_merge_kernel: set when the unit
-// began in an earlier block and ends in this one.
-struct TreeMerge {
-  int on, first_cta, first_slot;  // its pieces: slot first_slot of block first_cta, then slot 2 c' of the blocks up to c
-  int row0, n_rows, r0, g, pad;   // packed rows of its sequence: row r0 + i is token row0 + (r0 + i) / G
-};
 
 struct TreeArgs {
   TreeAttention a;
-  int G, min_tiles;
+  int G, ctas;
   float scale_log2;
-  float *part;       // [2 kTreeCtas] slots of [hd / 4][128 rows] float4
+  float *part;       // [2 kTreeCtas] slots of [hd / 4][128 rows] float4: block c's first piece in 2 c, its last in 2 c + 1
   float2 *state;     // [2 kTreeCtas][128]: (m, l) of each row
-  TreeMerge *merge;  // [kTreeCtas]
+  unsigned long long *flags;  // [2 kTreeCtas]: `ticket` while the slot holds a piece of this call
+  int *joined;       // [kTreeCtas]: blocks that have joined their share of the unit that ends in block c
+  unsigned long long ticket;  // this call's own number
   int *err;
 };
 
@@ -66,13 +67,13 @@ struct TreeSmem {
   static constexpr size_t q = 0;
   static constexpr size_t kring = q + tile;
   static constexpr size_t vring = kring + KR * tile;
-  static constexpr size_t xch = vring + KR * tile;         // [2 halves][128 rows] fp32; the block's scan before
-  static constexpr size_t flags = xch + 2 * 128 * 4;       // [kTreeFlags] bad halves of a K tile (2 bits)
+  static constexpr size_t xch = vring + KR * tile;         // [2 buffers][2 halves][128 rows] fp32
+  static constexpr size_t flags = xch + 2 * 2 * 128 * 4;       // [kTreeFlags] bad halves of a K tile (2 bits)
   static constexpr size_t bars = flags + kTreeFlags * 4;
   // q_full, k_full[KR], k_empty[KR], v_full[KR], v_empty[KR], s_full[2],
   // s_empty[2], p_full[2], p_empty[2], o_full, o_empty, drained[2]
   static constexpr int n_bars = 1 + 4 * KR + 8 + 4;
-  static constexpr size_t bytes = bars + n_bars * 8 + 16 + 1024;
+  static constexpr size_t bytes = bars + n_bars * 8 + 16;
 };
 
 // Rows and keys of one sequence; n = 0 when it has nothing to do or its rows
@@ -96,43 +97,124 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &p, int b) {
   return s;
 }
 
-__device__ __forceinline__ long long seq_tiles(const TreeArgs &p, const Seq &s) {
-  return (long long)p.a.Hkv * s.row_tiles * s.key_tiles;
+// The cost of a unit in key tiles, for the equal ranges: its tiles, and as many
+// more as starting it takes (rows staged, sums written out: 2500 cycles where a
+// tile takes 1500).  A range's tiles are those of its cost units that lie
+// behind the start-up of their unit.
+constexpr int kUnitCost = 2;
+
+// Cost of all its units; the host has checked that a batch's sum fits 31 bits.
+__device__ __forceinline__ int seq_cost(const TreeArgs &p, const Seq &s) {
+  return s.n ? p.a.Hkv * s.row_tiles * (s.key_tiles + kUnitCost) : 0;
 }
 
 // The pieces of a block's range: the key tiles [kt0, kt1) of unit (b, g, rt).
+// at: where the unit begins, relative to the range; left: what the range holds
+// behind the piece's end.
 struct Walk {
   Seq s;
-  int b, g, rt, kt0, kt1;
-  long long left;
-  __device__ __forceinline__ void begin(const TreeArgs &p, int b_, long long at, long long n) {
+  int b, g, rt, kt0, kt1, at, left;
+  __device__ __forceinline__ void clip(int from, int n) {  // cost units [from, from + n) of the unit
+    const int end = min(s.key_tiles + kUnitCost, from + n);
+    kt0 = max(0, from - kUnitCost);
+    kt1 = max(0, end - kUnitCost);
+    left = n - (end - from);
+  }
+  // false: the range holds no tile
+  __device__ __forceinline__ bool begin(const TreeArgs &p, int b_, int from, int n) {
     b = b_;
     s = load_seq(p, b);
-    left = n;
-    const long long u = at / s.key_tiles;
-    kt0 = (int)(at - u * s.key_tiles);
-    g = (int)(u / s.row_tiles);
-    rt = (int)(u - (long long)g * s.row_tiles);
-    kt1 = (int)min((long long)s.key_tiles, kt0 + left);
+    const int cost = s.key_tiles + kUnitCost, u = from / cost;
+    g = u / s.row_tiles;
+    rt = u - g * s.row_tiles;
+    at = u * cost - from;
+    clip(-at, n);
+    return kt0 < kt1 || next(p);
   }
   __device__ __forceinline__ bool next(const TreeArgs &p) {
-    left -= kt1 - kt0;
-    if (left <= 0) return false;
-    kt0 = 0;
-    if (++rt == s.row_tiles) {
-      rt = 0;
-      if (++g == p.a.Hkv) {
-        g = 0;
-        do {
-          if (++b >= p.a.n_seqs) return false;
-          s = load_seq(p, b);
-        } while (s.n == 0);
+    do {
+      if (left <= 0) return false;
+      at += s.key_tiles + kUnitCost;
+      if (++rt == s.row_tiles) {
+        rt = 0;
+        if (++g == p.a.Hkv) {
+          g = 0;
+          do {
+            if (++b >= p.a.n_seqs) return false;
+            s = load_seq(p, b);
+          } while (s.n == 0);
+        }
       }
-    }
-    kt1 = (int)min((long long)s.key_tiles, left);
+      clip(0, left);
+    } while (kt0 == kt1);
     return true;
   }
 };
+
+// A block's share of the batch's cost: `count` units of it from unit `at` of
+// sequence b on; per: what a block takes.  Found by every warp for itself: each lane adds up
+// a run of sequences, a scan over the lanes finds the sequence in which the
+// share begins.
+struct Range {
+  int b, at, count, per;
+};
+__device__ __forceinline__ Range block_range(const TreeArgs &p, int lane) {
+  const int run = ceil_div(p.a.n_seqs, 32), lo = min(p.a.n_seqs, lane * run), hi = min(p.a.n_seqs, lo + run);
+  constexpr int kMost = 1 << 30;  // more than an ascending batch's sum: offsets that overlap stop here
+  int mine = 0;
+#pragma unroll 4
+  for (int b = lo; b < hi; ++b) {
+    const Seq s = load_seq(p, b);
+    mine = (int)min((unsigned)mine + (unsigned)seq_cost(p, s), (unsigned)kMost);
+    if (s.bad && blockIdx.x == 0 && threadIdx.x < 32 && p.err) atomicExch(p.err + 1, kBadSequence);
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl = (int)min((unsigned)incl + (unsigned)v, (unsigned)kMost);
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  Range r;
+  r.per = (int)(((unsigned)total + (unsigned)p.ctas - 1) / (unsigned)p.ctas);
+  const long long first = (long long)r.per * blockIdx.x;
+  r.count = (int)min((long long)r.per, total - first);
+  r.b = -1;
+  r.at = 0;
+  const int start = (int)min(first, (long long)total);
+  int at = __shfl_up_sync(0xffffffffu, incl, 1);  // tiles of the lanes before
+  if (lane == 0) at = 0;
+  const bool here = start >= at && start < incl;
+  if (here) {
+    for (int b = lo; b < hi; ++b) {
+      const int n = seq_cost(p, load_seq(p, b));
+      if (start < at + n) {
+        r.b = b;
+        r.at = start - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  const int src = max(0, __ffs(__ballot_sync(0xffffffffu, here)) - 1);
+  r.b = __shfl_sync(0xffffffffu, r.b, src);
+  r.at = __shfl_sync(0xffffffffu, r.at, src);
+  if (r.b < 0) r.count = 0;
+  return r;
+}
+
+// A bounded wait that costs one test when the phase is over already.
+__device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
+  return tc::mbar_try_wait(b, parity) || tc::mbar_wait(b, parity, err, code, abort);
+}
+
+// The same for a whole warp, whose threads may leave the wait at different
+// times: they are together again afterwards, as the tensor-memory instructions
+// behind it ask.
+__device__ __forceinline__ void warp_wait(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
+  tree_wait(b, parity, err, code, abort);
+  __syncwarp();
+}
 
 // 64 mask bits of a row from drafted key d0 on (d0 may be negative: prefix
 // keys, seen), keys past the row's last one cleared.
@@ -158,12 +240,176 @@ __device__ __forceinline__ unsigned long long row_bits(const TreeArgs &p, const 
   return nv >= 64 ? v : v & ((1ull << nv) - 1);
 }
 
+__device__ __forceinline__ void st_flag(unsigned long long *p, unsigned long long v) {
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;\n" ::"l"(p), "l"(v) : "memory");  // after a fence
+}
+__device__ __forceinline__ unsigned long long ld_flag(const unsigned long long *p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];\n" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// The eight softmax warps meet (the form of the barrier that does not ask a
+// warp's threads to arrive together).
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.sync 6, 256;\n" ::: "memory"); }
+
+// A unit that spans the blocks first .. last: its pieces are slot first_slot and
+// slot 2 c of the blocks behind the first; row r0 + i is token row0 + (r0 + i) / G.
+struct Span {
+  int first, last, first_slot, row0, r0, n_rows, g;
+  __device__ __forceinline__ int slot(int s) const { return s == 0 ? first_slot : 2 * (first + s); }
+};
+// The span of the walk's unit; start: where the range begins.
+__device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, int start, int per) {
+  Span u;
+  const int begin = start + w.at, tiles = begin + kUnitCost;
+  u.first = tiles / per;
+  u.last = (tiles + w.s.key_tiles - 1) / per;
+  u.first_slot = 2 * u.first + (begin > u.first * per ? 1 : 0);  // a piece of the unit before comes first there
+  u.row0 = w.s.row0;
+  u.r0 = 128 * w.rt;
+  u.n_rows = min(128, w.s.n * p.G - u.r0);
+  u.g = w.g;
+  return u;
+}
+
+// The join's scratch, in the idle K ring.
+struct JoinSmem {
+  float2 state[128 + kTreeCtas + 8];  // [rows of the share][pieces] (m, l); .x becomes the weight
+  float4 sum[256];                    // a thread's sum, where several threads share a column's pieces
+};
+
+// This block's share of a unit's rows, out of the pieces of all its blocks:
+// weights 2^(m_s - m*) / L, pieces in the order of the keys.  Run by the 256
+// softmax threads (tid) after the block's last piece.  The last block to have
+// seen the unit's flags takes them down: a captured call, whose ticket is the
+// same every time, has to find them down.  The code runs once a launch, so it is
+// kept short: straight-line variants for each shape spent more time on fetching
+// instructions than the loads took.
+template <int HD>
+__device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsigned char *scratch, int tid,
+                                          volatile int *abort) {
+  constexpr int C = HD / 4, LC = HD == 128 ? 5 : 4;  // float4 columns of a row
+  const int n = u.last - u.first + 1, each = ceil_div(u.n_rows, n);
+  const int i0 = min(u.n_rows, ((int)blockIdx.x - u.first) * each), rows = min(u.n_rows, i0 + each) - i0;
+  if (rows <= 0) return;
+  JoinSmem *sm = (JoinSmem *)scratch;
+  if (tid < n) {
+    const unsigned long long *flag = p.flags + u.slot(tid);
+    const long long t0 = clock64();
+    while (ld_flag(flag) != p.ticket && !*abort) {
+      if (clock64() - t0 > tc::kWaitCycles) {
+        if (p.err) atomicExch(p.err, 63);
+        *abort = 1;
+      }
+    }
+  }
+  // the same decision in every thread: they go on to meet at barriers
+  int stop;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.red.or.pred q, 6, 256, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+      : "=r"(stop)
+      : "r"(*abort)
+      : "memory");
+  if (stop) return;
+  // Threads: 2^lr rows abreast x C columns x groups, a group taking `per` of the
+  // pieces; a thread holds 8 float4 at a time, 2^lb pieces of 8 >> lb rows.
+  int lr = 0;
+  while ((1 << lr) < rows && lr < 8 - LC) ++lr;
+  const int r = tid & ((1 << lr) - 1), col = (tid >> lr) & (C - 1), group = tid >> (lr + LC), groups = 256 >> (lr + LC);
+  const int per = ceil_div(n, groups), s0 = min(n, group * per), s1 = min(n, s0 + per);
+  const int lb = per <= 2 ? 1 : per <= 4 ? 2 : 3;
+  const float4 *src = (const float4 *)p.part + ((size_t)(2 * u.first) * C + col) * 128 + i0;
+  const int odd = (u.first_slot & 1) * (C * 128);  // the first block's slot is the second of its two
+  // (both loops count the same in every thread: there are barriers inside)
+  for (int b0 = 0; b0 < rows; b0 += (8 >> lb) << lr) {
+    const int base = b0 + r;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c0 = 0; c0 < per; c0 += 1 << lb) {
+      const int s = s0 + c0;
+      float4 o[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = base + ((k >> lb) << lr), sk = s + (k & ((1 << lb) - 1));
+        if (i < rows && sk < s1) o[k] = __ldcg(src + (size_t)sk * (2 * C * 128) + (sk ? 0 : odd) + i);
+      }
+      if (b0 == 0 && c0 == 0) {  // the weights, while the first pieces are in flight
+        for (int k = tid; k < rows * n; k += 256) {
+          const int i = k / n;
+          sm->state[k] = __ldcg(p.state + (size_t)u.slot(k - i * n) * 128 + i0 + i);
+        }
+        if (tid == 255 && atomicAdd(p.joined + u.last, 1) == ceil_div(u.n_rows, each) - 1) {
+#pragma unroll 1
+          for (int q = 0; q < n; ++q) p.flags[u.slot(q)] = 0;
+        }
+        softmax_sync();
+        const int lane = tid & 31;
+        for (int i = tid >> 5; i < rows; i += 8) {
+          float2 *st = sm->state + i * n;
+          float mx = __int_as_float(0xff800000), L = 0.0f;
+#pragma unroll 1
+          for (int q = lane; q < n; q += 32) mx = fmaxf(mx, st[q].x);
+#pragma unroll 1
+          for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+#pragma unroll 1
+          for (int q = lane; q < n; q += 32) {
+            const float f = st[q].x == __int_as_float(0xff800000) ? 0.0f : ex2(st[q].x - mx);
+            L += f * st[q].y;
+            st[q].x = f;
+          }
+#pragma unroll 1
+          for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll 1
+          for (int q = lane; q < n; q += 32) st[q].x *= inv;
+        }
+        softmax_sync();
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = base + ((k >> lb) << lr), sk = s + (k & ((1 << lb) - 1));
+        if (i < rows && sk < s1) {
+          const float f = sm->state[i * n + sk].x;
+          acc.x += f * o[k].x;
+          acc.y += f * o[k].y;
+          acc.z += f * o[k].z;
+          acc.w += f * o[k].w;
+        }
+        // a row is complete with its last piece; with several groups after all of them have theirs
+        if (groups == 1 && i < rows && sk == s1 - 1) {
+          const int rg = u.r0 + i0 + i, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
+          *(uint2 *)(p.a.out + (size_t)(u.row0 + t) * p.a.out_stride + (size_t)h * HD + 4 * col) =
+              make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+          acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+      }
+    }
+    if (groups > 1) {  // one round of rows: the groups' sums, in the order of the keys
+      sm->sum[tid] = acc;
+      softmax_sync();
+      if (group == 0 && r < rows) {
+#pragma unroll 1
+        for (int k = 1; k < groups; ++k) {
+          const float4 v = sm->sum[tid + (k << (lr + LC))];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+        const int rg = u.r0 + i0 + r, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
+        *(uint2 *)(p.a.out + (size_t)(u.row0 + t) * p.a.out_stride + (size_t)h * HD + 4 * col) =
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+      }
+    }
+  }
+  softmax_sync();  // the scratch is free again
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeArgs p) {
   using S = TreeSmem<HD>;
   constexpr int HB = S::HB, KR = S::KR;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *base = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) unsigned char base[];
   uint64_t *q_full = (uint64_t *)(base + S::bars);
   uint64_t *k_full = q_full + 1, *k_empty = k_full + KR;
   uint64_t *v_full = k_empty + KR, *v_empty = v_full + KR;
@@ -177,53 +423,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   auto v_tile = [&](int slot) { return base + S::vring + (size_t)slot * S::tile; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- this block's range of the batch's key tiles ---------------------------
-  // Each thread adds up a run of sequences; a scan over the threads finds the
-  // sequence in which the range begins.
-  long long *wsum = (long long *)(base + S::xch);       // [12] warp totals
-  long long *where = wsum + 12;                          // [2]: sequence, tile in it
-  int *err_seen = (int *)(where + 2);
-  const int run = ceil_div(p.a.n_seqs, kTreeThreads);
-  const int b_lo = threadIdx.x * run, b_hi = min(p.a.n_seqs, b_lo + run);
-  long long mine = 0;
-  if (threadIdx.x == 0) *err_seen = ld_err_word(p.err);
-  for (int b = b_lo; b < b_hi; ++b) {
-    const Seq s = load_seq(p, b);
-    mine += seq_tiles(p, s);
-    if (s.bad && blockIdx.x == 0 && p.err) atomicExch(p.err + 1, kBadSequence);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  long long total = 0, before = 0;
-  for (int w = 0; w < kTreeThreads / 32; ++w) {
-    if (w < warp) before += wsum[w];
-    total += wsum[w];
-  }
-  const long long per = max((total + gridDim.x - 1) / (long long)gridDim.x, (long long)p.min_tiles);
-  const long long start = per * blockIdx.x, count = min(per, total - start);
-  if (count <= 0 || *err_seen) {  // the same in every thread
-    if (threadIdx.x == 0) p.merge[blockIdx.x].on = 0;
+  if (tc::smem_u32(base) & 1023u) {  // the operand tiles' swizzle needs it: the same in every block
+    if (threadIdx.x == 0 && p.err) atomicExch(p.err, kShapeErrorBase + 5);
     return;
   }
-  long long at = before + incl - mine;
-  if (start >= at && start < at + mine) {
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long n = seq_tiles(p, load_seq(p, b));
-      if (start < at + n) {
-        where[0] = b;
-        where[1] = start - at;
-        break;
-      }
-      at += n;
-    }
-  }
-  if (threadIdx.x == 0) {
+  // Barriers and tensor memory are set up by warps 0 and 1 while every warp
+  // finds the block's range; the K producer (warp 0) goes on without waiting
+  // for the others.
+  if (warp == 0 && lane == 0) {
     *abort = 0;
     tc::mbar_init(q_full, 8);
     for (int i = 0; i < KR; ++i) {
@@ -244,39 +451,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
+  const Range range = block_range(p, lane);  // the same in every warp
+  Walk w;
+  if (range.count <= 0 || !w.begin(p, range.b, range.at, range.count)) return;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      tc::smem_u32(tmem_slot)),
                  "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // Barriers, `abort` and the tensor memory's address are there after this.
+  auto set_up = [&]() {
+    tc::fence_before();
+    __syncwarp();
+    asm volatile("bar.sync 5, %0;\n" ::"n"(kTreeThreads) : "memory");
+    tc::fence_after();
+  };
   // S double buffer: columns [0, 128) [128, 256); O: [256, 256 + HD); P double
   // buffer (bf16 pairs): [384, 448) [448, 512)
-  const uint32_t t_s = tmem, t_o = tmem + 256, t_p = tmem + 384;
-  Walk w;
-  w.begin(p, (int)where[0], where[1], count);
-  __syncthreads();  // `where` is read before the softmax exchange reuses its place
-
-  // The first unit, when it began in an earlier block and ends here, is joined
-  // by tree_merge_kernel.
-  if (threadIdx.x == 0) {
-    TreeMerge m = {};
-    m.on = w.kt0 > 0 && w.kt1 == w.s.key_tiles;
-    if (m.on) {
-      const long long t0 = start - w.kt0;  // where the unit begins
-      m.first_cta = (int)(t0 / per);
-      m.first_slot = 2 * m.first_cta + (t0 > m.first_cta * per ? 1 : 0);
-      m.row0 = w.s.row0;
-      m.r0 = 128 * w.rt;
-      m.n_rows = min(128, w.s.n * p.G - m.r0);
-      m.g = w.g;
-    }
-    p.merge[blockIdx.x] = m;
-  }
 
   // Tiles are numbered through all pieces of the block: tile i uses ring slot
   // i % KR and S and P buffer i & 1.
@@ -288,58 +480,68 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
     int issued = 0, slot = 0, phase = 0;
     bool ok = true;
+    int err_seen = 0;
+    if (is_k) {
+      __syncwarp();
+      err_seen = ld_err_word(p.err);
+      asm volatile("bar.arrive 5, %0;\n" ::"n"(kTreeThreads) : "memory");
+    } else {
+      set_up();
+    }
     do {
+      // Of the next 16 tiles each lane holds one 64-key half: where its rows
+      // are and how many are copied (the rest of the half becomes zero).  K:
+      // the page's slots past the last key too (their scores are masked); V:
+      // the sequence's own rows only (0 times anything must be 0).
       const int n_keys = w.s.pre + w.s.n;
       const int *table = p.a.page_tables + (size_t)w.b * p.a.max_pages;
-      int my_page = -1;
+      const bf16 *src = pool;
+      int rows = 0;
+      unsigned bad = 0;  // lanes whose page is outside the pools
       for (int kt = w.kt0; ok && kt < w.kt1; ++kt) {
-        // physical pages of the next 16 tiles' 64-key halves, one a lane; -1:
-        // past the last key, -2: a page outside the pools
         const int j = (kt - w.kt0) & 15;
         if (j == 0) {
           const int key = 128 * kt + 64 * lane;
-          my_page = -1;
+          bool off = false;
+          rows = 0;
           if (kt + (lane >> 1) < w.kt1 && key < n_keys) {
-            my_page = table[key / p.a.pg];
-            if (my_page < 0 || my_page >= p.a.n_pages) {
-              if (p.err) atomicExch(p.err + 1, kBadPage);
-              my_page = -2;
+            const int logical = key / p.a.pg, page = table[logical];
+            off = page < 0 || page >= p.a.n_pages;
+            if (!off) {
+              src = pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key - logical * p.a.pg) * 64;
+              rows = is_k ? 64 : min(64, n_keys - key);
+            } else if (p.err) {
+              atomicExch(p.err + 1, kBadPage);
             }
           }
+          bad = __ballot_sync(0xffffffffu, off);
         }
-        const int pgs[2] = {__shfl_sync(0xffffffffu, my_page, 2 * j), __shfl_sync(0xffffffffu, my_page, 2 * j + 1)};
         if (lane == 0) {
-          if (issued >= KR) ok = tc::mbar_wait(empty + slot, phase ^ 1, p.err, is_k ? 51 : 50, abort);
+          if (issued >= KR) ok = tree_wait(empty + slot, phase ^ 1, p.err, is_k ? 51 : 50, abort);
           if (*abort) ok = false;
           if (ok) {
-            if (is_k) flags[issued & (kTreeFlags - 1)] = (pgs[0] == -2 ? 1 : 0) | (pgs[1] == -2 ? 2 : 0);
-            unsigned char *dst = ring + (size_t)slot * S::tile;
-            uint64_t *bar = full + slot;
-            tc::mbar_expect_tx(bar, (uint32_t)S::tile);
-            const int key0 = 128 * kt, at0 = key0 % p.a.pg;
-            const bool whole = pgs[0] >= 0 && pgs[1] == pgs[0] && at0 + 128 <= p.a.pg && (is_k || key0 + 128 <= n_keys);
-            for (int h = 0; h < (whole ? 1 : 2); ++h) {
-              // rows copied from the page; the rest of the half is zero.  K: the
-              // page's slots past the last key too (their scores are masked);
-              // V: the sequence's own rows only (0 times anything must be 0).
-              const int key = key0 + 64 * h;
-              const int rows = whole ? 128 : pgs[h] < 0 ? 0 : is_k ? 64 : min(64, n_keys - key);
-              const bf16 *src = pool + ((size_t)max(pgs[h], 0) * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key % p.a.pg) * 64;
-              for (int b = 0; b < HB; ++b) {
-                unsigned char *d = dst + (size_t)b * 16384 + h * kAttnSlotHalfBytes;
-                if (rows > 0) tc::bulk_load(d, src + (size_t)b * p.a.pg * 64, 128u * rows, bar);
-                if (rows < 64) tc::bulk_load(d + 128 * rows, g_zero_half, 128u * (64 - rows), bar);
-              }
-            }
-            ++issued;
-            if (++slot == KR) {
-              slot = 0;
-              phase ^= 1;
-            }
+            if (is_k) flags[issued & (kTreeFlags - 1)] = (int)(bad >> (2 * j)) & 3;
+            tc::mbar_expect_tx(full + slot, (uint32_t)S::tile);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok) {
+          if ((lane >> 1) == j) {
+            unsigned char *d = ring + (size_t)slot * S::tile + (lane & 1) * kAttnSlotHalfBytes;
+#pragma unroll
+            for (int b = 0; b < HB; ++b) {
+              if (rows > 0) tc::bulk_load(d + (size_t)b * 16384, src + (size_t)b * p.a.pg * 64, 128u * rows, full + slot);
+              if (rows < 64) tc::bulk_load(d + (size_t)b * 16384 + 128 * rows, g_zero_half, 128u * (64 - rows), full + slot);
+            }
+          }
+          if (++issued == 1 && err_seen) *abort = 1;  // an earlier kernel gave up
+          if (++slot == KR) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
       }
+      __syncwarp();
     } while (ok && w.next(p));
     if (!ok && lane == 0) {  // gave up: wait (bounded) for the copies in flight
       for (int i = issued - 1; i >= 0 && i >= issued - KR; --i) {
@@ -349,17 +551,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
     }
   } else if (warp == 1 || warp == kTreePvWarp) {
+    set_up();
+    const uint32_t tmem = *tmem_slot, t_s = tmem, t_o = tmem + 256, t_p = tmem + 384;
     if (lane == 0) {
       bool ok = true;
       int i = 0, slot = 0, phase = 0, piece = 0;
       if (warp == 1) {  // ---- S = Q K^T
         const uint32_t idesc = tc::idesc_bf16(128, 128);
         do {
-          ok = tc::mbar_wait(q_full, piece & 1, p.err, 52, abort);
+          ok = tree_wait(q_full, piece & 1, p.err, 52, abort);
           for (int kt = w.kt0; ok && kt < w.kt1; ++kt, ++i) {
             const int buf = i & 1;
-            if (i >= 2) ok = tc::mbar_wait(s_empty + buf, ((i >> 1) - 1) & 1, p.err, 53, abort);
-            ok = ok && tc::mbar_wait(k_full + slot, phase, p.err, 54, abort);
+            if (i >= 2) ok = tree_wait(s_empty + buf, ((i >> 1) - 1) & 1, p.err, 53, abort);
+            ok = ok && tree_wait(k_full + slot, phase, p.err, 54, abort);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll
@@ -380,11 +584,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       } else {  // ---- O += P V
         const uint32_t idesc = tc::idesc_bf16(128, HD) | (1u << 16);  // B (V) N-contiguous
         do {
-          if (piece) ok = tc::mbar_wait(o_empty, (piece - 1) & 1, p.err, 55, abort);
+          if (piece) ok = tree_wait(o_empty, (piece - 1) & 1, p.err, 55, abort);
           for (int kt = w.kt0; ok && kt < w.kt1; ++kt, ++i) {
             const int buf = i & 1;
-            ok = tc::mbar_wait(p_full + buf, (i >> 1) & 1, p.err, 56, abort) &&
-                 tc::mbar_wait(v_full + slot, phase, p.err, 57, abort);
+            ok = tree_wait(p_full + buf, (i >> 1) & 1, p.err, 56, abort) &&
+                 tree_wait(v_full + slot, phase, p.err, 57, abort);
             if (!ok) break;
             tc::fence_after();
 #pragma unroll
@@ -418,22 +622,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     const int tid = (warp - (half ? 3 : 2)) * 32 + lane;  // 0 .. 255
     const float NEG = __int_as_float(0xff800000);
     const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-    float *xch = (float *)(base + S::xch);  // [2 halves][128 rows]
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;\n" ::"r"(1 + q4) : "memory"); };
+    float *xch = (float *)(base + S::xch);  // [2 buffers][2 halves][128 rows]
+    auto pair_sync = [&]() {
+      __syncwarp();
+      asm volatile("bar.sync %0, 64;\n" ::"r"(1 + q4) : "memory");
+    };
     // The piece's query rows into the operand tile (row r: token r / G, head g G + r % G).
     auto stage_q = [&](const Walk &u) {
       const int rows = min(128, u.s.n * p.G - 128 * u.rt);
-      for (int idx = tid; idx < rows * (HD / 8); idx += 256) {
-        const int r = idx / (HD / 8), c = idx & (HD / 8 - 1);
-        const int rg = 128 * u.rt + r, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
-        const uint4 v = *(const uint4 *)(p.a.q + (size_t)(u.s.row0 + t) * p.a.q_stride + (size_t)h * HD + 8 * c);
-        *(uint4 *)(base + S::q + (size_t)(c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      constexpr int kN = 128 * (HD / 8) / 256;  // chunks of a thread in a full tile
+      const int c = tid & (HD / 8 - 1);
+      uint4 v[kN];
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int r = (tid + 256 * k) / (HD / 8);
+        if (r < rows) {
+          const int rg = 128 * u.rt + r, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
+          v[k] = *(const uint4 *)(p.a.q + (size_t)(u.s.row0 + t) * p.a.q_stride + (size_t)h * HD + 8 * c);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int r = (tid + 256 * k) / (HD / 8);
+        if (r < rows) *(uint4 *)(base + S::q + (size_t)(c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       __syncwarp();
-      if (lane == 0) attn_arrive(q_full);
     };
     stage_q(w);
+    set_up();
+    if (lane == 0) attn_arrive(q_full);
+    const uint32_t tmem = *tmem_slot, t_s = tmem, t_o = tmem + 256, t_p = tmem + 384;
+    // the first unit, if it lies in earlier blocks too, and the last, if it goes
+    // on in later ones, are joined at the end (they may be the same)
+    const int start = range.per * (int)blockIdx.x;
+    const Span head = unit_span(p, w, start, range.per);
+    const bool join_head = w.kt0 > 0;
     int i = 0, piece = 0;
     bool more;
     do {
@@ -443,11 +667,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       float m = NEG, l = 0.0f;  // l: this half's share of the row sum
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++i) {
         const int buf = i & 1;
-        tc::mbar_wait(s_full + buf, (i >> 1) & 1, p.err, 58, abort);
+        warp_wait(s_full + buf, (i >> 1) & 1, p.err, 58, abort);
         if (!active) {
           // nothing to compute: the arrivals alone, P's after the buffer's last use
           if (lane == 0) attn_arrive(s_empty + buf);
-          if (i >= 2) tc::mbar_wait(p_empty + buf, ((i >> 1) - 1) & 1, p.err, 59, abort);
+          if (i >= 2) warp_wait(p_empty + buf, ((i >> 1) - 1) & 1, p.err, 59, abort);
           __syncwarp();
           if (lane == 0) attn_arrive(p_full + buf);
           continue;
@@ -479,49 +703,47 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            a0 = fmaxf(a0, __uint_as_float(x[c][j]));
-            a1 = fmaxf(a1, __uint_as_float(x[c][j + 1]));
-            a2 = fmaxf(a2, __uint_as_float(x[c][j + 2]));
-            a3 = fmaxf(a3, __uint_as_float(x[c][j + 3]));
+          for (int j = 0; j < 32; j += 8) {
+            a0 = fmaxf(fmaxf(a0, __uint_as_float(x[c][j])), __uint_as_float(x[c][j + 1]));
+            a1 = fmaxf(fmaxf(a1, __uint_as_float(x[c][j + 2])), __uint_as_float(x[c][j + 3]));
+            a2 = fmaxf(fmaxf(a2, __uint_as_float(x[c][j + 4])), __uint_as_float(x[c][j + 5]));
+            a3 = fmaxf(fmaxf(a3, __uint_as_float(x[c][j + 6])), __uint_as_float(x[c][j + 7]));
           }
         const float hmax = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
-        xch[half * 128 + row] = hmax;
+        float *ex = xch + buf * 256;  // the other buffer is in use until both have passed this sync
+        ex[half * 128 + row] = hmax;
         pair_sync();
-        const float tmax = fmaxf(hmax, xch[(half ^ 1) * 128 + row]) * p.scale_log2;
-        pair_sync();  // both read before the next tile's maxima overwrite the slots
+        const float tmax = fmaxf(hmax, ex[(half ^ 1) * 128 + row]) * p.scale_log2;
         const float m_new = fmaxf(m, tmax);
         const bool grow = m_new > m + kRescaleLog2;  // false while both are -inf; the same in both halves
         // P buffer i & 1 is free once P V of tile i - 2 is done
-        if (i >= 2) tc::mbar_wait(p_empty + buf, ((i >> 1) - 1) & 1, p.err, 60, abort);
+        if (i >= 2) warp_wait(p_empty + buf, ((i >> 1) - 1) & 1, p.err, 60, abort);
         const float m_old = m;
         if (grow) m = m_new;
         const float nmu = m == NEG ? 0.0f : -m;
-        float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+        const f32x2 scale2 = pair(p.scale_log2, p.scale_log2), nmu2 = pair(nmu, nmu);
+        f32x2 sum0 = pair(0.0f, 0.0f), sum1 = sum0;
         const uint32_t prow = t_p + 64 * buf + 32 * half + lane_off;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(x[c][j]), p.scale_log2, nmu));
-            const float p1 = ex2(fmaf(__uint_as_float(x[c][j + 1]), p.scale_log2, nmu));
-            const uint32_t k2 = pack_bf16(p0, p1);
-            pk[j >> 1] = k2;
-            const float r = __uint_as_float(k2 << 16) + __uint_as_float(k2 & 0xffff0000u);  // as rounded
-            if ((j & 6) == 0) s0 += r;
-            else if ((j & 6) == 2) s1 += r;
-            else if ((j & 6) == 4) s2 += r;
-            else s3 += r;
+            const float2 d = split(fma2(pair(__uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1])), scale2, nmu2));
+            const float p0 = ex2(d.x), p1 = ex2(d.y);
+            pk[j >> 1] = pack_bf16(p0, p1);
+            if (j & 2) sum1 = add2(sum1, pair(p0, p1));
+            else sum0 = add2(sum0, pair(p0, p1));
           }
           tmem_st16(prow + 16 * c, pk);
         }
+        const float2 sum = split(add2(sum0, sum1));
         // rows whose maximum grew: O (and l) to the new reference, O <- O 2^(m_old - m);
         // each half rescales its half of the O columns
         float f = 1.0f;
         if (__any_sync(0xffffffffu, grow) && kt > w.kt0) {
           // O must hold P V of every earlier tile of the piece: wait for tile i - 1's
-          tc::mbar_wait(p_empty + (buf ^ 1), ((i - 1) >> 1) & 1, p.err, 61, abort);
+          warp_wait(p_empty + (buf ^ 1), ((i - 1) >> 1) & 1, p.err, 61, abort);
           tc::fence_after();
           f = grow ? ex2(m_old - m) : 1.0f;  // m_old = -inf: 0 (O holds zeros)
 #pragma unroll 1
@@ -534,7 +756,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             tmem_st32(t_o + lane_off + 32 * c, o);
           }
         }
-        l = l * f + ((s0 + s1) + (s2 + s3));
+        l = l * f + (sum.x + sum.y);
         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");  // P (and O) written before the release
         tc::fence_before();
         __syncwarp();
@@ -543,17 +765,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       // every S of this piece is done (its last s_full): the next piece's rows
       Walk nx = w;
       more = nx.next(p);  // the same in all softmax warps (never cut short: they meet at named barriers)
-      if (more) stage_q(nx);
-      tc::mbar_wait(o_full, piece & 1, p.err, 62, abort);  // inactive warps too: o_empty counts one arrival of each a piece
+      if (more) {
+        stage_q(nx);
+        if (lane == 0) attn_arrive(q_full);
+      }
+      const bool full_unit = w.kt0 == 0 && w.kt1 == w.s.key_tiles;
+      const int slot = 2 * blockIdx.x + (piece ? 1 : 0);
+      warp_wait(o_full, piece & 1, p.err, 62, abort);  // inactive warps too: o_empty counts one arrival of each a piece
       if (active) {  // the row sum of both halves
-        xch[half * 128 + row] = l;
+        float *ex = xch + (i & 1) * 256;  // as the next tile's maxima
+        ex[half * 128 + row] = l;
         pair_sync();
-        const float lt = half ? xch[row] + l : l + xch[128 + row];  // keys 0-63 first
+        const float lt = half ? ex[row] + l : l + ex[128 + row];  // keys 0-63 first
         pair_sync();
         tc::fence_after();
-        const bool full_unit = w.kt0 == 0 && w.kt1 == w.s.key_tiles;
         const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-        const int slot = 2 * blockIdx.x + (piece ? 1 : 0);
         bf16 *dst = p.a.out + (size_t)(w.s.row0 + t) * p.a.out_stride + (size_t)h * HD;
         float4 *part = (float4 *)p.part + (size_t)slot * 128 * (HD / 4) + row;
 #pragma unroll 1
@@ -584,6 +810,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
       __syncwarp();
       if (lane == 0) attn_arrive(o_empty);
+      if (!more) {
+        // At the end, once (a fence in mid-stream waits for every store and load
+        // in flight, and the rings run dry): the flags of the first and the last
+        // piece, then this block's shares of the units they belong to.
+        const bool join_tail = w.kt1 < w.s.key_tiles && (piece || !join_head);
+        if (join_head || join_tail) {
+          __threadfence();
+          softmax_sync();
+          if (tid == 0) {
+            if (join_head && head.last == (int)blockIdx.x) {
+              p.joined[blockIdx.x] = 0;  // counted from here by those who see the flag
+              __threadfence();
+            }
+            if (join_head) st_flag(p.flags + 2 * blockIdx.x, p.ticket);
+            if (join_tail) st_flag(p.flags + slot, p.ticket);
+          }
+          __syncwarp();
+        }
+        // (one loop: the code of the join is there once)
+#pragma unroll 1
+        for (int k = join_head ? 0 : 1; k < (join_tail ? 2 : 1); ++k)
+          join_unit<HD>(p, k ? unit_span(p, w, start, range.per) : head, base + S::kring, tid, abort);
+      }
       w = nx;
       ++piece;
     } while (more);
@@ -593,75 +842,75 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   __syncthreads();
   if (warp == 1) {
     tc::fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(*tmem_slot), "r"(512u));
   }
-}
-
-// Joins the pieces of the units that span several blocks: weights 2^(m_s - m*),
-// pieces in the order of the keys.  Block (c, y): the unit that ends in block
-// c's first piece, rows y R .. y R + R - 1, one float4 column a thread.
-template <int HD>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs p) {
-  constexpr int R = 1024 / HD;  // rows per block: 256 threads, HD / 4 columns each
-  const TreeMerge m = p.merge[blockIdx.x];
-  const int i = R * blockIdx.y + (threadIdx.x & (R - 1)), col = threadIdx.x / R;
-  if (!m.on || i >= m.n_rows) return;
-  const int n = (int)blockIdx.x - m.first_cta + 1;  // pieces
-  auto slot = [&](int s) { return s == 0 ? m.first_slot : 2 * (m.first_cta + s); };
-  const float NEG = __int_as_float(0xff800000);
-  float mx = NEG;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) mx = fmaxf(mx, p.state[(size_t)slot(s) * 128 + i].x);
-  float L = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) {
-    const float2 ml = p.state[(size_t)slot(s) * 128 + i];
-    const float4 o = ((const float4 *)p.part)[((size_t)slot(s) * (HD / 4) + col) * 128 + i];
-    const float f = ml.x == NEG ? 0.0f : ex2(ml.x - mx);
-    L += f * ml.y;
-    acc.x += f * o.x;
-    acc.y += f * o.y;
-    acc.z += f * o.z;
-    acc.w += f * o.w;
-  }
-  const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-  const int rg = m.r0 + i, t = rg / p.G, h = m.g * p.G + rg - t * p.G;
-  *(uint2 *)(p.a.out + (size_t)(m.row0 + t) * p.a.out_stride + (size_t)h * HD + 4 * col) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 struct TreeWorkspace {
-  size_t part, state, merge, bytes;
+  size_t part, state, flags, joined, bytes;
 };
 TreeWorkspace tree_workspace(int hd) {
   TreeWorkspace w;
   w.part = 0;
   w.state = w.part + (size_t)2 * kTreeCtas * 128 * hd * 4;
-  w.merge = w.state + (size_t)2 * kTreeCtas * 128 * sizeof(float2);
-  w.bytes = w.merge + (size_t)kTreeCtas * sizeof(TreeMerge);
+  w.flags = w.state + (size_t)2 * kTreeCtas * 128 * sizeof(float2);
+  w.joined = w.flags + (size_t)2 * kTreeCtas * 8;
+  w.bytes = w.joined + (size_t)kTreeCtas * 4;
   return w;
 }
 
+// A number that no other call has: a flag word of a workspace whose contents
+// are arbitrary does not equal it.
+unsigned long long new_ticket() {
+  static std::atomic<unsigned long long> count{(unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count()};
+  unsigned long long x = count.fetch_add(1) * 0x9E3779B97F4A7C15ull;  // mixed as in splitmix64 (Steele et al., 2014)
+  x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
+  x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
+  x ^= x >> 31;
+  return x ? x : 1;
+}
+
+// Blocks of a launch on the current device (all of them run together), asked
+// once; 0: the kernel does not run there.
 template <int HD>
-cudaError_t launch_tree(const TreeArgs &p, cudaStream_t st) {
+cudaError_t tree_ctas(int *out) {
+  static int ctas[64];
+  static std::mutex mu;
   using S = TreeSmem<HD>;
   static_assert(S::bytes <= 232448, "shared memory of the tree attention kernel");
-  static unsigned long long attr_set = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !((attr_set >> dev) & 1ull)) {
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!ctas[dev]) {
+    int sms = 0, per_sm = 0;
     e = cudaFuncSetAttribute(tree_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, tree_attn_kernel<HD>, kTreeThreads, S::bytes);
     if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set |= 1ull << dev;
+    if (per_sm < 1) return cudaErrorLaunchOutOfResources;
+    ctas[dev] = sms < kTreeCtas ? sms : kTreeCtas;
   }
-  tree_attn_kernel<HD><<<kTreeCtas, kTreeThreads, S::bytes, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // no unit has more rows than the whole batch
-  const int rows = (int)min(128ll, (long long)p.a.n_tok * p.G);
-  tree_merge_kernel<HD><<<dim3(kTreeCtas, ceil_div(rows, 1024 / HD)), 256, 0, st>>>(p);
-  return cudaGetLastError();
+  *out = ctas[dev];
+  return cudaSuccess;
+}
+
+template <int HD>
+cudaError_t launch_tree(TreeArgs &p, cudaStream_t st) {
+  const cudaError_t e = tree_ctas<HD>(&p.ctas);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(kTreeThreads);
+  cfg.dynamicSmemBytes = TreeSmem<HD>::bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_attn_kernel<HD>, p);
 }
 
 }  // namespace
@@ -671,14 +920,15 @@ size_t tree_attention_workspace_bytes(int, int, int, int, int hd) { return tree_
 cudaError_t tree_attention(const TreeAttention &a, void *ws, int *err, cudaStream_t st) {
   if (a.n_tok == 0 || a.n_seqs == 0) return cudaSuccess;
   const TreeWorkspace w = tree_workspace(a.hd);
-  TreeArgs p;
+  TreeArgs p{};
   p.a = a;
   p.G = a.Hq / a.Hkv;
-  p.min_tiles = 1;
   p.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
   p.part = (float *)((unsigned char *)ws + w.part);
   p.state = (float2 *)((unsigned char *)ws + w.state);
-  p.merge = (TreeMerge *)((unsigned char *)ws + w.merge);
+  p.flags = (unsigned long long *)((unsigned char *)ws + w.flags);
+  p.joined = (int *)((unsigned char *)ws + w.joined);
+  p.ticket = new_ticket();
   p.err = err;
   return a.hd == 128 ? launch_tree<128>(p, st) : launch_tree<64>(p, st);
 }

@@ -389,6 +389,36 @@ def test_attention_repeats_bit_for_bit_and_ignores_the_workspace_contents():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+@pytest.mark.parametrize("hq,hkv,hd,pre,new", [
+    (12, 4, 64, [100 + 37 * j for j in range(40)], [1 + j % 5 for j in range(40)]),
+    (16, 8, 128, [9000, 3, 700, 0, 2500], [24, 1, 7, 13, 30]),
+    (4, 1, 64, [40000], [33]),
+    (8, 8, 128, [2048], [1]),
+])
+def test_attention_replayed_many_times_repeats_bit_for_bit(hq, hkv, hd, pre, new):
+    # units that span several blocks are joined between the blocks: a captured
+    # call, and calls in a row on one workspace, must find its flags down
+    rng = np.random.default_rng(16)
+    bt = Batch(rng, pre, new, hkv, hd, 128)
+    q, out = check_attention(bt, hq, None, rng)
+    n = dgp.dg_op_tree_attention_workspace_bytes(bt.T, len(pre), hq, hkv, hd)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device=dev())
+    again = torch.empty_like(out)
+    for _ in range(20):
+        again.fill_(7.0)
+        run_attention(bt, q, None, again, workspace=ws)
+        assert torch.equal(again, out)
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        for _ in range(3):
+            run_attention(bt, q, None, again, workspace=ws, stream=st)
+    for _ in range(50):
+        again.fill_(7.0)
+        g.replay()
+        assert torch.equal(again, out)
+
+
 def test_attention_reports_bad_pages_and_bad_sequences():
     rng = np.random.default_rng(15)
     bt = Batch(rng, [200, 50], [2, 3], 2, 64, 64)
