@@ -30,6 +30,8 @@
 //
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
+#include <limits.h>
+
 #include <atomic>
 #include <chrono>
 #include <mutex>
@@ -54,7 +56,7 @@ struct TreeArgs {
   float *part;       // [2 kTreeCtas] slots of [hd / 4][128 rows] float4: block c's first piece in 2 c, its last in 2 c + 1
   float2 *state;     // [2 kTreeCtas][128]: (m, l) of each row
   unsigned long long *flags;  // [2 kTreeCtas]: `ticket` while the slot holds a piece of this call
-  int *joined;       // [kTreeCtas]: blocks that have joined their share of the unit that ends in block c
+  int *joined;       // [kTreeCtas]: warps that have seen all flags of the unit that ends in block c
   unsigned long long ticket;  // this call's own number
   int *err;
 };
@@ -279,23 +281,11 @@ struct JoinSmem {
   float4 sum[256];                    // a thread's sum, where several threads share a column's pieces
 };
 
-// This block's share of a unit's rows, out of the pieces of all its blocks:
-// weights 2^(m_s - m*) / L, pieces in the order of the keys.  Run by the 256
-// softmax threads (tid) after the block's last piece.  The last block to have
-// seen the unit's flags takes them down: a captured call, whose ticket is the
-// same every time, has to find them down.  The code runs once a launch, so it is
-// kept short: straight-line variants for each shape spent more time on fetching
-// instructions than the loads took.
-template <int HD>
-__device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsigned char *scratch, int tid,
-                                          volatile int *abort) {
-  constexpr int C = HD / 4, LC = HD == 128 ? 5 : 4;  // float4 columns of a row
-  const int n = u.last - u.first + 1, each = ceil_div(u.n_rows, n);
-  const int i0 = min(u.n_rows, ((int)blockIdx.x - u.first) * each), rows = min(u.n_rows, i0 + each) - i0;
-  if (rows <= 0) return;
-  JoinSmem *sm = (JoinSmem *)scratch;
-  if (tid < n) {
-    const unsigned long long *flag = p.flags + u.slot(tid);
+// Waits (bounded) until the unit's pieces are there, flag s in lane s, s + 32 ..;
+// run by every softmax warp for itself.  False: given up.
+__device__ __forceinline__ bool pieces_ready(const TreeArgs &p, const Span &u, int n, int lane, volatile int *abort) {
+  for (int s = lane; s < n; s += 32) {
+    const unsigned long long *flag = p.flags + u.slot(s);
     const long long t0 = clock64();
     while (ld_flag(flag) != p.ticket && !*abort) {
       if (clock64() - t0 > tc::kWaitCycles) {
@@ -304,105 +294,164 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsi
       }
     }
   }
-  // the same decision in every thread: they go on to meet at barriers
-  int stop;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.red.or.pred q, 6, 256, p;\n selp.s32 %0, 1, 0, q;\n}\n"
-      : "=r"(stop)
-      : "r"(*abort)
-      : "memory");
-  if (stop) return;
-  // Threads: 2^lr rows abreast x C columns x groups, a group taking `per` of the
-  // pieces; a thread holds 8 float4 at a time, 2^lb pieces of 8 >> lb rows.
-  int lr = 0;
-  while ((1 << lr) < rows && lr < 8 - LC) ++lr;
-  const int r = tid & ((1 << lr) - 1), col = (tid >> lr) & (C - 1), group = tid >> (lr + LC), groups = 256 >> (lr + LC);
-  const int per = ceil_div(n, groups), s0 = min(n, group * per), s1 = min(n, s0 + per);
-  const int lb = per <= 2 ? 1 : per <= 4 ? 2 : 3;
-  const float4 *src = (const float4 *)p.part + ((size_t)(2 * u.first) * C + col) * 128 + i0;
-  const int odd = (u.first_slot & 1) * (C * 128);  // the first block's slot is the second of its two
-  // (both loops count the same in every thread: there are barriers inside)
-  for (int b0 = 0; b0 < rows; b0 += (8 >> lb) << lr) {
-    const int base = b0 + r;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c0 = 0; c0 < per; c0 += 1 << lb) {
-      const int s = s0 + c0;
+  __syncwarp();
+  return !__any_sync(0xffffffffu, *abort);
+}
+
+__device__ __forceinline__ void store_row4(const TreeArgs &p, const Span &u, int i, int hd, int col, float4 v, float inv) {
+  const int rg = u.r0 + i, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
+  *(uint2 *)(p.a.out + (size_t)(u.row0 + t) * p.a.out_stride + (size_t)h * hd + 4 * col) =
+      make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+}
+
+// This block's share of a unit's rows, out of the pieces of all its blocks:
+// weights 2^(m_s - m*), pieces in the order of the keys.  Run by the 256 softmax
+// threads (tid) after the block's last piece.  The last warp to have seen the
+// unit's flags takes them down: a captured call, whose ticket is the same every
+// time, has to find them down.  Latency bound, and run once a launch: what is
+// loaded is loaded together, and the code is kept short (straight-line variants
+// for each shape spent more time on fetching instructions).
+template <int HD>
+__device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsigned char *scratch, int tid,
+                                          volatile int *abort) {
+  constexpr int C = HD / 4, LC = HD == 128 ? 5 : 4;  // float4 columns of a row
+  const int n = u.last - u.first + 1, each = ceil_div(u.n_rows, n), lane = tid & 31;
+  const int i0 = min(u.n_rows, ((int)blockIdx.x - u.first) * each), rows = min(u.n_rows, i0 + each) - i0;
+  if (rows <= 0) return;
+  bool ready = pieces_ready(p, u, n, lane, abort);
+  int seen = 0;
+  if (lane == 0 && ready) seen = atomicAdd(p.joined + u.last, 1);
+  const float NEG = __int_as_float(0xff800000);
+  const float4 *src = (const float4 *)p.part + (size_t)(2 * u.first) * C * 128 + i0;
+  const float2 *state = p.state + (size_t)(2 * u.first) * 128 + i0;
+  const int odd = u.first_slot & 1;  // the first block's slot is the second of its two
+  if (n <= 8) {
+    // 256 >> LC rows abreast; a thread holds all (2^lb or fewer) pieces of 8 >> lb rows at a time
+    const int r = tid & ((256 >> LC) - 1), col = tid >> (8 - LC), lb = n <= 2 ? 1 : n <= 4 ? 2 : 3;
+    for (int b0 = 0; ready && b0 < rows; b0 += (8 >> lb) << (8 - LC)) {
       float4 o[8];
+      float2 ml[8];
+      float mx[8], w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = base + ((k >> lb) << lr), sk = s + (k & ((1 << lb) - 1));
-        if (i < rows && sk < s1) o[k] = __ldcg(src + (size_t)sk * (2 * C * 128) + (sk ? 0 : odd) + i);
-      }
-      if (b0 == 0 && c0 == 0) {  // the weights, while the first pieces are in flight
-        for (int k = tid; k < rows * n; k += 256) {
-          const int i = k / n;
-          sm->state[k] = __ldcg(p.state + (size_t)u.slot(k - i * n) * 128 + i0 + i);
+        const int i = b0 + r + ((k >> lb) << (8 - LC)), s = k & ((1 << lb) - 1), slot = 2 * s + (s ? 0 : odd);
+        ml[k] = make_float2(NEG, 0.0f);
+        if (i < rows && s < n) {
+          o[k] = __ldcg(src + ((size_t)slot * C + col) * 128 + i);
+          ml[k] = __ldcg(state + (size_t)slot * 128 + i);
         }
-        if (tid == 255 && atomicAdd(p.joined + u.last, 1) == ceil_div(u.n_rows, each) - 1) {
-#pragma unroll 1
-          for (int q = 0; q < n; ++q) p.flags[u.slot(q)] = 0;
-        }
-        softmax_sync();
-        const int lane = tid & 31;
-        for (int i = tid >> 5; i < rows; i += 8) {
-          float2 *st = sm->state + i * n;
-          float mx = __int_as_float(0xff800000), L = 0.0f;
-#pragma unroll 1
-          for (int q = lane; q < n; q += 32) mx = fmaxf(mx, st[q].x);
-#pragma unroll 1
-          for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-#pragma unroll 1
-          for (int q = lane; q < n; q += 32) {
-            const float f = st[q].x == __int_as_float(0xff800000) ? 0.0f : ex2(st[q].x - mx);
-            L += f * st[q].y;
-            st[q].x = f;
-          }
-#pragma unroll 1
-          for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-          const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-#pragma unroll 1
-          for (int q = lane; q < n; q += 32) st[q].x *= inv;
-        }
-        softmax_sync();
       }
 #pragma unroll
+      for (int k = 0; k < 8; ++k) mx[k] = ml[k].x;
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        if (d >> lb) break;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (!(k & d)) mx[k] = mx[k | d] = fmaxf(mx[k], mx[k | d]);
+      }
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float L = 0.0f;
+#pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = base + ((k >> lb) << lr), sk = s + (k & ((1 << lb) - 1));
-        if (i < rows && sk < s1) {
-          const float f = sm->state[i * n + sk].x;
-          acc.x += f * o[k].x;
-          acc.y += f * o[k].y;
-          acc.z += f * o[k].z;
-          acc.w += f * o[k].w;
+        const int i = b0 + r + ((k >> lb) << (8 - LC)), s = k & ((1 << lb) - 1);
+        w[k] = ml[k].x == NEG ? 0.0f : ex2(ml[k].x - mx[k]);
+        if (w[k] > 0.0f) {
+          L += w[k] * ml[k].y;
+          acc.x += w[k] * o[k].x;
+          acc.y += w[k] * o[k].y;
+          acc.z += w[k] * o[k].z;
+          acc.w += w[k] * o[k].w;
         }
-        // a row is complete with its last piece; with several groups after all of them have theirs
-        if (groups == 1 && i < rows && sk == s1 - 1) {
-          const int rg = u.r0 + i0 + i, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
-          *(uint2 *)(p.a.out + (size_t)(u.row0 + t) * p.a.out_stride + (size_t)h * HD + 4 * col) =
-              make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+        if (s == (1 << lb) - 1) {
+          if (i < rows) store_row4(p, u, i0 + i, HD, col, acc, L > 0.0f ? 1.0f / L : 0.0f);
           acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          L = 0.0f;
         }
       }
     }
-    if (groups > 1) {  // one round of rows: the groups' sums, in the order of the keys
-      sm->sum[tid] = acc;
-      softmax_sync();
-      if (group == 0 && r < rows) {
+  } else {
+    // Many pieces, few rows (no more than 128 / n of them in a share): 2^lr rows
+    // abreast x C columns x groups of threads that share the pieces, 8 in flight
+    // each; the rows' weights in shared memory, the groups' sums added there.
+    float2 *st = (float2 *)scratch;            // [rows][n]: (m, l); .x becomes the weight
+    float4 *sum = (float4 *)(scratch + 4096);  // [256]
+    int lr = 0;
+    while ((1 << lr) < rows && lr < 8 - LC) ++lr;
+    const int r = tid & ((1 << lr) - 1), col = (tid >> lr) & (C - 1), group = tid >> (lr + LC), lg = 8 - LC - lr;
+    const int per = (n + (1 << lg) - 1) >> lg, s0 = group * per, s1 = min(n, s0 + per);
+    // (the loops count the same in every thread: there are barriers inside)
+    for (int b0 = 0; b0 < rows; b0 += 1 << lr) {
+      const int i = b0 + r;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c0 = 0; c0 < per; c0 += 8) {
+        float4 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int s = s0 + c0 + k;
+          if (ready && i < rows && s < s1) o[k] = __ldcg(src + ((size_t)(2 * s + (s ? 0 : odd)) * C + col) * 128 + i);
+        }
+        if (b0 == 0 && c0 == 0) {  // the weights, while the first pieces are in flight: a warp a row
+          for (int q = tid >> 5; q < rows; q += 8) {
+            float mx = NEG, L = 0.0f;
 #pragma unroll 1
-        for (int k = 1; k < groups; ++k) {
-          const float4 v = sm->sum[tid + (k << (lr + LC))];
-          acc.x += v.x;
-          acc.y += v.y;
-          acc.z += v.z;
-          acc.w += v.w;
+            for (int s = lane; s < n; s += 32) {
+              float2 v = make_float2(NEG, 0.0f);
+              if (ready) v = __ldcg(state + (size_t)(2 * s + (s ? 0 : odd)) * 128 + q);
+              st[q * n + s] = v;
+              mx = fmaxf(mx, v.x);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+#pragma unroll 1
+            for (int s = lane; s < n; s += 32) {
+              const float2 v = st[q * n + s];
+              const float f = v.x == NEG ? 0.0f : ex2(v.x - mx);
+              L += f * v.y;
+              st[q * n + s].x = f;
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll 1
+            for (int s = lane; s < n; s += 32) st[q * n + s].x *= inv;
+          }
+          softmax_sync();
         }
-        const int rg = u.r0 + i0 + r, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
-        *(uint2 *)(p.a.out + (size_t)(u.row0 + t) * p.a.out_stride + (size_t)h * HD + 4 * col) =
-            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int s = s0 + c0 + k;
+          if (i < rows && s < s1) {
+            const float f = st[i * n + s].x;
+            acc.x += f * o[k].x;
+            acc.y += f * o[k].y;
+            acc.z += f * o[k].z;
+            acc.w += f * o[k].w;
+          }
+        }
       }
+      if (lg) {  // (one round of rows then)
+        sum[tid] = acc;
+        softmax_sync();
+        if (group == 0) {
+#pragma unroll 1
+          for (int k = 1; k < 1 << lg; ++k) {
+            const float4 v = sum[tid + (k << (lr + LC))];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+          }
+        }
+      }
+      if (ready && group == 0 && i < rows) store_row4(p, u, i0 + i, HD, col, acc, 1.0f);
     }
+    softmax_sync();  // the scratch is free again
   }
-  softmax_sync();  // the scratch is free again
+  if (lane == 0 && ready && seen == 8 * ceil_div(u.n_rows, each) - 1) {
+#pragma unroll 1
+    for (int s = 0; s < n; ++s) p.flags[u.slot(s)] = 0;
+  }
 }
 
 template <int HD>
@@ -488,34 +537,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     } else {
       set_up();
     }
+    // Of a run of up to 16 tiles each lane holds one 64-key half: its logical
+    // page, -1 past the last key.  The next run's entries of the page table (and
+    // the next unit's lengths) are loaded while this one's tiles are copied.
+    auto pages_of = [&](const Walk &u, int kt) {
+      const int key = 128 * kt + 64 * lane;
+      return kt + (lane >> 1) < u.kt1 && key < u.s.pre + u.s.n
+                 ? p.a.page_tables[(size_t)u.b * p.a.max_pages + key / p.a.pg] : INT_MIN;
+    };
+    int kt = w.kt0, page = pages_of(w, kt);
+    bool more = true;
     do {
-      // Of the next 16 tiles each lane holds one 64-key half: where its rows
-      // are and how many are copied (the rest of the half becomes zero).  K:
-      // the page's slots past the last key too (their scores are masked); V:
-      // the sequence's own rows only (0 times anything must be 0).
-      const int n_keys = w.s.pre + w.s.n;
-      const int *table = p.a.page_tables + (size_t)w.b * p.a.max_pages;
-      const bf16 *src = pool;
-      int rows = 0;
-      unsigned bad = 0;  // lanes whose page is outside the pools
-      for (int kt = w.kt0; ok && kt < w.kt1; ++kt) {
-        const int j = (kt - w.kt0) & 15;
-        if (j == 0) {
-          const int key = 128 * kt + 64 * lane;
-          bool off = false;
-          rows = 0;
-          if (kt + (lane >> 1) < w.kt1 && key < n_keys) {
-            const int logical = key / p.a.pg, page = table[logical];
-            off = page < 0 || page >= p.a.n_pages;
-            if (!off) {
-              src = pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key - logical * p.a.pg) * 64;
-              rows = is_k ? 64 : min(64, n_keys - key);
-            } else if (p.err) {
-              atomicExch(p.err + 1, kBadPage);
-            }
-          }
-          bad = __ballot_sync(0xffffffffu, off);
-        }
+      // Where the half's rows are and how many are copied (the rest of it becomes
+      // zero).  K: the page's slots past the last key too (their scores are
+      // masked); V: the sequence's own rows only (0 times anything must be 0).
+      const int n = min(16, w.kt1 - kt), key = 128 * kt + 64 * lane;
+      const bool off = page != INT_MIN && (page < 0 || page >= p.a.n_pages);
+      const int rows = page == INT_MIN || off ? 0 : is_k ? 64 : min(64, w.s.pre + w.s.n - key);
+      const bf16 *src = rows ? pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key % p.a.pg) * 64 : pool;
+      if (off && p.err) atomicExch(p.err + 1, kBadPage);
+      const unsigned bad = __ballot_sync(0xffffffffu, off);  // lanes whose page is outside the pools
+      Walk nw = w;
+      int next_page = 0;
+      for (int j = 0; ok && j < n; ++j) {
         if (lane == 0) {
           if (issued >= KR) ok = tree_wait(empty + slot, phase ^ 1, p.err, is_k ? 51 : 50, abort);
           if (*abort) ok = false;
@@ -540,9 +584,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             phase ^= 1;
           }
         }
+        __syncwarp();
+        if (j == 0) {
+          kt += n;
+          if (kt >= nw.kt1) {
+            more = nw.next(p);
+            kt = nw.kt0;
+          }
+          if (more) next_page = pages_of(nw, kt);
+        }
       }
-      __syncwarp();
-    } while (ok && w.next(p));
+      w = nw;
+      page = next_page;
+    } while (ok && more);
     if (!ok && lane == 0) {  // gave up: wait (bounded) for the copies in flight
       for (int i = issued - 1; i >= 0 && i >= issued - KR; --i) {
         const long long t0 = clock64();
@@ -649,6 +703,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       __syncwarp();
     };
+    // A line of 128 bytes a thread: all of a tile's rows (two lines of HD = 128).
+    auto request_q = [&](const Walk &u) {
+      const int rows = min(128, u.s.n * p.G - 128 * u.rt), r = tid / HB;
+      if (r < rows) {
+        const int rg = 128 * u.rt + r, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
+        asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p.a.q + (size_t)(u.s.row0 + t) * p.a.q_stride + (size_t)h * HD +
+                                                        64 * (tid % HB)));
+      }
+    };
     stage_q(w);
     set_up();
     if (lane == 0) attn_arrive(q_full);
@@ -659,12 +722,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     const Span head = unit_span(p, w, start, range.per);
     const bool join_head = w.kt0 > 0;
     int i = 0, piece = 0;
-    bool more;
-    do {
+    while (true) {
       const int rows = min(128, w.s.n * p.G - 128 * w.rt);
       const bool active = 32 * q4 < rows;  // the same in both warps of the quarter
       const int rg = 128 * w.rt + row, t = row < rows ? rg / p.G : 0, h = w.g * p.G + rg - t * p.G;
       float m = NEG, l = 0.0f;  // l: this half's share of the row sum
+      // the next piece, found while this one's first keys are on their way, and
+      // its rows requested: staging them later must not wait for memory
+      Walk nx = w;
+      const bool more = nx.next(p);  // the same in all softmax warps (never cut short: they meet at named barriers)
+      if (more) request_q(nx);
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++i) {
         const int buf = i & 1;
         warp_wait(s_full + buf, (i >> 1) & 1, p.err, 58, abort);
@@ -763,8 +830,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         if (lane == 0) attn_arrive(p_full + buf);
       }
       // every S of this piece is done (its last s_full): the next piece's rows
-      Walk nx = w;
-      more = nx.next(p);  // the same in all softmax warps (never cut short: they meet at named barriers)
       if (more) {
         stage_q(nx);
         if (lane == 0) attn_arrive(q_full);
@@ -816,26 +881,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         // piece, then this block's shares of the units they belong to.
         const bool join_tail = w.kt1 < w.s.key_tiles && (piece || !join_head);
         if (join_head || join_tail) {
+          if (tid == 0 && join_head && head.last == (int)blockIdx.x) p.joined[blockIdx.x] = 0;  // counted from here by those who see the flag
           __threadfence();
           softmax_sync();
           if (tid == 0) {
-            if (join_head && head.last == (int)blockIdx.x) {
-              p.joined[blockIdx.x] = 0;  // counted from here by those who see the flag
-              __threadfence();
-            }
             if (join_head) st_flag(p.flags + 2 * blockIdx.x, p.ticket);
             if (join_tail) st_flag(p.flags + slot, p.ticket);
           }
-          __syncwarp();
         }
         // (one loop: the code of the join is there once)
 #pragma unroll 1
         for (int k = join_head ? 0 : 1; k < (join_tail ? 2 : 1); ++k)
           join_unit<HD>(p, k ? unit_span(p, w, start, range.per) : head, base + S::kring, tid, abort);
       }
+      if (!more) break;
       w = nx;
       ++piece;
-    } while (more);
+    }
   }
   __syncwarp();  // lone-thread roles above: reconverge before the block-wide barrier
   tc::fence_before();
