@@ -9,6 +9,7 @@ fallback.
 """
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -175,6 +176,7 @@ _SIGS = {
     "dg_op_tree_attention": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                   _I64, _P, _SZ, _P]),
     "dg_op_token_logprobs": (_I, [_P, _I, _I64, _I, _I, _F, _P, _I, _P, _P, _P, _I, _P, _P, _P]),
+    "dg_op_packed": (_I, [_I, ctypes.c_char_p]),
 }
 
 
@@ -589,13 +591,25 @@ def dg_op_kv_append(k_new, v_new, k_pool, v_pool, page_table, n_layers, n_pages,
 
 # ---- serving drafted tokens (torch CUDA tensors on the current device) --------
 # The small calls of a decoding step take a few microseconds on the GPU, so the
-# checks here read each tensor attribute once and build no temporaries.
+# checks here read each tensor attribute once, and the arguments go over in one
+# block (dg_op_packed: "q" an integer or address, 0 for NULL, "d" a float).
 
 _BF16, _F32, _I32T, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_PACK_QK = struct.Struct("=qqqqqqqqqqqdqqdqqqqq").pack
+_PACK_APPEND = struct.Struct("=qqqqqqqqqqqqqqdqdqqqqq").pack
+_PACK_ATTEND = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqq").pack
+_PACK_LOGPROBS = struct.Struct("=qqqqqdqqqqqqqqq").pack
+DG_CALL_QK_NORM_ROPE, DG_CALL_ROPE_KV_APPEND, DG_CALL_TREE_ATTENTION, DG_CALL_TOKEN_LOGPROBS = range(4)
 
 
 def _einval(msg):
     raise DgError(DG_EINVAL, msg)
+
+
+def _call(which, args):
+    code = (_lib or load()).dg_op_packed(which, args)
+    if code:
+        _check(code)
 
 
 def _device(t):
@@ -608,12 +622,12 @@ def _device(t):
     return cur
 
 
-def _dense(t, what, kind, shape, dev):
-    """Address of a contiguous tensor of that type, shape and device (None: NULL)."""
+def _dense(t, what, kind, n, dev):
+    """Address of a contiguous tensor of that type, count and device (None: 0)."""
     if t is None:
-        return None
-    if t.dtype is not kind or t.shape != shape or not t.is_contiguous():
-        _einval(f"{what} must be a contiguous {kind} tensor of shape {tuple(shape)}")
+        return 0
+    if t.dtype is not kind or t.numel() != n or not t.is_contiguous():
+        _einval(f"{what} must be a contiguous {kind} tensor of {n} elements")
     if t.get_device() != dev:
         _einval(f"{what} is not on the current CUDA device")
     return t.data_ptr()
@@ -626,10 +640,9 @@ def _rows(t, what, kind, shape, dev):
     if t.get_device() != dev:
         _einval(f"{what} is not on the current CUDA device")
     row, head, one = t.stride()
-    hd = shape[2]
-    if (one != 1 or (head != hd and shape[1] > 1)) and t.numel():
+    if (one != 1 or (head != shape[2] and shape[1] > 1)) and t.numel():
         _einval(f"{what}: the heads of a row must be adjacent")
-    return t.data_ptr(), row if shape[0] > 1 else shape[1] * hd
+    return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
 
 
 def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, eps=1e-6, rope_base=10000.0,
@@ -645,8 +658,7 @@ def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, 
     if kind is not _BF16 and kind is not _F32:
         _einval("q and k must be bf16 or fp32")
     T, _, hd = some.shape
-    hq = hkv = 0
-    qp = qs = qo = qos = kp = ks = ko = kos = None
+    hq = hkv = qp = qs = qo = qos = kp = ks = ko = kos = 0
     if q is not None:
         shape = q.shape
         hq = shape[1]
@@ -659,10 +671,10 @@ def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, 
         hkv = shape[1]
         kp, ks = _rows(k, "k", kind, shape, dev)
         ko, kos = _rows(k_out, "k_out", _BF16, shape, dev)
-    _check(load().dg_op_qk_norm_rope(
-        qp, kp, 1 if kind is _F32 else 0, qs or 0, ks or 0, _dense(positions, "positions", _I32T, (T,), dev), T, hq,
-        hkv, hd, hd if rope_dim is None else rope_dim, rope_base, _dense(q_gain, "q_gain", _F32, (hd,), dev),
-        _dense(k_gain, "k_gain", _F32, (hd,), dev), eps, qo, qos or 0, ko, kos or 0, _stream(stream)))
+    _call(DG_CALL_QK_NORM_ROPE, _PACK_QK(
+        qp, kp, 1 if kind is _F32 else 0, qs, ks, _dense(positions, "positions", _I32T, T, dev), T, hq, hkv, hd,
+        hd if rope_dim is None else rope_dim, rope_base, _dense(q_gain, "q_gain", _F32, hd, dev),
+        _dense(k_gain, "k_gain", _F32, hd, dev), eps, qo, qos, ko, kos, _stream(stream) or 0))
 
 
 def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets, positions=None, k_gain=None,
@@ -680,13 +692,13 @@ def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets
     shape = (T, hkv, hd)
     kp, ks = _rows(k, "k", _BF16, shape, dev)
     vp, vs = _rows(v, "v", _BF16, shape, dev)
-    _check(load().dg_op_rope_kv_append(
-        kp, vp, ks, vs, _dense(positions, "positions", _I32T, (T,), dev),
-        _dense(prefix_lens, "prefix_lens", _I32T, (B,), dev), _dense(offsets, "offsets", _I32T, (B + 1,), dev),
-        _dense(page_tables, "page_tables", _I32T, table, dev), max_pages, B, T, hkv, hd,
-        hd if rope_dim is None else rope_dim, rope_base, _dense(k_gain, "k_gain", _F32, (hd,), dev), eps,
-        _dense(k_pool, "k_pool", _BF16, pool, dev), _dense(v_pool, "v_pool", _BF16, pool, dev), n_pages, pg,
-        _stream(stream)))
+    _call(DG_CALL_ROPE_KV_APPEND, _PACK_APPEND(
+        kp, vp, ks, vs, _dense(positions, "positions", _I32T, T, dev),
+        _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev),
+        _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages, B, T, hkv, hd,
+        hd if rope_dim is None else rope_dim, rope_base, _dense(k_gain, "k_gain", _F32, hd, dev), eps,
+        _dense(k_pool, "k_pool", _BF16, n_pages * hkv * pg * hd, dev),
+        _dense(v_pool, "v_pool", _BF16, n_pages * hkv * pg * hd, dev), n_pages, pg, _stream(stream) or 0))
 
 
 def dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd):
@@ -707,21 +719,21 @@ def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, t
     T = shape[0]
     qp, qs = _rows(q, "q", _BF16, shape, dev)
     op, os_ = _rows(out, "out", _BF16, shape, dev)
-    mp, words = None, 0
+    mp = words = wp = wn = 0
     if tree_mask is not None and T:
         words = tree_mask.shape[-1]
-        mp = _dense(tree_mask, "tree_mask", _I64T, (T, words), dev)
-    wp, wn = None, 0
+        mp = _dense(tree_mask, "tree_mask", _I64T, T * words, dev)
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != dev:
             _einval("the workspace must be contiguous, on the current CUDA device")
         wp, wn = workspace.data_ptr(), workspace.nbytes
-    _check(load().dg_op_tree_attention(
-        qp, qs, _dense(k_pool, "k_pool", _BF16, pool, dev), _dense(v_pool, "v_pool", _BF16, pool, dev),
-        _dense(page_tables, "page_tables", _I32T, table, dev), max_pages,
-        _dense(prefix_lens, "prefix_lens", _I32T, (B,), dev), _dense(offsets, "offsets", _I32T, (B + 1,), dev), mp,
-        words, B, T, shape[1], hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, wp, wn,
-        _stream(stream)))
+    n = n_pages * hkv * pg * hd
+    _call(DG_CALL_TREE_ATTENTION, _PACK_ATTEND(
+        qp, qs, _dense(k_pool, "k_pool", _BF16, n, dev), _dense(v_pool, "v_pool", _BF16, n, dev),
+        _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages,
+        _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev), mp, words, B,
+        T, shape[1], hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, wp, wn,
+        _stream(stream) or 0))
 
 
 def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_ids=None, top_logprobs=None,
@@ -741,10 +753,9 @@ def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_i
         _einval("tokens go with logprobs, top_logprobs with top_ids")
     given = 0 if tokens is None else tokens.shape[-1]
     k = 0 if top_ids is None else top_ids.shape[-1]
-    rows, pairs, tops = (T,), (T, given), (T, k)
-    _check(load().dg_op_token_logprobs(
+    _call(DG_CALL_TOKEN_LOGPROBS, _PACK_LOGPROBS(
         logits.data_ptr(), 1 if kind is _BF16 else 0, row if T > 1 else V, T, V, inv_tau,
-        _dense(tokens, "tokens", _I32T, pairs, dev), given, _dense(logprobs, "logprobs", _F32, pairs, dev),
-        _dense(entropy, "entropy", _F32, rows, dev), _dense(lse, "lse", _F32, rows, dev), k,
-        _dense(top_ids, "top_ids", _I32T, tops, dev), _dense(top_logprobs, "top_logprobs", _F32, tops, dev),
-        _stream(stream)))
+        _dense(tokens, "tokens", _I32T, T * given, dev), given, _dense(logprobs, "logprobs", _F32, T * given, dev),
+        _dense(entropy, "entropy", _F32, T, dev), _dense(lse, "lse", _F32, T, dev), k,
+        _dense(top_ids, "top_ids", _I32T, T * k, dev), _dense(top_logprobs, "top_logprobs", _F32, T * k, dev),
+        _stream(stream) or 0))

@@ -1777,3 +1777,75 @@ int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_st
 }
 
 }  // extern "C"
+
+namespace {
+
+// Reads packed arguments in order.
+struct Packed {
+  const int64_t *at;
+  bool fits = true;
+  int64_t i64() { return *at++; }
+  int32_t i32() {
+    const int64_t v = *at++;
+    if (v < INT32_MIN || v > INT32_MAX) fits = false;
+    return (int32_t)v;
+  }
+  float f() {
+    double v;
+    memcpy(&v, at++, sizeof(v));
+    return (float)v;
+  }
+  template <typename T>
+  T *ptr() { return (T *)(uintptr_t)*at++; }
+};
+
+}  // namespace
+
+extern "C" int dg_op_packed(int32_t call, const void *args) {
+  if (!args) return fail(DG_EINVAL, "null args");
+  Packed a{(const int64_t *)args};
+  // (braced initialisers are evaluated in order; call arguments need not be)
+  switch (call) {
+    case DG_CALL_QK_NORM_ROPE: {
+      struct { const void *q, *k; int32_t in_f32; int64_t qs, ks; const int32_t *pos; int32_t n, hq, hkv, hd, rd; float base;
+               const float *qg, *kg; float eps; uint16_t *qo; int64_t qos; uint16_t *ko; int64_t kos; void *st; }
+      c{a.ptr<const void>(), a.ptr<const void>(), a.i32(), a.i64(), a.i64(), a.ptr<const int32_t>(), a.i32(), a.i32(), a.i32(),
+        a.i32(), a.i32(), a.f(), a.ptr<const float>(), a.ptr<const float>(), a.f(), a.ptr<uint16_t>(), a.i64(),
+        a.ptr<uint16_t>(), a.i64(), a.ptr<void>()};
+      if (!a.fits) break;
+      return dg_op_qk_norm_rope(c.q, c.k, c.in_f32, c.qs, c.ks, c.pos, c.n, c.hq, c.hkv, c.hd, c.rd, c.base, c.qg, c.kg, c.eps,
+                                c.qo, c.qos, c.ko, c.kos, c.st);
+    }
+    case DG_CALL_ROPE_KV_APPEND: {
+      struct { const uint16_t *k, *v; int64_t ks, vs; const int32_t *pos, *pre, *off, *tab; int32_t mp, b, n, hkv, hd, rd;
+               float base; const float *kg; float eps; uint16_t *kp, *vp; int32_t np, pg; void *st; }
+      c{a.ptr<const uint16_t>(), a.ptr<const uint16_t>(), a.i64(), a.i64(), a.ptr<const int32_t>(), a.ptr<const int32_t>(),
+        a.ptr<const int32_t>(), a.ptr<const int32_t>(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.f(),
+        a.ptr<const float>(), a.f(), a.ptr<uint16_t>(), a.ptr<uint16_t>(), a.i32(), a.i32(), a.ptr<void>()};
+      if (!a.fits) break;
+      return dg_op_rope_kv_append(c.k, c.v, c.ks, c.vs, c.pos, c.pre, c.off, c.tab, c.mp, c.b, c.n, c.hkv, c.hd, c.rd, c.base,
+                                  c.kg, c.eps, c.kp, c.vp, c.np, c.pg, c.st);
+    }
+    case DG_CALL_TREE_ATTENTION: {
+      struct { const uint16_t *q; int64_t qs; const uint16_t *kp, *vp; const int32_t *tab; int32_t mp; const int32_t *pre, *off;
+               const uint64_t *mask; int32_t mw, b, n, hq, hkv, hd, pg, np; float scale; uint16_t *out; int64_t os; void *ws;
+               int64_t wn; void *st; }
+      c{a.ptr<const uint16_t>(), a.i64(), a.ptr<const uint16_t>(), a.ptr<const uint16_t>(), a.ptr<const int32_t>(), a.i32(),
+        a.ptr<const int32_t>(), a.ptr<const int32_t>(), a.ptr<const uint64_t>(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(),
+        a.i32(), a.i32(), a.i32(), a.f(), a.ptr<uint16_t>(), a.i64(), a.ptr<void>(), a.i64(), a.ptr<void>()};
+      if (!a.fits || c.wn < 0) break;
+      return dg_op_tree_attention(c.q, c.qs, c.kp, c.vp, c.tab, c.mp, c.pre, c.off, c.mask, c.mw, c.b, c.n, c.hq, c.hkv, c.hd,
+                                  c.pg, c.np, c.scale, c.out, c.os, c.ws, (size_t)c.wn, c.st);
+    }
+    case DG_CALL_TOKEN_LOGPROBS: {
+      struct { const void *x; int32_t bf; int64_t rs; int32_t rows, v; float it; const int32_t *tok; int32_t ng; float *lp, *en, *lse;
+               int32_t k; int32_t *ids; float *tlp; void *st; }
+      c{a.ptr<const void>(), a.i32(), a.i64(), a.i32(), a.i32(), a.f(), a.ptr<const int32_t>(), a.i32(), a.ptr<float>(),
+        a.ptr<float>(), a.ptr<float>(), a.i32(), a.ptr<int32_t>(), a.ptr<float>(), a.ptr<void>()};
+      if (!a.fits) break;
+      return dg_op_token_logprobs(c.x, c.bf, c.rs, c.rows, c.v, c.it, c.tok, c.ng, c.lp, c.en, c.lse, c.k, c.ids, c.tlp, c.st);
+    }
+    default: return fail(DG_EINVAL, "unknown call %d", call);
+  }
+  return fail(DG_EINVAL, "an integer argument is out of range");
+}

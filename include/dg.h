@@ -668,6 +668,18 @@ int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_st
                          float *logprobs, float *entropy, float *lse, int32_t top_k,
                          int32_t *top_ids, float *top_logprobs, void *stream);
 
+/* The four calls above with their arguments packed into one block, for bindings
+ * in which marshalling some twenty arguments one by one takes longer than the
+ * launch: args holds the call's parameters in order, 8 bytes each, integers and
+ * pointers as int64, floats as double (host memory, read during the call).
+ * call: DG_CALL_*.  Returns what the call returns; DG_EINVAL for an integer that
+ * does not fit its parameter. */
+enum {
+    DG_CALL_QK_NORM_ROPE = 0, DG_CALL_ROPE_KV_APPEND = 1, DG_CALL_TREE_ATTENTION = 2,
+    DG_CALL_TOKEN_LOGPROBS = 3
+};
+int dg_op_packed(int32_t call, const void *args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -99,6 +99,34 @@ def test_empty_calls_succeed_without_a_gpu(L):
     assert call(L.dg_op_token_logprobs, LP, rows=0, logits=None) == dgp.DG_OK
 
 
+def packed(args):
+    import struct
+    return struct.pack("=" + "".join("d" if isinstance(a, float) else "q" for a in args), *[0 if a is None else a for a in args])
+
+
+@pytest.mark.parametrize("which,base,change", [
+    (0, QK, dict(hd=96)), (0, QK, dict(ko_stride=1016)), (1, AP, dict(n_pages=0)), (1, AP, dict(eps=0.0, k_gain=A)), (2, AT, dict(scale=-1.0)),
+    (2, AT, dict(pg=100)), (3, LP, dict(top_k=33)), (3, LP, dict(top_ids=None)),
+])
+def test_packed_calls_give_the_answers_of_the_calls(L, which, base, change):
+    # (an empty call is accepted, a bad one refused with the same message)
+    names = ("dg_op_qk_norm_rope", "dg_op_rope_kv_append", "dg_op_tree_attention", "dg_op_token_logprobs")
+    empty = dict(rows=0) if which == 3 else dict(n_tok=0)
+    assert L.dg_op_packed(which, packed({**base, **empty}.values())) == dgp.DG_OK
+    assert call(getattr(L, names[which]), base, **change) == dgp.DG_EINVAL
+    message = L.dg_last_error()
+    assert L.dg_op_packed(which, packed({**base, **change}.values())) == dgp.DG_EINVAL
+    assert L.dg_last_error() == message
+
+
+def test_packed_calls_refuse_unknown_calls_and_wide_integers(L):
+    assert L.dg_op_packed(4, packed(QK.values())) == dgp.DG_EINVAL
+    assert L.dg_op_packed(0, None) == dgp.DG_EINVAL
+    for which, base, name in ((0, QK, "n_tok"), (1, AP, "max_pages"), (2, AT, "n_pages"), (3, LP, "V")):
+        assert L.dg_op_packed(which, packed({**base, name: 1 << 33}.values())) == dgp.DG_EINVAL
+        assert b"range" in L.dg_last_error()
+
+
 def test_binding_refuses_tensors_that_are_not_on_the_device():
     t = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     i = torch.zeros(2, dtype=torch.int32)
