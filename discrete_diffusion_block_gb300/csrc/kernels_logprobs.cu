@@ -14,10 +14,14 @@
 // lane, in descending order of a 64-bit key (order-preserving bits of the
 // value, then the complement of the index: equal values go to the lower
 // index).  A list starts empty, so nearly every entry of a warp's first
-// batches would enter it; the k-th largest of the block's thread maxima of the
-// first batch is a lower bound of the block's k-th best entry, and entries
-// below it are dropped at one compare per batch: of a row of 262144 random
-// logits about k * 262144 / 8192 reach a list, however many warps share it.
+// batches would enter it.  The k-th largest of the running maxima of 64 groups
+// of threads is a lower bound of the block's k-th best entry, close to it (the
+// groups' maxima are mostly the best entries themselves), and cheap: entries
+// below are dropped at one compare per batch, with the bound renewed after 1, 2,
+// 4, 8 ... batches, and about k + k log2(batches) of a block's random logits
+// reach a list.  At the end the lists' entries above the bound, a few more than
+// k, are gathered and each finds its place by counting the larger ones.
+#include "f32x2.cuh"
 #include "gemm_tc.cuh"
 #include "internal.h"
 
@@ -26,7 +30,6 @@ namespace dg {
 namespace {
 
 constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
-constexpr int kVecs = 4;            // 16-byte vectors of a thread's batch
 constexpr int kMaxLpCluster = 16;   // blocks of a row (a non-portable cluster size)
 constexpr float kLn2f = 0.693147180559945309f;
 
@@ -51,13 +54,6 @@ __device__ __forceinline__ void rebase(RowSum &r, float m, float c) {
   r.m = m;
 }
 
-__device__ __forceinline__ RowSum merge(RowSum x, RowSum y, float c) {
-  const float m = fmaxf(x.m, y.m);
-  rebase(x, m, c);
-  rebase(y, m, c);
-  return RowSum{m, x.s + y.s, x.a + y.a};
-}
-
 // Order-preserving bits of a value; NaN counts as -inf, -0 as 0.  0 is below all.
 __device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t b = v != v ? 0xff800000u : __float_as_uint(v + 0.0f);
@@ -67,54 +63,68 @@ __device__ __forceinline__ float order_value(uint32_t b) {
   return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
 }
 
-template <typename K>
-__device__ __forceinline__ K larger(K a, K b) { return a > b ? a : b; }
-template <typename K>
-__device__ __forceinline__ K smaller(K a, K b) { return a < b ? a : b; }
+constexpr int kGroups = 64;  // of 8 threads; no fewer than the largest k
 
-// The 32 largest of two descending lists, one entry a lane, descending.
-template <typename K>
-__device__ __forceinline__ K merge_lists(K x, K y) {
-  const int lane = threadIdx.x & 31;
-  x = larger(x, __shfl_sync(0xffffffffu, y, 31 - lane));  // bitonic
+// The k-th largest of the groups' maxima, from each thread's (order bits; 0:
+// none); run by the whole block, on two buffers in turn.  Each group counts the
+// larger ones (ties in group order), its threads an eighth each.
+struct __align__(16) GroupMax {
+  uint32_t max[kGroups], bound;
+};
+__device__ __forceinline__ uint32_t group_bound(uint32_t mine, int k, GroupMax *s) {
+  const int group = threadIdx.x >> 3, part = threadIdx.x & 7;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const K z = __shfl_xor_sync(0xffffffffu, x, o);
-    x = (lane & o) ? smaller(x, z) : larger(x, z);
-  }
-  return x;
-}
-
-// 32 entries, one a lane, into descending order.
-template <typename K>
-__device__ __forceinline__ K sort_lanes(K x) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int n = 2; n <= 32; n <<= 1)
-#pragma unroll
-    for (int o = n >> 1; o; o >>= 1) {
-      const K z = __shfl_xor_sync(0xffffffffu, x, o);
-      const bool first = !(lane & o), down = !(lane & n);
-      x = (first == down) ? larger(x, z) : smaller(x, z);
-    }
-  return x;
-}
-
-// The block's warps' lists (one per warp, kLpWarps of them) joined in shared
-// memory, pairwise; list[0] holds the result after the call.
-template <typename K>
-__device__ __forceinline__ void join_lists(K (*list)[32], K mine) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  list[warp][lane] = mine;
-#pragma unroll
-  for (int n = kLpWarps / 2; n; n >>= 1) {
-    __syncthreads();
-    if (warp < n) {
-      mine = merge_lists(mine, list[warp + n][lane]);
-      list[warp][lane] = mine;
-    }
-  }
+  for (int o = 4; o; o >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+  if (part == 0) s->max[group] = mine;
   __syncthreads();
+  const uint4 v = *(const uint4 *)(s->max + 8 * part), w = *(const uint4 *)(s->max + 8 * part + 4);
+  const uint32_t m[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+  const int before = group - 8 * part;  // entries of this eighth that lie before the group
+  int above = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) above += m[e] > mine || (m[e] == mine && e < before);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+  if (part == 0 && above == k - 1) s->bound = mine;
+  __syncthreads();
+  return s->bound;
+}
+
+// Entries collected in shared memory, and the k best of them in order.
+struct Picks {
+  int n;
+  unsigned long long key[kLpThreads];
+  unsigned long long top[32];
+};
+__device__ __forceinline__ void collect(Picks *s, unsigned long long key, bool in) {
+  const int lane = threadIdx.x & 31;
+  const unsigned m = __ballot_sync(0xffffffffu, in);
+  int at = 0;
+  if (lane == 0 && m) at = atomicAdd(&s->n, __popc(m));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+  if (in) s->key[at] = key;
+}
+// After a barrier: entry t finds its place; top[] is complete after the next one.
+__device__ __forceinline__ void place(Picks *s, int k) {
+  const int n = s->n, t = threadIdx.x;
+  if (t >= n) return;
+  const unsigned long long mine = s->key[t];
+  int above = 0;
+  for (int q = 0; q < n; ++q) above += s->key[q] > mine;
+  if (above < k) s->top[above] = mine;
+}
+
+// Largest of the lanes' raw logits (NaN not among them).
+__device__ __forceinline__ float lanes_max(float m) {
+  return order_value(__reduce_max_sync(0xffffffffu, order_bits(m)));
+}
+// The lanes' sums, of `n` lanes each (a power of two), moved to maximum m and added.
+__device__ __forceinline__ void lanes_sum(RowSum &r, float m, float c, int n) {
+  rebase(r, m, c);
+  for (int o = n / 2; o; o >>= 1) {
+    r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+    r.a += __shfl_xor_sync(0xffffffffu, r.a, o);
+  }
 }
 
 // Elements of a thread's batch, held as loaded.
@@ -122,7 +132,7 @@ template <typename T>
 struct Batch;
 template <>
 struct Batch<float> {
-  static constexpr int E = 4;  // elements of a vector
+  static constexpr int E = 4, kVecs = 4;  // elements of a vector, vectors of a batch
   uint4 r[kVecs];
   __device__ __forceinline__ float at(int j) const { return __uint_as_float((&r[j >> 2].x)[j & 3]); }
   __device__ __forceinline__ float max() const {
@@ -137,7 +147,7 @@ struct Batch<float> {
 };
 template <>
 struct Batch<bf16> {
-  static constexpr int E = 8;
+  static constexpr int E = 8, kVecs = 2;  // more spill: 301 rows of 50001 take 15.3 us with 2, 17.8 with 4
   uint4 r[kVecs];
   __device__ __forceinline__ float at(int j) const {
     const uint32_t w = (&r[j >> 3].x)[(j >> 1) & 3];
@@ -155,6 +165,18 @@ struct Batch<bf16> {
   static __device__ __forceinline__ uint32_t absent() { return 0xff80ff80u; }
 };
 
+// One of 16 values by halving.
+template <class F>
+__device__ __forceinline__ float pick16(int j, F at) {
+  float a[8], b[4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = (j & 8) ? at(8 + i) : at(i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = (j & 4) ? a[4 + i] : a[i];
+  const float c = (j & 2) ? b[2] : b[0], d = (j & 2) ? b[3] : b[1];
+  return (j & 1) ? d : c;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t elem_bits(const T *p);
 template <>
@@ -171,15 +193,20 @@ struct LpArgs {
 
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __grid_constant__ LpArgs p) {
-  constexpr int E = Batch<T>::E, N = E * kVecs;
-  __shared__ unsigned long long s_top[kLpWarps][32];
-  __shared__ uint32_t s_bound[kLpWarps][32];
-  __shared__ RowSum s_sum[kLpWarps];
+  static_assert(Batch<T>::E * Batch<T>::kVecs == 16, "pick16");
+  constexpr int E = Batch<T>::E, kVecs = Batch<T>::kVecs, N = E * kVecs;
+  __shared__ Picks s_pick;
+  __shared__ __align__(16) GroupMax s_max[2];
+  __shared__ RowSum s_sum[kLpWarps], s_part[kMaxLpCluster];
+  __shared__ float s_wmax[kLpWarps];
+  __shared__ unsigned long long s_list[kMaxLpCluster][32];  // the blocks' best entries, pushed into the first one's
   // every block of the launch sees the same cluster size
   if (p.cluster > 1 && cluster_ctas() != (uint32_t)p.cluster) {
     if (threadIdx.x == 0 && p.err) atomicExch(p.err, kShapeErrorBase + 4);
     return;
   }
+  // (the peers are running once all have arrived: waited for before the exchange)
+  if (p.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x / p.cluster, rank = blockIdx.x - row * p.cluster;
   const int V = p.a.V, k = p.a.top_k;
@@ -190,6 +217,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   const long long n_vec = ((long long)V + lead + E - 1) / E;
   const long long per = (n_vec + p.cluster - 1) / p.cluster;
   const long long v_begin = per * rank, v_end = min(n_vec, v_begin + per);
+  if (threadIdx.x == 0) s_pick.n = 0;
   auto load = [&](Batch<T> &b, long long v0) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
@@ -217,39 +245,52 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   uint32_t bound = 0;                    // entries below it are not among the block's k best
   Batch<T> cur, nxt;
   constexpr long long kStep = (long long)kLpThreads * kVecs;
-  long long refresh = v_begin + kStep;  // the batch after which the bound is renewed
+  long long renew = v_begin;             // the batch with which the bound is renewed
+  int turn = 0;
   load(cur, v_begin);
+  // the given tokens' logits, early (the first block looks them up at the end)
+  int my_id = -1;
+  uint32_t my_bits = 0;
+  if (rank == 0 && threadIdx.x < p.a.n_given) {
+    my_id = p.a.tokens[(size_t)row * p.a.n_given + threadIdx.x];
+    if (my_id >= 0 && my_id < V) my_bits = elem_bits(x + my_id);
+  }
   for (long long v0 = v_begin; v0 < v_end; v0 += kStep) {
     if (v0 + kStep < v_end) load(nxt, v0 + kStep);
     const float mb = cur.max();
     if (mb > r.m) rebase(r, mb, p.c);
     const float m = r.m > -INFINITY ? r.m : 0.0f;
+    const f32x2 minus_m = pair(-m, -m), cc = pair(p.c, p.c);
+    f32x2 sum = pair(0.0f, 0.0f), dot = sum;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float d = (cur.at(j) - m) * p.c, e = ex2_approx(d);
-      r.s += e;  // NaN here marks the row
-      r.a += e * fmaxf(d, -1000.0f);
+    for (int j = 0; j < N; j += 2) {
+      const float2 d = split(mul2(add2(pair(cur.at(j), cur.at(j + 1)), minus_m), cc));
+      const f32x2 e = pair(ex2_approx(d.x), ex2_approx(d.y));
+      sum = add2(sum, e);  // NaN here marks the row
+      dot = fma2(e, pair(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f)), dot);
     }
+    const float2 sums = split(sum), dots = split(dot);
+    r.s += sums.x + sums.y;
+    r.a += dots.x + dots.y;
     if (k) {
       const uint32_t ob = order_bits(mb);
-      if (v0 == v_begin) {  // the block's bound; a thread without entries has none
-        join_lists(s_bound, sort_lanes(v0 + threadIdx.x < v_end ? ob : 0u));
-        bound = s_bound[0][k - 1];
+      if (v0 == renew) {  // after batches 1, 2, 4, 8 ...: from the threads' running maxima
+        renew = v_begin + 2 * (renew + kStep - v_begin) - kStep;
+        // a thread without entries so far has none (its first vector lies behind the end)
+        bound = max(bound, group_bound(v_begin + threadIdx.x < v_end ? order_bits(r.m) : 0u, k, s_max + turn));
+        turn ^= 1;
       }
       // later batches hold higher indices, so an equal value does not enter a full list
       if (__any_sync(0xffffffffu, ob >= bound && (ob > (uint32_t)(kth >> 32) || kth == 0))) {
         // the lane's candidates (NaN among them: the exact test drops it)
-        const uint32_t low = larger(bound, (uint32_t)(kth >> 32));
+        const uint32_t low = max(bound, (uint32_t)(kth >> 32));
         const float lim = low ? order_value(low) : -INFINITY;
         uint32_t mask = 0;
 #pragma unroll
         for (int j = 0; j < N; ++j) mask |= cur.at(j) < lim ? 0u : 1u << j;
         while (__any_sync(0xffffffffu, mask != 0)) {
           const int j = __ffs(mask) - 1;
-          float v = 0.0f;
-#pragma unroll
-          for (int q = 0; q < N; ++q)
-            if (q == j) v = cur.at(q);
+          const float v = pick16(j & 15, [&](int q) { return cur.at(q); });
           const long long at_v = v0 + (j / E) * kLpThreads + threadIdx.x, i = at_v * E - lead + j % E;
           const uint32_t o = order_bits(v);
           const unsigned long long key = ((unsigned long long)o << 32) | (uint32_t)~(uint32_t)i;
@@ -257,22 +298,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
           mask &= mask - 1;
           while (todo) {
             const unsigned long long n = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
-            const int at = __popc(__ballot_sync(0xffffffffu, best > n));  // entries before it
+            const int at = __popc(__ballot_sync(0xffffffffu, best > n));  // entries before it (32: it drops out)
             const unsigned long long up = __shfl_up_sync(0xffffffffu, best, 1);
             if (lane == at) best = n;
             else if (lane > at) best = up;
-            kth = __shfl_sync(0xffffffffu, best, k - 1);
             todo &= todo - 1;
-            todo &= __ballot_sync(0xffffffffu, key > kth);
           }
-        }
-      }
-      // after 2, 4, 8 ... batches: the k-th entry of all the block's lists so far
-      if (v0 == refresh) {
-        refresh = v_begin + 2 * (refresh + kStep - v_begin) - kStep;
-        if (v0 + kStep < v_end) {
-          join_lists(s_bound, (uint32_t)(best >> 32));
-          bound = larger(bound, s_bound[0][k - 1]);
+          kth = __shfl_sync(0xffffffffu, best, k - 1);
         }
       }
     }
@@ -280,51 +312,54 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   }
 
   // ---- the block's state, then the row's ------------------------------------------
-  for (int o = 16; o; o >>= 1) {
-    RowSum q;
-    q.m = __shfl_xor_sync(0xffffffffu, r.m, o);
-    q.s = __shfl_xor_sync(0xffffffffu, r.s, o);
-    q.a = __shfl_xor_sync(0xffffffffu, r.a, o);
-    r = merge(r, q, p.c);
-  }
-  if (lane == 0) s_sum[warp] = r;
-  if (k) join_lists(s_top, best);
+  const float wm = lanes_max(r.m);
+  if (lane == 0) s_wmax[warp] = wm;
+  if (k && v_begin < v_end) bound = max(bound, group_bound(v_begin + threadIdx.x < v_end ? order_bits(r.m) : 0u, k, s_max + turn));
   else __syncthreads();
-  if (warp == 0) {
-    r = s_sum[0];
-    for (int w = 1; w < kLpWarps; ++w) r = merge(r, s_sum[w], p.c);
-  }
+  lanes_sum(r, lanes_max(s_wmax[lane & (kLpWarps - 1)]), p.c, 32);
+  if (lane == 0) s_sum[warp] = r;
+  if (k) collect(&s_pick, best, best != 0 && (uint32_t)(best >> 32) >= bound);
+  __syncthreads();
+  if (k) place(&s_pick, k);
+  r = s_sum[lane & (kLpWarps - 1)];
+  lanes_sum(r, r.m, p.c, kLpWarps);  // in every warp
+  __syncthreads();
   if (p.cluster > 1) {
-    __syncthreads();
-    if (threadIdx.x == 0) s_sum[0] = r;
-    __syncwarp();
-    tc::cluster_sync();
-    if (rank == 0) {  // warp w takes block w's state
-      RowSum q{-INFINITY, 0.0f, 0.0f};
-      unsigned long long l = 0;
-      if (warp < p.cluster) {
-        const uint32_t at = tc::cluster_addr(tc::smem_u32(&s_sum[0]), (uint32_t)warp);
-        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(q.m) : "r"(at) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(q.s) : "r"(at + 4) : "memory");
-        asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(q.a) : "r"(at + 8) : "memory");
-        asm volatile("ld.shared::cluster.u64 %0, [%1];\n"
-                     : "=l"(l)
-                     : "r"(tc::cluster_addr(tc::smem_u32(&s_top[0][lane]), (uint32_t)warp))
+    // Every block pushes its sums and entries (0: none) into the first block's
+    // shared memory; nothing is read from the others, which end here.
+    asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+    if (warp == 0) {
+      const unsigned long long key = lane < min(k, s_pick.n) ? s_pick.top[lane] : 0ull;
+      asm volatile("st.shared::cluster.u64 [%0], %1;\n" ::"r"(tc::cluster_addr(tc::smem_u32(&s_list[rank][lane]), 0u)), "l"(key)
+                   : "memory");
+      const float v = lane == 0 ? r.m : lane == 1 ? r.s : r.a;
+      if (lane < 3)
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(tc::cluster_addr(tc::smem_u32(&s_part[rank]) + 4 * lane, 0u)),
+                     "f"(v)
                      : "memory");
-      }
-      __syncthreads();  // this block's own state is read before it is overwritten
-      if (lane == 0) s_sum[warp] = q;
-      if (k) join_lists(s_top, l);
-      else __syncthreads();
-      if (warp == 0) {
-        r = s_sum[0];
-        for (int w = 1; w < p.cluster; ++w) r = merge(r, s_sum[w], p.c);
-      }
     }
     __syncwarp();
-    tc::cluster_sync();  // the peers' states have been read
+    tc::cluster_sync();
+    if (rank != 0) return;
+    RowSum q{-INFINITY, 0.0f, 0.0f};
+    unsigned long long kth_w = 0;  // no entry below some block's k-th is among the row's k best
+    if (lane < p.cluster) {
+      q = s_part[lane];
+      if (k) kth_w = s_list[lane][k - 1];
+    }
+    r = q;
+    lanes_sum(r, lanes_max(q.m), p.c, 32);
+    if (k) {
+      for (int o = 16; o; o >>= 1) kth_w = max(kth_w, __shfl_xor_sync(0xffffffffu, kth_w, o));
+      if (threadIdx.x == 0) s_pick.n = 0;
+      __syncthreads();
+      const unsigned long long l = warp < p.cluster ? s_list[warp][lane] : 0ull;
+      collect(&s_pick, l, l != 0 && l >= kth_w);
+      __syncthreads();
+      place(&s_pick, k);
+      __syncthreads();
+    }
   }
-  if (rank != 0 || warp != 0) return;
   const float nan = __int_as_float(0x7fc00000);
   const float top = r.m * p.a.inv_tau;
   const bool bad = !(r.s >= 0.0f) || top == INFINITY;  // a NaN entry, or +inf
@@ -333,27 +368,28 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
     if (bad) return nan;
     return raw == -INFINITY ? raw : (raw * p.a.inv_tau - top) - logs;
   };
-  if (lane == 0) {
+  if (threadIdx.x == 0) {
     if (p.a.lse) p.a.lse[row] = top + logs;
     if (p.a.entropy) p.a.entropy[row] = bad ? nan : (r.s > 0.0f ? logs - kLn2f * (r.a / r.s) : 0.0f);
   }
-  if (lane < k) {
-    const unsigned long long key = s_top[0][lane];
-    p.a.top_ids[(size_t)row * k + lane] = (int)~(uint32_t)key;
-    if (p.a.top_logprobs) p.a.top_logprobs[(size_t)row * k + lane] = logprob(order_value((uint32_t)(key >> 32)));
+  if (threadIdx.x < k) {
+    const unsigned long long key = s_pick.top[threadIdx.x];
+    p.a.top_ids[(size_t)row * k + threadIdx.x] = (int)~(uint32_t)key;
+    if (p.a.top_logprobs) p.a.top_logprobs[(size_t)row * k + threadIdx.x] = logprob(order_value((uint32_t)(key >> 32)));
   }
-  for (int j = lane; j < p.a.n_given; j += 32) {
-    const size_t at = (size_t)row * p.a.n_given + j;
-    const int id = p.a.tokens[at];
+  for (int j = threadIdx.x; j < p.a.n_given; j += kLpThreads) {
+    if (j >= kLpThreads) {
+      my_id = p.a.tokens[(size_t)row * p.a.n_given + j];
+      if (my_id >= 0 && my_id < V) my_bits = elem_bits(x + my_id);
+    }
     float lp = 0.0f;  // -1: no token here
-    if (id >= 0 && id < V) {
-      const uint32_t b = elem_bits(x + id);
-      lp = logprob(__uint_as_float(sizeof(T) == 4 ? b : b << 16));
-    } else if (id != -1) {
+    if (my_id >= 0 && my_id < V) {
+      lp = logprob(__uint_as_float(sizeof(T) == 4 ? my_bits : my_bits << 16));
+    } else if (my_id != -1) {
       lp = nan;
       if (p.err) atomicExch(p.err + 1, kBadToken);
     }
-    p.a.logprobs[at] = lp;
+    p.a.logprobs[(size_t)row * p.a.n_given + j] = lp;
   }
 }
 
@@ -394,6 +430,8 @@ cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st) {
   p.c = (float)(1.4426950408889634 * (double)a.inv_tau);
   p.err = err;
   // blocks per row: two for every SM in all, no fewer than 8192 entries each
+  // (1024 rows of 262144: 186 us with one, 220 with two: joining costs more than
+  // the last wave's idle SMs; one row: 7.7 us with 16)
   int c = 1;
   while (c < kMaxLpCluster && (long long)a.rows * c * 2 <= 2 * 152 && a.V / (2 * c) >= 8192) c *= 2;
   p.cluster = c;
