@@ -1740,7 +1740,7 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
   CKR(check_rows("out", out, out_stride, n_tok, n_q_heads, head_dim, 8));
   if (n_tok == 0 || n_seqs == 0) return DG_OK;
   if (q == out) return fail(DG_EINVAL, "out must not be q");
-  const int64_t key_tiles = ((int64_t)max_pages * page_size + 127) / 128 + 2;  // with a unit's start-up cost
+  const int64_t key_tiles = ((int64_t)max_pages * page_size + 127) / 128 + dg::kTreeUnitCost;
   const int64_t row_tiles = (int64_t)n_tok * (n_q_heads / n_kv_heads) / 128 + n_seqs;
   if (key_tiles * n_kv_heads > INT32_MAX / 2 / row_tiles) return fail(DG_EINVAL, "the batch's page tables span too many keys");
   const size_t need = dg::tree_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);

@@ -283,6 +283,7 @@ struct TreeAttention {
   bf16 *out;
   long long out_stride;
 };
+constexpr int kTreeUnitCost = 4;  // cost of starting a unit of rows, in key tiles
 size_t tree_attention_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int hd);
 cudaError_t tree_attention(const TreeAttention &a, void *ws, int *err, cudaStream_t st);
 

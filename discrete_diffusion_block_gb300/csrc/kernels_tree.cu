@@ -99,15 +99,17 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &p, int b) {
   return s;
 }
 
-// The cost of a unit in key tiles, for the equal ranges: its tiles, and as many
-// more as starting it takes (rows staged, sums written out: 2500 cycles where a
-// tile takes 1500).  A range's tiles are those of its cost units that lie
-// behind the start-up of their unit.
-constexpr int kUnitCost = 2;
+// The cost of a unit in key tiles, for the equal ranges: its tiles, and
+// kTreeUnitCost more for starting it (rows staged, the first tile's way through
+// all stages, sums written out and joined).  A range's tiles are those of its
+// cost units that lie behind the start-up of their unit.  Measured with 2, 4, 6
+// in its place: one sequence of 61 tokens over 32k keys 36.3, 35.8, 36.4 us; 40
+// ragged sequences of 5 tokens 26.7, 26.7, 28.3; 64 sequences of 24 tokens over
+// 16k 258, 260, 263; batches of many short sequences 4 to 10 % less with 4.
 
 // Cost of all its units; the host has checked that a batch's sum fits 31 bits.
 __device__ __forceinline__ int seq_cost(const TreeArgs &p, const Seq &s) {
-  return s.n ? p.a.Hkv * s.row_tiles * (s.key_tiles + kUnitCost) : 0;
+  return s.n ? p.a.Hkv * s.row_tiles * (s.key_tiles + kTreeUnitCost) : 0;
 }
 
 // The pieces of a block's range: the key tiles [kt0, kt1) of unit (b, g, rt).
@@ -117,16 +119,16 @@ struct Walk {
   Seq s;
   int b, g, rt, kt0, kt1, at, left;
   __device__ __forceinline__ void clip(int from, int n) {  // cost units [from, from + n) of the unit
-    const int end = min(s.key_tiles + kUnitCost, from + n);
-    kt0 = max(0, from - kUnitCost);
-    kt1 = max(0, end - kUnitCost);
+    const int end = min(s.key_tiles + kTreeUnitCost, from + n);
+    kt0 = max(0, from - kTreeUnitCost);
+    kt1 = max(0, end - kTreeUnitCost);
     left = n - (end - from);
   }
   // false: the range holds no tile
   __device__ __forceinline__ bool begin(const TreeArgs &p, int b_, int from, int n) {
     b = b_;
     s = load_seq(p, b);
-    const int cost = s.key_tiles + kUnitCost, u = from / cost;
+    const int cost = s.key_tiles + kTreeUnitCost, u = from / cost;
     g = u / s.row_tiles;
     rt = u - g * s.row_tiles;
     at = u * cost - from;
@@ -136,7 +138,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const TreeArgs &p) {
     do {
       if (left <= 0) return false;
-      at += s.key_tiles + kUnitCost;
+      at += s.key_tiles + kTreeUnitCost;
       if (++rt == s.row_tiles) {
         rt = 0;
         if (++g == p.a.Hkv) {
@@ -264,7 +266,7 @@ struct Span {
 // The span of the walk's unit; start: where the range begins.
 __device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, int start, int per) {
   Span u;
-  const int begin = start + w.at, tiles = begin + kUnitCost;
+  const int begin = start + w.at, tiles = begin + kTreeUnitCost;
   u.first = tiles / per;
   u.last = (tiles + w.s.key_tiles - 1) / per;
   u.first_slot = 2 * u.first + (begin > u.first * per ? 1 : 0);  // a piece of the unit before comes first there
