@@ -14,14 +14,21 @@
 // at position 10^6).  Its top 32 bits split exactly into a quadrant and a
 // remainder in [-pi/4, pi/4], whose sine and cosine are Taylor sums.
 //
-// Bound by the bytes of the rows.  Layout: a head is handled by hd / 16 lanes.
-// Lane i < rd / 16 holds the 8-element chunks i and i + rd / 16, whose elements
-// rotate with one another, the lanes behind it the chunks 2 i and 2 i + 1: the
-// rotation needs no exchange between lanes, and loads and stores are 16 bytes
-// wide.  A block takes a few tokens at a time, all their heads at once: while
-// the rows are in flight its threads compute the tokens' sines and cosines
-// once each, multiplied with the gains, into shared memory, from where every
-// head of a token takes them.
+// Bound by the bytes of the rows: 16384 tokens of 16 + 8 heads of 128 (201 MB in
+// and out) take 34.7 us, 5.8 TB/s; a plain addition that reads and writes as
+// much takes 33.2.
+//
+// Layout: a head is handled by hd / 16 lanes.  Lane i < rd / 16 holds the
+// 8-element chunks i and i + rd / 16, whose elements rotate with one another, the
+// lanes behind it the chunks 2 i and 2 i + 1: the rotation needs no exchange
+// between lanes, and loads and stores are 16 bytes wide.  A warp takes a token
+// at a time, and of its heads as many as the lanes hold, twice over: the token's
+// sines and cosines are computed once, multiplied with the gains, into the warp's
+// own shared memory, from where every head takes them.  The rows of the next
+// groups of heads, the next token's too, are on their way to shared memory
+// meanwhile (each lane copies and reads its own chunks), so no warp waits for
+// another.  A block of some tokens that loaded, met at a barrier and stored took
+// 40.8 us, although as many bytes were on their way: its phases did not overlap.
 #include <math.h>
 
 #include "f32x2.cuh"
@@ -31,29 +38,42 @@ namespace dg {
 
 namespace {
 
-constexpr int kRopeThreads = 512;   // most threads of a block
+// Warps of a block and resident blocks, and the groups of heads a warp has on
+// their way: 16384 tokens of 16 + 8 heads of 128 take 34.7 us and 17,400 tokens
+// appended to 8 heads 26.4 us with (2 blocks, 3 stages), 35.1 and 26.9 with
+// (2, 4), 34.6 and 28.5 with (3, 3), 41.1 and 33.8 with (3, 6).
+constexpr int kRopeWarps = 8, kRopeBlocks = 2, kStages = 3;
 constexpr int kMaxHalfRope = 128;
-constexpr int kRopeSmem = 64 << 10;  // most shared memory of a block's factors
 
 // Frequencies of the rotation in turns, as 64-bit fractions.
 struct RopeFreq {
   unsigned long long turn[kMaxHalfRope];
 };
 
-// A lane's two chunks of a head as loaded.
+// A lane's two chunks of a head as loaded, and its way through shared memory:
+// piece n of lane l at stage[32 n + l], which the lane itself copies and reads.
 template <typename T>
 struct Chunks {
-  uint4 a[sizeof(T) / 2], b[sizeof(T) / 2];
-};
-
-template <typename T>
-__device__ __forceinline__ void load_chunks(Chunks<T> &x, const T *head, int c0, int c1) {
+  static constexpr int kPieces = sizeof(T);  // of 16 bytes
+  uint4 a[kPieces / 2], b[kPieces / 2];
+  static __device__ __forceinline__ void request(uint4 *stage, const T *head, int c0, int c1) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-    x.a[i] = ((const uint4 *)(head + 8 * c0))[i];
-    x.b[i] = ((const uint4 *)(head + 8 * c1))[i];
+    for (int i = 0; i < kPieces / 2; ++i) {
+      copy16(stage + 32 * i, (const uint4 *)(head + 8 * c0) + i);
+      copy16(stage + 32 * (kPieces / 2 + i), (const uint4 *)(head + 8 * c1) + i);
+    }
   }
-}
+  __device__ __forceinline__ void read(const uint4 *stage) {
+#pragma unroll
+    for (int i = 0; i < kPieces / 2; ++i) {
+      a[i] = stage[32 * i];
+      b[i] = stage[32 * (kPieces / 2 + i)];
+    }
+  }
+  static __device__ __forceinline__ void copy16(uint4 *to, const uint4 *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+  }
+};
 
 // Eight values of a chunk as four pairs.
 __device__ __forceinline__ void unpack8(const uint4 (&w)[1], f32x2 *x) {
@@ -127,62 +147,77 @@ __device__ __forceinline__ float2 turn_angle(unsigned long long turn, int pos) {
 // (without rotation a ga, b gb), as float4 [ga c, -gb s, gb c, ga s][2][lanes]:
 // lane i's eight values of each, four to a float4, lanes adjacent: 2 HD floats.
 
-// Factors of pair j (element j of the lanes' first chunks and its partner).
+// Factors of the pairs j and j + 1 (j even; elements j, j + 1 of the lanes'
+// first chunks and their partners).
 template <int HD>
-__device__ __forceinline__ void put_factors(float *to, int j, int rd16, const float *gain, float2 sc) {
+__device__ __forceinline__ void put_factors(float *to, int j, int rd16, const float *gain, float2 sc0, float2 sc1) {
   constexpr int L = HD / 16;
   const int i = j >> 3, e = j & 7;
   int c0, c1;
   lane_chunks(i, rd16, &c0, &c1);
-  const float ga = gain ? gain[8 * c0 + e] : 1.0f, gb = gain ? gain[8 * c1 + e] : 1.0f;
-  float *at = to + ((e >> 2) * L + i) * 4 + (e & 3);
-  at[0 * 8 * L] = ga * sc.y;
-  at[1 * 8 * L] = -gb * sc.x;
-  at[2 * 8 * L] = gb * sc.y;
-  at[3 * 8 * L] = ga * sc.x;
+  float2 ga = make_float2(1.0f, 1.0f), gb = ga;
+  if (gain) {
+    ga = *(const float2 *)(gain + 8 * c0 + e);
+    gb = *(const float2 *)(gain + 8 * c1 + e);
+  }
+  float2 *at = (float2 *)(to + ((e >> 2) * L + i) * 4 + (e & 3));
+  at[0 * 4 * L] = make_float2(ga.x * sc0.y, ga.y * sc1.y);
+  at[1 * 4 * L] = make_float2(-gb.x * sc0.x, -gb.y * sc1.x);
+  at[2 * 4 * L] = make_float2(gb.x * sc0.y, gb.y * sc1.y);
+  at[3 * 4 * L] = make_float2(ga.x * sc0.x, ga.y * sc1.x);
 }
 
-// Norm (any: some head of the launch has one; normed: this one) and rotation of
-// a lane's chunks with its token's factors.
-template <int HD>
-__device__ __forceinline__ void turn_head(f32x2 *a, f32x2 *b, bool any, bool normed, float eps, bool turns, const float *factors, int i) {
+// Norm (any: some head of the launch has one; normed: this side's) and rotation
+// of a lane's chunks of U heads with their token's factors (a head's first
+// chunk: x[u][0..3], its second: x[u][4..7]); live: the heads to take, the same
+// in the whole warp.
+template <int HD, int U>
+__device__ __forceinline__ void turn_heads(f32x2 (&x)[U][8], int live, bool any, bool normed, float eps, bool turns,
+                                           const float *factors, int i) {
   constexpr int L = HD / 16;
   if (any) {
-    const float r = head_scale<HD>(a, b, eps);
-    const f32x2 rr = pair(r, r);
-    if (normed) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a[e] = mul2(a[e], rr);
-        b[e] = mul2(b[e], rr);
-      }
+    for (int u = 0; u < U; ++u) {
+      if (u >= live) break;
+      const float s = head_scale<HD>(x[u], x[u] + 4, eps), r = normed ? s : 1.0f;
+      const f32x2 rr = pair(r, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = mul2(x[u][e], rr);
     }
   }
 #pragma unroll
   for (int e = 0; e < 4; e += 2) {
     const ulonglong2 *at = (const ulonglong2 *)factors + (e >> 1) * L + i;
     const ulonglong2 ac = at[0], bc = at[4 * L];
-    const f32x2 x0 = a[e], x1 = a[e + 1], y0 = b[e], y1 = b[e + 1];
-    a[e] = mul2(x0, ac.x);
-    a[e + 1] = mul2(x1, ac.y);
-    b[e] = mul2(y0, bc.x);
-    b[e + 1] = mul2(y1, bc.y);
+    ulonglong2 bs, as;
     if (turns) {
-      const ulonglong2 bs = at[2 * L], as = at[6 * L];
-      a[e] = fma2(y0, bs.x, a[e]);
-      a[e + 1] = fma2(y1, bs.y, a[e + 1]);
-      b[e] = fma2(x0, as.x, b[e]);
-      b[e + 1] = fma2(x1, as.y, b[e + 1]);
+      bs = at[2 * L];
+      as = at[6 * L];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u >= live) break;
+      f32x2 *a = x[u] + e, *b = x[u] + 4 + e;
+      const f32x2 x0 = a[0], x1 = a[1], y0 = b[0], y1 = b[1];
+      a[0] = mul2(x0, ac.x);
+      a[1] = mul2(x1, ac.y);
+      b[0] = mul2(y0, bc.x);
+      b[1] = mul2(y1, bc.y);
+      if (turns) {
+        a[0] = fma2(y0, bs.x, a[0]);
+        a[1] = fma2(y1, bs.y, a[1]);
+        b[0] = fma2(x0, as.x, b[0]);
+        b[1] = fma2(x1, as.y, b[1]);
+      }
     }
   }
 }
 
-// How a launch is laid out: a block's threads are `abreast` tokens x heads x
-// lanes (heads in `rounds` turns when they exceed a block), and each takes up
-// to `deep` tokens at a time.
+// How a launch is laid out: a token's heads are groups of U 32 / (hd / 16)
+// heads, those of the first side and then those of the second; a warp's item is
+// a token, or one of its `parts` of `each` groups.
 struct RopePlan {
-  int abreast, deep, heads, rounds, threads, grid;
-  size_t smem;
+  int parts, each, groups, first;  // groups: of both sides; first: of the first side
 };
 
 struct QkArgs {
@@ -197,70 +232,112 @@ struct QkArgs {
   RopePlan plan;
 };
 
-// Tokens a thread has in flight (of bf16 rows; half as many of fp32 rows or of
-// keys with values) and the resident blocks the registers are held down for:
-// 16384 tokens of 16 + 8 heads of 128 take 40.8 us with (2, 2), 46.3 with
-// (4, 2), 50.4 with (2, 1): latency, not bytes, rules below half occupancy.
-constexpr int kDeep = 2, kRopeBlocks = 2;
+// Where a warp is: group g of [g0, g1) of token t; end: it has no more.
+struct At {
+  uint32_t item, t;
+  int g, g0, g1;
+  __device__ __forceinline__ At(const RopePlan &p, uint32_t it, int n_tok) { set(p, it, n_tok); }
+  __device__ __forceinline__ void set(const RopePlan &p, uint32_t it, int n_tok) {
+    item = t = it;
+    g0 = 0;
+    if (p.parts > 1) {
+      t = it / p.parts;
+      g0 = (int)(it - t * p.parts) * p.each;
+    }
+    g = g0;
+    g1 = t < (uint32_t)n_tok ? min(g0 + p.each, p.groups) : 0;
+  }
+  __device__ __forceinline__ bool end() const { return g >= g1; }
+};
+
+// Shared memory of a warp in 16-byte pieces: the rows of kStages groups on their
+// way, then the token's factors.
+template <typename T, int HD, int U, int SIDES>
+struct RopeSmem {
+  static constexpr int stage = 32 * U * Chunks<T>::kPieces;
+  static constexpr int warp = kStages * stage + SIDES * (2 * HD * 4 / 16);
+};
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) qk_norm_rope_kernel(const __grid_constant__ QkArgs p,
-                                                                    const __grid_constant__ RopeFreq f) {
-  constexpr int L = HD / 16, F = 2 * HD, kU = sizeof(T) == 2 ? kDeep : kDeep / 2;
-  extern __shared__ float4 s_factors4[];
-  float *s_factors = (float *)s_factors4;  // [token][q, k][F]
-  __shared__ unsigned long long s_turn[kMaxHalfRope];
-  for (int j = threadIdx.x; j < 8 * p.rd16; j += blockDim.x) s_turn[j] = f.turn[j];
-  __syncthreads();
-  const int i = threadIdx.x & (L - 1), H = p.Hq + p.Hkv;
-  const int tt = (threadIdx.x / L) / p.plan.heads, h_mine = threadIdx.x / L - tt * p.plan.heads;
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) qk_norm_rope_kernel(const __grid_constant__ QkArgs p,
+                                                                            const __grid_constant__ RopeFreq f) {
+  constexpr int L = HD / 16, F = 2 * HD, U = sizeof(T) == 2 ? 2 : 1, step = 32 / L;
+  using S = RopeSmem<T, HD, U, 2>;
+  extern __shared__ uint4 s_rope[];
+  __shared__ __align__(16) unsigned long long s_turn[kMaxHalfRope];
+  const int lane = threadIdx.x & 31, i = lane & (L - 1), n_warps = blockDim.x >> 5;
+  uint4 *stages = s_rope + (threadIdx.x >> 5) * S::warp + lane;
+  float *factors = (float *)(s_rope + (threadIdx.x >> 5) * S::warp + kStages * S::stage);  // [q, k][F]
   int c0, c1;
   lane_chunks(i, p.rd16, &c0, &c1);
-  const bool turns = i < p.rd16;
-  const int block_toks = p.plan.abreast * min(kU, p.plan.deep);
-  for (long long t0 = (long long)blockIdx.x * block_toks; t0 < p.n_tok; t0 += (long long)gridDim.x * block_toks) {
-    const int n_here = (int)min((long long)block_toks, p.n_tok - t0);
-    for (int round = 0; round < p.plan.rounds; ++round) {
-      const int h = round * p.plan.heads + h_mine;
-      const bool is_q = h < p.Hq, live = tt < p.plan.abreast && h < H;
-      const T *src = (is_q ? (const T *)p.q + t0 * p.q_stride + (long long)h * HD
-                           : (const T *)p.k + t0 * p.k_stride + (long long)(h - p.Hq) * HD);
-      const long long stride = is_q ? p.q_stride : p.k_stride;
-      Chunks<T> x[kU];
+  const bool turns = i < p.rd16, any = p.q_gain || p.k_gain;
+  const uint32_t stride = gridDim.x * n_warps;
+  At at(p.plan, blockIdx.x * n_warps + (threadIdx.x >> 5), p.n_tok), ahead = at;
+  // a lane's heads of a group: h, h + step, ..
+  auto head_of = [&](const At &at) { return U * step * (at.g < p.plan.first ? at.g : at.g - p.plan.first) + lane / L; };
+  // requests the rows of the group `ahead`, and goes on to the next
+  auto request = [&](int stage) {
+    if (!ahead.end()) {
+      const bool is_q = ahead.g < p.plan.first;
+      const int h = head_of(ahead), n = (is_q ? p.Hq : p.Hkv) - h;
+      const T *src = (is_q ? (const T *)p.q + ahead.t * p.q_stride : (const T *)p.k + ahead.t * p.k_stride) +
+                     (long long)h * HD;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = tt + u * p.plan.abreast;
-        if (live && t < n_here) load_chunks(x[u], src + t * stride, c0, c1);
-      }
-      if (round == 0) {  // the factors, while the rows are in flight
-        __syncthreads();  // the last tokens' have been read
-        for (int it = threadIdx.x; it < n_here * (HD / 2); it += blockDim.x) {
-          const int t = it / (HD / 2), j = it & (HD / 2 - 1);
-          float2 sc = make_float2(0.0f, 1.0f);
-          if (j < 8 * p.rd16) sc = turn_angle(s_turn[j], p.positions[t0 + t]);
-          if (p.Hq) put_factors<HD>(s_factors + (2 * t) * F, j, p.rd16, p.q_gain, sc);
-          if (p.Hkv) put_factors<HD>(s_factors + (2 * t + 1) * F, j, p.rd16, p.k_gain, sc);
-        }
-        __syncthreads();
-      }
-      bf16 *dst = is_q ? p.q_out + t0 * p.q_out_stride + (long long)h * HD
-                       : p.k_out + t0 * p.k_out_stride + (long long)(h - p.Hq) * HD;
-      const long long dst_stride = is_q ? p.q_out_stride : p.k_out_stride;
-      const bool normed = is_q ? p.q_gain != nullptr : p.k_gain != nullptr;
+      for (int u = 0; u < U; ++u)
+        if (u * step < n) Chunks<T>::request(stages + stage * S::stage + 32 * u * Chunks<T>::kPieces, src + u * step * HD, c0, c1);
+      if (++ahead.g == ahead.g1) ahead.set(p.plan, ahead.item + stride, p.n_tok);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = tt + u * p.plan.abreast;
-        if (u * p.plan.abreast >= n_here) break;  // the same in the whole block
-        f32x2 a[4], b[4];
-        unpack8(x[u].a, a);
-        unpack8(x[u].b, b);
-        turn_head<HD>(a, b, p.q_gain || p.k_gain, normed, p.eps, turns, s_factors + (2 * min(t, n_here - 1) + !is_q) * F, i);
-        if (live && t < n_here) {
-          *(uint4 *)(dst + t * dst_stride + 8 * c0) = pack8(a);
-          *(uint4 *)(dst + t * dst_stride + 8 * c1) = pack8(b);
+  for (int k = 0; k < kStages - 1; ++k) request(k);
+  int stage = 0, pos = p.rd16 && !at.end() ? p.positions[at.t] : 0;
+  for (int j = threadIdx.x; j < 8 * p.rd16; j += blockDim.x) s_turn[j] = f.turn[j];
+  __syncthreads();
+  while (!at.end()) {
+    // the token's factors, while its rows are in flight
+#pragma unroll
+    for (int j = 2 * lane; j < HD / 2; j += 64) {
+      float2 sc0 = make_float2(0.0f, 1.0f), sc1 = sc0;
+      if (j < 8 * p.rd16) {
+        const ulonglong2 turn = *(const ulonglong2 *)(s_turn + j);
+        sc0 = turn_angle(turn.x, pos);
+        sc1 = turn_angle(turn.y, pos);
+      }
+      if (at.g0 < p.plan.first) put_factors<HD>(factors, j, p.rd16, p.q_gain, sc0, sc1);
+      if (at.g1 > p.plan.first) put_factors<HD>(factors + F, j, p.rd16, p.k_gain, sc0, sc1);
+    }
+    __syncwarp();
+    At next = at;
+    next.set(p.plan, at.item + stride, p.n_tok);
+    if (p.rd16 && !next.end()) pos = p.positions[next.t];
+    for (; !at.end(); ++at.g) {
+      const bool is_q = at.g < p.plan.first;
+      const int h = head_of(at), n = (is_q ? p.Hq : p.Hkv) - h;
+      const int live = n + lane / L > step ? U : 1;  // whether any lane has a second head
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
+      f32x2 x[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        Chunks<T> raw;
+        raw.read(stages + stage * S::stage + 32 * u * Chunks<T>::kPieces);
+        unpack8(raw.a, x[u]);
+        unpack8(raw.b, x[u] + 4);
+      }
+      request(stage ? stage - 1 : kStages - 1);  // the stage that was read last
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      turn_heads<HD, U>(x, live, any, is_q ? p.q_gain != nullptr : p.k_gain != nullptr, p.eps, turns, factors + (is_q ? 0 : F), i);
+      bf16 *dst = (is_q ? p.q_out + at.t * p.q_out_stride : p.k_out + at.t * p.k_out_stride) + (long long)h * HD;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u * step < n) {
+          *(uint4 *)(dst + u * step * HD + 8 * c0) = pack8(x[u]);
+          *(uint4 *)(dst + u * step * HD + 8 * c1) = pack8(x[u] + 4);
         }
       }
     }
+    __syncwarp();  // the factors have been read
+    at = next;
   }
 }
 
@@ -298,89 +375,127 @@ struct Place {
   int page, slot, pos;
 };
 
-// Laid out as qk_norm_rope_kernel: keys normed and rotated, values copied, both
-// into the token's page slot.
+// Laid out as qk_norm_rope_kernel, the sides being keys and values: keys normed
+// and rotated, values copied, both into the token's page slot.
 template <int HD>
-__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks) rope_kv_append_kernel(const __grid_constant__ AppendArgs p,
-                                                                      const __grid_constant__ RopeFreq f) {
-  constexpr int L = HD / 16, F = 2 * HD, kU = kDeep / 2;
-  extern __shared__ float4 s_factors4[];
-  float *s_factors = (float *)s_factors4;  // [token][F]
-  __shared__ unsigned long long s_turn[kMaxHalfRope];
-  __shared__ Place s_place[kRopeThreads / 4 * kU];
-  for (int j = threadIdx.x; j < 8 * p.rd16; j += blockDim.x) s_turn[j] = f.turn[j];
-  __syncthreads();
-  const int i = threadIdx.x & (L - 1);
-  const int tt = (threadIdx.x / L) / p.plan.heads, h_mine = threadIdx.x / L - tt * p.plan.heads;
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_kernel(const __grid_constant__ AppendArgs p,
+                                                                              const __grid_constant__ RopeFreq f) {
+  constexpr int L = HD / 16, U = 2, step = 32 / L;
+  using S = RopeSmem<bf16, HD, U, 1>;
+  extern __shared__ uint4 s_rope[];
+  __shared__ __align__(16) unsigned long long s_turn[kMaxHalfRope];
+  const int lane = threadIdx.x & 31, i = lane & (L - 1), n_warps = blockDim.x >> 5;
+  uint4 *stages = s_rope + (threadIdx.x >> 5) * S::warp + lane;
+  float *factors = (float *)(s_rope + (threadIdx.x >> 5) * S::warp + kStages * S::stage);
   int c0, c1;
   lane_chunks(i, p.rd16, &c0, &c1);
   const bool turns = i < p.rd16;
-  const int block_toks = p.plan.abreast * min(kU, p.plan.deep);
-  for (long long t0 = (long long)blockIdx.x * block_toks; t0 < p.n_tok; t0 += (long long)gridDim.x * block_toks) {
-    const int n_here = (int)min((long long)block_toks, p.n_tok - t0);
-    for (int round = 0; round < p.plan.rounds; ++round) {
-      const int h = round * p.plan.heads + h_mine;
-      const bool live = tt < p.plan.abreast && h < p.Hkv;
-      const bf16 *ks = p.k + t0 * p.k_stride + (long long)h * HD, *vs = p.v + t0 * p.v_stride + (long long)h * HD;
-      Chunks<bf16> x[kU], y[kU];
+  const uint32_t stride = gridDim.x * n_warps;
+  At at(p.plan, blockIdx.x * n_warps + (threadIdx.x >> 5), p.n_tok), ahead = at;
+  auto head_of = [&](const At &at) { return U * step * (at.g < p.plan.first ? at.g : at.g - p.plan.first) + lane / L; };
+  auto request = [&](int stage) {
+    if (!ahead.end()) {
+      const int h = head_of(ahead);
+      const bf16 *src = (ahead.g < p.plan.first ? p.k + ahead.t * p.k_stride : p.v + ahead.t * p.v_stride) +
+                        (long long)h * HD;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = tt + u * p.plan.abreast;
-        if (live && t < n_here) {
-          load_chunks(x[u], ks + t * p.k_stride, c0, c1);
-          load_chunks(y[u], vs + t * p.v_stride, c0, c1);
+      for (int u = 0; u < U; ++u)
+        if (h + u * step < p.Hkv) Chunks<bf16>::request(stages + stage * S::stage + 64 * u, src + u * step * HD, c0, c1);
+      if (++ahead.g == ahead.g1) ahead.set(p.plan, ahead.item + stride, p.n_tok);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  // where token t's rows go; the same in the whole warp
+  auto place_of = [&](int t) {
+    const int b = row_sequence(p.offsets, p.n_seqs, t);
+    Place to{-1, 0, 0};
+    if (b >= p.n_seqs) return to;  // rows behind the last sequence are left alone
+    const long long slot = b < 0 ? -1 : (long long)p.prefix[b] + t - p.offsets[b];
+    if (slot >= 0 && slot < min((long long)p.max_pages * p.pg, 0x7fffffffll)) {
+      const int logical = (int)slot / p.pg;
+      to.page = p.tables[(long long)b * p.max_pages + logical];
+      to.slot = (int)slot - logical * p.pg;
+      to.pos = (int)slot;
+    }
+    if (to.page < 0 || to.page >= p.n_pages) {  // not written, reported by dg_op_status
+      to.page = -1;
+      if (lane == 0 && p.err) atomicExch(p.err + 1, kBadPage);
+    }
+    return to;
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) request(k);
+  Place to{-1, 0, 0};
+  int stage = 0, pos = 0;
+  if (!at.end()) {
+    to = place_of((int)at.t);
+    pos = p.positions ? p.positions[at.t] : to.pos;
+  }
+  for (int j = threadIdx.x; j < 8 * p.rd16; j += blockDim.x) s_turn[j] = f.turn[j];
+  __syncthreads();
+  while (!at.end()) {
+    if (at.g0 < p.plan.first) {  // the token's factors, while its rows are in flight
+#pragma unroll
+      for (int j = 2 * lane; j < HD / 2; j += 64) {
+        float2 sc0 = make_float2(0.0f, 1.0f), sc1 = sc0;
+        if (j < 8 * p.rd16) {
+          const ulonglong2 turn = *(const ulonglong2 *)(s_turn + j);
+          sc0 = turn_angle(turn.x, pos);
+          sc1 = turn_angle(turn.y, pos);
+        }
+        put_factors<HD>(factors, j, p.rd16, p.k_gain, sc0, sc1);
+      }
+    }
+    __syncwarp();
+    At next = at;
+    next.set(p.plan, at.item + stride, p.n_tok);
+    Place next_to{-1, 0, 0};
+    if (!next.end()) {
+      next_to = place_of((int)next.t);
+      pos = p.positions ? p.positions[next.t] : next_to.pos;
+    }
+    for (; !at.end(); ++at.g) {
+      const int h = head_of(at);
+      const bool is_k = at.g < p.plan.first;
+      const int live = p.Hkv - h + lane / L > step ? U : 1;
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
+      Chunks<bf16> y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) y[u].read(stages + stage * S::stage + 64 * u);
+      if (is_k) {
+        f32x2 x[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          unpack8(y[u].a, x[u]);
+          unpack8(y[u].b, x[u] + 4);
+        }
+        turn_heads<HD, U>(x, live, p.k_gain != nullptr, true, p.eps, turns, factors, i);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          y[u].a[0] = pack8(x[u]);
+          y[u].b[0] = pack8(x[u] + 4);
         }
       }
-      if (round == 0) {  // slots and factors, while the rows are in flight
-        __syncthreads();  // the last tokens' have been read
-        for (int t = threadIdx.x >> 5; t < n_here; t += blockDim.x >> 5) {
-          const int row = (int)t0 + t, b = row_sequence(p.offsets, p.n_seqs, row);
-          Place at{-1, 0, 0};
-          if (b < p.n_seqs) {  // rows behind the last sequence are left alone
-            const long long slot = b < 0 ? -1 : (long long)p.prefix[b] + row - p.offsets[b];
-            if (slot >= 0 && slot < min((long long)p.max_pages * p.pg, 0x7fffffffll)) {
-              const int logical = (int)slot / p.pg;
-              at.page = p.tables[(long long)b * p.max_pages + logical];
-              at.slot = (int)slot - logical * p.pg;
-              at.pos = (int)slot;
-            }
-            if (at.page < 0 || at.page >= p.n_pages) {  // not written, reported by dg_op_status
-              at.page = -1;
-              if ((threadIdx.x & 31) == 0 && p.err) atomicExch(p.err + 1, kBadPage);
-            }
+      request(stage ? stage - 1 : kStages - 1);  // the stage that was read last
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      if (to.page >= 0) {
+        const long long head = (long long)p.pg * HD;
+        const int s7 = to.slot & 7;
+        bf16 *dst = (is_k ? p.k_pool : p.v_pool) + ((long long)to.page * p.Hkv + h) * head + (long long)to.slot * 64;
+        bf16 *d0 = dst + (long long)(c0 >> 3) * p.pg * 64 + (((c0 & 7) ^ s7) << 3);
+        bf16 *d1 = dst + (long long)(c1 >> 3) * p.pg * 64 + (((c1 & 7) ^ s7) << 3);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (h + u * step < p.Hkv) {
+            *(uint4 *)(d0 + u * step * head) = y[u].a[0];
+            *(uint4 *)(d1 + u * step * head) = y[u].b[0];
           }
-          if ((threadIdx.x & 31) == 0) s_place[t] = at;
-        }
-        if (!p.positions) __syncthreads();  // the angles go by the slots
-        for (int it = threadIdx.x; it < n_here * (HD / 2); it += blockDim.x) {
-          const int t = it / (HD / 2), j = it & (HD / 2 - 1);
-          float2 sc = make_float2(0.0f, 1.0f);
-          if (j < 8 * p.rd16) sc = turn_angle(s_turn[j], p.positions ? p.positions[t0 + t] : s_place[t].pos);
-          put_factors<HD>(s_factors + t * F, j, p.rd16, p.k_gain, sc);
-        }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = tt + u * p.plan.abreast;
-        if (u * p.plan.abreast >= n_here) break;  // the same in the whole block
-        f32x2 a[4], b[4];
-        unpack8(x[u].a, a);
-        unpack8(x[u].b, b);
-        const int ts = min(t, n_here - 1);
-        turn_head<HD>(a, b, p.k_gain != nullptr, p.k_gain != nullptr, p.eps, turns, s_factors + ts * F, i);
-        const Place at = s_place[ts];
-        if (live && t < n_here && at.page >= 0) {
-          const long long blk = ((long long)at.page * p.Hkv + h) * p.pg * HD + (long long)at.slot * 64;
-          const long long a0 = blk + (long long)(c0 >> 3) * p.pg * 64 + (((c0 & 7) ^ (at.slot & 7)) << 3);
-          const long long a1 = blk + (long long)(c1 >> 3) * p.pg * 64 + (((c1 & 7) ^ (at.slot & 7)) << 3);
-          *(uint4 *)(p.k_pool + a0) = pack8(a);
-          *(uint4 *)(p.k_pool + a1) = pack8(b);
-          *(uint4 *)(p.v_pool + a0) = y[u].a[0];
-          *(uint4 *)(p.v_pool + a1) = y[u].b[0];
         }
       }
     }
+    __syncwarp();  // the factors have been read
+    at = next;
+    to = next_to;
   }
 }
 
@@ -402,49 +517,60 @@ const RopeFreq &rope_frequencies(int rope_dim, float base) {
   return f;
 }
 
-// heads: of all sides; sides: factor sets per token; in_flight: tokens a thread
-// loads at once.
-RopePlan rope_plan(int n_tok, int heads, int hd, int sides, int in_flight) {
-  RopePlan r;
-  const int lanes = hd / 16;
-  r.heads = heads * lanes <= kRopeThreads ? heads : kRopeThreads / lanes;
-  r.rounds = (heads + r.heads - 1) / r.heads;
-  r.abreast = 256 / (r.heads * lanes);
-  if (r.abreast < 1) r.abreast = 1;
-  r.deep = in_flight;
-  const size_t per_tok = (size_t)sides * 2 * hd * sizeof(float);
-  while (r.abreast > 1 && r.abreast * r.deep * per_tok > kRopeSmem) --r.abreast;
-  // fewer tokens a block while the blocks do not fill the machine
-  while (r.deep > 1 && (long long)r.abreast * r.deep * 152 * 4 > n_tok) r.deep /= 2;
-  while (r.abreast > 1 && (long long)r.abreast * 152 * 2 > n_tok) r.abreast /= 2;
-  r.threads = (r.abreast * r.heads * lanes + 31) / 32 * 32;
-  const int toks = r.abreast * r.deep, blocks = (n_tok + toks - 1) / toks;
-  r.grid = blocks < 152 * 32 ? blocks : 152 * 32;
-  r.smem = toks * per_tok;
+struct RopeLaunch {
+  RopePlan plan;
+  int grid, threads;
+};
+
+// first, second: heads of the two sides; group: heads of a group.
+RopeLaunch rope_plan(int n_tok, int first, int second, int group) {
+  RopeLaunch r;
+  RopePlan &p = r.plan;
+  p.first = (first + group - 1) / group;
+  p.groups = p.first + (second + group - 1) / group;
+  // parts of a token, each with factors of its own, only while whole tokens
+  // would leave warps without work
+  constexpr int most = 152 * kRopeBlocks * kRopeWarps;
+  int want = most / n_tok;
+  if (want > p.groups) want = p.groups;
+  if (want < 1) want = 1;
+  p.each = (p.groups + want - 1) / want;
+  p.parts = (p.groups + p.each - 1) / p.each;
+  const long long items = (long long)n_tok * p.parts;
+  const int warps = (int)(items < 152 * kRopeWarps ? (items + 151) / 152 : kRopeWarps);
+  // every warp the same count of items
+  const long long rounds = (items + most - 1) / most;
+  r.threads = 32 * warps;
+  r.grid = (int)((items + rounds * warps - 1) / (rounds * warps));
   return r;
+}
+
+// A kernel's blocks may ask for more than the 48 KiB that need no leave.
+template <typename K>
+cudaError_t rope_smem(K kern, size_t bytes) {
+  return bytes > (40 << 10) ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
 template <typename T, int HD>
 cudaError_t launch_qk(QkArgs p, const RopeFreq &f, cudaStream_t st) {
-  p.plan = rope_plan(p.n_tok, p.Hq + p.Hkv, HD, 2, sizeof(T) == 2 ? kDeep : kDeep / 2);
-  auto kern = qk_norm_rope_kernel<T, HD>;
-  if (p.plan.smem > (48 << 10) - 2048) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeSmem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<p.plan.grid, p.plan.threads, p.plan.smem, st>>>(p, f);
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;
+  const RopeLaunch l = rope_plan(p.n_tok, p.Hq, p.Hkv, 32 / (HD / 16) * U);
+  p.plan = l.plan;
+  const size_t smem = l.threads / 32 * RopeSmem<T, HD, U, 2>::warp * 16;
+  const cudaError_t e = rope_smem(qk_norm_rope_kernel<T, HD>, smem);
+  if (e != cudaSuccess) return e;
+  qk_norm_rope_kernel<T, HD><<<l.grid, l.threads, smem, st>>>(p, f);
   return cudaGetLastError();
 }
 
 template <int HD>
 cudaError_t launch_append(AppendArgs p, const RopeFreq &f, cudaStream_t st) {
-  p.plan = rope_plan(p.n_tok, p.Hkv, HD, 1, kDeep / 2);
-  auto kern = rope_kv_append_kernel<HD>;
-  if (p.plan.smem > (48 << 10) - 8192) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRopeSmem);
-    if (e != cudaSuccess) return e;
-  }
-  kern<<<p.plan.grid, p.plan.threads, p.plan.smem, st>>>(p, f);
+  const RopeLaunch l = rope_plan(p.n_tok, p.Hkv, p.Hkv, 32 / (HD / 16) * 2);
+  p.plan = l.plan;
+  const size_t smem = l.threads / 32 * RopeSmem<bf16, HD, 2, 1>::warp * 16;
+  const cudaError_t e = rope_smem(rope_kv_append_kernel<HD>, smem);
+  if (e != cudaSuccess) return e;
+  rope_kv_append_kernel<HD><<<l.grid, l.threads, smem, st>>>(p, f);
   return cudaGetLastError();
 }
 
