@@ -260,7 +260,8 @@ __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.sync 6, 2
 // A unit that spans the blocks first .. last: its pieces are slot first_slot and
 // slot 2 c of the blocks behind the first; row r0 + i is token row0 + (r0 + i) / G.
 struct Span {
-  int first, last, first_slot, row0, r0, n_rows, g;
+  int first, last, first_slot, row0, r0, g;
+  int shares, i0, rows;  // blocks with a share of its rows; this block's: rows i0 .. i0 + rows - 1
   __device__ __forceinline__ int slot(int s) const { return s == 0 ? first_slot : 2 * (first + s); }
 };
 // The span of the walk's unit; start: where the range begins.
@@ -272,15 +273,19 @@ __device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, int 
   u.first_slot = 2 * u.first + (begin > u.first * per ? 1 : 0);  // a piece of the unit before comes first there
   u.row0 = w.s.row0;
   u.r0 = 128 * w.rt;
-  u.n_rows = min(128, w.s.n * p.G - u.r0);
   u.g = w.g;
+  const int n_rows = min(128, w.s.n * p.G - u.r0), each = ceil_div(n_rows, u.last - u.first + 1);
+  u.shares = ceil_div(n_rows, each);
+  u.i0 = min(n_rows, ((int)blockIdx.x - u.first) * each);
+  u.rows = min(n_rows, u.i0 + each) - u.i0;
   return u;
 }
 
-// The join's scratch, in the idle K ring.
+// The join's scratch, in the idle rings.
 struct JoinSmem {
-  float2 state[128 + kTreeCtas + 8];  // [rows of the share][pieces] (m, l); .x becomes the weight
-  float4 sum[256];                    // a thread's sum, where several threads share a column's pieces
+  float2 state[512];      // [rows of the share][pieces], 128 + kTreeCtas at most: (m, l); .x becomes the weight
+  float4 sum[256];        // a thread's sum, where several threads share a column's pieces
+  float4 piece[32][256];  // [k][thread]: the pieces a thread adds up, copied by itself
 };
 
 // Waits (bounded) until the unit's pieces are there, flag s in lane s, s + 32 ..;
@@ -307,36 +312,39 @@ __device__ __forceinline__ void store_row4(const TreeArgs &p, const Span &u, int
 }
 
 // This block's share of a unit's rows, out of the pieces of all its blocks:
-// weights 2^(m_s - m*), pieces in the order of the keys.  Run by the 256 softmax
-// threads (tid) after the block's last piece.  The last warp to have seen the
-// unit's flags takes them down: a captured call, whose ticket is the same every
-// time, has to find them down.  Latency bound, and run once a launch: what is
-// loaded is loaded together, and the code is kept short (straight-line variants
-// for each shape spent more time on fetching instructions).
+// weights 2^(m_s - m*), pieces in the order of the keys.  Run by 2^lt of the
+// softmax threads (tid of them; 256 for more than kFewPieces) after the block's
+// last piece.  The last warp to have seen the unit's flags takes them down: a
+// captured call, whose ticket is the same every time, has to find them down.
+// Latency bound, and run once a launch: what is loaded is loaded together, and
+// the code is kept short (straight-line variants for each shape spent more time
+// on fetching instructions).
+constexpr int kFewPieces = 8;
 template <int HD>
-__device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsigned char *scratch, int tid,
+__device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, JoinSmem *scratch, int tid, int lt,
                                           volatile int *abort) {
   constexpr int C = HD / 4, LC = HD == 128 ? 5 : 4;  // float4 columns of a row
-  const int n = u.last - u.first + 1, each = ceil_div(u.n_rows, n), lane = tid & 31;
-  const int i0 = min(u.n_rows, ((int)blockIdx.x - u.first) * each), rows = min(u.n_rows, i0 + each) - i0;
+  const int n = u.last - u.first + 1, i0 = u.i0, rows = u.rows, lane = tid & 31;
   if (rows <= 0) return;
   bool ready = pieces_ready(p, u, n, lane, abort);
+  static_assert(sizeof(JoinSmem) <= 2 * TreeSmem<HD>::KR * TreeSmem<HD>::tile, "the rings");
+  const int mine = 256 >> lt;  // a share counts 8, whether 8 warps join it or 4
   int seen = 0;
-  if (lane == 0 && ready) seen = atomicAdd(p.joined + u.last, 1);
+  if (lane == 0 && ready) seen = atomicAdd(p.joined + u.last, mine) + mine;
   const float NEG = __int_as_float(0xff800000);
   const float4 *src = (const float4 *)p.part + (size_t)(2 * u.first) * C * 128 + i0;
   const float2 *state = p.state + (size_t)(2 * u.first) * 128 + i0;
   const int odd = u.first_slot & 1;  // the first block's slot is the second of its two
-  if (n <= 8) {
-    // 256 >> LC rows abreast; a thread holds all (2^lb or fewer) pieces of 8 >> lb rows at a time
-    const int r = tid & ((256 >> LC) - 1), col = tid >> (8 - LC), lb = n <= 2 ? 1 : n <= 4 ? 2 : 3;
-    for (int b0 = 0; ready && b0 < rows; b0 += (8 >> lb) << (8 - LC)) {
+  if (n <= kFewPieces) {
+    // 2^(lt - LC) rows abreast; a thread holds all (2^lb or fewer) pieces of 8 >> lb rows at a time
+    const int la = lt - LC, r = tid & ((1 << la) - 1), col = tid >> la, lb = n <= 2 ? 1 : n <= 4 ? 2 : 3;
+    for (int b0 = 0; ready && b0 < rows; b0 += (8 >> lb) << la) {
       float4 o[8];
       float2 ml[8];
       float mx[8], w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = b0 + r + ((k >> lb) << (8 - LC)), s = k & ((1 << lb) - 1), slot = 2 * s + (s ? 0 : odd);
+        const int i = b0 + r + ((k >> lb) << la), s = k & ((1 << lb) - 1), slot = 2 * s + (s ? 0 : odd);
         ml[k] = make_float2(NEG, 0.0f);
         if (i < rows && s < n) {
           o[k] = __ldcg(src + ((size_t)slot * C + col) * 128 + i);
@@ -356,7 +364,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsi
       float L = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int i = b0 + r + ((k >> lb) << (8 - LC)), s = k & ((1 << lb) - 1);
+        const int i = b0 + r + ((k >> lb) << la), s = k & ((1 << lb) - 1);
         w[k] = ml[k].x == NEG ? 0.0f : ex2(ml[k].x - mx[k]);
         if (w[k] > 0.0f) {
           L += w[k] * ml[k].y;
@@ -373,72 +381,73 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsi
       }
     }
   } else {
-    // Many pieces, few rows (no more than 128 / n of them in a share): 2^lr rows
-    // abreast x C columns x groups of threads that share the pieces, 8 in flight
-    // each; the rows' weights in shared memory, the groups' sums added there.
-    float2 *st = (float2 *)scratch;            // [rows][n]: (m, l); .x becomes the weight
-    float4 *sum = (float4 *)(scratch + 4096);  // [256]
+    // Many pieces, few rows (128 / n of them in a share): 2^lr rows abreast x C
+    // columns x groups of threads that share the pieces.  A thread copies all its
+    // pieces to shared memory at once (32 at most: 63 pieces of 3 rows); the rows'
+    // weights and the groups' sums go there too.
     int lr = 0;
     while ((1 << lr) < rows && lr < 8 - LC) ++lr;
     const int r = tid & ((1 << lr) - 1), col = (tid >> lr) & (C - 1), group = tid >> (lr + LC), lg = 8 - LC - lr;
     const int per = (n + (1 << lg) - 1) >> lg, s0 = group * per, s1 = min(n, s0 + per);
-    // (the loops count the same in every thread: there are barriers inside)
+    int k = 0;
+    for (int i = r; ready && i < rows; i += 1 << lr) {
+#pragma unroll 4
+      for (int s = s0; s < s1; ++s, ++k)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(&scratch->piece[k][tid])),
+                     "l"(src + ((size_t)(2 * s + (s ? 0 : odd)) * C + col) * 128 + i)
+                     : "memory");
+    }
+    // the weights, while the pieces are in flight: a warp a row
+    float2 *st = scratch->state;
+    for (int q = tid >> 5; q < rows; q += 8) {
+      float mx = NEG, L = 0.0f;
+#pragma unroll 1
+      for (int s = lane; s < n; s += 32) {
+        float2 v = make_float2(NEG, 0.0f);
+        if (ready) v = __ldcg(state + (size_t)(2 * s + (s ? 0 : odd)) * 128 + q);
+        st[q * n + s] = v;
+        mx = fmaxf(mx, v.x);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+#pragma unroll 1
+      for (int s = lane; s < n; s += 32) {
+        const float2 v = st[q * n + s];
+        const float f = v.x == NEG ? 0.0f : ex2(v.x - mx);
+        L += f * v.y;
+        st[q * n + s].x = f;
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll 1
+      for (int s = lane; s < n; s += 32) st[q * n + s].x *= inv;
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    softmax_sync();
+    k = 0;
+    // (the rounds count the same in every thread: there is a barrier inside)
     for (int b0 = 0; b0 < rows; b0 += 1 << lr) {
       const int i = b0 + r;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int c0 = 0; c0 < per; c0 += 8) {
-        float4 o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int s = s0 + c0 + k;
-          if (ready && i < rows && s < s1) o[k] = __ldcg(src + ((size_t)(2 * s + (s ? 0 : odd)) * C + col) * 128 + i);
-        }
-        if (b0 == 0 && c0 == 0) {  // the weights, while the first pieces are in flight: a warp a row
-          for (int q = tid >> 5; q < rows; q += 8) {
-            float mx = NEG, L = 0.0f;
-#pragma unroll 1
-            for (int s = lane; s < n; s += 32) {
-              float2 v = make_float2(NEG, 0.0f);
-              if (ready) v = __ldcg(state + (size_t)(2 * s + (s ? 0 : odd)) * 128 + q);
-              st[q * n + s] = v;
-              mx = fmaxf(mx, v.x);
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-#pragma unroll 1
-            for (int s = lane; s < n; s += 32) {
-              const float2 v = st[q * n + s];
-              const float f = v.x == NEG ? 0.0f : ex2(v.x - mx);
-              L += f * v.y;
-              st[q * n + s].x = f;
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-            const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-#pragma unroll 1
-            for (int s = lane; s < n; s += 32) st[q * n + s].x *= inv;
-          }
-          softmax_sync();
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int s = s0 + c0 + k;
-          if (i < rows && s < s1) {
-            const float f = st[i * n + s].x;
-            acc.x += f * o[k].x;
-            acc.y += f * o[k].y;
-            acc.z += f * o[k].z;
-            acc.w += f * o[k].w;
-          }
+      if (ready && i < rows) {
+#pragma unroll 4
+        for (int s = s0; s < s1; ++s, ++k) {
+          const float f = st[i * n + s].x;
+          const float4 v = scratch->piece[k][tid];
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
         }
       }
       if (lg) {  // (one round of rows then)
-        sum[tid] = acc;
+        scratch->sum[tid] = acc;
         softmax_sync();
         if (group == 0) {
 #pragma unroll 1
-          for (int k = 1; k < 1 << lg; ++k) {
-            const float4 v = sum[tid + (k << (lr + LC))];
+          for (int g = 1; g < 1 << lg; ++g) {
+            const float4 v = scratch->sum[tid + (g << (lr + LC))];
             acc.x += v.x;
             acc.y += v.y;
             acc.z += v.z;
@@ -450,7 +459,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, unsi
     }
     softmax_sync();  // the scratch is free again
   }
-  if (lane == 0 && ready && seen == 8 * ceil_div(u.n_rows, each) - 1) {
+  if (lane == 0 && ready && seen == 8 * u.shares) {
 #pragma unroll 1
     for (int s = 0; s < n; ++s) p.flags[u.slot(s)] = 0;
   }
@@ -882,8 +891,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         // in flight, and the rings run dry): the flags of the first and the last
         // piece, then this block's shares of the units they belong to.
         const bool join_tail = w.kt1 < w.s.key_tiles && (piece || !join_head);
+        const Span tail = unit_span(p, w, start, range.per);
         if (join_head || join_tail) {
           if (tid == 0 && join_head && head.last == (int)blockIdx.x) p.joined[blockIdx.x] = 0;  // counted from here by those who see the flag
+          // (found out while the fence waits)
+          asm volatile("" ::"r"(tail.first), "r"(tail.last), "r"(tail.first_slot), "r"(tail.shares), "r"(tail.i0), "r"(tail.rows));
           __threadfence();
           softmax_sync();
           if (tid == 0) {
@@ -891,10 +903,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             if (join_tail) st_flag(p.flags + slot, p.ticket);
           }
         }
-        // (one loop: the code of the join is there once)
+        // Two units of few pieces are joined at once, by four warps each: nothing
+        // there waits for the other warps.  (One loop: the code is there once.)
+        const bool both = join_head && join_tail && head.last - head.first < kFewPieces && tail.last - tail.first < kFewPieces;
 #pragma unroll 1
-        for (int k = join_head ? 0 : 1; k < (join_tail ? 2 : 1); ++k)
-          join_unit<HD>(p, k ? unit_span(p, w, start, range.per) : head, base + S::kring, tid, abort);
+        for (int k = join_head ? 0 : 1; k < (join_tail ? 2 : 1); ++k) {
+          if (both && k != tid >> 7) continue;
+          join_unit<HD>(p, k ? tail : head, (JoinSmem *)(base + S::kring), both ? tid & 127 : tid, both ? 7 : 8, abort);
+        }
       }
       if (!more) break;
       w = nx;
