@@ -21,6 +21,8 @@
 // 4, 8 ... batches, and about k + k log2(batches) of a block's random logits
 // reach a list.  At the end the lists' entries above the bound, a few more than
 // k, are gathered and each finds its place by counting the larger ones.
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "gemm_tc.cuh"
 #include "internal.h"
@@ -136,12 +138,13 @@ struct Batch<float> {
   uint4 r[kVecs];
   __device__ __forceinline__ float at(int j) const { return __uint_as_float((&r[j >> 2].x)[j & 3]); }
   __device__ __forceinline__ float max() const {
-    float m[4];
+    float m[2] = {at(0), at(1)};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) m[j] = at(j);
-#pragma unroll
-    for (int j = 4; j < 4 * kVecs; ++j) m[j & 3] = fmaxf(m[j & 3], at(j));
-    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    for (int j = 2; j < 4 * kVecs - 2; j += 4) {
+      m[0] = fmaxf(fmaxf(m[0], at(j)), at(j + 1));
+      m[1] = fmaxf(fmaxf(m[1], at(j + 2)), at(j + 3));
+    }
+    return fmaxf(fmaxf(fmaxf(m[0], m[1]), at(4 * kVecs - 2)), at(4 * kVecs - 1));
   }
   static __device__ __forceinline__ uint32_t absent() { return 0xff800000u; }
 };
@@ -213,24 +216,32 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   const T *x = (const T *)p.a.logits + (size_t)row * p.a.row_stride;
   // 16-byte vectors from the boundary at or before the row on; vector j holds
   // the entries j E - lead ..; entries outside the row are not read
-  const int lead = (int)(((uintptr_t)x & 15) / sizeof(T));
-  const long long n_vec = ((long long)V + lead + E - 1) / E;
-  const long long per = (n_vec + p.cluster - 1) / p.cluster;
-  const long long v_begin = per * rank, v_end = min(n_vec, v_begin + per);
+  const uint32_t lead = (uint32_t)(((uintptr_t)x & 15) / sizeof(T));
+  const uint32_t n_vec = ((uint32_t)V + lead + E - 1) / E;  // V < 2^31: an entry's index fits 32 bits, a batch past the end too
+  const uint32_t per = (n_vec + p.cluster - 1) / p.cluster;
+  const uint32_t v_begin = min(n_vec, per * rank), v_end = min(n_vec, v_begin + per);
   if (threadIdx.x == 0) s_pick.n = 0;
-  auto load = [&](Batch<T> &b, long long v0) {
+  constexpr uint32_t kStep = (uint32_t)kLpThreads * kVecs;
+  auto load = [&](Batch<T> &b, uint32_t v0) {
+    const uint32_t v1 = v0 + threadIdx.x;
+    if (v0 * E >= lead && v0 + kStep <= v_end && (v0 + kStep) * E - lead <= (uint32_t)V) {  // all of the batch lies in the row
+      const uint4 *at = (const uint4 *)(x + (v1 * E - lead));
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) b.r[u] = __ldcs(at + u * kLpThreads);
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      const long long v = v0 + u * kLpThreads + threadIdx.x, i0 = v * E - lead;
-      if (v < v_end && i0 >= 0 && i0 + E <= V) {
-        b.r[u] = __ldcs((const uint4 *)(x + i0));
+      const uint32_t v = v1 + u * kLpThreads;
+      if (v < v_end && v * E >= lead && v * E - lead + E <= (uint32_t)V) {
+        b.r[u] = __ldcs((const uint4 *)(x + (v * E - lead)));
       } else {
         uint32_t w[4] = {Batch<T>::absent(), Batch<T>::absent(), Batch<T>::absent(), Batch<T>::absent()};
         if (v < v_end) {
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            if (i0 + e >= 0 && i0 + e < V) {
-              const uint32_t bits = elem_bits(x + i0 + e);
+            if (v * E + e >= lead && v * E + e - lead < (uint32_t)V) {
+              const uint32_t bits = elem_bits(x + (v * E + e - lead));
               if (sizeof(T) == 4) w[e & 3] = bits;
               else w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | (bits << 16) : (w[e >> 1] & 0xffff0000u) | bits;
             }
@@ -243,9 +254,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   RowSum r{-INFINITY, 0.0f, 0.0f};
   unsigned long long best = 0, kth = 0;  // the warp's list; its k-th entry
   uint32_t bound = 0;                    // entries below it are not among the block's k best
+  float bound_v = -INFINITY, kth_v = -INFINITY;  // both as values
+  bool masked = false;                   // the warp has met entries of -inf
   Batch<T> cur, nxt;
-  constexpr long long kStep = (long long)kLpThreads * kVecs;
-  long long renew = v_begin;             // the batch with which the bound is renewed
+  uint32_t renew = v_begin;              // the batch with which the bound is renewed
   int turn = 0;
   load(cur, v_begin);
   // the given tokens' logits, early (the first block looks them up at the end)
@@ -255,33 +267,46 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
     my_id = p.a.tokens[(size_t)row * p.a.n_given + threadIdx.x];
     if (my_id >= 0 && my_id < V) my_bits = elem_bits(x + my_id);
   }
-  for (long long v0 = v_begin; v0 < v_end; v0 += kStep) {
+  for (uint32_t v0 = v_begin; v0 < v_end; v0 += kStep) {
     if (v0 + kStep < v_end) load(nxt, v0 + kStep);
-    const float mb = cur.max();
+    const float mb = fmaxf(cur.max(), -INFINITY);  // (NaN: none)
     if (mb > r.m) rebase(r, mb, p.c);
     const float m = r.m > -INFINITY ? r.m : 0.0f;
     const f32x2 minus_m = pair(-m, -m), cc = pair(p.c, p.c);
-    f32x2 sum = pair(0.0f, 0.0f), dot = sum;
+    f32x2 sum, dot;
+    // An entry of -inf has weight 0, but 0 times its distance is NaN: once a warp
+    // has met one, distances are held above -1000.
+    auto add_up = [&](auto low) {
+      sum = dot = pair(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      const float2 d = split(mul2(add2(pair(cur.at(j), cur.at(j + 1)), minus_m), cc));
-      const f32x2 e = pair(ex2_approx(d.x), ex2_approx(d.y));
-      sum = add2(sum, e);  // NaN here marks the row
-      dot = fma2(e, pair(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f)), dot);
+      for (int j = 0; j < N; j += 2) {
+        f32x2 d2 = mul2(add2(pair(cur.at(j), cur.at(j + 1)), minus_m), cc);
+        const float2 d = split(d2);
+        const f32x2 e = pair(ex2_approx(d.x), ex2_approx(d.y));
+        if constexpr (decltype(low)::value) d2 = pair(fmaxf(d.x, -1000.0f), fmaxf(d.y, -1000.0f));
+        sum = add2(sum, e);  // NaN here marks the row
+        dot = fma2(e, d2, dot);
+      }
+    };
+    if (!masked) {
+      add_up(std::false_type());
+      const float2 t = split(dot);
+      masked = __any_sync(0xffffffffu, !(t.x + t.y > -INFINITY));
     }
+    if (masked) add_up(std::true_type());
     const float2 sums = split(sum), dots = split(dot);
     r.s += sums.x + sums.y;
     r.a += dots.x + dots.y;
     if (k) {
-      const uint32_t ob = order_bits(mb);
       if (v0 == renew) {  // after batches 1, 2, 4, 8 ...: from the threads' running maxima
         renew = v_begin + 2 * (renew + kStep - v_begin) - kStep;
         // a thread without entries so far has none (its first vector lies behind the end)
         bound = max(bound, group_bound(v_begin + threadIdx.x < v_end ? order_bits(r.m) : 0u, k, s_max + turn));
         turn ^= 1;
+        if (bound) bound_v = order_value(bound);
       }
       // later batches hold higher indices, so an equal value does not enter a full list
-      if (__any_sync(0xffffffffu, ob >= bound && (ob > (uint32_t)(kth >> 32) || kth == 0))) {
+      if (__any_sync(0xffffffffu, mb >= bound_v && (mb > kth_v || kth == 0))) {
         // the lane's candidates (NaN among them: the exact test drops it)
         const uint32_t low = max(bound, (uint32_t)(kth >> 32));
         const float lim = low ? order_value(low) : -INFINITY;
@@ -291,10 +316,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
         while (__any_sync(0xffffffffu, mask != 0)) {
           const int j = __ffs(mask) - 1;
           const float v = pick16(j & 15, [&](int q) { return cur.at(q); });
-          const long long at_v = v0 + (j / E) * kLpThreads + threadIdx.x, i = at_v * E - lead + j % E;
+          const uint32_t at_v = v0 + (j / E) * kLpThreads + threadIdx.x, i = at_v * E + j % E - lead;  // (before the row: past V)
           const uint32_t o = order_bits(v);
-          const unsigned long long key = ((unsigned long long)o << 32) | (uint32_t)~(uint32_t)i;
-          unsigned todo = __ballot_sync(0xffffffffu, mask && at_v < v_end && i >= 0 && i < V && o >= bound && key > kth);
+          const unsigned long long key = ((unsigned long long)o << 32) | ~i;
+          unsigned todo = __ballot_sync(0xffffffffu, mask && at_v < v_end && i < (uint32_t)V && o >= bound && key > kth);
           mask &= mask - 1;
           while (todo) {
             const unsigned long long n = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
@@ -306,6 +331,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
           }
           kth = __shfl_sync(0xffffffffu, best, k - 1);
         }
+        if (kth) kth_v = order_value((uint32_t)(kth >> 32));
       }
     }
     cur = nxt;
