@@ -3,12 +3,14 @@
 // S = sum e^(y - m), A = sum e^(y - m) (y - m):
 //   log p(v) = (y_v - m) - log S,  lse = m + log S,  entropy = log S - A / S.
 //
-// Bound by the logits' bytes, each read once.  A row is split over the blocks
-// of a cluster when there are fewer rows than blocks fit the machine, and
-// their states joined through distributed shared memory (one launch, no
-// workspace).  A thread takes a batch of kVecs 16-byte vectors at a time, the
-// next batch already in flight, and moves its running maximum once per batch;
-// sums are kept in units of log2, fp32.
+// Bound by the logits' bytes, each read once: 1024 rows of 262144 fp32 take 167 us,
+// 6.4 TB/s.  (It was 186 us with per-vector checks and every distance clamped: the
+// instructions of an entry, not loads in flight; batches on their way through
+// shared memory, more of them, were slower.)  A row is split over the blocks of a
+// cluster when there are few rows, and their states joined through distributed
+// shared memory (one launch, no workspace).  A thread takes a batch of kVecs
+// 16-byte vectors at a time, the next batch already in flight, and moves its
+// running maximum once per batch; sums are kept in units of log2, fp32.
 //
 // The most likely tokens: each warp keeps a list of its 32 best entries, one a
 // lane, in descending order of a 64-bit key (order-preserving bits of the
@@ -150,7 +152,7 @@ struct Batch<float> {
 };
 template <>
 struct Batch<bf16> {
-  static constexpr int E = 8, kVecs = 2;  // more spill: 301 rows of 50001 take 15.3 us with 2, 17.8 with 4
+  static constexpr int E = 8, kVecs = 2;  // more spill: 301 rows of 50001 take 14.4 us with 2, 19.0 with 4
   uint4 r[kVecs];
   __device__ __forceinline__ float at(int j) const {
     const uint32_t w = (&r[j >> 3].x)[(j >> 1) & 3];
@@ -455,11 +457,13 @@ cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st) {
   p.a = a;
   p.c = (float)(1.4426950408889634 * (double)a.inv_tau);
   p.err = err;
-  // blocks per row: two for every SM in all, no fewer than 8192 entries each
-  // (1024 rows of 262144: 186 us with one, 220 with two: joining costs more than
-  // the last wave's idle SMs; one row: 7.7 us with 16)
+  // Blocks per row: as many as leave one to an SM, with more than 4096 entries
+  // each.  One row of 262144: 22.0, 11.5, 8.9, 7.1 us with 1, 4, 8, 16; 12 rows 22.7,
+  // 11.9, 9.3, 9.4; 64 rows of 131072: 16.7, 13.0, 13.0, 17.2 with 1, 2, 4, 8, 100 of 32768:
+  // 7.9, 9.3, 11.8 with 1, 2, 4 (large clusters leave SMs without a block); 16 of 32768: 5.9
+  // with 4, 7.7 with 8.
   int c = 1;
-  while (c < kMaxLpCluster && (long long)a.rows * c * 2 <= 2 * 152 && a.V / (2 * c) >= 8192) c *= 2;
+  while (c < kMaxLpCluster && (long long)a.rows * c * 2 <= 152 && a.V / (2 * c) > 4096) c *= 2;
   p.cluster = c;
   return a.is_bf16 ? launch<bf16>(p, st) : launch<float>(p, st);
 }
