@@ -316,13 +316,13 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
 #pragma unroll
         for (int j = 0; j < N; ++j) mask |= cur.at(j) < lim ? 0u : 1u << j;
         while (__any_sync(0xffffffffu, mask != 0)) {
-          const int j = __ffs(mask) - 1;
+          const int j = 31 - __clz(mask);  // the last first: rows in rising order enter fewer (1024 x 262144: 1.3 ms, else 3.3)
           const float v = pick16(j & 15, [&](int q) { return cur.at(q); });
           const uint32_t at_v = v0 + (j / E) * kLpThreads + threadIdx.x, i = at_v * E + j % E - lead;  // (before the row: past V)
           const uint32_t o = order_bits(v);
           const unsigned long long key = ((unsigned long long)o << 32) | ~i;
           unsigned todo = __ballot_sync(0xffffffffu, mask && at_v < v_end && i < (uint32_t)V && o >= bound && key > kth);
-          mask &= mask - 1;
+          mask &= ~(1u << (j & 31));
           while (todo) {
             const unsigned long long n = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
             const int at = __popc(__ballot_sync(0xffffffffu, best > n));  // entries before it (32: it drops out)
