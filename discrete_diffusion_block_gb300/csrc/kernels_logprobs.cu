@@ -23,6 +23,7 @@
 // 4, 8 ... batches, and about k + k log2(batches) of a block's random logits
 // reach a list.  At the end the lists' entries above the bound, a few more than
 // k, are gathered and each finds its place by counting the larger ones.
+#include <atomic>
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -430,7 +431,7 @@ cudaError_t launch(const LpArgs &p, cudaStream_t st) {
   cudaLaunchAttribute attr[1];
   if (p.cluster > 1) {
     if (p.cluster > 8) {
-      static unsigned long long attr_set = 0;
+      static std::atomic<unsigned long long> attr_set{0};
       int dev = 0;
       cudaError_t e = cudaGetDevice(&dev);
       if (e != cudaSuccess) return e;

@@ -409,8 +409,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_k
   auto place_of = [&](int t) {
     const int b = row_sequence(p.offsets, p.n_seqs, t);
     Place to{-1, 0, 0};
-    if (b >= p.n_seqs) return to;  // rows behind the last sequence are left alone
-    const long long slot = b < 0 ? -1 : (long long)p.prefix[b] + t - p.offsets[b];
+    if (b < 0 || b >= p.n_seqs) return to;  // rows of no sequence take no part
+    const long long slot = (long long)p.prefix[b] + t - p.offsets[b];
     if (slot >= 0 && slot < min((long long)p.max_pages * p.pg, 0x7fffffffll)) {
       const int logical = (int)slot / p.pg;
       to.page = p.tables[(long long)b * p.max_pages + logical];
@@ -545,10 +545,13 @@ RopeLaunch rope_plan(int n_tok, int first, int second, int group) {
   return r;
 }
 
-// A kernel's blocks may ask for more than the 48 KiB that need no leave.
+// A kernel's blocks may ask for more than the 48 KiB that need no leave: it is
+// taken for the most a block asks for, whatever this call does (another thread
+// may be about to launch a larger one).
 template <typename K>
-cudaError_t rope_smem(K kern, size_t bytes) {
-  return bytes > (40 << 10) ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+cudaError_t rope_smem(K kern, size_t bytes, size_t per_warp) {
+  if (bytes <= (40 << 10)) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kRopeWarps * per_warp));
 }
 
 template <typename T, int HD>
@@ -556,8 +559,9 @@ cudaError_t launch_qk(QkArgs p, const RopeFreq &f, cudaStream_t st) {
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   const RopeLaunch l = rope_plan(p.n_tok, p.Hq, p.Hkv, 32 / (HD / 16) * U);
   p.plan = l.plan;
-  const size_t smem = l.threads / 32 * RopeSmem<T, HD, U, 2>::warp * 16;
-  const cudaError_t e = rope_smem(qk_norm_rope_kernel<T, HD>, smem);
+  constexpr size_t per_warp = RopeSmem<T, HD, U, 2>::warp * 16;
+  const size_t smem = l.threads / 32 * per_warp;
+  const cudaError_t e = rope_smem(qk_norm_rope_kernel<T, HD>, smem, per_warp);
   if (e != cudaSuccess) return e;
   qk_norm_rope_kernel<T, HD><<<l.grid, l.threads, smem, st>>>(p, f);
   return cudaGetLastError();
@@ -567,8 +571,9 @@ template <int HD>
 cudaError_t launch_append(AppendArgs p, const RopeFreq &f, cudaStream_t st) {
   const RopeLaunch l = rope_plan(p.n_tok, p.Hkv, p.Hkv, 32 / (HD / 16) * 2);
   p.plan = l.plan;
-  const size_t smem = l.threads / 32 * RopeSmem<bf16, HD, 2, 1>::warp * 16;
-  const cudaError_t e = rope_smem(rope_kv_append_kernel<HD>, smem);
+  constexpr size_t per_warp = RopeSmem<bf16, HD, 2, 1>::warp * 16;
+  const size_t smem = l.threads / 32 * per_warp;
+  const cudaError_t e = rope_smem(rope_kv_append_kernel<HD>, smem, per_warp);
   if (e != cudaSuccess) return e;
   rope_kv_append_kernel<HD><<<l.grid, l.threads, smem, st>>>(p, f);
   return cudaGetLastError();

@@ -563,8 +563,9 @@ int dg_op_kv_append(const uint16_t *k_new, const uint16_t *v_new, uint16_t *k_po
  * offsets[b + 1] - 1 belong to sequence b (offsets: device int32
  * [n_seqs + 1], ascending from 0 or later); the first of them takes the
  * sequence's logical slot prefix_lens[b] (device int32 [n_seqs]: its cached
- * tokens).  Rows behind offsets[n_seqs] (a batch padded for a captured step)
- * take no part: what they hold does not matter, and they are left as they are.  Sequence b's logical page j is
+ * tokens).  Rows before offsets[0] or behind offsets[n_seqs] (a batch padded for
+ * a captured step) take no part: what they hold does not matter, and they are
+ * left as they are.  Sequence b's logical page j is
  * page_tables[b * max_pages + j] (device int32 [n_seqs][max_pages]).  Lengths
  * live on the device, so a captured call can be replayed with other ones.
  * Rows of heads are `stride` elements apart (a multiple of 8, >= heads *
@@ -608,8 +609,9 @@ int dg_op_qk_norm_rope(const void *q, const void *k, int32_t in_f32, int64_t q_s
  *   v_pool      device bf16 pools of one layer, layout of
  *               dg_op_canvas_attention, 16-byte aligned
  * A row whose slot lies outside the page table (or whose page outside the
- * pools) is not written and is reported by dg_op_status.  Shapes as
- * dg_op_qk_norm_rope; page_size >= 1. */
+ * pools) is not written and is reported by dg_op_status.  Rows must not go to
+ * one slot of one page (a slot that several sequences share holds what either
+ * of them left).  Shapes as dg_op_qk_norm_rope; page_size >= 1. */
 int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
                          const int32_t *positions, const int32_t *prefix_lens,
                          const int32_t *offsets, const int32_t *page_tables, int32_t max_pages,
@@ -635,7 +637,10 @@ int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride,
  * scale > 0; head_dim in {64, 128}; n_q_heads / n_kv_heads <= 128; page_size a
  * multiple of 64.  workspace: device scratch of
  * dg_op_tree_attention_workspace_bytes() bytes, 16-byte aligned, contents
- * arbitrary; calls that overlap on the GPU need one each. */
+ * arbitrary; calls that overlap on the GPU need one each.  The launch is
+ * cooperative (its blocks run together and wait, bounded, for one another).
+ * Once dg_op_status has told of a wait that gave up, clear the workspace before
+ * a captured call is replayed with it. */
 size_t dg_op_tree_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
                                             int32_t n_kv_heads, int32_t head_dim);
 int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool,

@@ -5,6 +5,10 @@ against plain numpy evaluations in 64 bits.
 Tolerances.  A bf16 result is one rounding away from its fp32 value (2^-8
 relative); the terms added to that are stated at each check.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -63,7 +67,7 @@ def head_ref(x, gain, pos, rope, base=10000.0, eps=1e-6):
 
 def head_tol(y, mag):
     # norm: at most 21 roundings of the sum, rsqrt within 2 ulp, two products;
-    # angle within 2^-25 half turns, sincospif within 2 ulp, two products and a sum
+    # angle within 2^-25 half turns, sine and cosine within 2 ulp, two products and a sum
     return U16 * np.abs(y) + 64 * U32 * mag
 
 
@@ -675,3 +679,195 @@ def test_the_operators_captured_and_replayed_with_other_lengths():
         for name in ("k_pool", "v_pool"):
             getattr(t.bt, name).copy_(getattr(s.bt, name)[:t.bt.n_pages])
         t.check()
+
+
+# ---- calls at the edges of what the documentation allows ----------------------------------------
+
+@pytest.mark.parametrize("T,hq,hkv,hd,rope,f32", [
+    (1, 130, 7, 64, 64, False), (3, 1, 33, 256, 256, False), (2, 40, 40, 128, 96, True), (2433, 3, 1, 64, 48, False),
+    (4865, 17, 1, 128, 128, False), (5000, 2, 2, 64, 64, True), (700, 1, 9, 256, 32, True),
+])
+def test_qk_norm_rope_with_tokens_split_and_in_turns(T, hq, hkv, hd, rope, f32):
+    # a token's heads over several warps, warps with many tokens, groups of heads partly filled
+    rng = np.random.default_rng(T + 7 * hq)
+    dt = torch.float32 if f32 else torch.bfloat16
+    q, k = randn(rng, T, hq, hd, dtype=dt).to(dev()), randn(rng, T, hkv, hd, dtype=dt).to(dev())
+    pos = rng.integers(0, 1 << 20, T).astype(np.int32)
+    gain = randn(rng, hd, dtype=torch.float32).to(dev())
+    qo, ko = (torch.full(x.shape, 7.0, dtype=torch.bfloat16, device=dev()) for x in (q, k))
+    dgp.dg_op_qk_norm_rope(q, k, i32(pos), qo, ko, q_gain=None, k_gain=gain, rope_dim=rope)
+    for x, g, o in ((q, None, qo), (k, f64(gain), ko)):
+        y, mag = head_ref(f64(x), g, pos, rope)
+        assert (np.abs(f64(o) - y) <= head_tol(y, mag)).all()
+
+
+def shifted(bt, by):
+    """The batch's rows behind `by` rows that belong to no sequence."""
+    bt.off = bt.off + by
+    bt.T += by
+    bt.d["offsets"] = i32(bt.off)
+    return bt
+
+
+def test_rows_before_the_first_sequence_take_no_part():
+    rng = np.random.default_rng(41)
+    bt = shifted(Batch(rng, [200, 70], [9, 4], 2, 64, 64), 3)
+    q = randn(rng, bt.T, 4, 64).to(dev())
+    out = torch.full((bt.T, 4, 64), 7.0, dtype=torch.bfloat16, device=dev())
+    run_attention(bt, q, None, out)
+    ref, mag = attention_ref(f64(q), bt, None, 64 ** -0.5)
+    lo, hi = int(bt.off[0]), int(bt.off[-1])
+    got = f64(out)
+    assert (np.abs(got - ref)[lo:hi] <= attention_tol(ref[lo:hi], mag[lo:hi])).all()
+    assert (got[:lo] == 7.0).all() and (got[hi:] == 7.0).all()
+    rows = randn(rng, bt.T, 2, 64).to(dev())
+    rows[:lo] = float("nan")
+    was = bt.v_pool.clone()
+    dgp.dg_op_rope_kv_append(rows, rows, bt.k_pool, bt.v_pool, **bt.d)
+    dgp.dg_op_status()
+    vp, old = pool_rows(bt.v_pool.float()), pool_rows(was.float())
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        for i in range(n):
+            page, s = bt.table[b, (p + i) // 64], (p + i) % 64
+            assert np.array_equal(vp[page, s], f64(rows)[bt.off[b] + i])
+            old[page, s] = vp[page, s]
+    assert np.array_equal(vp, old, equal_nan=True)
+
+
+def test_thousands_of_short_sequences():
+    rng = np.random.default_rng(42)
+    pre, new = rng.integers(0, 5, 3000), rng.integers(0, 3, 3000)
+    bt = Batch(rng, pre, new, 1, 64, 64)
+    check_attention(bt, 2, None, rng)
+    rows = randn(rng, bt.T, 1, 64).to(dev())
+    dgp.dg_op_rope_kv_append(rows, rows, bt.k_pool, bt.v_pool, **bt.d, rope_dim=0)
+    dgp.dg_op_status()
+    kp, x = pool_rows(bt.k_pool.float()), f64(rows)
+    for b, (p, n) in enumerate(zip(pre, new)):
+        for i in range(n):
+            assert np.array_equal(kp[bt.table[b, 0], p + i], x[bt.off[b] + i])
+
+
+def test_pools_and_rows_past_32_bit_offsets():
+    # pools of 2^31 and more elements: the results of a small pool, page for page
+    rng = np.random.default_rng(43)
+    bt = Batch(rng, [300, 40], [5, 3], 8, 128, 128)
+    q = randn(rng, bt.T, 16, 128).to(dev())
+    k = randn(rng, bt.T, 8, 128).to(dev())
+    n_big = 16384 + 64
+    at = n_big - bt.n_pages
+    big = []
+    for pool in (bt.k_pool, bt.v_pool):
+        b = torch.zeros(n_big, 8, 128, 128, dtype=torch.bfloat16, device=dev())
+        b[at:] = pool
+        big.append(b)
+    outs = []
+    for pools, shift in (((bt.k_pool, bt.v_pool), 0), (big, at)):
+        d = dict(bt.d, page_tables=i32(np.where(bt.table < 0, bt.table, bt.table + shift)))
+        dgp.dg_op_rope_kv_append(k, k, *pools, **d)
+        out = torch.zeros(bt.T, 16, 128, dtype=torch.bfloat16, device=dev())
+        ws = torch.zeros(dgp.dg_op_tree_attention_workspace_bytes(bt.T, 2, 16, 8, 128), dtype=torch.uint8, device=dev())
+        dgp.dg_op_tree_attention(q, *pools, **d, tree_mask=None, out=out, workspace=ws)
+        outs.append(out)
+    dgp.dg_op_status()
+    assert torch.equal(outs[0], outs[1]) and outs[0].any()
+    for pool, b in zip((bt.k_pool, bt.v_pool), big):
+        assert torch.equal(b[at:].view(torch.int16), pool.view(torch.int16))
+    # rows that lie 2^30 elements apart
+    far = big[0].view(-1)
+    x = far.as_strided((3, 1000), (2 ** 30, 1))
+    x.copy_(randn(rng, 3, 1000).to(dev()))
+    check_logprobs(x, rng.integers(0, 1000, (3, 1)), 5)
+    h = far.as_strided((3, 2, 64), (2 ** 30, 64, 1))
+    pos = i32([0, 9, 70000])
+    a, b = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=dev()), torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=dev())
+    dgp.dg_op_qk_norm_rope(h.contiguous(), None, pos, a, None)
+    dgp.dg_op_qk_norm_rope(h, None, pos, h, None)
+    b.copy_(h)
+    assert torch.equal(a, b)
+
+
+def test_empty_tensors_through_the_binding():
+    e = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device=dev())  # noqa: E731
+    pool = torch.zeros(2, 2, 64, 64, dtype=torch.bfloat16, device=dev())
+    none = dict(page_tables=i32(np.zeros((3, 1))), prefix_lens=i32([0, 0, 0]), offsets=i32([0, 0, 0, 0]))
+    dgp.dg_op_rope_kv_append(e(0, 2, 64), e(0, 2, 64), pool, pool.clone(), **none)
+    dgp.dg_op_tree_attention(e(0, 4, 64), pool, pool, **none, tree_mask=None, out=e(0, 4, 64), workspace=None)
+    q = torch.ones(4, 4, 64, dtype=torch.bfloat16, device=dev())
+    out = torch.full_like(q, 7.0)
+    ws = torch.zeros(dgp.dg_op_tree_attention_workspace_bytes(4, 3, 4, 2, 64), dtype=torch.uint8, device=dev())
+    dgp.dg_op_tree_attention(q, pool, pool, **none, tree_mask=None, out=out, workspace=ws)     # rows, but no sequence has any
+    no_seqs = dict(page_tables=i32(np.zeros((0, 1))), prefix_lens=i32([]), offsets=i32([0]))
+    dgp.dg_op_tree_attention(q, pool, pool, **no_seqs, tree_mask=None, out=out, workspace=None)
+    dgp.dg_op_rope_kv_append(q[:, :2], q[:, :2], pool, pool, **no_seqs)
+    assert (out == 7.0).all() and not pool.any()
+    dgp.dg_op_token_logprobs(e(0, 9, dtype=torch.float32), e(0, 1, dtype=torch.int32), e(0, 1, dtype=torch.float32))
+    dgp.dg_op_status()
+
+
+def test_captured_calls_that_share_a_workspace_take_turns():
+    # two captured calls and an eager one of other shapes, one after the other on one workspace
+    rng = np.random.default_rng(44)
+    ws = torch.full((max(dgp.dg_op_tree_attention_workspace_bytes(200, 8, 16, 8, hd) for hd in (64, 128)),), 0x5A, dtype=torch.uint8, device=dev())
+    calls, st = [], torch.cuda.Stream()
+    for hq, hkv, hd, pre, new in ((16, 8, 128, [5000, 30], [24, 2]), (12, 4, 64, [3000, 2500, 7], [5, 5, 1]), (8, 1, 128, [9000], [61])):
+        bt = Batch(rng, pre, new, hkv, hd, 128)
+        q, ref = check_attention(bt, hq, None, rng)
+        out = torch.full_like(ref, 7.0)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            run_attention(bt, q, None, out, workspace=ws, stream=st)
+        calls.append((bt, q, out, ref, g))
+    for turn in range(30):
+        bt, q, out, ref, g = calls[turn % 3]
+        out.fill_(7.0)
+        if turn % 5 == 4:
+            run_attention(bt, q, None, out, workspace=ws)
+        else:
+            g.replay()
+        assert torch.equal(out, ref)
+
+
+FIRST_CALL = """
+import numpy as np, torch
+import discrete_diffusion_block_gb300 as dgp
+dgp.load()
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+i = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+rows, pools = r(9, 16, 128), [r(12, 4, 128, 128), r(12, 4, 128, 128)]
+d = dict(page_tables=i([[0, 1, 2, 3, 4, 5, 6, 7], [8, 9, 10, 11, 0, 0, 0, 0]]), prefix_lens=i([1000, 300]), offsets=i([0, 5, 9]))
+pos = i([1000, 1001, 1002, 1003, 1004, 300, 301, 302, 303])
+q, out, logits = torch.zeros(9, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(9, 8, 128, dtype=torch.bfloat16, device="cuda"), r(9, 40000)
+ws = torch.zeros(dgp.dg_op_tree_attention_workspace_bytes(9, 2, 8, 4, 128), dtype=torch.uint8, device="cuda")
+tok, lp, H, ids = i([[3]] * 9), torch.zeros(9, 1, device="cuda"), torch.zeros(9, device="cuda"), torch.zeros(9, 4, dtype=torch.int32, device="cuda")
+def step(st):
+    dgp.dg_op_qk_norm_rope(rows[:, :8], None, pos, q, None, stream=st)
+    dgp.dg_op_rope_kv_append(rows[:, 8:12], rows[:, 12:], *pools, **d, stream=st)
+    dgp.dg_op_tree_attention(q, *pools, **d, tree_mask=None, out=out, workspace=ws, stream=st)
+    dgp.dg_op_token_logprobs(logits, tok, lp, H, None, ids, None, stream=st)
+st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=st):
+    step(st)
+graph.replay()
+torch.cuda.synchronize()
+dgp.dg_op_status()
+was = [t.clone() for t in (q, out, lp, H, ids, *pools)]
+assert all(bool(t.any()) for t in was)
+for t in (q, out, lp, H, ids):
+    t.zero_()
+torch.cuda.synchronize()
+step(None)
+torch.cuda.synchronize()
+dgp.dg_op_status()
+assert all(torch.equal(a, b) for a, b in zip(was, (q, out, lp, H, ids, *pools)))
+print("the same")
+"""
+
+
+def test_the_first_call_of_a_process_can_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "the same" in p.stdout, p.stderr[-2000:]
