@@ -39,7 +39,7 @@ namespace dg {
 namespace {
 
 // Warps of a block and resident blocks, and the groups of heads a warp has on
-// their way: 16384 tokens of 16 + 8 heads of 128 take 34.7 us and 17,400 tokens
+// their way: 16384 tokens of 16 + 8 heads of 128 take 34.7 us and 17,667 tokens
 // appended to 8 heads 26.4 us with (2 blocks, 3 stages), 35.1 and 26.9 with
 // (2, 4), 34.6 and 28.5 with (3, 3), 41.1 and 33.8 with (3, 6).
 constexpr int kRopeWarps = 8, kRopeBlocks = 2, kStages = 3;

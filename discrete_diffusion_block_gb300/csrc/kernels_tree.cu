@@ -28,6 +28,17 @@
 // stage the next unit's rows as soon as the last S of a unit is done.  Quarters
 // without rows (a few drafted tokens fill one) skip the arithmetic.
 //
+// Measured (16 query and 8 KV heads of 128 unless stated): 64 sequences of 24
+// tokens over 16k keys 260 us, 95 % of what their bytes need; 40 ragged sequences
+// of 5 tokens (12 and 4 heads of 64) 25.4 us; one of 61 tokens over 32k 36.4 us, of
+// which the keys' bytes take 20 and the rest is start (3.5), the last tile and the
+// join (2.5 + 5.6); one token over 2k keys 11.7 us, all of it latency.
+// Slower and not kept: the pieces joined over a cluster's shared memory, or by a
+// kernel of their own; rows copied into idle quarters of a tile; no range shorter
+// than 3 tiles (one token over 2k: 12.0 us); one part of a unit per block where the
+// units allow (16 sequences of one token over 2k 32.5 -> 29.0 us, but 0.5 us more for
+// every small call and 266 us for the large one).
+//
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
 #include <limits.h>
