@@ -3,8 +3,8 @@
 // S = sum e^(y - m), A = sum e^(y - m) (y - m):
 //   log p(v) = (y_v - m) - log S,  lse = m + log S,  entropy = log S - A / S.
 //
-// Bound by the logits' bytes, each read once: 1024 rows of 262144 fp32 take 167 us,
-// 6.4 TB/s.  (It was 186 us with per-vector checks and every distance clamped: the
+// Bound by the logits' bytes, each read once: 1024 rows of 262144 fp32 take 162 us,
+// 6.6 TB/s.  (It was 186 us with per-vector checks and every distance clamped: the
 // instructions of an entry, not loads in flight; batches on their way through
 // shared memory, more of them, were slower.)  A row is split over the blocks of a
 // cluster when there are few rows, and their states joined through distributed
@@ -19,10 +19,12 @@
 // batches would enter it.  The k-th largest of the running maxima of 64 groups
 // of threads is a lower bound of the block's k-th best entry, close to it (the
 // groups' maxima are mostly the best entries themselves), and cheap: entries
-// below are dropped at one compare per batch, with the bound renewed after 1, 2,
-// 4, 8 ... batches, and about k + k log2(batches) of a block's random logits
-// reach a list.  At the end the lists' entries above the bound, a few more than
-// k, are gathered and each finds its place by counting the larger ones.
+// below are dropped at one compare per batch, with the bound renewed after 1, 4,
+// 16 ... batches (after 1, 2, 4, 8 ..., 1024 rows of 262144 take 166 us; after 1, 8,
+// 64 ..., 301 rows of 50001 with k = 32 take 23.6 us instead of 17.7), and about
+// k + 1.5 k log2(batches) of a block's random logits reach a list.  At the end the
+// lists' entries above the bound, at most a few times k, are gathered and each
+// finds its place by counting the larger ones.
 #include <atomic>
 #include <type_traits>
 
@@ -68,20 +70,28 @@ __device__ __forceinline__ float order_value(uint32_t b) {
   return __uint_as_float((b & 0x80000000u) ? b & 0x7fffffffu : ~b);
 }
 
-constexpr int kGroups = 64;  // of 8 threads; no fewer than the largest k
+constexpr int kGroups = 64;  // no fewer than the largest k
 
-// The k-th largest of the groups' maxima, from each thread's (order bits; 0:
-// none); run by the whole block, on two buffers in turn.  Each group counts the
-// larger ones (ties in group order), its threads an eighth each.
+// The k-th largest of the maxima of up to 64 groups of threads, from each thread's
+// (order bits; 0: none); run by the whole block, on two buffers in turn.  Groups
+// are of 2^lg <= 8 threads.  Eight threads count the larger ones of a group (ties
+// in group order), an eighth each.
 struct __align__(16) GroupMax {
   uint32_t max[kGroups], bound;
 };
-__device__ __forceinline__ uint32_t group_bound(uint32_t mine, int k, GroupMax *s) {
+__device__ __forceinline__ uint32_t group_bound(uint32_t mine, int k, int lg, GroupMax *s) {
   const int group = threadIdx.x >> 3, part = threadIdx.x & 7;
+  if (lg == 3) {
 #pragma unroll
-  for (int o = 4; o; o >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
-  if (part == 0) s->max[group] = mine;
-  __syncthreads();
+    for (int o = 4; o; o >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    if (part == 0) s->max[group] = mine;
+    __syncthreads();
+  } else {
+    for (int o = (1 << lg) >> 1; o; o >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
+    if ((threadIdx.x & ((1 << lg) - 1)) == 0 && threadIdx.x < kGroups << lg) s->max[threadIdx.x >> lg] = mine;
+    __syncthreads();
+    mine = s->max[group];
+  }
   const uint4 v = *(const uint4 *)(s->max + 8 * part), w = *(const uint4 *)(s->max + 8 * part + 4);
   const uint32_t m[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
   const int before = group - 8 * part;  // entries of this eighth that lie before the group
@@ -153,7 +163,7 @@ struct Batch<float> {
 };
 template <>
 struct Batch<bf16> {
-  static constexpr int E = 8, kVecs = 2;  // more spill: 301 rows of 50001 take 14.4 us with 2, 19.0 with 4
+  static constexpr int E = 8, kVecs = 2;  // more spill: 301 rows of 50001 took 14.4 us with 2, 19.0 with 4
   uint4 r[kVecs];
   __device__ __forceinline__ float at(int j) const {
     const uint32_t w = (&r[j >> 3].x)[(j >> 1) & 3];
@@ -261,6 +271,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   bool masked = false;                   // the warp has met entries of -inf
   Batch<T> cur, nxt;
   uint32_t renew = v_begin;              // the batch with which the bound is renewed
+  // groups of as few threads as make 64 of those that have entries: a short row's
+  // bound would else be loose (1024 entries of bf16, k = 32: 20.1 -> 7.3 us)
+  const int lg = v_end - v_begin > 4 * kGroups ? 3 : v_end - v_begin > 2 * kGroups ? 2 : v_end - v_begin > kGroups ? 1 : 0;
   int turn = 0;
   load(cur, v_begin);
   // the given tokens' logits, early (the first block looks them up at the end)
@@ -301,10 +314,10 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
     r.s += sums.x + sums.y;
     r.a += dots.x + dots.y;
     if (k) {
-      if (v0 == renew) {  // after batches 1, 2, 4, 8 ...: from the threads' running maxima
-        renew = v_begin + 2 * (renew + kStep - v_begin) - kStep;
+      if (v0 == renew) {  // after batches 1, 4, 16 ...: from the threads' running maxima
+        renew = v_begin + 4 * (renew + kStep - v_begin) - kStep;
         // a thread without entries so far has none (its first vector lies behind the end)
-        bound = max(bound, group_bound(v_begin + threadIdx.x < v_end ? order_bits(r.m) : 0u, k, s_max + turn));
+        bound = max(bound, group_bound(v_begin + threadIdx.x < v_end ? order_bits(r.m) : 0u, k, lg, s_max + turn));
         turn ^= 1;
         if (bound) bound_v = order_value(bound);
       }
@@ -343,16 +356,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   // ---- the block's state, then the row's ------------------------------------------
   const float wm = lanes_max(r.m);
   if (lane == 0) s_wmax[warp] = wm;
-  if (k && v_begin < v_end) bound = max(bound, group_bound(v_begin + threadIdx.x < v_end ? order_bits(r.m) : 0u, k, s_max + turn));
-  else __syncthreads();
-  lanes_sum(r, lanes_max(s_wmax[lane & (kLpWarps - 1)]), p.c, 32);
-  if (lane == 0) s_sum[warp] = r;
   if (k) collect(&s_pick, best, best != 0 && (uint32_t)(best >> 32) >= bound);
   __syncthreads();
+  lanes_sum(r, lanes_max(s_wmax[lane & (kLpWarps - 1)]), p.c, 32);
+  if (lane == 0) s_sum[warp] = r;
   if (k) place(&s_pick, k);
+  __syncthreads();
   r = s_sum[lane & (kLpWarps - 1)];
   lanes_sum(r, r.m, p.c, kLpWarps);  // in every warp
-  __syncthreads();
   if (p.cluster > 1) {
     // Every block pushes its sums and entries (0: none) into the first block's
     // shared memory; nothing is read from the others, which end here.
@@ -459,10 +470,10 @@ cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st) {
   p.c = (float)(1.4426950408889634 * (double)a.inv_tau);
   p.err = err;
   // Blocks per row: as many as leave one to an SM, with more than 4096 entries
-  // each.  One row of 262144: 22.0, 11.5, 8.9, 7.1 us with 1, 4, 8, 16; 12 rows 22.7,
-  // 11.9, 9.3, 9.4; 64 rows of 131072: 16.7, 13.0, 13.0, 17.2 with 1, 2, 4, 8, 100 of 32768:
-  // 7.9, 9.3, 11.8 with 1, 2, 4 (large clusters leave SMs without a block); 16 of 32768: 5.9
-  // with 4, 7.7 with 8.
+  // each.  One row of 262144: 20.5, 10.4, 8.2, 6.4 us with 1, 4, 8, 16; 12 rows 21.3,
+  // 11.0, 8.7, 8.8; 64 rows of 131072: 15.8, 11.9, 12.3, 15.5 with 1, 2, 4, 8; 100 of
+  // 32768: 7.3, 8.4, 10.9 with 1, 2, 4 (large clusters leave SMs without a block); 16
+  // of 32768: 5.6 with 4, 7.4 with 8.
   int c = 1;
   while (c < kMaxLpCluster && (long long)a.rows * c * 2 <= 152 && a.V / (2 * c) > 4096) c *= 2;
   p.cluster = c;
