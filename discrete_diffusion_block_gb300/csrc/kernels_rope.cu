@@ -375,7 +375,8 @@ struct Place {
   int page, slot, pos;
 };
 
-// Laid out as qk_norm_rope_kernel, the sides being keys and values: keys normed
+// Laid out as qk_norm_rope_kernel, but that the groups run through the heads of
+// the keys and on into those of the values (few heads fill one group): keys normed
 // and rotated, values copied, both into the token's page slot.
 template <int HD>
 __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_kernel(const __grid_constant__ AppendArgs p,
@@ -392,15 +393,18 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_k
   const bool turns = i < p.rd16;
   const uint32_t stride = gridDim.x * n_warps;
   At at(p.plan, blockIdx.x * n_warps + (threadIdx.x >> 5), p.n_tok), ahead = at;
-  auto head_of = [&](const At &at) { return U * step * (at.g < p.plan.first ? at.g : at.g - p.plan.first) + lane / L; };
+  // a lane's heads of a group: h, h + step, .. of the keys' heads and then the values'
+  auto head_of = [&](const At &at) { return U * step * at.g + lane / L; };
   auto request = [&](int stage) {
     if (!ahead.end()) {
       const int h = head_of(ahead);
-      const bf16 *src = (ahead.g < p.plan.first ? p.k + ahead.t * p.k_stride : p.v + ahead.t * p.v_stride) +
-                        (long long)h * HD;
+      const bf16 *k = p.k + ahead.t * p.k_stride, *v = p.v + ahead.t * p.v_stride - (long long)p.Hkv * HD;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (h + u * step < p.Hkv) Chunks<bf16>::request(stages + stage * S::stage + 64 * u, src + u * step * HD, c0, c1);
+      for (int u = 0; u < U; ++u) {
+        const int hu = h + u * step;
+        if (hu < 2 * p.Hkv)
+          Chunks<bf16>::request(stages + stage * S::stage + 64 * u, (hu < p.Hkv ? k : v) + (long long)hu * HD, c0, c1);
+      }
       if (++ahead.g == ahead.g1) ahead.set(p.plan, ahead.item + stride, p.n_tok);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_k
   for (int j = threadIdx.x; j < 8 * p.rd16; j += blockDim.x) s_turn[j] = f.turn[j];
   __syncthreads();
   while (!at.end()) {
-    if (at.g0 < p.plan.first) {  // the token's factors, while its rows are in flight
+    if (U * step * at.g0 < p.Hkv) {  // the token's factors, while its rows are in flight
 #pragma unroll
       for (int j = 2 * lane; j < HD / 2; j += 64) {
         float2 sc0 = make_float2(0.0f, 1.0f), sc1 = sc0;
@@ -455,25 +459,25 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_k
       pos = p.positions ? p.positions[next.t] : next_to.pos;
     }
     for (; !at.end(); ++at.g) {
-      const int h = head_of(at);
-      const bool is_k = at.g < p.plan.first;
-      const int live = p.Hkv - h + lane / L > step ? U : 1;
+      const int h = head_of(at), keys = p.Hkv - U * step * at.g;  // keys: the group's, if more than 0
       asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
       Chunks<bf16> y[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) y[u].read(stages + stage * S::stage + 64 * u);
-      if (is_k) {
+      if (keys > 0) {
         f32x2 x[U][8];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           unpack8(y[u].a, x[u]);
           unpack8(y[u].b, x[u] + 4);
         }
-        turn_heads<HD, U>(x, live, p.k_gain != nullptr, true, p.eps, turns, factors, i);
+        turn_heads<HD, U>(x, keys > step ? U : 1, p.k_gain != nullptr, true, p.eps, turns, factors, i);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          y[u].a[0] = pack8(x[u]);
-          y[u].b[0] = pack8(x[u] + 4);
+          if (h + u * step < p.Hkv) {
+            y[u].a[0] = pack8(x[u]);
+            y[u].b[0] = pack8(x[u] + 4);
+          }
         }
       }
       request(stage ? stage - 1 : kStages - 1);  // the stage that was read last
@@ -481,14 +485,16 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeBlocks) rope_kv_append_k
       if (to.page >= 0) {
         const long long head = (long long)p.pg * HD;
         const int s7 = to.slot & 7;
-        bf16 *dst = (is_k ? p.k_pool : p.v_pool) + ((long long)to.page * p.Hkv + h) * head + (long long)to.slot * 64;
-        bf16 *d0 = dst + (long long)(c0 >> 3) * p.pg * 64 + (((c0 & 7) ^ s7) << 3);
-        bf16 *d1 = dst + (long long)(c1 >> 3) * p.pg * 64 + (((c1 & 7) ^ s7) << 3);
+        const long long at0 = (long long)to.page * p.Hkv * head + (long long)to.slot * 64;
+        const long long d0 = (long long)(c0 >> 3) * p.pg * 64 + (((c0 & 7) ^ s7) << 3);
+        const long long d1 = (long long)(c1 >> 3) * p.pg * 64 + (((c1 & 7) ^ s7) << 3);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (h + u * step < p.Hkv) {
-            *(uint4 *)(d0 + u * step * head) = y[u].a[0];
-            *(uint4 *)(d1 + u * step * head) = y[u].b[0];
+          const int hu = h + u * step;
+          if (hu < 2 * p.Hkv) {
+            bf16 *dst = (hu < p.Hkv ? p.k_pool : p.v_pool) + at0 + (hu < p.Hkv ? hu : hu - p.Hkv) * head;
+            *(uint4 *)(dst + d0) = y[u].a[0];
+            *(uint4 *)(dst + d1) = y[u].b[0];
           }
         }
       }
@@ -569,7 +575,7 @@ cudaError_t launch_qk(QkArgs p, const RopeFreq &f, cudaStream_t st) {
 
 template <int HD>
 cudaError_t launch_append(AppendArgs p, const RopeFreq &f, cudaStream_t st) {
-  const RopeLaunch l = rope_plan(p.n_tok, p.Hkv, p.Hkv, 32 / (HD / 16) * 2);
+  const RopeLaunch l = rope_plan(p.n_tok, 2 * p.Hkv, 0, 32 / (HD / 16) * 2);
   p.plan = l.plan;
   constexpr size_t per_warp = RopeSmem<bf16, HD, 2, 1>::warp * 16;
   const size_t smem = l.threads / 32 * per_warp;
