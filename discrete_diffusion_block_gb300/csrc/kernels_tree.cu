@@ -13,7 +13,8 @@
 // device: every block adds up the units' key tiles, and all blocks take equal
 // ranges of that sum (a range may end inside a unit, and hold several small
 // ones), so that the memory pipes of all SMs stay equally busy however uneven
-// the batch is.  A unit that lies in one range is written out by its block.  Of
+// the batch is; or, with few units, a part of one unit each (block_range).  A unit
+// that lies in one range is written out by its block.  Of
 // one that spans several, each block leaves fp32 partial sums and softmax
 // states in the workspace and raises a flag; after its own work, each joins a
 // share of the unit's rows, once all the unit's flags are up.  The blocks wait
@@ -30,14 +31,13 @@
 //
 // Measured (16 query and 8 KV heads of 128 unless stated): 64 sequences of 24
 // tokens over 16k keys 260 us, 95 % of what their bytes need; 40 ragged sequences
-// of 5 tokens (12 and 4 heads of 64) 25.4 us; one of 61 tokens over 32k 36.4 us, of
+// of 5 tokens (12 and 4 heads of 64) 25.5 us; one of 61 tokens over 32k 35.6 us, of
 // which the keys' bytes take 20 and the rest is start (3.5), the last tile and the
-// join (2.5 + 5.6); one token over 2k keys 11.7 us, all of it latency.
+// join (8); one token over 2k keys 11.3 us, all of it latency.
 // Slower and not kept: the pieces joined over a cluster's shared memory, or by a
 // kernel of their own; rows copied into idle quarters of a tile; no range shorter
-// than 3 tiles (one token over 2k: 12.0 us); one part of a unit per block where the
-// units allow (16 sequences of one token over 2k 32.5 -> 29.0 us, but 0.5 us more for
-// every small call and 266 us for the large one).
+// than 3 tiles (one token over 2k: 0.3 us more); the join's code gone through
+// beforehand by the idle producers (2 us more).
 //
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
@@ -62,8 +62,8 @@ constexpr int kTreeFlags = 8;       // K tiles whose bad-page flags are kept: mo
 
 struct TreeArgs {
   TreeAttention a;
-  int G, ctas;
-  float scale_log2;
+  int G, ctas, may_part;  // may_part: units may be no more than blocks
+  float scale_log2, inv_ctas;
   float *part;       // [2 kTreeCtas] slots of [hd / 4][128 rows] float4: block c's first piece in 2 c, its last in 2 c + 1
   float2 *state;     // [2 kTreeCtas][128]: (m, l) of each row
   unsigned long long *flags;  // [2 kTreeCtas]: `ticket` while the slot holds a piece of this call
@@ -86,7 +86,8 @@ struct TreeSmem {
   // q_full, k_full[KR], k_empty[KR], v_full[KR], v_empty[KR], s_full[2],
   // s_empty[2], p_full[2], p_empty[2], o_full, o_empty, drained[2]
   static constexpr int n_bars = 1 + 4 * KR + 8 + 4;
-  static constexpr size_t bytes = bars + n_bars * 8 + 16;
+  static constexpr size_t share = bars + n_bars * 8 + 16;  // BlockShare
+  static constexpr size_t bytes = share + 64;
 };
 
 // Rows and keys of one sequence; n = 0 when it has nothing to do or its rows
@@ -118,7 +119,8 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &p, int b) {
 // ragged sequences of 5 tokens 26.7, 26.7, 28.3; 64 sequences of 24 tokens over
 // 16k 258, 260, 263; batches of many short sequences 4 to 10 % less with 4.
 
-// Cost of all its units; the host has checked that a batch's sum fits 31 bits.
+// Its units, and the cost of them all; the host has checked that a batch's sum fits 31 bits.
+__device__ __forceinline__ int seq_units(const TreeArgs &p, const Seq &s) { return s.n ? p.a.Hkv * s.row_tiles : 0; }
 __device__ __forceinline__ int seq_cost(const TreeArgs &p, const Seq &s) {
   return s.n ? p.a.Hkv * s.row_tiles * (s.key_tiles + kTreeUnitCost) : 0;
 }
@@ -134,6 +136,22 @@ struct Walk {
     kt0 = max(0, from - kTreeUnitCost);
     kt1 = max(0, end - kTreeUnitCost);
     left = n - (end - from);
+  }
+  // one of k equal parts of the sequence's unit u; false: it holds no tile
+  __device__ __forceinline__ bool begin_part(const TreeArgs &p, int b_, int u, int part, int k) {
+    b = b_;
+    s = load_seq(p, b);
+    g = u;
+    rt = 0;
+    if (s.row_tiles > 1) {
+      g = u / s.row_tiles;
+      rt = u - g * s.row_tiles;
+    }
+    const int each = ceil_div(s.key_tiles, k);
+    kt0 = part * each;
+    kt1 = min(s.key_tiles, kt0 + each);
+    at = left = 0;
+    return kt0 < kt1;
   }
   // false: the range holds no tile
   __device__ __forceinline__ bool begin(const TreeArgs &p, int b_, int from, int n) {
@@ -166,23 +184,52 @@ struct Walk {
   }
 };
 
-// A block's share of the batch's cost: `count` units of it from unit `at` of
-// sequence b on; per: what a block takes.  Found by every warp for itself: each lane adds up
-// a run of sequences, a scan over the lanes finds the sequence in which the
-// share begins.
+constexpr int kFewPieces = 8;  // pieces of a unit that are joined without barriers
+constexpr float kWholeTiles = 4;  // key tiles of a unit that is not worth splitting
+
+// A block's share of the batch: `count` cost units from unit `at` of sequence b
+// on, of the equal ranges of `per`; or (k > 0) the part-th of k parts of one unit
+// of rows, the at-th of the sequence; unit: its number.  Found by every warp for
+// itself: each lane adds up a run of sequences, a scan over the lanes finds the
+// sequence in which the share begins.
+//
+// Equal ranges keep every block busy whatever the lengths, but most blocks end
+// one unit and begin another, and a unit's pieces are many.  Where every unit can
+// have blocks of its own (there are no more units than blocks) and parts of the
+// longest are hardly larger than the equal ranges, a block takes one part: 16
+// sequences of one token over 2k keys 32.2 -> 28.9 us, two of 61 over 8k 29.8 ->
+// 24.5, one token over 2k 11.7 -> 11.3.  8 parts at most if that is enough, as they
+// are joined without barriers; and units of up to 4 tiles stay whole, as a join
+// takes as long as 4 tiles (4 sequences of 45 tokens over 273: 13.4 -> 10.5 us).  The
+// choice itself costs batches of single tiles 0.2 to 0.4 us.
 struct Range {
-  int b, at, count, per;
+  int b, at, count, per, k, unit, part;
 };
 __device__ __forceinline__ Range block_range(const TreeArgs &p, int lane) {
   const int run = ceil_div(p.a.n_seqs, 32), lo = min(p.a.n_seqs, lane * run), hi = min(p.a.n_seqs, lo + run);
   constexpr int kMost = 1 << 30;  // more than an ascending batch's sum: offsets that overlap stop here
-  int mine = 0;
+  int mine = 0, units = 0, longest = 0;
 #pragma unroll 4
   for (int b = lo; b < hi; ++b) {
     const Seq s = load_seq(p, b);
     mine = (int)min((unsigned)mine + (unsigned)seq_cost(p, s), (unsigned)kMost);
+    units = min(units + min(seq_units(p, s), kTreeCtas + 1), kTreeCtas + 1);
+    longest = max(longest, s.key_tiles);
     if (s.bad && blockIdx.x == 0 && threadIdx.x < 32 && p.err) atomicExch(p.err + 1, kBadSequence);
   }
+  Range r;
+  r.k = 0;
+  if (p.may_part) {
+    const int all = __reduce_add_sync(0xffffffffu, units);
+    if (all <= p.ctas && all > 0) {
+      // (in floating point: the choice need not be exact, only the same everywhere)
+      const float cost = (float)__reduce_add_sync(0xffffffffu, (unsigned)mine), most = (float)__reduce_max_sync(0xffffffffu, longest);
+      const int k = (int)__fdividef((float)p.ctas + 0.5f, (float)all), few = most <= kWholeTiles ? 1 : min(k, kFewPieces);
+      const float limit = cost * p.inv_ctas + 1.5f;
+      r.k = most <= max(limit, kWholeTiles) * few ? few : most <= limit * k ? k : 0;
+    }
+  }
+  if (r.k) mine = units;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -190,19 +237,27 @@ __device__ __forceinline__ Range block_range(const TreeArgs &p, int lane) {
     if (lane >= o) incl = (int)min((unsigned)incl + (unsigned)v, (unsigned)kMost);
   }
   const int total = __shfl_sync(0xffffffffu, incl, 31);
-  Range r;
-  r.per = (int)(((unsigned)total + (unsigned)p.ctas - 1) / (unsigned)p.ctas);
-  const long long first = (long long)r.per * blockIdx.x;
+  long long first;
+  if (r.k) {
+    r.per = 1;
+    r.unit = (int)__fdividef((float)blockIdx.x + 0.5f, (float)r.k);  // blocks and parts are few: exact
+    r.part = blockIdx.x - r.unit * r.k;
+    first = r.unit;
+  } else {
+    r.per = (int)(((unsigned)total + (unsigned)p.ctas - 1) / (unsigned)p.ctas);
+    first = (long long)r.per * blockIdx.x;
+  }
   r.count = (int)min((long long)r.per, total - first);
   r.b = -1;
   r.at = 0;
   const int start = (int)min(first, (long long)total);
-  int at = __shfl_up_sync(0xffffffffu, incl, 1);  // tiles of the lanes before
+  int at = __shfl_up_sync(0xffffffffu, incl, 1);  // those of the lanes before
   if (lane == 0) at = 0;
   const bool here = start >= at && start < incl;
   if (here) {
     for (int b = lo; b < hi; ++b) {
-      const int n = seq_cost(p, load_seq(p, b));
+      const Seq s = load_seq(p, b);
+      const int n = r.k ? seq_units(p, s) : seq_cost(p, s);
       if (start < at + n) {
         r.b = b;
         r.at = start - at;
@@ -275,13 +330,19 @@ struct Span {
   int shares, i0, rows;  // blocks with a share of its rows; this block's: rows i0 .. i0 + rows - 1
   __device__ __forceinline__ int slot(int s) const { return s == 0 ? first_slot : 2 * (first + s); }
 };
-// The span of the walk's unit; start: where the range begins.
-__device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, int start, int per) {
+// The span of the walk's unit in the block's range.
+__device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, const Range &r) {
   Span u;
-  const int begin = start + w.at, tiles = begin + kTreeUnitCost;
-  u.first = tiles / per;
-  u.last = (tiles + w.s.key_tiles - 1) / per;
-  u.first_slot = 2 * u.first + (begin > u.first * per ? 1 : 0);  // a piece of the unit before comes first there
+  if (r.k) {
+    u.first = r.unit * r.k;
+    u.last = u.first + (w.s.key_tiles - 1) / ceil_div(w.s.key_tiles, r.k);
+    u.first_slot = 2 * u.first;
+  } else {
+    const int begin = r.per * (int)blockIdx.x + w.at, tiles = begin + kTreeUnitCost;
+    u.first = tiles / r.per;
+    u.last = (tiles + w.s.key_tiles - 1) / r.per;
+    u.first_slot = 2 * u.first + (begin > u.first * r.per ? 1 : 0);  // a piece of the unit before comes first there
+  }
   u.row0 = w.s.row0;
   u.r0 = 128 * w.rt;
   u.g = w.g;
@@ -291,6 +352,14 @@ __device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, int 
   u.rows = min(n_rows, u.i0 + each) - u.i0;
   return u;
 }
+
+// What the softmax warps need at their end, kept in shared memory: registers are
+// short in their loop.
+struct BlockShare {
+  Range range;
+  Span head;  // of the first unit
+};
+static_assert(sizeof(BlockShare) <= 64, "shared memory");
 
 // The join's scratch, in the idle rings.
 struct JoinSmem {
@@ -330,7 +399,6 @@ __device__ __forceinline__ void store_row4(const TreeArgs &p, const Span &u, int
 // Latency bound, and run once a launch: what is loaded is loaded together, and
 // the code is kept short (straight-line variants for each shape spent more time
 // on fetching instructions).
-constexpr int kFewPieces = 8;
 template <int HD>
 __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, JoinSmem *scratch, int tid, int lt,
                                           volatile int *abort) {
@@ -524,7 +592,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   }
   const Range range = block_range(p, lane);  // the same in every warp
   Walk w;
-  if (range.count <= 0 || !w.begin(p, range.b, range.at, range.count)) return;
+  if (range.count <= 0 || !(range.k ? w.begin_part(p, range.b, range.at, range.part, range.k)
+                                    : w.begin(p, range.b, range.at, range.count)))
+    return;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      tc::smem_u32(tmem_slot)),
@@ -734,14 +804,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
                                                         64 * (tid % HB)));
       }
     };
+    BlockShare *share = (BlockShare *)(base + S::share);
+    if (tid == 0) share->range = range;
     stage_q(w);
     set_up();
     if (lane == 0) attn_arrive(q_full);
+    if (tid == 0) share->head = unit_span(p, w, range);  // (read behind a softmax_sync)
     const uint32_t tmem = *tmem_slot, t_s = tmem, t_o = tmem + 256, t_p = tmem + 384;
     // the first unit, if it lies in earlier blocks too, and the last, if it goes
     // on in later ones, are joined at the end (they may be the same)
-    const int start = range.per * (int)blockIdx.x;
-    const Span head = unit_span(p, w, start, range.per);
     const bool join_head = w.kt0 > 0;
     int i = 0, piece = 0;
     while (true) {
@@ -902,9 +973,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         // in flight, and the rings run dry): the flags of the first and the last
         // piece, then this block's shares of the units they belong to.
         const bool join_tail = w.kt1 < w.s.key_tiles && (piece || !join_head);
-        const Span tail = unit_span(p, w, start, range.per);
+        const Span tail = unit_span(p, w, share->range);
         if (join_head || join_tail) {
-          if (tid == 0 && join_head && head.last == (int)blockIdx.x) p.joined[blockIdx.x] = 0;  // counted from here by those who see the flag
+          // counted from here by those who see the flag
+          if (tid == 0 && join_head && share->head.last == (int)blockIdx.x) p.joined[blockIdx.x] = 0;
           // (found out while the fence waits)
           asm volatile("" ::"r"(tail.first), "r"(tail.last), "r"(tail.first_slot), "r"(tail.shares), "r"(tail.i0), "r"(tail.rows));
           __threadfence();
@@ -914,6 +986,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             if (join_tail) st_flag(p.flags + slot, p.ticket);
           }
         }
+        const Span head = share->head;
         // Two units of few pieces are joined at once, by four warps each: nothing
         // there waits for the other warps.  (One loop: the code is there once.)
         const bool both = join_head && join_tail && head.last - head.first < kFewPieces && tail.last - tail.first < kFewPieces;
@@ -991,6 +1064,9 @@ template <int HD>
 cudaError_t launch_tree(TreeArgs &p, cudaStream_t st) {
   const cudaError_t e = tree_ctas<HD>(&p.ctas);
   if (e != cudaSuccess) return e;
+  p.inv_ctas = 1.0f / (float)p.ctas;
+  // (no use asking where the rows in full tiles are more units than blocks)
+  p.may_part = (long long)p.a.Hkv * p.a.n_tok * p.G / 128 <= p.ctas && p.a.Hkv <= p.ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.ctas);
   cfg.blockDim = dim3(kTreeThreads);

@@ -398,6 +398,10 @@ def test_attention_repeats_bit_for_bit_and_ignores_the_workspace_contents():
     (16, 8, 128, [9000, 3, 700, 0, 2500], [24, 1, 7, 13, 30]),
     (4, 1, 64, [40000], [33]),
     (8, 8, 128, [2048], [1]),
+    (16, 8, 128, [2000 + 3 * j for j in range(16)], [1] * 16),
+    (8, 2, 128, [4000, 4100], [61, 33]),
+    (4, 1, 64, [9000, 100], [3, 40]),
+    (6, 3, 64, [500, 130, 400, 1], [2, 2, 2, 2]),
 ])
 def test_attention_replayed_many_times_repeats_bit_for_bit(hq, hkv, hd, pre, new):
     # units that span several blocks are joined between the blocks: a captured
