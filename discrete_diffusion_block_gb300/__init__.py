@@ -594,6 +594,7 @@ def dg_op_kv_append(k_new, v_new, k_pool, v_pool, page_table, n_layers, n_pages,
 # checks here read each tensor attribute once, and the arguments go over in one
 # block (dg_op_packed: "q" an integer or address, 0 for NULL, "d" a float).
 
+_current_device = torch.cuda.current_device
 _BF16, _F32, _I32T, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _PACK_QK = struct.Struct("=qqqqqqqqqqqdqqdqqqqq").pack
 _PACK_APPEND = struct.Struct("=qqqqqqqqqqqqqqdqdqqqqq").pack
@@ -614,12 +615,12 @@ def _call(which, args):
 
 def _device(t):
     """The current CUDA device, which t lies on."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         _einval("a tensor is not on a CUDA device")
-    cur = torch.cuda.current_device()
-    if t.get_device() != cur:
+    if dev != _current_device():
         _einval("a tensor is not on the current CUDA device")
-    return cur
+    return dev
 
 
 def _dense(t, what, kind, n, dev):
@@ -633,16 +634,17 @@ def _dense(t, what, kind, n, dev):
     return t.data_ptr()
 
 
-def _rows(t, what, kind, shape, dev):
-    """(address, row stride) of a [rows][heads][hd] tensor whose rows may be strided."""
+def _rows(t, what, kind, shape, one_row, dev):
+    """(address, row stride) of a [rows][heads][hd] tensor whose rows may be
+    strided; one_row: heads * hd where there are no two rows to be apart, else 0."""
     if t.dtype is not kind or t.shape != shape:
         _einval(f"{what} must be a {kind} tensor of shape {tuple(shape)}")
     if t.get_device() != dev:
         _einval(f"{what} is not on the current CUDA device")
     row, head, one = t.stride()
-    if (one != 1 or (head != shape[2] and shape[1] > 1)) and t.numel():
+    if (one != 1 or head != shape[2]) and (one != 1 or shape[1] > 1) and t.numel():
         _einval(f"{what}: the heads of a row must be adjacent")
-    return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
+    return t.data_ptr(), one_row or row
 
 
 def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, eps=1e-6, rope_base=10000.0,
@@ -662,15 +664,17 @@ def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, 
     if q is not None:
         shape = q.shape
         hq = shape[1]
-        qp, qs = _rows(q, "q", kind, shape, dev)
-        qo, qos = _rows(q_out, "q_out", _BF16, shape, dev)
+        one_row = 0 if T > 1 else hq * hd
+        qp, qs = _rows(q, "q", kind, shape, one_row, dev)
+        qo, qos = _rows(q_out, "q_out", _BF16, shape, one_row, dev)
     if k is not None:
         shape = k.shape
         if len(shape) != 3 or shape[0] != T or shape[2] != hd:
             _einval("q and k must agree in rows and head_dim")
         hkv = shape[1]
-        kp, ks = _rows(k, "k", kind, shape, dev)
-        ko, kos = _rows(k_out, "k_out", _BF16, shape, dev)
+        one_row = 0 if T > 1 else hkv * hd
+        kp, ks = _rows(k, "k", kind, shape, one_row, dev)
+        ko, kos = _rows(k_out, "k_out", _BF16, shape, one_row, dev)
     _call(DG_CALL_QK_NORM_ROPE, _PACK_QK(
         qp, kp, 1 if kind is _F32 else 0, qs, ks, _dense(positions, "positions", _I32T, T, dev), T, hq, hkv, hd,
         hd if rope_dim is None else rope_dim, rope_base, _dense(q_gain, "q_gain", _F32, hd, dev),
@@ -690,8 +694,9 @@ def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets
     B, max_pages = table
     T = k.shape[0]
     shape = (T, hkv, hd)
-    kp, ks = _rows(k, "k", _BF16, shape, dev)
-    vp, vs = _rows(v, "v", _BF16, shape, dev)
+    one_row = 0 if T > 1 else hkv * hd
+    kp, ks = _rows(k, "k", _BF16, shape, one_row, dev)
+    vp, vs = _rows(v, "v", _BF16, shape, one_row, dev)
     _call(DG_CALL_ROPE_KV_APPEND, _PACK_APPEND(
         kp, vp, ks, vs, _dense(positions, "positions", _I32T, T, dev),
         _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev),
@@ -717,8 +722,9 @@ def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, t
     n_pages, hkv, pg, hd = pool
     B, max_pages = table
     T = shape[0]
-    qp, qs = _rows(q, "q", _BF16, shape, dev)
-    op, os_ = _rows(out, "out", _BF16, shape, dev)
+    one_row = 0 if T > 1 else shape[1] * hd
+    qp, qs = _rows(q, "q", _BF16, shape, one_row, dev)
+    op, os_ = _rows(out, "out", _BF16, shape, one_row, dev)
     mp = words = wp = wn = 0
     if tree_mask is not None and T:
         words = tree_mask.shape[-1]
