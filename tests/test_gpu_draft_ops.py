@@ -875,3 +875,27 @@ def test_the_first_call_of_a_process_can_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and "the same" in p.stdout, p.stderr[-2000:]
+
+
+def test_attention_on_several_streams_among_other_kernels():
+    # the blocks of a call wait for one another: calls on other streams, and
+    # kernels that hold some of the SMs, must not come between them
+    rng = np.random.default_rng(45)
+    calls = []
+    for hq, hkv, hd, pre, new in ((16, 8, 128, [6000, 3000], [24, 2]), (12, 4, 64, [3000] * 20, [5] * 20), (8, 1, 128, [9000], [61])):
+        bt = Batch(rng, pre, new, hkv, hd, 128)
+        q, ref = check_attention(bt, hq, None, rng)
+        ws = torch.zeros(dgp.dg_op_tree_attention_workspace_bytes(bt.T, len(pre), hq, hkv, hd), dtype=torch.uint8, device=dev())
+        calls.append((bt, q, torch.full_like(ref, 7.0), ref, ws, torch.cuda.Stream()))
+    a = torch.randn(512, 512, device=dev())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(40):
+        with torch.cuda.stream(side):
+            a = torch.tanh(a @ a)
+        for bt, q, out, _, ws, st in calls:
+            run_attention(bt, q, None, out, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    dgp.dg_op_status()
+    for _, _, out, ref, _, _ in calls:
+        assert torch.equal(out, ref)
