@@ -114,10 +114,10 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &p, int b) {
 // The cost of a unit in key tiles, for the equal ranges: its tiles, and
 // kTreeUnitCost more for starting it (rows staged, the first tile's way through
 // all stages, sums written out and joined).  A range's tiles are those of its
-// cost units that lie behind the start-up of their unit.  Measured with 2, 4, 6
-// in its place: one sequence of 61 tokens over 32k keys 36.3, 35.8, 36.4 us; 40
-// ragged sequences of 5 tokens 26.7, 26.7, 28.3; 64 sequences of 24 tokens over
-// 16k 258, 260, 263; batches of many short sequences 4 to 10 % less with 4.
+// cost units that lie behind the start-up of their unit.  Measured with 2, 3, 4, 5
+// in its place: 40 ragged sequences of 5 tokens 24.9, 24.8, 25.5, 26.2 us; 15 of 22
+// over 5.5k 20.2, 20.6, 19.4, 20.2; 30 of 6 over 4.7k 18.1, 17.4, 16.9, 16.8; 64 of
+// 24 over 16k 260 with each.
 
 // Its units, and the cost of them all; the host has checked that a batch's sum fits 31 bits.
 __device__ __forceinline__ int seq_units(const TreeArgs &p, const Seq &s) { return s.n ? p.a.Hkv * s.row_tiles : 0; }
