@@ -17,6 +17,7 @@
 // prefix .. prefix + C - 1): attention then treats prefix and canvas keys
 // uniformly, and the KV-append forward overwrites those slots with the
 // clean canvas's K/V.
+#include <atomic>
 #include <chrono>
 #include <cmath>
 #include <cstdarg>
@@ -1356,7 +1357,9 @@ namespace {
 
 // Status words of the kernel-level entry points, one set per device that loads
 // the library: a bounded device-side wait that gives up writes its code to
-// [0], and the attention writes 39 to [1] for a page index outside the pools.  It is a
+// [1], and calls that meet a bad page, sequence or token write theirs to [2];
+// kernels get the address of [1].  [0] is the epoch: another number after each
+// clearing of [1], in the same 8 bytes (the tree attention reads both).  It is a
 // file-scope device array rather than an allocation, so that the entry points
 // that must not allocate can use it too; it is zero when the library is
 // loaded, sticky (a later kernel that sees it set skips its waits), and read
@@ -1377,7 +1380,7 @@ int op_status_ptr(int **out) {
   if (!g_status_ptr[dev]) {
     void *p = nullptr;
     CK(cudaGetSymbolAddress(&p, g_op_status));
-    g_status_ptr[dev] = (int *)p;
+    g_status_ptr[dev] = (int *)p + 1;
   }
   *out = g_status_ptr[dev];
   return DG_OK;
@@ -1407,6 +1410,11 @@ int dg_op_status(void *stream) {
   int v[2] = {0, 0};
   CK(cudaMemcpy(v, st, sizeof(v), cudaMemcpyDeviceToHost));
   if (v[0] == 0 && v[1] == 0) return DG_OK;
+  if (v[0]) {  // a new epoch, before the record is cleared
+    static std::atomic<int32_t> epochs{0};
+    const int32_t epoch = ++epochs;
+    CK(cudaMemcpy(st - 1, &epoch, sizeof(epoch), cudaMemcpyHostToDevice));
+  }
   CK(cudaMemset(st, 0, sizeof(v)));
   if (v[0]) return device_fail(v[0]);
   if (v[1] == dg::kBadSequence)

@@ -58,6 +58,7 @@ namespace {
 constexpr int kTreeThreads = 384;
 constexpr int kTreePvWarp = 11;
 constexpr int kTreeCtas = 152;      // most blocks: one per SM
+constexpr int kTreeGaveUp = 63;     // status code of a join that gave up, or of a block that did after an earlier kernel
 constexpr int kTreeFlags = 8;       // K tiles whose bad-page flags are kept: more than are ever in flight
 
 struct TreeArgs {
@@ -66,7 +67,7 @@ struct TreeArgs {
   float scale_log2, inv_ctas;
   float *part;       // [2 kTreeCtas] slots of [hd / 4][128 rows] float4: block c's first piece in 2 c, its last in 2 c + 1
   float2 *state;     // [2 kTreeCtas][128]: (m, l) of each row
-  unsigned long long *flags;  // [2 kTreeCtas]: `ticket` while the slot holds a piece of this call
+  unsigned long long *flags;  // [2 kTreeCtas]: the launch's value (BlockShare) while the slot holds a piece of this launch
   int *joined;       // [kTreeCtas]: warps that have seen all flags of the unit that ends in block c
   unsigned long long ticket;  // this call's own number
   int *err;
@@ -87,7 +88,7 @@ struct TreeSmem {
   // s_empty[2], p_full[2], p_empty[2], o_full, o_empty, drained[2]
   static constexpr int n_bars = 1 + 4 * KR + 8 + 4;
   static constexpr size_t share = bars + n_bars * 8 + 16;  // BlockShare
-  static constexpr size_t bytes = share + 64;
+  static constexpr size_t bytes = share + 80;
 };
 
 // Rows and keys of one sequence; n = 0 when it has nothing to do or its rows
@@ -356,10 +357,26 @@ __device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, cons
 // What the softmax warps need at their end, kept in shared memory: registers are
 // short in their loop.
 struct BlockShare {
+  // A raised flag of this launch: the call's ticket, plus the epoch of the status
+  // word.  A launch that gives up may leave flags up, and a captured call has the
+  // same ticket in every replay; but a launch that gives up also leaves its code in
+  // the status word, later launches give up while that is set, and dg_op_status,
+  // which clears it, moves the epoch on first.  So no launch takes an earlier one's
+  // flags for its own.
+  unsigned long long up;
   Range range;
   Span head;  // of the first unit
 };
-static_assert(sizeof(BlockShare) <= 64, "shared memory");
+static_assert(sizeof(BlockShare) <= 80, "shared memory");
+
+// The status word (in the high half: 0, or what an earlier kernel gave up with) and
+// its epoch (low half) in one load: a clear status is never seen with the epoch
+// before the clearing.
+__device__ __forceinline__ unsigned long long ld_status(const int *err) {
+  unsigned long long v = 0;
+  if (err) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];\n" : "=l"(v) : "l"(err - 1) : "memory");
+  return v;
+}
 
 // The join's scratch, in the idle rings.
 struct JoinSmem {
@@ -370,13 +387,14 @@ struct JoinSmem {
 
 // Waits (bounded) until the unit's pieces are there, flag s in lane s, s + 32 ..;
 // run by every softmax warp for itself.  False: given up.
-__device__ __forceinline__ bool pieces_ready(const TreeArgs &p, const Span &u, int n, int lane, volatile int *abort) {
+__device__ __forceinline__ bool pieces_ready(const TreeArgs &p, const Span &u, int n, int lane, unsigned long long up,
+                                             volatile int *abort) {
   for (int s = lane; s < n; s += 32) {
     const unsigned long long *flag = p.flags + u.slot(s);
     const long long t0 = clock64();
-    while (ld_flag(flag) != p.ticket && !*abort) {
+    while (ld_flag(flag) != up && !*abort) {
       if (clock64() - t0 > tc::kWaitCycles) {
-        if (p.err) atomicExch(p.err, 63);
+        if (p.err) atomicExch(p.err, kTreeGaveUp);
         *abort = 1;
       }
     }
@@ -394,18 +412,18 @@ __device__ __forceinline__ void store_row4(const TreeArgs &p, const Span &u, int
 // This block's share of a unit's rows, out of the pieces of all its blocks:
 // weights 2^(m_s - m*), pieces in the order of the keys.  Run by 2^lt of the
 // softmax threads (tid of them; 256 for more than kFewPieces) after the block's
-// last piece.  The last warp to have seen the unit's flags takes them down: a
-// captured call, whose ticket is the same every time, has to find them down.
+// last piece.  The last warp to have seen the unit's flags takes them down: the
+// next replay of a captured call, whose ticket is the same, has to find them down.
 // Latency bound, and run once a launch: what is loaded is loaded together, and
 // the code is kept short (straight-line variants for each shape spent more time
 // on fetching instructions).
 template <int HD>
 __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, JoinSmem *scratch, int tid, int lt,
-                                          volatile int *abort) {
+                                          unsigned long long up, volatile int *abort) {
   constexpr int C = HD / 4, LC = HD == 128 ? 5 : 4;  // float4 columns of a row
   const int n = u.last - u.first + 1, i0 = u.i0, rows = u.rows, lane = tid & 31;
   if (rows <= 0) return;
-  bool ready = pieces_ready(p, u, n, lane, abort);
+  bool ready = pieces_ready(p, u, n, lane, up, abort);
   static_assert(sizeof(JoinSmem) <= 2 * TreeSmem<HD>::KR * TreeSmem<HD>::tile, "the rings");
   const int mine = 256 >> lt;  // a share counts 8, whether 8 warps join it or 4
   int seen = 0;
@@ -805,9 +823,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       }
     };
     BlockShare *share = (BlockShare *)(base + S::share);
+    const unsigned long long status = tid == 0 ? ld_status(p.err) : 0;
     if (tid == 0) share->range = range;
     stage_q(w);
     set_up();
+    if (tid == 0) {
+      share->up = p.ticket + (uint32_t)status;  // (read behind a softmax_sync, as the head)
+      if (status >> 32) *abort = 1;
+    }
     if (lane == 0) attn_arrive(q_full);
     if (tid == 0) share->head = unit_span(p, w, range);  // (read behind a softmax_sync)
     const uint32_t tmem = *tmem_slot, t_s = tmem, t_o = tmem + 256, t_p = tmem + 384;
@@ -982,8 +1005,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           __threadfence();
           softmax_sync();
           if (tid == 0) {
-            if (join_head) st_flag(p.flags + 2 * blockIdx.x, p.ticket);
-            if (join_tail) st_flag(p.flags + slot, p.ticket);
+            if (join_head) st_flag(p.flags + 2 * blockIdx.x, share->up);
+            if (join_tail) st_flag(p.flags + slot, share->up);
           }
         }
         const Span head = share->head;
@@ -993,7 +1016,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll 1
         for (int k = join_head ? 0 : 1; k < (join_tail ? 2 : 1); ++k) {
           if (both && k != tid >> 7) continue;
-          join_unit<HD>(p, k ? tail : head, (JoinSmem *)(base + S::kring), both ? tid & 127 : tid, both ? 7 : 8, abort);
+          join_unit<HD>(p, k ? tail : head, (JoinSmem *)(base + S::kring), both ? tid & 127 : tid, both ? 7 : 8, share->up, abort);
         }
       }
       if (!more) break;
@@ -1004,6 +1027,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   __syncwarp();  // lone-thread roles above: reconverge before the block-wide barrier
   tc::fence_before();
   __syncthreads();
+  // given up: the record stands behind the launch, even if it was cleared meanwhile
+  if (threadIdx.x == 0 && *abort && p.err) atomicCAS(p.err, 0, kTreeGaveUp);
   if (warp == 1) {
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(*tmem_slot), "r"(512u));

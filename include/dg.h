@@ -639,8 +639,8 @@ int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride,
  * dg_op_tree_attention_workspace_bytes() bytes, 16-byte aligned, contents
  * arbitrary; calls that overlap on the GPU need one each.  The launch is
  * cooperative (its blocks run together and wait, bounded, for one another).
- * Once dg_op_status has told of a wait that gave up, clear the workspace before
- * a captured call is replayed with it. */
+ * After a failure that dg_op_status has told of, a captured call can be replayed
+ * with its workspace as it is. */
 size_t dg_op_tree_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
                                             int32_t n_kv_heads, int32_t head_dim);
 int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool,

@@ -1,0 +1,53 @@
+"""The operators that serve drafted tokens after failures, on values at the ends
+of their types and in calls that other tests do not make, against the plain numpy
+evaluations of test_gpu_draft_ops."""
+import numpy as np
+import pytest
+import torch
+
+import discrete_diffusion_block_gb300 as dgp
+from gpu_util import dev
+from test_gpu_draft_ops import Batch, _clean_status, _lib, randn, run_attention  # noqa: F401  (fixtures among them)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- after a failure ------------------------------------------------------------------
+
+@pytest.mark.parametrize("hq,hkv,hd,pre,new", [
+    (16, 8, 128, [9000, 3, 700, 0, 2500], [24, 1, 7, 13, 30]),
+    (4, 1, 64, [40000], [33]),
+    (8, 8, 128, [2048], [1]),
+    (8, 2, 128, [4000, 4100], [61, 33]),
+])
+def test_a_captured_attention_recovers_from_a_failure(hq, hkv, hd, pre, new):
+    # A launch that finds the record of an earlier failure set gives up and leaves
+    # flags of its pieces up in the workspace; the replays after dg_op_status has
+    # told of it must not take them for their own.  Each turn has queries of its
+    # own: pieces of another turn would show.
+    rng = np.random.default_rng(51)
+    bt = Batch(rng, pre, new, hkv, hd, 128)
+    n = dgp.dg_op_tree_attention_workspace_bytes(bt.T, len(pre), hq, hkv, hd)
+    ws = torch.zeros(n, dtype=torch.uint8, device=dev())
+    q, out = randn(rng, bt.T, hq, hd).to(dev()), torch.empty(bt.T, hq, hd, dtype=torch.bfloat16, device=dev())
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        run_attention(bt, q, None, out, workspace=ws, stream=st)
+    for turn in range(12):
+        dgp.dg_op_wait_selftest(20_000)
+        g.replay()
+        torch.cuda.synchronize()
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert e.value.code == dgp.DG_ETIMEOUT
+        dgp.dg_op_status()                                  # cleared
+        for _ in range(3):
+            q.copy_(randn(rng, bt.T, hq, hd))
+            want = torch.full_like(out, 7.0)
+            run_attention(bt, q, None, want)                # a workspace of its own
+            out.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+            dgp.dg_op_status()
+            assert torch.equal(out, want), turn
