@@ -463,7 +463,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, Join
       for (int k = 0; k < 8; ++k) {
         const int i = b0 + r + ((k >> lb) << la), s = k & ((1 << lb) - 1);
         w[k] = ml[k].x == NEG ? 0.0f : ex2(ml[k].x - mx[k]);
-        if (w[k] > 0.0f) {
+        if (w[k] != 0.0f) {  // (NaN too)
           L += w[k] * ml[k].y;
           acc.x += w[k] * o[k].x;
           acc.y += w[k] * o[k].y;
@@ -986,7 +986,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
                                                                    __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
           }
         }
-        if (!full_unit && half == 0 && row < rows) p.state[(size_t)slot * 128 + row] = make_float2(m, lt);
+        // (a row whose sum is NaN: its weight in the join is inf - inf, so the row is NaN)
+        if (!full_unit && half == 0 && row < rows) p.state[(size_t)slot * 128 + row] = make_float2(lt == lt ? m : -NEG, lt);
         tc::fence_before();
       }
       __syncwarp();

@@ -7,7 +7,8 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_draft_ops import Batch, _clean_status, _lib, randn, run_attention  # noqa: F401  (fixtures among them)
+from test_gpu_draft_ops import (Batch, _clean_status, _lib, attention_ref, attention_tol, f64,  # noqa: F401  (fixtures)
+                                randn, run_attention)
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +52,26 @@ def test_a_captured_attention_recovers_from_a_failure(hq, hkv, hd, pre, new):
             torch.cuda.synchronize()
             dgp.dg_op_status()
             assert torch.equal(out, want), turn
+
+
+# ---- values at the ends of their types --------------------------------------------------
+
+@pytest.mark.parametrize("hq,hkv,hd,pre,new", [
+    (8, 8, 128, [2048], [3]),                     # a unit in a few pieces
+    (4, 1, 64, [40000], [3]),                     # in many
+    (4, 2, 64, [10], [3]),                        # in one
+])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_a_number_gives_nan_and_stays_apart(hq, hkv, hd, pre, new, value):
+    rng = np.random.default_rng(53)
+    bt = Batch(rng, pre, new, hkv, hd, 64)
+    q = randn(rng, bt.T, hq, hd)
+    q[1, 2, 5] = value
+    out = torch.full((bt.T, hq, hd), 7.0, dtype=torch.bfloat16, device=dev())
+    run_attention(bt, q.to(dev()), None, out)
+    q[1, 2, 5] = 0.0
+    ref, mag = attention_ref(f64(q), bt, None, hd ** -0.5)
+    got, n = f64(out), int(bt.off[-1])
+    assert np.isnan(got[1, 2]).all()
+    got[1, 2] = ref[1, 2]
+    assert (np.abs(got[:n] - ref[:n]) <= attention_tol(ref[:n], mag[:n])).all()
