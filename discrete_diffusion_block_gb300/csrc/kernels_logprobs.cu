@@ -403,14 +403,18 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const __g
   const float nan = __int_as_float(0x7fc00000);
   const float top = r.m * p.a.inv_tau;
   const bool bad = !(r.s >= 0.0f) || top == INFINITY;  // a NaN entry, or +inf
+  // every y is -inf: the entries are, or (where their lowest value fills a masked
+  // row) their products with 1 / tau
+  const bool none = top == -INFINITY;
   const float logs = bad ? nan : (r.s > 0.0f ? logf(r.s) : 0.0f);
   auto logprob = [&](float raw) {
     if (bad) return nan;
-    return raw == -INFINITY ? raw : (raw * p.a.inv_tau - top) - logs;
+    const float y = __fmul_rn(raw, p.a.inv_tau);  // rounded, as top is: not part of the difference
+    return y == -INFINITY ? y : (y - top) - logs;
   };
   if (threadIdx.x == 0) {
     if (p.a.lse) p.a.lse[row] = top + logs;
-    if (p.a.entropy) p.a.entropy[row] = bad ? nan : (r.s > 0.0f ? logs - kLn2f * (r.a / r.s) : 0.0f);
+    if (p.a.entropy) p.a.entropy[row] = bad ? nan : none ? 0.0f : logs - kLn2f * (r.a / r.s);
   }
   if (threadIdx.x < k) {
     const unsigned long long key = s_pick.top[threadIdx.x];

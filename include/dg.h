@@ -663,9 +663,9 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
  *                                order, equal ones by ascending index
  *                                (top_logprobs may be NULL)
  * logits: device fp32 (bf16 when logits_bf16 != 0) rows, row_stride >= V
- * elements apart, of the elements' natural alignment.  Entries of -inf have
- * probability 0 (a row of nothing else: lse -inf, entropy 0, log
- * probabilities -inf).  A row that holds a NaN, or whose y reaches +inf, gives
+ * elements apart, of the elements' natural alignment.  Entries whose y is -inf
+ * have probability 0 (a row of nothing else: lse -inf, entropy 0, log
+ * probabilities -inf; y of the lowest fp32 value is -inf when inv_tau > 1).  A row that holds a NaN, or whose y reaches +inf, gives
  * NaN throughout (NaN entries order as -inf).  tokens device int32
  * [rows][n_given]; n_given >= 0; top_k in [0, min(32, V)]; inv_tau > 0. */
 int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_stride, int32_t rows,

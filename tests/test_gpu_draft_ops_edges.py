@@ -7,8 +7,8 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_draft_ops import (Batch, _clean_status, _lib, attention_ref, attention_tol, f64,  # noqa: F401  (fixtures)
-                                randn, run_attention)
+from test_gpu_draft_ops import (Batch, _clean_status, _lib, attention_ref, attention_tol, check_logprobs,  # noqa: F401  (fixtures)
+                                f64, randn, run_attention)
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,19 @@ def test_a_query_that_is_not_a_number_gives_nan_and_stays_apart(hq, hkv, hd, pre
     assert np.isnan(got[1, 2]).all()
     got[1, 2] = ref[1, 2]
     assert (np.abs(got[:n] - ref[:n]) <= attention_tol(ref[:n], mag[:n])).all()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [700, 131072])
+def test_logprobs_of_rows_that_overflow_downwards(V, bf16):
+    low = float(torch.finfo(torch.bfloat16 if bf16 else torch.float32).min)
+    x = np.full((4, V), low, np.float32)
+    x[1, V // 3] = 2.0
+    x[2, V - 1] = low / 2
+    x[3, 5], x[3, 6] = low / 2, -np.inf
+    x = torch.from_numpy(x)
+    x = (x.to(torch.bfloat16) if bf16 else x).to(dev())
+    tokens = np.array([[0, V - 1], [V // 3, 0], [V - 1, 0], [5, 6]])
+    for tau in (0.7, 0.3, 1.0, 2.0):
+        for r in range(4):                           # (tolerances go by the largest value of a call)
+            check_logprobs(x[r:r + 1], tokens[r:r + 1], 20, 1.0 / tau)
