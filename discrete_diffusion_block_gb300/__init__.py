@@ -727,7 +727,10 @@ def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, t
     op, os_ = _rows(out, "out", _BF16, shape, one_row, dev)
     mp = words = wp = wn = 0
     if tree_mask is not None and T:
-        words = tree_mask.shape[-1]
+        mask = tree_mask.shape
+        if len(mask) != 2 or mask[0] != T or mask[1] < 1:
+            _einval("tree_mask must be [rows][words], of one word at least")
+        words = mask[1]
         mp = _dense(tree_mask, "tree_mask", _I64T, T * words, dev)
     if workspace is not None:
         if not workspace.is_contiguous() or workspace.get_device() != dev:

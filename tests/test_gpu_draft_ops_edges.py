@@ -91,3 +91,19 @@ def test_logprobs_of_rows_that_overflow_downwards(V, bf16):
     for tau in (0.7, 0.3, 1.0, 2.0):
         for r in range(4):                           # (tolerances go by the largest value of a call)
             check_logprobs(x[r:r + 1], tokens[r:r + 1], 20, 1.0 / tau)
+
+
+# ---- refusals of the binding ---------------------------------------------------------------
+
+def test_an_empty_mask_is_refused():
+    rng = np.random.default_rng(54)
+    bt = Batch(rng, [100], [4], 2, 64, 64)
+    q = randn(rng, bt.T, 4, 64).to(dev())
+    out = torch.full_like(q, 7.0)
+    ws = torch.zeros(dgp.dg_op_tree_attention_workspace_bytes(bt.T, 1, 4, 2, 64), dtype=torch.uint8, device=dev())
+    for shape in ((bt.T, 0), (bt.T,), (1, bt.T), (bt.T, 1, 1)):
+        mask = torch.zeros(shape, dtype=torch.int64, device=dev())
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_tree_attention(q, bt.k_pool, bt.v_pool, **bt.d, tree_mask=mask, out=out, workspace=ws)
+        assert e.value.code == dgp.DG_EINVAL and "tree_mask" in str(e.value)
+    assert (out == 7.0).all()
