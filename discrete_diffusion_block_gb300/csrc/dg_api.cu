@@ -1637,6 +1637,10 @@ namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
+// A factor of scores or logits: the kernels multiply with its product with
+// log2(e), which has to be finite too.
+bool is_factor(float x) { return x > 0.0f && x <= 2.3e38f; }
+
 // Rows of `heads` heads: present, 16-byte aligned, far enough apart.
 int check_rows(const char *what, const void *p, int64_t stride, int32_t n_tok, int32_t heads, int32_t head_dim,
                int elems16) {
@@ -1740,7 +1744,7 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
   if ((int64_t)n_tok * n_q_heads > INT32_MAX - 128) return fail(DG_EINVAL, "too many rows of heads");
   if (head_dim != 64 && head_dim != 128) return fail(DG_EINVAL, "head_dim must be 64 or 128");
   if (page_size < 64 || page_size % 64) return fail(DG_EINVAL, "page_size must be a positive multiple of 64");
-  if (!(scale > 0.0f && scale < INFINITY)) return fail(DG_EINVAL, "scale must be finite and > 0");
+  if (!is_factor(scale)) return fail(DG_EINVAL, "scale must be in (0, 2.3e38]");
   if (tree_mask ? mask_words < 1 : mask_words != 0)
     return fail(DG_EINVAL, "mask_words must be at least 1 with a mask, 0 without");
   CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, v_pool, n_pages));
@@ -1769,7 +1773,7 @@ int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_st
                          float *lse, int32_t top_k, int32_t *top_ids, float *top_logprobs, void *stream) {
   if (rows < 0 || V < 1 || n_given < 0) return fail(DG_EINVAL, "rows, n_given >= 0 and V >= 1 required");
   if (top_k < 0 || top_k > 32 || top_k > V) return fail(DG_EINVAL, "top_k must be in [0, min(32, V)]");
-  if (!(inv_tau > 0.0f && inv_tau < INFINITY)) return fail(DG_EINVAL, "inv_tau must be finite and > 0");
+  if (!is_factor(inv_tau)) return fail(DG_EINVAL, "inv_tau must be in (0, 2.3e38]");
   if (rows == 0) return DG_OK;
   if (!logits) return fail(DG_EINVAL, "null logits");
   if ((uintptr_t)logits % (logits_bf16 ? 2 : 4)) return fail(DG_EINVAL, "logits are not aligned to their elements");

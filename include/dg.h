@@ -634,7 +634,7 @@ int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride,
  * whose slots outside the page table is skipped (its rows are left alone),
  * keys of a page outside the pools are skipped; both are reported by
  * dg_op_status.
- * scale > 0; head_dim in {64, 128}; n_q_heads / n_kv_heads <= 128; page_size a
+ * scale in (0, 2.3e38]; head_dim in {64, 128}; n_q_heads / n_kv_heads <= 128; page_size a
  * multiple of 64.  workspace: device scratch of
  * dg_op_tree_attention_workspace_bytes() bytes, 16-byte aligned, contents
  * arbitrary; calls that overlap on the GPU need one each.  The launch is
@@ -665,9 +665,10 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
  * logits: device fp32 (bf16 when logits_bf16 != 0) rows, row_stride >= V
  * elements apart, of the elements' natural alignment.  Entries whose y is -inf
  * have probability 0 (a row of nothing else: lse -inf, entropy 0, log
- * probabilities -inf; y of the lowest fp32 value is -inf when inv_tau > 1).  A row that holds a NaN, or whose y reaches +inf, gives
- * NaN throughout (NaN entries order as -inf).  tokens device int32
- * [rows][n_given]; n_given >= 0; top_k in [0, min(32, V)]; inv_tau > 0. */
+ * probabilities -inf; y of the lowest fp32 value is -inf when inv_tau > 1).  A
+ * row that holds a NaN, or whose y reaches +inf, gives NaN throughout (NaN
+ * entries order as -inf).  tokens device int32 [rows][n_given]; n_given >= 0;
+ * top_k in [0, min(32, V)]; inv_tau in (0, 2.3e38]. */
 int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_stride, int32_t rows,
                          int32_t V, float inv_tau, const int32_t *tokens, int32_t n_given,
                          float *logprobs, float *entropy, float *lse, int32_t top_k,
