@@ -483,7 +483,10 @@ def dg_op_attention_workspace_bytes(n_prefix, n_new, Hq, Hkv, hd):
 
 def dg_op_status(stream=None):
     """Raises DgError if a kernel-level call since the last check recorded a
-    device-side failure (bounded wait timeout, bad page index)."""
+    device-side failure (bounded wait timeout, bad page index).  Without `stream`
+    it waits for the legacy stream and for torch's current one."""
+    if stream is None and torch.cuda.is_initialized():
+        torch.cuda.current_stream().synchronize()
     _check(load().dg_op_status(_stream(stream)))
 
 
@@ -593,8 +596,12 @@ def dg_op_kv_append(k_new, v_new, k_pool, v_pool, page_table, n_layers, n_pages,
 # The small calls of a decoding step take a few microseconds on the GPU, so the
 # checks here read each tensor attribute once, and the arguments go over in one
 # block (dg_op_packed: "q" an integer or address, 0 for NULL, "d" a float).
+# Without `stream` these four go to torch's current stream, as the torch operations
+# around them do, and are captured with them (the calls above: the legacy stream).
 
 _current_device = torch.cuda.current_device
+# (the stream's address alone: torch.cuda.current_stream() also makes an object)
+_current_stream = torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32T, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _PACK_QK = struct.Struct("=qqqqqqqqqqqdqqdqqqqq").pack
 _PACK_APPEND = struct.Struct("=qqqqqqqqqqqqqqdqdqqqqq").pack
@@ -621,6 +628,10 @@ def _device(t):
     if dev != _current_device():
         _einval("a tensor is not on the current CUDA device")
     return dev
+
+
+def _stream_on(stream, dev):
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 def _dense(t, what, kind, n, dev):
@@ -651,7 +662,8 @@ def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, 
                        rope_dim=None, stream=None):
     """q, k: [T][heads][hd] bf16 or fp32 (rows may be strided); q_out, k_out
     bf16 of the same shapes; positions int32 [T]; gains fp32 [hd] or None (no
-    norm).  k and k_out (or q and q_out) may be None."""
+    norm).  k and k_out (or q and q_out) may be None.  stream None: torch's
+    current one."""
     some = q if q is not None else k
     if some is None or some.dim() != 3 or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         _einval("q and q_out, k and k_out go together, [rows][heads][head_dim] each, and one pair is needed")
@@ -678,14 +690,14 @@ def dg_op_qk_norm_rope(q, k, positions, q_out, k_out, q_gain=None, k_gain=None, 
     _call(DG_CALL_QK_NORM_ROPE, _PACK_QK(
         qp, kp, 1 if kind is _F32 else 0, qs, ks, _dense(positions, "positions", _I32T, T, dev), T, hq, hkv, hd,
         hd if rope_dim is None else rope_dim, rope_base, _dense(q_gain, "q_gain", _F32, hd, dev),
-        _dense(k_gain, "k_gain", _F32, hd, dev), eps, qo, qos, ko, kos, _stream(stream) or 0))
+        _dense(k_gain, "k_gain", _F32, hd, dev), eps, qo, qos, ko, kos, _stream_on(stream, dev)))
 
 
 def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets, positions=None, k_gain=None,
                          eps=1e-6, rope_base=10000.0, rope_dim=None, stream=None):
     """k, v: [T][Hkv][hd] bf16 (rows may be strided); pools
     [n_pages][Hkv][page_size][hd]; page_tables int32 [B][max_pages];
-    prefix_lens int32 [B]; offsets int32 [B + 1]."""
+    prefix_lens int32 [B]; offsets int32 [B + 1].  stream None: torch's current one."""
     dev = _device(k_pool)
     pool, table = k_pool.shape, page_tables.shape
     if len(pool) != 4 or len(table) != 2 or k.dim() != 3:
@@ -703,7 +715,7 @@ def dg_op_rope_kv_append(k, v, k_pool, v_pool, page_tables, prefix_lens, offsets
         _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages, B, T, hkv, hd,
         hd if rope_dim is None else rope_dim, rope_base, _dense(k_gain, "k_gain", _F32, hd, dev), eps,
         _dense(k_pool, "k_pool", _BF16, n_pages * hkv * pg * hd, dev),
-        _dense(v_pool, "v_pool", _BF16, n_pages * hkv * pg * hd, dev), n_pages, pg, _stream(stream) or 0))
+        _dense(v_pool, "v_pool", _BF16, n_pages * hkv * pg * hd, dev), n_pages, pg, _stream_on(stream, dev)))
 
 
 def dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd):
@@ -714,7 +726,8 @@ def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, t
                          stream=None):
     """q, out: [T][Hq][hd] bf16 (rows may be strided); tree_mask int64
     [T][words] (bit d: the row sees drafted token d of its sequence) or None
-    (causal); workspace: a contiguous tensor or None; scale None: 1 / sqrt(hd)."""
+    (causal); workspace: a contiguous tensor or None; scale None: 1 / sqrt(hd);
+    stream None: torch's current one."""
     dev = _device(k_pool)
     pool, table, shape = k_pool.shape, page_tables.shape, q.shape
     if len(pool) != 4 or len(table) != 2 or len(shape) != 3 or shape[2] != pool[3]:
@@ -742,14 +755,15 @@ def dg_op_tree_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, t
         _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages,
         _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev), mp, words, B,
         T, shape[1], hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, wp, wn,
-        _stream(stream) or 0))
+        _stream_on(stream, dev)))
 
 
 def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_ids=None, top_logprobs=None,
                          inv_tau=1.0, stream=None):
     """logits: [T][V] fp32 or bf16 (rows may be strided); tokens int32
     [T][given] and logprobs fp32 [T][given] (None: none given); entropy, lse
-    fp32 [T]; top_ids int32 [T][k], top_logprobs fp32 [T][k]."""
+    fp32 [T]; top_ids int32 [T][k], top_logprobs fp32 [T][k].  stream None:
+    torch's current one."""
     dev = _device(logits)
     kind = logits.dtype
     if logits.dim() != 2 or (kind is not _BF16 and kind is not _F32):
@@ -767,4 +781,4 @@ def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_i
         _dense(tokens, "tokens", _I32T, T * given, dev), given, _dense(logprobs, "logprobs", _F32, T * given, dev),
         _dense(entropy, "entropy", _F32, T, dev), _dense(lse, "lse", _F32, T, dev), k,
         _dense(top_ids, "top_ids", _I32T, T * k, dev), _dense(top_logprobs, "top_logprobs", _F32, T * k, dev),
-        _stream(stream) or 0))
+        _stream_on(stream, dev)))

@@ -7,8 +7,8 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_draft_ops import (Batch, _clean_status, _lib, attention_ref, attention_tol, check_logprobs,  # noqa: F401  (fixtures)
-                                f64, randn, run_attention)
+from test_gpu_draft_ops import (Batch, Step, _clean_status, _lib, attention_ref, attention_tol,  # noqa: F401  (fixtures)
+                                check_logprobs, f64, i32, randn, run_attention)
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,51 @@ def test_an_empty_mask_is_refused():
             dgp.dg_op_tree_attention(q, bt.k_pool, bt.v_pool, **bt.d, tree_mask=mask, out=out, workspace=ws)
         assert e.value.code == dgp.DG_EINVAL and "tree_mask" in str(e.value)
     assert (out == 7.0).all()
+
+
+# ---- torch's current stream ----------------------------------------------------------------
+
+def test_calls_without_a_stream_take_the_current_one():
+    rng = np.random.default_rng(55)
+    s = Step(rng, [500, 20], [30, 3], pad=1)
+    s.run()                                          # (a kernel's first launch may wait for the GPU)
+    rows, st = s.rows.clone(), torch.cuda.Stream()
+    s.rows.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)                # some ms in which the rows are not there yet
+        s.rows.copy_(rows)
+        s.run()
+    torch.cuda.synchronize()
+    dgp.dg_op_status()
+    s.check()
+
+
+def test_calls_without_a_stream_are_captured():
+    rng = np.random.default_rng(56)
+    s = Step(rng, [500, 20], [30, 3], pad=1)
+    s.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.run()
+    s.rows.copy_(randn(rng, *s.rows.shape))
+    for t in (s.q, s.out, s.logits, s.lp, s.H, s.ids):
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    dgp.dg_op_status()
+    s.check()
+
+
+def test_status_without_a_stream_waits_for_the_current_one():
+    x = torch.zeros(1, 100, device=dev())
+    lp, tok = torch.zeros(1, 1, device=dev()), i32([[100]])
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+        dgp.dg_op_token_logprobs(x, tok, lp, stream=st)
+        with pytest.raises(dgp.DgError):
+            dgp.dg_op_status()
+    torch.cuda.synchronize()
