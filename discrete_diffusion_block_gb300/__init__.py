@@ -10,10 +10,10 @@ fallback.
 import ctypes
 import os
 import struct
+import sys
 from dataclasses import dataclass
 
 import numpy as np
-import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
@@ -485,7 +485,8 @@ def dg_op_status(stream=None):
     """Raises DgError if a kernel-level call since the last check recorded a
     device-side failure (bounded wait timeout, bad page index).  Without `stream`
     it waits for the legacy stream and for torch's current one."""
-    if stream is None and torch.cuda.is_initialized():
+    torch = sys.modules.get("torch")
+    if stream is None and torch is not None and torch.cuda.is_initialized():
         torch.cuda.current_stream().synchronize()
     _check(load().dg_op_status(_stream(stream)))
 
@@ -599,10 +600,20 @@ def dg_op_kv_append(k_new, v_new, k_pool, v_pool, page_table, n_layers, n_pages,
 # Without `stream` these four go to torch's current stream, as the torch operations
 # around them do, and are captured with them (the calls above: the legacy stream).
 
-_current_device = torch.cuda.current_device
-# (the stream's address alone: torch.cuda.current_stream() also makes an object)
-_current_stream = torch._C._cuda_getCurrentRawStream
-_BF16, _F32, _I32T, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_current_device = None
+
+
+def _use_torch():
+    # the first call that is given torch tensors looks up what it needs of torch:
+    # the rest of the module works without it
+    global _current_device, _current_stream, _BF16, _F32, _I32T, _I64T
+    import torch
+    # (the stream's address alone: torch.cuda.current_stream() also makes an object)
+    _current_stream = torch._C._cuda_getCurrentRawStream
+    _BF16, _F32, _I32T, _I64T = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    _current_device = torch.cuda.current_device
+
+
 _PACK_QK = struct.Struct("=qqqqqqqqqqqdqqdqqqqq").pack
 _PACK_APPEND = struct.Struct("=qqqqqqqqqqqqqqdqdqqqqq").pack
 _PACK_ATTEND = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqq").pack
@@ -625,6 +636,8 @@ def _device(t):
     dev = t.get_device()
     if dev < 0:
         _einval("a tensor is not on a CUDA device")
+    if _current_device is None:
+        _use_torch()
     if dev != _current_device():
         _einval("a tensor is not on the current CUDA device")
     return dev
