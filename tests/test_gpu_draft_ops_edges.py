@@ -7,8 +7,9 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_draft_ops import (Batch, Step, _clean_status, _lib, attention_ref, attention_tol,  # noqa: F401  (fixtures)
-                                check_logprobs, f64, i32, randn, run_attention)
+from test_draft_ops_host import packed
+from test_gpu_draft_ops import (U32, Batch, Step, _clean_status, _lib, attention_ref, attention_tol,  # noqa: F401  (fixtures)
+                                check_logprobs, f64, i32, randn, run_attention, run_logprobs)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,7 +91,8 @@ def test_logprobs_of_rows_that_overflow_downwards(V, bf16):
     tokens = np.array([[0, V - 1], [V // 3, 0], [V - 1, 0], [5, 6]])
     for tau in (0.7, 0.3, 1.0, 2.0):
         for r in range(4):                           # (tolerances go by the largest value of a call)
-            check_logprobs(x[r:r + 1], tokens[r:r + 1], 20, 1.0 / tau)
+            with np.errstate(over="ignore"):         # (the reference's products)
+                check_logprobs(x[r:r + 1], tokens[r:r + 1], 20, 1.0 / tau)
 
 
 # ---- refusals of the binding ---------------------------------------------------------------
@@ -155,3 +157,94 @@ def test_status_without_a_stream_waits_for_the_current_one():
         with pytest.raises(dgp.DgError):
             dgp.dg_op_status()
     torch.cuda.synchronize()
+
+
+# ---- log probabilities of rows split over several blocks, and of many given tokens ------------
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_logprobs_of_split_rows_ties_order_and_masks(bf16):
+    # 16 rows and fewer of 131072 and more entries are split over several blocks
+    V = 131072
+    rng = np.random.default_rng(61)
+    at = np.arange(V)
+    rows = [np.zeros(V), at // 512, -(at // 512), np.where(at < V - 3, -np.inf, 1.0), np.where(at < 5, 1.0, -np.inf), np.full(V, -np.inf),
+            np.where(at // 8192 % 2, -np.inf, rng.integers(0, 3, V)), np.where(rng.random(V) < 0.999, -np.inf, rng.integers(0, 3, V)),
+            np.where(at % 8192 == 0, 3.0, 0.0), np.where(at == 77777, 80.0, -80.0)]
+    x = torch.from_numpy(np.stack(rows).astype(np.float32))
+    x = (x.to(torch.bfloat16) if bf16 else x).to(dev())
+    tokens = rng.integers(0, V, (len(rows), 3))
+    tokens[:, 1], tokens[9, 2] = V - 1, 77777
+    check_logprobs(x, tokens, 32)
+    check_logprobs(x[3:5], tokens[3:5], 7)
+    check_logprobs(x[6:7, :V - 5], tokens[6:7, :1] // 2, 32, 0.5)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("at", [0, 60000, 131071])
+def test_logprobs_of_split_rows_with_one_bad_entry(bf16, at):
+    V = 131072
+    x = torch.zeros(4, V, dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
+    x[1, at], x[2, at], x[3, at] = float("nan"), float("inf"), float("-inf")
+    lp, H, lse, ids, top = run_logprobs(x, np.array([[at], [at], [at], [(at + 1) % V]]), 4)
+    dgp.dg_op_status()
+    for r in (1, 2):
+        assert np.isnan(lp[r]).all() and np.isnan(H[r]) and np.isnan(lse[r]) and np.isnan(top[r]).all()
+    first = [i for i in range(5) if i != at][:4]
+    assert np.array_equal(ids[0], range(4)) and np.array_equal(ids[1], first) and np.array_equal(ids[3], first)
+    assert np.array_equal(ids[2], [at] + [i for i in range(4) if i != at][:3])
+    # V or V - 1 equal entries: sums of equal terms, then the log's and the subtraction's roundings
+    tol = 4 * (V / 256 + 64) * U32
+    for r, n in ((0, V), (3, V - 1)):
+        assert abs(lp[r, 0] + np.log(n)) <= tol and abs(lse[r] - np.log(n)) <= tol and abs(H[r] - np.log(n)) <= 13 * tol
+
+
+@pytest.mark.parametrize("T,V", [(3, 900), (2, 131072)])
+def test_logprobs_of_many_given_tokens(T, V):
+    rng = np.random.default_rng(62)
+    x = torch.from_numpy((rng.standard_normal((T, V)) * 3).astype(np.float32)).to(dev())
+    tokens = rng.integers(0, V, (T, 1300))
+    tokens[:, 511:514], tokens[:, 1299] = [-1, V - 1, -1], 0
+    check_logprobs(x, tokens, 3)
+
+
+# ---- the packed-argument form -----------------------------------------------------------------
+
+def test_packed_calls_do_what_the_calls_do():
+    # every argument of a full call through both entries
+    L = dgp.load()
+    rng = np.random.default_rng(63)
+    bt = Batch(rng, [200, 70], [9, 4], 2, 64, 64)
+    T = bt.T
+    rows = randn(rng, T, 10, 64).to(dev())
+    gq, gk = (randn(rng, 64, dtype=torch.float32).to(dev()) for _ in range(2))
+    pos = i32(rng.integers(0, 1000, T))
+    mask = torch.from_numpy(rng.integers(0, 1 << 40, (T, 2))).to(dev())
+    ws = torch.zeros(dgp.dg_op_tree_attention_workspace_bytes(T, 2, 4, 2, 64), dtype=torch.uint8, device=dev())
+    logits = (randn(rng, T, 603, dtype=torch.float32) * 4).to(dev())
+    tok = i32(rng.integers(0, 600, (T, 2)))
+    d, row = bt.d, rows.stride(0)
+
+    def both(which, name, out, args):
+        got = []
+        for go in (lambda a: getattr(L, name)(*a), lambda a: L.dg_op_packed(which, packed(a))):
+            for o, init in out:
+                o.copy_(init)
+            assert go([a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]) == dgp.DG_OK
+            got.append([o.clone() for o, _ in out])
+        dgp.dg_op_status()
+        for a, b, (o, init) in zip(*got, out):
+            bits = torch.int16 if a.dtype is torch.bfloat16 else a.dtype
+            assert torch.equal(a.view(bits), b.view(bits)) and not torch.equal(a.view(bits), init.view(bits))
+
+    fill = lambda *s, dtype=torch.bfloat16: (torch.empty(*s, dtype=dtype, device=dev()), torch.full(s, 7, dtype=dtype, device=dev()))  # noqa: E731
+    q, k = fill(T, 4, 64), fill(T, 3, 64)
+    both(0, "dg_op_qk_norm_rope", [q, k], [rows, rows[:, 4:], 0, row, row, pos, T, 4, 2, 64, 32, 500.0, gq, gk, 1e-3, q[0], 256, k[0], 192, None])
+    pools = [(p, p.clone()) for p in (bt.k_pool, bt.v_pool)]
+    both(1, "dg_op_rope_kv_append", pools, [rows[:, 4:], rows[:, 7:], row, row, pos, d["prefix_lens"], d["offsets"], d["page_tables"], bt.max_pages, 2,
+                                            T, 2, 64, 48, 700.0, gk, 1e-2, bt.k_pool, bt.v_pool, bt.n_pages, 64, None])
+    o = fill(T, 5, 64)
+    both(2, "dg_op_tree_attention", [o], [rows, row, bt.k_pool, bt.v_pool, d["page_tables"], bt.max_pages, d["prefix_lens"], d["offsets"], mask, 2, 2, T,
+                                          4, 2, 64, 64, bt.n_pages, 0.2, o[0], 320, ws, ws.numel(), None])
+    f = lambda *s: fill(*s, dtype=torch.float32)  # noqa: E731
+    lp, H, lse, ids, top = f(T, 2), f(T), f(T), fill(T, 5, dtype=torch.int32), f(T, 5)
+    both(3, "dg_op_token_logprobs", [lp, H, lse, ids, top], [logits, 0, 603, T, 600, 0.8, tok, 2, lp[0], H[0], lse[0], 5, ids[0], top[0], None])
