@@ -30,10 +30,11 @@
 // without rows (a few drafted tokens fill one) skip the arithmetic.
 //
 // Measured (16 query and 8 KV heads of 128 unless stated): 64 sequences of 24
-// tokens over 16k keys 260 us, 95 % of what their bytes need; 40 ragged sequences
-// of 5 tokens (12 and 4 heads of 64) 25.5 us; one of 61 tokens over 32k 35.6 us, of
-// which the keys' bytes take 20 and the rest is start (3.5), the last tile and the
-// join (8); one token over 2k keys 11.3 us, all of it latency.
+// tokens over 16k keys 261 us, 6.4 TB/s; 40 ragged sequences of 5 tokens (12 and 4
+// heads of 64) 25.4 us; one of 61 tokens over 32k 36 us, of which the keys' stream
+// takes 19, at 7.1 TB/s, and launch (2), start (3.5), the last tile and the join (8)
+// most of the rest; one token over 2k keys 11.3 to 12.1 us (by machine), all of it
+// latency; 16 sequences of one token over 2k 28.8 us.
 // Slower and not kept: the pieces joined over a cluster's shared memory, or by a
 // kernel of their own; rows copied into idle quarters of a tile; no range shorter
 // than 3 tiles (one token over 2k: 0.3 us more); the join's code gone through

@@ -611,7 +611,9 @@ int dg_op_qk_norm_rope(const void *q, const void *k, int32_t in_f32, int64_t q_s
  * A row whose slot lies outside the page table (or whose page outside the
  * pools) is not written and is reported by dg_op_status.  Rows must not go to
  * one slot of one page (a slot that several sequences share holds what either
- * of them left).  Shapes as dg_op_qk_norm_rope; page_size >= 1. */
+ * of them left).  Shapes as dg_op_qk_norm_rope; page_size >= 1.  (The library's
+ * attention reads pools of head_dim 64 and 128 in pages of multiples of 64
+ * slots; other pools are for kernels of the caller's.) */
 int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride, int64_t v_stride,
                          const int32_t *positions, const int32_t *prefix_lens,
                          const int32_t *offsets, const int32_t *page_tables, int32_t max_pages,
@@ -627,7 +629,9 @@ int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride,
  * d (slot prefix_lens[b] + d) that the row sees: bit d % 64 of word
  * tree_mask[row * mask_words + d / 64] (device uint64; bits past mask_words *
  * 64 read as 0), or d <= t where tree_mask is NULL (one new token per
- * sequence: the plain decoding step).  A row that sees no key is zero.
+ * sequence: the plain decoding step).  A row that sees no key is zero.  Scores,
+ * softmax sums and the output's sums are fp32; each p_j is rounded to bf16 for
+ * the product with v_j (the sum of the p_j is not), as in dg_op_canvas_attention.
  *   q, out       device bf16 rows [n_tok][n_q_heads][head_dim]
  * Keys and values of the sequence's own slots must be finite; the pages' other
  * slots may hold anything.  A sequence whose rows lie outside [0, n_tok) or
@@ -640,7 +644,8 @@ int dg_op_rope_kv_append(const uint16_t *k, const uint16_t *v, int64_t k_stride,
  * arbitrary; calls that overlap on the GPU need one each.  The launch is
  * cooperative (its blocks run together and wait, bounded, for one another).
  * After a failure that dg_op_status has told of, a captured call can be replayed
- * with its workspace as it is. */
+ * with its workspace as it is; a launch that was in flight then, and gave up
+ * too, is reported by the next dg_op_status. */
 size_t dg_op_tree_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
                                             int32_t n_kv_heads, int32_t head_dim);
 int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool,
