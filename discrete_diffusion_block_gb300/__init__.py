@@ -173,6 +173,9 @@ _SIGS = {
     "dg_op_rope_kv_append": (_I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _F, _P, _P,
                                   _I, _I, _P]),
     "dg_op_tree_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dg_op_window_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dg_op_window_attention": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _I64,
+                                    _P, _P, _SZ, _P]),
     "dg_op_tree_attention": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                   _I64, _P, _SZ, _P]),
     "dg_op_token_logprobs": (_I, [_P, _I, _I64, _I, _I, _F, _P, _I, _P, _P, _P, _I, _P, _P, _P]),
@@ -618,6 +621,8 @@ _PACK_QK = struct.Struct("=qqqqqqqqqqqdqqdqqqqq").pack
 _PACK_APPEND = struct.Struct("=qqqqqqqqqqqqqqdqdqqqqq").pack
 _PACK_ATTEND = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqq").pack
 _PACK_LOGPROBS = struct.Struct("=qqqqqdqqqqqqqqq").pack
+_PACK_WINDOW = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqqq").pack
+DG_CALL_WINDOW_ATTENTION = 8
 DG_CALL_QK_NORM_ROPE, DG_CALL_ROPE_KV_APPEND, DG_CALL_TREE_ATTENTION, DG_CALL_TOKEN_LOGPROBS = range(4)
 
 
@@ -795,3 +800,44 @@ def dg_op_token_logprobs(logits, tokens, logprobs, entropy=None, lse=None, top_i
         _dense(entropy, "entropy", _F32, T, dev), _dense(lse, "lse", _F32, T, dev), k,
         _dense(top_ids, "top_ids", _I32T, T * k, dev), _dense(top_logprobs, "top_logprobs", _F32, T * k, dev),
         _stream_on(stream, dev)))
+
+
+# ---- bounded caches of long contexts (conventions of the section above) --------
+
+def dg_op_window_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd):
+    return load().dg_op_window_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd)
+
+
+def _batch(q, k_pool, page_tables):
+    """(device, pool's shape, table's shape, q's address and stride) of a call over the paged cache."""
+    dev = _device(k_pool)
+    pool, table, shape = k_pool.shape, page_tables.shape, q.shape
+    if len(pool) != 4 or len(table) != 2 or len(shape) != 3 or shape[2] != pool[3]:
+        _einval("pools are [n_pages][heads][page_size][head_dim], page_tables [sequences][pages], q [rows][heads][head_dim]")
+    one_row = 0 if shape[0] > 1 else shape[1] * shape[2]
+    return (dev, pool, table, *_rows(q, "q", _BF16, shape, one_row, dev))
+
+
+def _scratch(workspace, dev):
+    if workspace is None:
+        return 0, 0
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        _einval("the workspace must be contiguous, on the current CUDA device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def dg_op_window_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets, out, workspace, window=0, sinks=0, lse=None,
+                           scale=None, stream=None):
+    """q, out: [T][Hq][hd] bf16 (rows may be strided); lse fp32 [T][Hq] or None;
+    window 0: all keys; workspace: a contiguous tensor or None; scale None:
+    1 / sqrt(hd); stream None: torch's current one."""
+    dev, (n_pages, hkv, pg, hd), (B, max_pages), qp, qs = _batch(q, k_pool, page_tables)
+    T, hq, _ = shape = q.shape
+    op, os_ = _rows(out, "out", _BF16, shape, 0 if T > 1 else hq * hd, dev)
+    n = n_pages * hkv * pg * hd
+    _call(DG_CALL_WINDOW_ATTENTION, _PACK_WINDOW(
+        qp, qs, _dense(k_pool, "k_pool", _BF16, n, dev), _dense(v_pool, "v_pool", _BF16, n, dev),
+        _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages,
+        _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev), window, sinks, B, T, hq,
+        hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, _dense(lse, "lse", _F32, T * hq, dev),
+        *_scratch(workspace, dev), _stream_on(stream, dev)))

@@ -17,6 +17,7 @@
 // prefix .. prefix + C - 1): attention then treats prefix and canvas keys
 // uniformly, and the KV-append forward overwrites those slots with the
 // clean canvas's K/V.
+#include <algorithm>
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -1663,6 +1664,31 @@ int check_rope(int32_t n_tok, int32_t head_dim, int32_t rope_dim, float rope_bas
   return DG_OK;
 }
 
+// Shapes of the packed rows that attend to paged keys.
+int check_attended(int32_t n_tok, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t page_size, float scale) {
+  if (n_tok < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 128)
+    return fail(DG_EINVAL, "unsupported head counts or row count");
+  if ((int64_t)n_tok * n_q_heads > INT32_MAX - 128) return fail(DG_EINVAL, "too many rows of heads");
+  if (head_dim != 64 && head_dim != 128) return fail(DG_EINVAL, "head_dim must be 64 or 128");
+  if (page_size < 64 || page_size % 64) return fail(DG_EINVAL, "page_size must be a positive multiple of 64");
+  if (!is_factor(scale)) return fail(DG_EINVAL, "scale must be in (0, 2.3e38]");
+  return DG_OK;
+}
+
+// The batch's key tiles, over all tiles of rows, fit the kernels' 32-bit sums.
+int check_span(int32_t max_pages, int32_t page_size, int32_t n_tok, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads) {
+  const int64_t key_tiles = ((int64_t)max_pages * page_size + 127) / 128 + dg::kTreeUnitCost;
+  const int64_t row_tiles = (int64_t)n_tok * (n_q_heads / n_kv_heads) / 128 + n_seqs;
+  if (key_tiles * n_kv_heads > INT32_MAX / 2 / row_tiles) return fail(DG_EINVAL, "the batch's page tables span too many keys");
+  return DG_OK;
+}
+
+int check_workspace(const void *workspace, size_t bytes, size_t need) {
+  if (bytes < need || (need && !workspace)) return fail(DG_EINVAL, "workspace too small (%zu bytes, needs %zu)", bytes, need);
+  if (!aligned16(workspace)) return fail(DG_EINVAL, "the workspace is not 16-byte aligned");
+  return DG_OK;
+}
+
 int check_batch(const int32_t *prefix_lens, const int32_t *offsets, const int32_t *page_tables, int32_t max_pages,
                 int32_t n_seqs, const void *k_pool, const void *v_pool, int32_t n_pages) {
   if (n_seqs < 0 || max_pages < 0) return fail(DG_EINVAL, "negative sequence or page count");
@@ -1739,12 +1765,7 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
                          int32_t n_tok, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t page_size,
                          int32_t n_pages, float scale, uint16_t *out, int64_t out_stride, void *workspace,
                          size_t workspace_bytes, void *stream) {
-  if (n_tok < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 128)
-    return fail(DG_EINVAL, "unsupported head counts or row count");
-  if ((int64_t)n_tok * n_q_heads > INT32_MAX - 128) return fail(DG_EINVAL, "too many rows of heads");
-  if (head_dim != 64 && head_dim != 128) return fail(DG_EINVAL, "head_dim must be 64 or 128");
-  if (page_size < 64 || page_size % 64) return fail(DG_EINVAL, "page_size must be a positive multiple of 64");
-  if (!is_factor(scale)) return fail(DG_EINVAL, "scale must be in (0, 2.3e38]");
+  CKR(check_attended(n_tok, n_q_heads, n_kv_heads, head_dim, page_size, scale));
   if (tree_mask ? mask_words < 1 : mask_words != 0)
     return fail(DG_EINVAL, "mask_words must be at least 1 with a mask, 0 without");
   CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, v_pool, n_pages));
@@ -1752,18 +1773,47 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
   CKR(check_rows("out", out, out_stride, n_tok, n_q_heads, head_dim, 8));
   if (n_tok == 0 || n_seqs == 0) return DG_OK;
   if (q == out) return fail(DG_EINVAL, "out must not be q");
-  const int64_t key_tiles = ((int64_t)max_pages * page_size + 127) / 128 + dg::kTreeUnitCost;
-  const int64_t row_tiles = (int64_t)n_tok * (n_q_heads / n_kv_heads) / 128 + n_seqs;
-  if (key_tiles * n_kv_heads > INT32_MAX / 2 / row_tiles) return fail(DG_EINVAL, "the batch's page tables span too many keys");
+  CKR(check_span(max_pages, page_size, n_tok, n_seqs, n_q_heads, n_kv_heads));
   const size_t need = dg::tree_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);
-  if (workspace_bytes < need || (need && !workspace))
-    return fail(DG_EINVAL, "workspace too small (%zu bytes, needs %zu)", workspace_bytes, need);
-  if (!aligned16(workspace)) return fail(DG_EINVAL, "the workspace is not 16-byte aligned");
+  CKR(check_workspace(workspace, workspace_bytes, need));
   int *status = nullptr;
   CKR(op_status_ptr(&status));
   dg::TreeAttention a{(const bf16 *)q, q_stride, (const bf16 *)k_pool, (const bf16 *)v_pool, page_tables, max_pages,
                       prefix_lens, offsets, (const unsigned long long *)tree_mask, mask_words, n_seqs, n_tok,
                       n_q_heads, n_kv_heads, head_dim, page_size, n_pages, scale, (bf16 *)out, out_stride};
+  CK(dg::tree_attention(a, workspace, status, (cudaStream_t)stream));
+  return DG_OK;
+}
+
+size_t dg_op_window_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                              int32_t head_dim) {
+  return dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);
+}
+
+int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool, const uint16_t *v_pool,
+                           const int32_t *page_tables, int32_t max_pages, const int32_t *prefix_lens,
+                           const int32_t *offsets, int32_t window, int32_t sinks, int32_t n_seqs, int32_t n_tok,
+                           int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int32_t page_size,
+                           int32_t n_pages, float scale, uint16_t *out, int64_t out_stride, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+  CKR(check_attended(n_tok, n_q_heads, n_kv_heads, head_dim, page_size, scale));
+  if (window < 0 || sinks < 0) return fail(DG_EINVAL, "window and sinks must not be negative");
+  CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, v_pool, n_pages));
+  CKR(check_rows("q", q, q_stride, n_tok, n_q_heads, head_dim, 8));
+  CKR(check_rows("out", out, out_stride, n_tok, n_q_heads, head_dim, 8));
+  if ((uintptr_t)lse % 4) return fail(DG_EINVAL, "lse is not aligned to its elements");
+  if (n_tok == 0 || n_seqs == 0) return DG_OK;
+  if (q == out) return fail(DG_EINVAL, "out must not be q");
+  CKR(check_span(max_pages, page_size, n_tok, n_seqs, n_q_heads, n_kv_heads));
+  CKR(check_workspace(workspace, workspace_bytes,
+                      dg_op_window_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim)));
+  int *status = nullptr;
+  CKR(op_status_ptr(&status));
+  // (a window of all keys: no slot is 2^31 - 1 keys behind another)
+  dg::TreeAttention a{(const bf16 *)q, q_stride, (const bf16 *)k_pool, (const bf16 *)v_pool, page_tables, max_pages,
+                      prefix_lens, offsets, nullptr, 0, n_seqs, n_tok, n_q_heads, n_kv_heads, head_dim, page_size,
+                      n_pages, scale, (bf16 *)out, out_stride, window ? window : INT32_MAX,
+                      window ? std::min(sinks, (int32_t)0x7fffff00) : 0, lse};
   CK(dg::tree_attention(a, workspace, status, (cudaStream_t)stream));
   return DG_OK;
 }
@@ -1856,6 +1906,17 @@ extern "C" int dg_op_packed(int32_t call, const void *args) {
         a.ptr<float>(), a.ptr<float>(), a.i32(), a.ptr<int32_t>(), a.ptr<float>(), a.ptr<void>()};
       if (!a.fits) break;
       return dg_op_token_logprobs(c.x, c.bf, c.rs, c.rows, c.v, c.it, c.tok, c.ng, c.lp, c.en, c.lse, c.k, c.ids, c.tlp, c.st);
+    }
+    case DG_CALL_WINDOW_ATTENTION: {
+      struct { const uint16_t *q; int64_t qs; const uint16_t *kp, *vp; const int32_t *tab; int32_t mp; const int32_t *pre, *off;
+               int32_t win, sinks, b, n, hq, hkv, hd, pg, np; float scale; uint16_t *out; int64_t os; float *lse; void *ws; int64_t wn;
+               void *st; }
+      c{a.ptr<const uint16_t>(), a.i64(), a.ptr<const uint16_t>(), a.ptr<const uint16_t>(), a.ptr<const int32_t>(), a.i32(),
+        a.ptr<const int32_t>(), a.ptr<const int32_t>(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(),
+        a.i32(), a.f(), a.ptr<uint16_t>(), a.i64(), a.ptr<float>(), a.ptr<void>(), a.i64(), a.ptr<void>()};
+      if (!a.fits || c.wn < 0) break;
+      return dg_op_window_attention(c.q, c.qs, c.kp, c.vp, c.tab, c.mp, c.pre, c.off, c.win, c.sinks, c.b, c.n, c.hq, c.hkv, c.hd,
+                                    c.pg, c.np, c.scale, c.out, c.os, c.lse, c.ws, (size_t)c.wn, c.st);
     }
     default: return fail(DG_EINVAL, "unknown call %d", call);
   }

@@ -282,6 +282,10 @@ struct TreeAttention {
   float scale;
   bf16 *out;
   long long out_stride;
+  // a sliding window (no mask): a token sees `window` keys up to itself and the
+  // sequence's first `sinks`; 0: as the mask says
+  int window = 0, sinks = 0;
+  float *lse = nullptr;  // [n_tok][Hq] with a window, may be null
 };
 constexpr int kTreeUnitCost = 4;  // cost of starting a unit of rows, in key tiles
 size_t tree_attention_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int hd);

@@ -56,6 +56,7 @@ namespace dg {
 
 namespace {
 
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kTreeThreads = 384;
 constexpr int kTreePvWarp = 11;
 constexpr int kTreeCtas = 152;      // most blocks: one per SM
@@ -113,6 +114,32 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &p, int b) {
   return s;
 }
 
+// The key tiles of a row tile (tokens t0 .. t1 - 1 of its sequence): without a
+// window all of the sequence's; with one those of the first tokens that stay
+// visible, then those between the first token's window and the last token.
+struct Keys {
+  int sink, first, count;  // tile i is key tile i for i < sink, else i - sink + first
+  int low, at, end;        // the first token lies at slot `at`, its window begins at slot low; keys end before slot `end`
+};
+template <bool WIN>
+__device__ __forceinline__ Keys unit_keys(const TreeArgs &p, const Seq &s, int rt) {
+  Keys k;
+  if constexpr (!WIN) {
+    k.sink = k.first = k.low = k.at = 0;
+    k.count = s.key_tiles;
+    k.end = s.pre + s.n;
+  } else {
+    const int t0 = 128 * rt / p.G, t1 = min(s.n, ceil_div(128 * (rt + 1), p.G));
+    k.at = s.pre + t0;
+    k.low = max(0, k.at - p.a.window + 1);
+    k.end = s.pre + t1;
+    k.first = k.low >> 7;
+    k.sink = min((p.a.sinks + 127) >> 7, k.first);
+    k.count = k.sink + ((k.end + 127) >> 7) - k.first;
+  }
+  return k;
+}
+
 // The cost of a unit in key tiles, for the equal ranges: its tiles, and
 // kTreeUnitCost more for starting it (rows staged, the first tile's way through
 // all stages, sums written out and joined).  A range's tiles are those of its
@@ -123,18 +150,39 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &p, int b) {
 
 // Its units, and the cost of them all; the host has checked that a batch's sum fits 31 bits.
 __device__ __forceinline__ int seq_units(const TreeArgs &p, const Seq &s) { return s.n ? p.a.Hkv * s.row_tiles : 0; }
+template <bool WIN>
+__device__ __forceinline__ int head_cost(const TreeArgs &p, const Seq &s) {  // of one KV head
+  if constexpr (!WIN) return s.row_tiles * (s.key_tiles + kTreeUnitCost);
+  int sum = 0;
+#pragma unroll 1
+  for (int rt = 0; rt < s.row_tiles; ++rt) sum += unit_keys<WIN>(p, s, rt).count + kTreeUnitCost;
+  return sum;
+}
+template <bool WIN>
 __device__ __forceinline__ int seq_cost(const TreeArgs &p, const Seq &s) {
-  return s.n ? p.a.Hkv * s.row_tiles * (s.key_tiles + kTreeUnitCost) : 0;
+  return s.n ? p.a.Hkv * head_cost<WIN>(p, s) : 0;
+}
+// The most key tiles that a unit of the sequence has (with a window: no fewer).
+template <bool WIN>
+__device__ __forceinline__ int seq_longest(const TreeArgs &p, const Seq &s) {
+  if (!WIN || s.n == 0) return s.key_tiles;
+  if (s.row_tiles == 1) return unit_keys<WIN>(p, s, 0).count;
+  return (int)min((long long)s.key_tiles, ((long long)p.a.window + p.a.sinks + 127 / p.G + 1 + 2 * 127 + 127) >> 7);
 }
 
 // The pieces of a block's range: the key tiles [kt0, kt1) of unit (b, g, rt).
 // at: where the unit begins, relative to the range; left: what the range holds
 // behind the piece's end.
+template <bool WIN>
 struct Walk {
   Seq s;
+  Keys keys;
   int b, g, rt, kt0, kt1, at, left;
+  __device__ __forceinline__ int key_tile(int kt) const { return !WIN || kt < keys.sink ? kt : kt - keys.sink + keys.first; }
+  __device__ __forceinline__ int tiles() const { return WIN ? keys.count : s.key_tiles; }
+  __device__ __forceinline__ int end() const { return WIN ? keys.end : s.pre + s.n; }
   __device__ __forceinline__ void clip(int from, int n) {  // cost units [from, from + n) of the unit
-    const int end = min(s.key_tiles + kTreeUnitCost, from + n);
+    const int end = min(tiles() + kTreeUnitCost, from + n);
     kt0 = max(0, from - kTreeUnitCost);
     kt1 = max(0, end - kTreeUnitCost);
     left = n - (end - from);
@@ -149,9 +197,10 @@ struct Walk {
       g = u / s.row_tiles;
       rt = u - g * s.row_tiles;
     }
-    const int each = ceil_div(s.key_tiles, k);
+    keys = unit_keys<WIN>(p, s, rt);
+    const int each = ceil_div(tiles(), k);
     kt0 = part * each;
-    kt1 = min(s.key_tiles, kt0 + each);
+    kt1 = min(tiles(), kt0 + each);
     at = left = 0;
     return kt0 < kt1;
   }
@@ -159,17 +208,31 @@ struct Walk {
   __device__ __forceinline__ bool begin(const TreeArgs &p, int b_, int from, int n) {
     b = b_;
     s = load_seq(p, b);
-    const int cost = s.key_tiles + kTreeUnitCost, u = from / cost;
-    g = u / s.row_tiles;
-    rt = u - g * s.row_tiles;
-    at = u * cost - from;
+    if (!WIN || s.row_tiles == 1) {
+      keys = unit_keys<WIN>(p, s, 0);
+      const int cost = tiles() + kTreeUnitCost, u = from / cost;
+      g = u / s.row_tiles;
+      rt = u - g * s.row_tiles;
+      at = u * cost - from;
+    } else {  // (the last unit ends behind `from`)
+      const int head = head_cost<WIN>(p, s);
+      g = from / head;
+      at = g * head - from;
+      rt = 0;
+      keys = unit_keys<WIN>(p, s, 0);
+#pragma unroll 1
+      while (at + keys.count + kTreeUnitCost <= 0) {
+        at += keys.count + kTreeUnitCost;
+        keys = unit_keys<WIN>(p, s, ++rt);
+      }
+    }
     clip(-at, n);
     return kt0 < kt1 || next(p);
   }
   __device__ __forceinline__ bool next(const TreeArgs &p) {
     do {
       if (left <= 0) return false;
-      at += s.key_tiles + kTreeUnitCost;
+      at += tiles() + kTreeUnitCost;
       if (++rt == s.row_tiles) {
         rt = 0;
         if (++g == p.a.Hkv) {
@@ -180,6 +243,7 @@ struct Walk {
           } while (s.n == 0);
         }
       }
+      keys = unit_keys<WIN>(p, s, rt);
       clip(0, left);
     } while (kt0 == kt1);
     return true;
@@ -207,6 +271,7 @@ constexpr float kWholeTiles = 4;  // key tiles of a unit that is not worth split
 struct Range {
   int b, at, count, per, k, unit, part;
 };
+template <bool WIN>
 __device__ __forceinline__ Range block_range(const TreeArgs &p, int lane) {
   const int run = ceil_div(p.a.n_seqs, 32), lo = min(p.a.n_seqs, lane * run), hi = min(p.a.n_seqs, lo + run);
   constexpr int kMost = 1 << 30;  // more than an ascending batch's sum: offsets that overlap stop here
@@ -214,9 +279,9 @@ __device__ __forceinline__ Range block_range(const TreeArgs &p, int lane) {
 #pragma unroll 4
   for (int b = lo; b < hi; ++b) {
     const Seq s = load_seq(p, b);
-    mine = (int)min((unsigned)mine + (unsigned)seq_cost(p, s), (unsigned)kMost);
+    mine = (int)min((unsigned)mine + (unsigned)seq_cost<WIN>(p, s), (unsigned)kMost);
     units = min(units + min(seq_units(p, s), kTreeCtas + 1), kTreeCtas + 1);
-    longest = max(longest, s.key_tiles);
+    longest = max(longest, seq_longest<WIN>(p, s));
     if (s.bad && blockIdx.x == 0 && threadIdx.x < 32 && p.err) atomicExch(p.err + 1, kBadSequence);
   }
   Range r;
@@ -259,7 +324,7 @@ __device__ __forceinline__ Range block_range(const TreeArgs &p, int lane) {
   if (here) {
     for (int b = lo; b < hi; ++b) {
       const Seq s = load_seq(p, b);
-      const int n = r.k ? seq_units(p, s) : seq_cost(p, s);
+      const int n = r.k ? seq_units(p, s) : seq_cost<WIN>(p, s);
       if (start < at + n) {
         r.b = b;
         r.at = start - at;
@@ -286,6 +351,15 @@ __device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, int *err
 __device__ __forceinline__ void warp_wait(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
   tree_wait(b, parity, err, code, abort);
   __syncwarp();
+}
+
+// The 64 keys from slot key0 on that a row at slot `at` sees through its window.
+__device__ __forceinline__ unsigned long long window_bits(const TreeArgs &p, int at, int key0) {
+  const int up = at + 1 - key0, low = max(0, at - p.a.window + 1) - key0, sink = p.a.sinks - key0;
+  if (up <= 0) return 0ull;
+  unsigned long long v = low <= 0 ? ~0ull : low >= 64 ? 0ull : ~0ull << low;
+  if (sink > 0) v |= sink >= 64 ? ~0ull : (1ull << sink) - 1;
+  return up >= 64 ? v : v & ((1ull << up) - 1);
 }
 
 // 64 mask bits of a row from drafted key d0 on (d0 may be negative: prefix
@@ -333,16 +407,17 @@ struct Span {
   __device__ __forceinline__ int slot(int s) const { return s == 0 ? first_slot : 2 * (first + s); }
 };
 // The span of the walk's unit in the block's range.
-__device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk &w, const Range &r) {
+template <bool WIN>
+__device__ __forceinline__ Span unit_span(const TreeArgs &p, const Walk<WIN> &w, const Range &r) {
   Span u;
   if (r.k) {
     u.first = r.unit * r.k;
-    u.last = u.first + (w.s.key_tiles - 1) / ceil_div(w.s.key_tiles, r.k);
+    u.last = u.first + (w.tiles() - 1) / ceil_div(w.tiles(), r.k);
     u.first_slot = 2 * u.first;
   } else {
     const int begin = r.per * (int)blockIdx.x + w.at, tiles = begin + kTreeUnitCost;
     u.first = tiles / r.per;
-    u.last = (tiles + w.s.key_tiles - 1) / r.per;
+    u.last = (tiles + w.tiles() - 1) / r.per;
     u.first_slot = 2 * u.first + (begin > u.first * r.per ? 1 : 0);  // a piece of the unit before comes first there
   }
   u.row0 = w.s.row0;
@@ -410,6 +485,12 @@ __device__ __forceinline__ void store_row4(const TreeArgs &p, const Span &u, int
       make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
 }
 
+// The log-sum-exp of row i: l the sum of 2^(score - m).
+__device__ __forceinline__ void store_lse(const TreeArgs &p, const Span &u, int i, float m, float l) {
+  const int rg = u.r0 + i, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
+  p.a.lse[(size_t)(u.row0 + t) * p.a.Hq + h] = fmaf(m, kLn2, logf(l));
+}
+
 // This block's share of a unit's rows, out of the pieces of all its blocks:
 // weights 2^(m_s - m*), pieces in the order of the keys.  Run by 2^lt of the
 // softmax threads (tid of them; 256 for more than kFewPieces) after the block's
@@ -418,7 +499,7 @@ __device__ __forceinline__ void store_row4(const TreeArgs &p, const Span &u, int
 // Latency bound, and run once a launch: what is loaded is loaded together, and
 // the code is kept short (straight-line variants for each shape spent more time
 // on fetching instructions).
-template <int HD>
+template <int HD, bool WIN>
 __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, JoinSmem *scratch, int tid, int lt,
                                           unsigned long long up, volatile int *abort) {
   constexpr int C = HD / 4, LC = HD == 128 ? 5 : 4;  // float4 columns of a row
@@ -473,6 +554,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, Join
         }
         if (s == (1 << lb) - 1) {
           if (i < rows) store_row4(p, u, i0 + i, HD, col, acc, L > 0.0f ? 1.0f / L : 0.0f);
+          if (WIN && i < rows && col == 0 && p.a.lse) store_lse(p, u, i0 + i, mx[k], L);
           acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           L = 0.0f;
         }
@@ -517,6 +599,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, Join
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+      if (WIN && ready && lane == 0 && p.a.lse) store_lse(p, u, i0 + q, mx, L);
       const float inv = L > 0.0f ? 1.0f / L : 0.0f;
 #pragma unroll 1
       for (int s = lane; s < n; s += 32) st[q * n + s].x *= inv;
@@ -563,7 +646,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs &p, const Span &u, Join
   }
 }
 
-template <int HD>
+template <int HD, bool WIN>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid_constant__ TreeArgs p) {
   using S = TreeSmem<HD>;
   constexpr int HB = S::HB, KR = S::KR;
@@ -609,8 +692,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
-  const Range range = block_range(p, lane);  // the same in every warp
-  Walk w;
+  const Range range = block_range<WIN>(p, lane);  // the same in every warp
+  Walk<WIN> w;
   if (range.count <= 0 || !(range.k ? w.begin_part(p, range.b, range.at, range.part, range.k)
                                     : w.begin(p, range.b, range.at, range.count)))
     return;
@@ -651,9 +734,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     // Of a run of up to 16 tiles each lane holds one 64-key half: its logical
     // page, -1 past the last key.  The next run's entries of the page table (and
     // the next unit's lengths) are loaded while this one's tiles are copied.
-    auto pages_of = [&](const Walk &u, int kt) {
-      const int key = 128 * kt + 64 * lane;
-      return kt + (lane >> 1) < u.kt1 && key < u.s.pre + u.s.n
+    auto half_key = [&](const Walk<WIN> &u, int kt) {
+      return WIN ? 128 * u.key_tile(kt + (lane >> 1)) + 64 * (lane & 1) : 128 * kt + 64 * lane;
+    };
+    auto pages_of = [&](const Walk<WIN> &u, int kt) {
+      const int key = half_key(u, kt);
+      // (halves that no row sees are not read, nor their entries of the table)
+      return kt + (lane >> 1) < u.kt1 && key < u.end() && (!WIN || key + 64 > u.keys.low || key < p.a.sinks)
                  ? p.a.page_tables[(size_t)u.b * p.a.max_pages + key / p.a.pg] : INT_MIN;
     };
     int kt = w.kt0, page = pages_of(w, kt);
@@ -661,14 +748,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     do {
       // Where the half's rows are and how many are copied (the rest of it becomes
       // zero).  K: the page's slots past the last key too (their scores are
-      // masked); V: the sequence's own rows only (0 times anything must be 0).
-      const int n = min(16, w.kt1 - kt), key = 128 * kt + 64 * lane;
+      // masked); V: the sequence's own rows only (0 times anything must be 0), with a
+      // window those up to row `sink` and from row `low` on.
+      const int n = min(16, w.kt1 - kt), key = half_key(w, kt);
       const bool off = page != INT_MIN && (page < 0 || page >= p.a.n_pages);
-      const int rows = page == INT_MIN || off ? 0 : is_k ? 64 : min(64, w.s.pre + w.s.n - key);
+      const int rows = page == INT_MIN || off ? 0 : is_k ? 64 : min(64, w.end() - key);
+      int sink = 0, low = 0;
+      if (WIN && !is_k) {
+        sink = min(max(p.a.sinks - key, 0), rows);
+        low = max(sink, min(max(w.keys.low - key, 0), rows));
+      }
       const bf16 *src = rows ? pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key % p.a.pg) * 64 : pool;
       if (off && p.err) atomicExch(p.err + 1, kBadPage);
       const unsigned bad = __ballot_sync(0xffffffffu, off);  // lanes whose page is outside the pools
-      Walk nw = w;
+      Walk<WIN> nw = w;
       int next_page = 0;
       for (int j = 0; ok && j < n; ++j) {
         if (lane == 0) {
@@ -685,7 +778,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
             unsigned char *d = ring + (size_t)slot * S::tile + (lane & 1) * kAttnSlotHalfBytes;
 #pragma unroll
             for (int b = 0; b < HB; ++b) {
-              if (rows > 0) tc::bulk_load(d + (size_t)b * 16384, src + (size_t)b * p.a.pg * 64, 128u * rows, full + slot);
+              unsigned char *db = d + (size_t)b * 16384;
+              const bf16 *sb = src + (size_t)b * p.a.pg * 64;
+              if (WIN && low > sink) {
+                if (sink > 0) tc::bulk_load(db, sb, 128u * sink, full + slot);
+                tc::bulk_load(db + 128 * sink, g_zero_half, 128u * (low - sink), full + slot);
+                if (rows > low) tc::bulk_load(db + 128 * low, sb + 64 * low, 128u * (rows - low), full + slot);
+              } else if (rows > 0) {
+                tc::bulk_load(db, sb, 128u * rows, full + slot);
+              }
               if (rows < 64) tc::bulk_load(d + (size_t)b * 16384 + 128 * rows, g_zero_half, 128u * (64 - rows), full + slot);
             }
           }
@@ -793,7 +894,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       asm volatile("bar.sync %0, 64;\n" ::"r"(1 + q4) : "memory");
     };
     // The piece's query rows into the operand tile (row r: token r / G, head g G + r % G).
-    auto stage_q = [&](const Walk &u) {
+    auto stage_q = [&](const Walk<WIN> &u) {
       const int rows = min(128, u.s.n * p.G - 128 * u.rt);
       constexpr int kN = 128 * (HD / 8) / 256;  // chunks of a thread in a full tile
       const int c = tid & (HD / 8 - 1);
@@ -815,7 +916,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       __syncwarp();
     };
     // A line of 128 bytes a thread: all of a tile's rows (two lines of HD = 128).
-    auto request_q = [&](const Walk &u) {
+    auto request_q = [&](const Walk<WIN> &u) {
       const int rows = min(128, u.s.n * p.G - 128 * u.rt), r = tid / HB;
       if (r < rows) {
         const int rg = 128 * u.rt + r, t = rg / p.G, h = u.g * p.G + rg - t * p.G;
@@ -846,7 +947,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       float m = NEG, l = 0.0f;  // l: this half's share of the row sum
       // the next piece, found while this one's first keys are on their way, and
       // its rows requested: staging them later must not wait for memory
-      Walk nx = w;
+      Walk<WIN> nx = w;
       const bool more = nx.next(p);  // the same in all softmax warps (never cut short: they meet at named barriers)
       if (more) request_q(nx);
       for (int kt = w.kt0; kt < w.kt1; ++kt, ++i) {
@@ -861,7 +962,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           continue;
         }
         tc::fence_after();
-        const int key_base = 128 * kt + 64 * half;
+        const int key_base = 128 * w.key_tile(kt) + 64 * half;
         uint32_t x[2][32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) tc::tmem_ld32(t_s + buf * 128 + lane_off + 64 * half + 32 * c, x[c]);
@@ -872,8 +973,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         __syncwarp();
         if (lane == 0) attn_arrive(s_empty + buf);
         // keys the row must not see are -inf: only where drafted keys begin, or a page was bad
-        if (key_base + 64 > w.s.pre || bad) {
-          unsigned long long see = (bad >> half) & 1 ? 0ull : row_bits(p, w.s, t, key_base - w.s.pre);
+        // (with a window: where keys are behind the first row's, or before the last row's window)
+        const bool some = WIN ? key_base + 64 > w.keys.at + 1 ||
+                                    (key_base < w.keys.end - p.a.window && key_base + 64 > p.a.sinks)
+                              : key_base + 64 > w.s.pre;
+        if (some || bad) {
+          unsigned long long see = (bad >> half) & 1 ? 0ull
+                                   : WIN             ? window_bits(p, w.s.pre + t, key_base)
+                                                     : row_bits(p, w.s, t, key_base - w.s.pre);
           if (row >= rows) see = 0ull;
           const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
@@ -951,7 +1058,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         stage_q(nx);
         if (lane == 0) attn_arrive(q_full);
       }
-      const bool full_unit = w.kt0 == 0 && w.kt1 == w.s.key_tiles;
+      const bool full_unit = w.kt0 == 0 && w.kt1 == w.tiles();
       const int slot = 2 * blockIdx.x + (piece ? 1 : 0);
       warp_wait(o_full, piece & 1, p.err, 62, abort);  // inactive warps too: o_empty counts one arrival of each a piece
       if (active) {  // the row sum of both halves
@@ -988,6 +1095,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
           }
         }
         // (a row whose sum is NaN: its weight in the join is inf - inf, so the row is NaN)
+        if (WIN && full_unit && half == 0 && row < rows && p.a.lse)
+          p.a.lse[(size_t)(w.s.row0 + t) * p.a.Hq + h] = fmaf(m, kLn2, logf(lt));
         if (!full_unit && half == 0 && row < rows) p.state[(size_t)slot * 128 + row] = make_float2(lt == lt ? m : -NEG, lt);
         tc::fence_before();
       }
@@ -997,7 +1106,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
         // At the end, once (a fence in mid-stream waits for every store and load
         // in flight, and the rings run dry): the flags of the first and the last
         // piece, then this block's shares of the units they belong to.
-        const bool join_tail = w.kt1 < w.s.key_tiles && (piece || !join_head);
+        const bool join_tail = w.kt1 < w.tiles() && (piece || !join_head);
         const Span tail = unit_span(p, w, share->range);
         if (join_head || join_tail) {
           // counted from here by those who see the flag
@@ -1018,7 +1127,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll 1
         for (int k = join_head ? 0 : 1; k < (join_tail ? 2 : 1); ++k) {
           if (both && k != tid >> 7) continue;
-          join_unit<HD>(p, k ? tail : head, (JoinSmem *)(base + S::kring), both ? tid & 127 : tid, both ? 7 : 8, share->up, abort);
+          join_unit<HD, WIN>(p, k ? tail : head, (JoinSmem *)(base + S::kring), both ? tid & 127 : tid, both ? 7 : 8, share->up, abort);
         }
       }
       if (!more) break;
@@ -1063,7 +1172,7 @@ unsigned long long new_ticket() {
 
 // Blocks of a launch on the current device (all of them run together), asked
 // once; 0: the kernel does not run there.
-template <int HD>
+template <int HD, bool WIN>
 cudaError_t tree_ctas(int *out) {
   static int ctas[64];
   static std::mutex mu;
@@ -1076,9 +1185,9 @@ cudaError_t tree_ctas(int *out) {
   std::lock_guard<std::mutex> lock(mu);
   if (!ctas[dev]) {
     int sms = 0, per_sm = 0;
-    e = cudaFuncSetAttribute(tree_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes);
+    e = cudaFuncSetAttribute(tree_attn_kernel<HD, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::bytes);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, tree_attn_kernel<HD>, kTreeThreads, S::bytes);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, tree_attn_kernel<HD, WIN>, kTreeThreads, S::bytes);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorLaunchOutOfResources;
     ctas[dev] = sms < kTreeCtas ? sms : kTreeCtas;
@@ -1087,9 +1196,9 @@ cudaError_t tree_ctas(int *out) {
   return cudaSuccess;
 }
 
-template <int HD>
+template <int HD, bool WIN>
 cudaError_t launch_tree(TreeArgs &p, cudaStream_t st) {
-  const cudaError_t e = tree_ctas<HD>(&p.ctas);
+  const cudaError_t e = tree_ctas<HD, WIN>(&p.ctas);
   if (e != cudaSuccess) return e;
   p.inv_ctas = 1.0f / (float)p.ctas;
   // (no use asking where the rows in full tiles are more units than blocks)
@@ -1104,7 +1213,7 @@ cudaError_t launch_tree(TreeArgs &p, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_attn_kernel<HD>, p);
+  return cudaLaunchKernelEx(&cfg, tree_attn_kernel<HD, WIN>, p);
 }
 
 }  // namespace
@@ -1124,7 +1233,8 @@ cudaError_t tree_attention(const TreeAttention &a, void *ws, int *err, cudaStrea
   p.joined = (int *)((unsigned char *)ws + w.joined);
   p.ticket = new_ticket();
   p.err = err;
-  return a.hd == 128 ? launch_tree<128>(p, st) : launch_tree<64>(p, st);
+  if (a.window) return a.hd == 128 ? launch_tree<128, true>(p, st) : launch_tree<64, true>(p, st);
+  return a.hd == 128 ? launch_tree<128, false>(p, st) : launch_tree<64, false>(p, st);
 }
 
 }  // namespace dg

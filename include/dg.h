@@ -679,7 +679,38 @@ int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_st
                          float *logprobs, float *entropy, float *lse, int32_t top_k,
                          int32_t *top_ids, float *top_logprobs, void *stream);
 
-/* The four calls above with their arguments packed into one block, for bindings
+/* ---- bounded caches of long contexts ---------------------------------------
+ * Three calls for contexts that outgrow the cache a server wants to hold, over
+ * the packed rows and pages of the section above (and beside its calls: norms
+ * and rotation, append): new tokens attend to a sliding window and to the
+ * sequence's first tokens, the attention weight that each cached key gathers is
+ * summed up, and the keys that gathered least are evicted.  No counterpart in
+ * the report, whose prefix only grows.
+ *
+ * Attention of new tokens (a chunk of a prompt, or one token per sequence) over
+ * the paged cache, their own keys and values already appended: row
+ * offsets[b] + t lies at slot s = prefix_lens[b] + t of its sequence and sees
+ * the slots j <= s with j > s - window (itself and the window - 1 before it) or
+ * j < sinks; window 0: all of them (sinks are then unused).  For query head h
+ * (KV head h / (Hq / Hkv))
+ *   out = sum_j p_j v_j,  p = softmax_j(x_j),  x_j = scale q . k_j,
+ *   lse [n_tok][n_q_heads] = log sum_j e^{x_j}   (device fp32, may be NULL).
+ * Roundings as in dg_op_tree_attention, whose conditions hold too: rows, pages,
+ * bad sequences and pages, shapes, scale, workspace, cooperative launch; out must
+ * not be q.  Keys and values that a row of the sequence sees must be finite; all
+ * else may hold anything: pages of which no row of the sequence sees a slot are not
+ * read, nor their entries of the table (they may have been given back). */
+size_t dg_op_window_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
+                                              int32_t n_kv_heads, int32_t head_dim);
+int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool,
+                           const uint16_t *v_pool, const int32_t *page_tables, int32_t max_pages,
+                           const int32_t *prefix_lens, const int32_t *offsets, int32_t window,
+                           int32_t sinks, int32_t n_seqs, int32_t n_tok, int32_t n_q_heads,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages,
+                           float scale, uint16_t *out, int64_t out_stride, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* The calls of the two sections above with their arguments packed into one block, for bindings
  * in which marshalling some twenty arguments one by one takes longer than the
  * launch: args holds the call's parameters in order, 8 bytes each, integers and
  * pointers as int64, floats as double (host memory, read during the call).
@@ -687,7 +718,7 @@ int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_st
  * does not fit its parameter. */
 enum {
     DG_CALL_QK_NORM_ROPE = 0, DG_CALL_ROPE_KV_APPEND = 1, DG_CALL_TREE_ATTENTION = 2,
-    DG_CALL_TOKEN_LOGPROBS = 3
+    DG_CALL_TOKEN_LOGPROBS = 3, DG_CALL_WINDOW_ATTENTION = 8
 };
 int dg_op_packed(int32_t call, const void *args);
 

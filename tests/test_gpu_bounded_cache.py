@@ -1,0 +1,254 @@
+"""The operators that bound a long context's cache (windowed attention with
+first tokens that stay visible, attention weight per cached key, eviction)
+against plain numpy evaluations in 64 bits.
+
+Tolerances: those of the draft-serving tests for bf16 outputs; each check of an
+fp32 result states the roundings it counts.
+"""
+import numpy as np
+import pytest
+import torch
+
+import discrete_diffusion_block_gb300 as dgp
+from gpu_util import dev
+from test_gpu_draft_ops import U32, Batch, _clean_status, _lib, attention_tol, f64, i32, randn  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+HEADS = [(16, 8, 128), (4, 2, 64), (12, 4, 64), (8, 1, 128), (5, 5, 64), (7, 1, 64)]
+
+
+# ---- references -------------------------------------------------------------------
+
+def visible(p, n, window, sinks):
+    """[n][p + n]: the key slots that new token t, at slot p + t, sees."""
+    s, j = p + np.arange(n)[:, None], np.arange(p + n)[None]
+    return (j <= s) & ((j > s - window) | (j < sinks)) if window else j <= s
+
+
+def place(pool, table, slots, x):
+    """x [n][heads][hd] into the given slots of a sequence (16-byte chunk c of a slot's 64-wide sub-block at c ^ (slot % 8))."""
+    hkv, pg, hd = pool.shape[1:]
+    page, slot = torch.from_numpy(table[slots // pg]).long()[:, None], torch.from_numpy(slots % pg).long()[:, None]
+    at = torch.arange(8)[None] ^ (slot % 8)
+    pool.view(-1, hkv, hd // 64, pg, 8, 8)[page, :, :, slot, at] = x.view(-1, hkv, hd // 64, 8, 8).permute(0, 3, 1, 2, 4)
+
+
+def hide(bt, window, sinks, first=0):
+    """NaN into the keys and values that no new token from `first` on sees; pages
+    that hold no other ones leave the table."""
+    pools = [bt.k_pool.cpu(), bt.v_pool.cpu()]
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        if n == 0:
+            continue
+        seen = visible(p, n, window, sinks)[first:].any(0)
+        gone = np.nonzero(~seen)[0]
+        for pool in pools:
+            place(pool, bt.table[b], gone, torch.full((len(gone), bt.hkv, bt.hd), float("nan"), dtype=torch.bfloat16))
+        for j in range(-(-(p + n) // bt.pg)):
+            if not seen[j * bt.pg:(j + 1) * bt.pg].any():
+                bt.table[b, j] = -9
+    for mine, pool in zip((bt.k_pool, bt.v_pool), pools):
+        mine.copy_(pool)
+    bt.d["page_tables"].copy_(i32(bt.table))
+
+
+def window_ref(q, bt, window, sinks, scale):
+    """out, sum_j p_j |v_j|, lse and the largest sum of |products| of a score, in 64 bits."""
+    hq = q.shape[1]
+    G = hq // bt.hkv
+    out, mag, lse, top = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:2]), np.zeros(q.shape[:2])
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        see = visible(p, n, window, sinks)
+        for t0 in range(0, n, 64):
+            t1 = min(n, t0 + 64)
+            j = np.nonzero(see[t0:t1].any(0))[0]
+            rows = slice(bt.off[b] + t0, bt.off[b] + t1)
+            for h in range(hq):
+                k, v, x = bt.keys[b][j, h // G], bt.vals[b][j, h // G], q[rows, h]
+                s = np.where(see[t0:t1][:, j], x @ k.T * scale, -np.inf)
+                m = s.max(1, keepdims=True)
+                e = np.exp(s - m)
+                lse[rows, h] = m[:, 0] + np.log(e.sum(1))
+                e /= e.sum(1, keepdims=True)
+                out[rows, h], mag[rows, h] = e @ v, e @ np.abs(v)
+                top[rows, h] = (np.where(see[t0:t1][:, j], np.abs(x) @ np.abs(k).T * scale, 0)).max(1)
+    return out, mag, lse, top
+
+
+def lse_tol(lse, top, hd, tiles):
+    # scores: hd products and their sum, scaled; the sum over keys (64 of a tile's half in a
+    # chain, then tile by tile and piece by piece) of exponentials within 4 ulp; the logarithm
+    return U32 * ((hd + 8) * top + 8 * np.abs(lse) + 64 + tiles + 32)
+
+
+# ---- windowed attention ------------------------------------------------------------------
+
+def window_workspace(T, B, hq, hkv, hd, fill=0xFF):
+    n = dgp.dg_op_window_attention_workspace_bytes(T, B, hq, hkv, hd)
+    return torch.full((max(n, 1),), fill, dtype=torch.uint8, device=dev())
+
+
+def run_window(bt, q, window, sinks, out, lse=None, scale=None, stream=None, workspace=None):
+    ws = window_workspace(q.shape[0], len(bt.pre), q.shape[1], bt.hkv, bt.hd) if workspace is None else workspace
+    dgp.dg_op_window_attention(q, bt.k_pool, bt.v_pool, **bt.d, out=out, workspace=ws, window=window, sinks=sinks, lse=lse, scale=scale,
+                               stream=stream)
+
+
+def check_window(bt, hq, window, sinks, rng, scale=None, strided=False, hidden=True):
+    if strided:
+        q = randn(rng, bt.T, hq + 3, bt.hd).to(dev())[:, 1:1 + hq]
+        out = torch.full((bt.T, 2 * hq, bt.hd), 7.0, dtype=torch.bfloat16, device=dev())[:, hq:]
+    else:
+        q = randn(rng, bt.T, hq, bt.hd).to(dev())
+        out = torch.full((bt.T, hq, bt.hd), 7.0, dtype=torch.bfloat16, device=dev())
+    lse = torch.full((bt.T, hq), 7.0, device=dev())
+    if hidden and window:
+        hide(bt, window, sinks)
+    run_window(bt, q, window, sinks, out, lse, scale)
+    dgp.dg_op_status()
+    ref, mag, z, top = window_ref(f64(q), bt, window, sinks, bt.hd ** -0.5 if scale is None else scale)
+    n = int(bt.off[-1])
+    got, got_z = f64(out), f64(lse)
+    assert (np.abs(got[:n] - ref[:n]) <= attention_tol(ref[:n], mag[:n])).all(), np.abs(got[:n] - ref[:n]).max()
+    tiles = max((p + m for p, m in zip(bt.pre, bt.new)), default=0) / 128 + 2
+    assert (np.abs(got_z[:n] - z[:n]) <= lse_tol(z[:n], top[:n], bt.hd, tiles)).all(), np.abs(got_z[:n] - z[:n]).max()
+    assert (got[n:] == 7.0).all() and (got_z[n:] == 7.0).all()           # rows behind the last sequence
+    return q, out, lse
+
+
+@pytest.mark.parametrize("hq,hkv,hd", HEADS)
+@pytest.mark.parametrize("pre,window,sinks,pg", [
+    (0, 1, 0, 128), (1, 1, 1, 64), (63, 64, 0, 64), (64, 64, 4, 128), (127, 128, 0, 192), (128, 127, 4, 128), (129, 300, 1, 64),
+    (700, 1, 0, 64), (700, 64, 64, 128), (701, 65, 63, 128), (1000, 200, 65, 64), (1000, 200, 130, 192), (1000, 128, 2000, 128),
+    (1999, 0, 0, 128), (1999, 2 ** 31 - 1, 2 ** 31 - 1, 128),
+])
+def test_window_of_single_tokens(hq, hkv, hd, pre, window, sinks, pg):
+    rng = np.random.default_rng(pre + window % 1000)
+    check_window(Batch(rng, [pre], [1], hkv, hd, pg), hq, window, sinks, rng)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,pg,pre,new", [
+    (16, 8, 128, 128, [300], [17]),
+    (16, 8, 128, 128, [0, 2000, 130], [64, 3, 0]),
+    (12, 4, 64, 64, [100, 0, 5, 640, 0], [5, 1, 0, 133, 2]),
+    (16, 4, 128, 192, [190, 191], [63, 66]),
+    (32, 1, 64, 64, [70], [90]),
+    (6, 2, 64, 128, [0], [500]),
+    (16, 8, 128, 128, [0], [700]),
+    (7, 1, 128, 64, [11] * 40, [j % 5 for j in range(40)]),
+    (4, 2, 64, 64, [j * 7 for j in range(200)], [1] * 200),
+    (128, 1, 64, 64, [20, 64], [30, 1]),
+    (3, 1, 64, 64, [1000, 3], [333, 257]),
+])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 3), (64, 4), (100, 0), (129, 130), (333, 70)])
+def test_window_of_batches(hq, hkv, hd, pg, pre, new, window, sinks):
+    rng = np.random.default_rng(len(pre) + hq)
+    bt = Batch(rng, pre, new, hkv, hd, pg)
+    check_window(bt, hq, window, sinks, rng, strided=window % 2 == 1)
+
+
+@pytest.mark.parametrize("pre,new,window,sinks", [([20011], [2], 5000, 4), ([20011], [2], 0, 0), ([9000, 4], [1, 1], 8000, 200)])
+def test_window_over_a_long_context_with_a_scale(pre, new, window, sinks):
+    rng = np.random.default_rng(11)
+    check_window(Batch(rng, pre, new, 2, 128, 128), 4, window, sinks, rng, scale=0.3)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,pre,new,window", [
+    (16, 8, 128, [3000, 10, 777], [20, 1, 8], 2000),
+    (12, 4, 64, [100 + 37 * j for j in range(40)], [1 + j % 5 for j in range(40)], 1000),
+    (8, 8, 128, [8000], [1], 4096),
+    (4, 1, 64, [40000], [33], 0),
+    (16, 8, 128, [0], [2000], 500),
+])
+def test_window_repeats_bit_for_bit(hq, hkv, hd, pre, new, window):
+    rng = np.random.default_rng(14)
+    bt = Batch(rng, pre, new, hkv, hd, 128)
+    q = randn(rng, bt.T, hq, hd).to(dev())
+    first = None
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    out, lse = torch.zeros(bt.T, hq, hd, dtype=torch.bfloat16, device=dev()), torch.zeros(bt.T, hq, device=dev())
+    ws = window_workspace(bt.T, len(pre), hq, hkv, hd)
+    for fill in (0, 0xFF, 0x7F):
+        run_window(bt, q, window, 4, out, lse, workspace=window_workspace(bt.T, len(pre), hq, hkv, hd, fill))
+        if first is None:
+            first = out.clone(), lse.clone()
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        for _ in range(3):
+            run_window(bt, q, window, 4, out, lse, workspace=ws, stream=st)
+    for _ in range(30):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        n = int(bt.off[-1])
+        assert torch.equal(out[:n], first[0][:n]) and torch.equal(lse[:n], first[1][:n])
+
+
+def test_window_without_lse_and_with_all_keys_is_the_causal_attention():
+    rng = np.random.default_rng(17)
+    bt = Batch(rng, [300, 40], [70, 5], 4, 64, 64)
+    q, out, _ = check_window(bt, 8, 0, 0, rng)
+    again = torch.full_like(out, 7.0)
+    run_window(bt, q, 10 ** 6, 0, again)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("pre,new", [([200, 50], [2, 3]), ([200, 50], [400, 3])])
+def test_window_reports_bad_pages_and_bad_sequences(pre, new):
+    rng = np.random.default_rng(15)
+    bt = Batch(rng, pre, new, 2, 64, 64)
+    n0, n = new[0], sum(new)
+    q = randn(rng, bt.T, 4, 64).to(dev())
+    good, lse = torch.zeros(bt.T, 4, 64, dtype=torch.bfloat16, device=dev()), torch.zeros(bt.T, 4, device=dev())
+    run_window(bt, q, 180, 4, good, lse)
+    for entry in ((0, 1, bt.n_pages), (0, 0, -1)):
+        bad = bt.table.copy()
+        bad[entry[0], entry[1]] = entry[2]
+        out, z = torch.zeros_like(good), torch.zeros_like(lse)
+        keep, bt.d = bt.d, dict(bt.d, page_tables=i32(bad))
+        run_window(bt, q, 180, 4, out, z)
+        bt.d = keep
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert e.value.code == dgp.DG_EINVAL and "page" in str(e.value)
+        assert torch.isfinite(out.float()).all() and torch.equal(out[n0:n], good[n0:n]) and torch.equal(z[n0:n], lse[n0:n])
+    for change in (dict(prefix_lens=i32([10 ** 6, 50])), dict(prefix_lens=i32([-1, 50])), dict(prefix_lens=i32([2 ** 31 - 1, 50]))):
+        out = torch.full_like(good, 7.0)
+        keep, bt.d = bt.d, dict(bt.d, **change)
+        run_window(bt, q, 180, 4, out)
+        bt.d = keep
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert "sequence" in str(e.value)
+        assert (out[:n0] == 7.0).all() and torch.equal(out[n0:n], good[n0:n])
+
+
+def test_window_rows_whose_only_keys_lie_on_a_bad_page_are_zero():
+    rng = np.random.default_rng(18)
+    bt = Batch(rng, [200], [1], 2, 64, 64)
+    bt.table[0, 3] = bt.n_pages
+    bt.d["page_tables"].copy_(i32(bt.table))
+    out, lse = torch.full((bt.T, 4, 64), 7.0, dtype=torch.bfloat16, device=dev()), torch.full((bt.T, 4), 7.0, device=dev())
+    run_window(bt, randn(rng, bt.T, 4, 64).to(dev()), 5, 0, out, lse)
+    with pytest.raises(dgp.DgError):
+        dgp.dg_op_status()
+    assert (out[0] == 0).all() and (lse[0] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("pre,new,window", [([2048], [3], 0), ([40000], [3], 39000), ([10], [3], 4), ([100], [600], 300)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_window_of_a_query_that_is_not_a_number_stays_apart(pre, new, window, value):
+    rng = np.random.default_rng(53)
+    bt = Batch(rng, pre, new, 2, 64, 64)
+    q = randn(rng, bt.T, 4, 64)
+    q[1, 2, 5] = value
+    out, lse = torch.full((bt.T, 4, 64), 7.0, dtype=torch.bfloat16, device=dev()), torch.full((bt.T, 4), 7.0, device=dev())
+    run_window(bt, q.to(dev()), window, 1, out, lse)
+    q[1, 2, 5] = 0.0
+    ref, mag, z, top = window_ref(f64(q), bt, window, 1, 0.125)
+    got, got_z, n = f64(out), f64(lse), int(bt.off[-1])
+    assert np.isnan(got[1, 2]).all() and not np.isfinite(got_z[1, 2])
+    got[1, 2], got_z[1, 2] = ref[1, 2], z[1, 2]
+    assert (np.abs(got[:n] - ref[:n]) <= attention_tol(ref[:n], mag[:n])).all()
+    assert (np.abs(got_z[:n] - z[:n]) <= lse_tol(z[:n], top[:n], 64, (pre[0] + new[0]) / 128 + 2)).all()
