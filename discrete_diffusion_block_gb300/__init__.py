@@ -178,6 +178,7 @@ _SIGS = {
                                     _P, _P, _SZ, _P]),
     "dg_op_tree_attention": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                   _I64, _P, _SZ, _P]),
+    "dg_op_cache_evict": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "dg_op_token_logprobs": (_I, [_P, _I, _I64, _I, _I, _F, _P, _I, _P, _P, _P, _I, _P, _P, _P]),
     "dg_op_packed": (_I, [_I, ctypes.c_char_p]),
 }
@@ -622,7 +623,8 @@ _PACK_APPEND = struct.Struct("=qqqqqqqqqqqqqqdqdqqqqq").pack
 _PACK_ATTEND = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqq").pack
 _PACK_LOGPROBS = struct.Struct("=qqqqqdqqqqqqqqq").pack
 _PACK_WINDOW = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqqq").pack
-DG_CALL_WINDOW_ATTENTION = 8
+_PACK_EVICT = struct.Struct("=qqqqqqqqqqqqqqqqqqq").pack
+DG_CALL_WINDOW_ATTENTION, DG_CALL_CACHE_EVICT = 8, 10
 DG_CALL_QK_NORM_ROPE, DG_CALL_ROPE_KV_APPEND, DG_CALL_TREE_ATTENTION, DG_CALL_TOKEN_LOGPROBS = range(4)
 
 
@@ -841,3 +843,23 @@ def dg_op_window_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets,
         _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev), window, sinks, B, T, hq,
         hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, _dense(lse, "lse", _F32, T * hq, dev),
         *_scratch(workspace, dev), _stream_on(stream, dev)))
+
+
+def dg_op_cache_evict(k_pool, v_pool, mass_pool, page_tables, out_tables, lens, out_lens, budget, sinks=0, recent=0, kept=None,
+                      stream=None):
+    """mass_pool fp32 [n_pages][Hkv][page_size]; page_tables and out_tables int32
+    [B][pages] (the same tensor: in place); lens, out_lens int32 [B]; kept int32
+    [B][Hkv][budget] or None; stream None: torch's current one."""
+    dev = _device(k_pool)
+    pool, table, out_table = k_pool.shape, page_tables.shape, out_tables.shape
+    if len(pool) != 4 or len(table) != 2 or len(out_table) != 2 or out_table[0] != table[0]:
+        _einval("pools are [n_pages][heads][page_size][head_dim], page_tables and out_tables [sequences][pages]")
+    n_pages, hkv, pg, hd = pool
+    B, max_pages = table
+    n = n_pages * hkv * pg
+    _call(DG_CALL_CACHE_EVICT, _PACK_EVICT(
+        _dense(k_pool, "k_pool", _BF16, n * hd, dev), _dense(v_pool, "v_pool", _BF16, n * hd, dev),
+        _dense(mass_pool, "mass_pool", _F32, n, dev), _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages,
+        _dense(out_tables, "out_tables", _I32T, B * out_table[1], dev), out_table[1], _dense(lens, "lens", _I32T, B, dev), B, hkv, hd,
+        pg, n_pages, budget, sinks, recent, _dense(out_lens, "out_lens", _I32T, B, dev),
+        _dense(kept, "kept", _I32T, B * hkv * budget, dev), _stream_on(stream, dev)))

@@ -1818,6 +1818,31 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
   return DG_OK;
 }
 
+int dg_op_cache_evict(uint16_t *k_pool, uint16_t *v_pool, float *mass_pool, const int32_t *page_tables, int32_t max_pages,
+                      const int32_t *out_tables, int32_t out_max_pages, const int32_t *lens, int32_t n_seqs,
+                      int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages, int32_t budget,
+                      int32_t sinks, int32_t recent, int32_t *out_lens, int32_t *kept, void *stream) {
+  if (n_kv_heads < 1 || page_size < 1) return fail(DG_EINVAL, "n_kv_heads and page_size must be at least 1");
+  if (head_dim != 64 && head_dim != 128) return fail(DG_EINVAL, "head_dim must be 64 or 128");
+  if (n_seqs < 0 || max_pages < 0 || out_max_pages < 0) return fail(DG_EINVAL, "negative sequence or page count");
+  if ((int64_t)n_seqs * n_kv_heads > INT32_MAX / 8) return fail(DG_EINVAL, "too many heads of sequences");
+  if (!k_pool || !v_pool || !mass_pool) return fail(DG_EINVAL, "null pool");
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return fail(DG_EINVAL, "a pool is not 16-byte aligned");
+  if ((uintptr_t)mass_pool % 4) return fail(DG_EINVAL, "mass_pool is not aligned to its elements");
+  if (n_pages < 1) return fail(DG_EINVAL, "n_pages must be at least 1");
+  if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return fail(DG_EINVAL, "budget >= 1, sinks, recent >= 0 and sinks + recent <= budget required");
+  if (n_seqs == 0) return DG_OK;
+  if (!lens || !out_lens || (max_pages && !page_tables) || (out_max_pages && !out_tables)) return fail(DG_EINVAL, "null pointer");
+  if (lens == out_lens) return fail(DG_EINVAL, "out_lens must not be lens");
+  int *status = nullptr;
+  CKR(op_status_ptr(&status));
+  dg::CacheEvict a{(bf16 *)k_pool, (bf16 *)v_pool, mass_pool, page_tables, max_pages, out_tables, out_max_pages, lens,
+                   n_seqs, n_kv_heads, head_dim, page_size, n_pages, budget, sinks, recent, out_lens, kept};
+  CK(dg::cache_evict(a, status, (cudaStream_t)stream));
+  return DG_OK;
+}
+
 int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_stride, int32_t rows, int32_t V,
                          float inv_tau, const int32_t *tokens, int32_t n_given, float *logprobs, float *entropy,
                          float *lse, int32_t top_k, int32_t *top_ids, float *top_logprobs, void *stream) {
@@ -1917,6 +1942,16 @@ extern "C" int dg_op_packed(int32_t call, const void *args) {
       if (!a.fits || c.wn < 0) break;
       return dg_op_window_attention(c.q, c.qs, c.kp, c.vp, c.tab, c.mp, c.pre, c.off, c.win, c.sinks, c.b, c.n, c.hq, c.hkv, c.hd,
                                     c.pg, c.np, c.scale, c.out, c.os, c.lse, c.ws, (size_t)c.wn, c.st);
+    }
+    case DG_CALL_CACHE_EVICT: {
+      struct { uint16_t *kp, *vp; float *mass; const int32_t *tab; int32_t mp; const int32_t *ot; int32_t omp; const int32_t *lens;
+               int32_t b, hkv, hd, pg, np, budget, sinks, recent; int32_t *ol, *kept; void *st; }
+      c{a.ptr<uint16_t>(), a.ptr<uint16_t>(), a.ptr<float>(), a.ptr<const int32_t>(), a.i32(), a.ptr<const int32_t>(), a.i32(),
+        a.ptr<const int32_t>(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.ptr<int32_t>(),
+        a.ptr<int32_t>(), a.ptr<void>()};
+      if (!a.fits) break;
+      return dg_op_cache_evict(c.kp, c.vp, c.mass, c.tab, c.mp, c.ot, c.omp, c.lens, c.b, c.hkv, c.hd, c.pg, c.np, c.budget, c.sinks,
+                               c.recent, c.ol, c.kept, c.st);
     }
     default: return fail(DG_EINVAL, "unknown call %d", call);
   }

@@ -306,4 +306,19 @@ struct TokenLogprobs {
 };
 cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st);
 
+// ---- bounded caches (kernels_tree.cu: windowed attention; kernels_evict.cu) ----
+struct CacheEvict {
+  bf16 *k_pool, *v_pool;
+  float *mass;  // [n_pages][Hkv][pg]
+  const int *page_tables;
+  int max_pages;
+  const int *out_tables;
+  int out_max_pages;
+  const int *lens;
+  int n_seqs, Hkv, hd, pg, n_pages, budget, sinks, recent;
+  int *out_lens, *kept;
+};
+constexpr int kEvictMostSlots = 262144;  // of a sequence: its bits lie in shared memory
+cudaError_t cache_evict(const CacheEvict &a, int *err, cudaStream_t st);
+
 }  // namespace dg

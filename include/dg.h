@@ -710,6 +710,34 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
                            float scale, uint16_t *out, int64_t out_stride, float *lse,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* Eviction by accumulated weight.  Sequence b has lens[b] cached tokens (device
+ * int32); every KV head of a longer one than `budget` keeps its first `sinks`
+ * slots, its last `recent`, and of those between them the budget - sinks - recent
+ * of the largest weight (equal ones by ascending slot; NaN below all others); a
+ * sequence within the budget keeps all.  The kept keys, values and weights move to
+ * slots 0, 1, .. of the sequence's pages out_tables[b * out_max_pages + ..] (device
+ * int32 [n_seqs][out_max_pages]), in the order of their slots; all other slots are
+ * left as they are.  A sequence's pages in out_tables are either its own, entry by
+ * entry (it is compacted in place), or pages that no sequence of the call reads or
+ * moves to (pages that sequences share stay whole then).
+ *   k_pool,
+ *   v_pool      device bf16 pools of one layer, layout of dg_op_canvas_attention
+ *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size]: the weights
+ *   out_lens    device int32 [n_seqs]: min(lens[b], budget); must not overlap lens
+ *   kept        device int32 [n_seqs][n_kv_heads][budget]: the slot that each kept
+ *               token had, -1 behind the last (may be NULL)
+ * Heads keep different tokens: from then on a slot is not a position (rotate and
+ * append new tokens with positions of their own).  A sequence of a negative length,
+ * of more than 262144 slots, or whose slots or kept ones lie outside the tables, and
+ * one with a page outside the pools is left as it is (out_lens and kept -1) and
+ * reported by dg_op_status.  head_dim in {64, 128}; page_size >= 1; budget >= 1;
+ * sinks + recent <= budget. */
+int dg_op_cache_evict(uint16_t *k_pool, uint16_t *v_pool, float *mass_pool,
+                      const int32_t *page_tables, int32_t max_pages, const int32_t *out_tables,
+                      int32_t out_max_pages, const int32_t *lens, int32_t n_seqs, int32_t n_kv_heads,
+                      int32_t head_dim, int32_t page_size, int32_t n_pages, int32_t budget,
+                      int32_t sinks, int32_t recent, int32_t *out_lens, int32_t *kept, void *stream);
+
 /* The calls of the two sections above with their arguments packed into one block, for bindings
  * in which marshalling some twenty arguments one by one takes longer than the
  * launch: args holds the call's parameters in order, 8 bytes each, integers and
@@ -718,7 +746,8 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
  * does not fit its parameter. */
 enum {
     DG_CALL_QK_NORM_ROPE = 0, DG_CALL_ROPE_KV_APPEND = 1, DG_CALL_TREE_ATTENTION = 2,
-    DG_CALL_TOKEN_LOGPROBS = 3, DG_CALL_WINDOW_ATTENTION = 8
+    DG_CALL_TOKEN_LOGPROBS = 3, DG_CALL_WINDOW_ATTENTION = 8,
+  DG_CALL_CACHE_EVICT = 10
 };
 int dg_op_packed(int32_t call, const void *args);
 

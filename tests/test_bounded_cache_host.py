@@ -31,7 +31,23 @@ def test_window_attention_checks_its_workspace(L):  # noqa: F811
     assert L.dg_op_window_attention_workspace_bytes(5, 2, 16, 0, 128) == 0
 
 
-CALLS = [("dg_op_window_attention", 8, WA, dict(n_tok=0), dict(scale=-1.0), "n_pages")]
+EV = dict(k_pool=A, v_pool=A, mass=A, tables=A, max_pages=4, out_tables=2 * A, out_max=4, lens=A, n_seqs=2, hkv=8, hd=128, pg=128, n_pages=9,
+          budget=200, sinks=4, recent=30, out_lens=2 * A, kept=A, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(k_pool=None), dict(v_pool=None), dict(mass=None), dict(k_pool=A + 8), dict(mass=A + 2), dict(tables=None), dict(out_tables=None),
+    dict(lens=None), dict(out_lens=None), dict(out_lens=A), dict(max_pages=-1), dict(out_max=-1), dict(n_seqs=-1), dict(hkv=0), dict(hd=96),
+    dict(hd=256), dict(pg=0), dict(n_pages=0), dict(budget=0), dict(sinks=-1), dict(recent=-1), dict(sinks=100, recent=101),
+    dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), dict(n_seqs=1 << 30),
+])
+def test_cache_evict_refuses(L, change):  # noqa: F811
+    assert call(L.dg_op_cache_evict, EV, **change) == dgp.DG_EINVAL
+    assert L.dg_last_error()
+
+
+CALLS = [("dg_op_window_attention", 8, WA, dict(n_tok=0), dict(scale=-1.0), "n_pages"),
+         ("dg_op_cache_evict", 10, EV, dict(n_seqs=0), dict(budget=0), "recent")]
 
 
 @pytest.mark.parametrize("name,which,base,empty,bad,wide", CALLS)
@@ -50,7 +66,8 @@ def test_empty_calls_succeed_and_packed_ones_answer_as_the_calls(L, name, which,
 def test_binding_refuses_tensors_that_are_not_on_the_device():
     t, i = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
     pool = torch.zeros(2, 4, 64, 64, dtype=torch.bfloat16)
-    calls = [lambda: dgp.dg_op_window_attention(t, pool, pool, i[:, None], i, torch.zeros(3, dtype=torch.int32), t.clone(), None)]
+    calls = [lambda: dgp.dg_op_window_attention(t, pool, pool, i[:, None], i, torch.zeros(3, dtype=torch.int32), t.clone(), None),
+             lambda: dgp.dg_op_cache_evict(pool, pool, torch.zeros(2, 4, 64), i[:, None], i[:, None], i, i.clone(), 5)]
     for c in calls:
         with pytest.raises(dgp.DgError) as e:
             c()

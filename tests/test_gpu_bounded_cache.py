@@ -252,3 +252,201 @@ def test_window_of_a_query_that_is_not_a_number_stays_apart(pre, new, window, va
     got[1, 2], got_z[1, 2] = ref[1, 2], z[1, 2]
     assert (np.abs(got[:n] - ref[:n]) <= attention_tol(ref[:n], mag[:n])).all()
     assert (np.abs(got_z[:n] - z[:n]) <= lse_tol(z[:n], top[:n], 64, (pre[0] + new[0]) / 128 + 2)).all()
+
+
+# ---- eviction ----------------------------------------------------------------------------
+
+class Cache:
+    """Sequences over shuffled pages with a weight per slot and KV head, and other
+    pages (or the same) for what stays. Pages are shared between the first two
+    sequences where `shared`."""
+
+    def __init__(self, rng, lens, hkv, hd, pg, budget, in_place=False, shared=0, weights=None, dtype=torch.bfloat16):
+        self.lens, self.hkv, self.hd, self.pg, self.budget = list(lens), hkv, hd, pg, budget
+        need = [-(-n // pg) for n in lens]
+        kept = [-(-min(n, budget) // pg) for n in lens]
+        self.n_pages = sum(need) + (0 if in_place else sum(kept)) + 1
+        perm = list(rng.permutation(self.n_pages))
+        self.table = np.full((len(lens), max(need) + 1), -5, np.int32)
+        self.out = np.full((len(lens), max(kept) + 1), -5, np.int32)
+        for b, m in enumerate(need):
+            self.table[b, :m] = [perm.pop() for _ in range(m)]
+        if shared:
+            self.table[1, :shared] = self.table[0, :shared]
+        for b, m in enumerate(kept):
+            self.out[b, :m] = self.table[b, :m] if in_place else [perm.pop() for _ in range(m)]
+        shape = (self.n_pages, hkv, pg, hd)
+        self.k, self.v = (torch.from_numpy(rng.integers(0, 2 ** 16, shape, dtype=np.uint16).view(np.int16)) for _ in range(2))    # any bits
+        self.mass = (np.exp(2 * rng.standard_normal(shape[:3])) if weights is None else weights(shape[:3])).astype(np.float32)
+
+    def ref(self, sinks, recent):
+        """Pools in slot order, weights, lengths and kept slots after the eviction."""
+        order = [pool_view(x) for x in (self.k, self.v)]
+        k, v, mass = (np.array(x) for x in (*order, self.mass))
+        kept = np.full((len(self.lens), self.hkv, self.budget), -1, np.int32)
+        for b, n in enumerate(self.lens):
+            for h in range(self.hkv):
+                j = np.arange(n)
+                if n > self.budget:
+                    mid = j[sinks:n - recent]
+                    w = self.mass[self.table[b, mid // self.pg], h, mid % self.pg].astype(np.float64)
+                    best = sorted(range(len(mid)), key=lambda i: (np.isnan(w[i]), 0.0 if np.isnan(w[i]) else -w[i], i))
+                    j = np.concatenate([j[:sinks], np.sort(mid[best[:self.budget - sinks - recent]]), j[n - recent:]])
+                kept[b, h, :len(j)] = j
+                d = np.arange(len(j))
+                dst, src = (self.out[b, d // self.pg], d % self.pg), (self.table[b, j // self.pg], j % self.pg)
+                for x, old in ((k, order[0]), (v, order[1])):
+                    x[dst[0], dst[1], h] = old[src[0], src[1], h]
+                mass[dst[0], h, dst[1]] = self.mass[src[0], h, src[1]]
+        return k, v, mass, np.minimum(self.lens, self.budget), kept
+
+    def on_gpu(self):
+        d = dict(k_pool=self.k.to(dev()).view(torch.bfloat16), v_pool=self.v.to(dev()).view(torch.bfloat16),
+                 mass_pool=torch.from_numpy(self.mass).to(dev()), page_tables=i32(self.table), lens=i32(self.lens),
+                 out_lens=i32([7] * len(self.lens)), kept=torch.full((len(self.lens), self.hkv, self.budget), 7, dtype=torch.int32, device=dev()))
+        d["out_tables"] = i32(self.out)
+        return d
+
+
+def pool_view(pool):
+    """The pool's bits in slot order: [n_pages][pg][heads][hd] int16."""
+    from test_gpu_draft_ops import pool_rows
+    return pool_rows(pool.view(torch.int16) if isinstance(pool, torch.Tensor) else pool)
+
+
+def same_floats(a, b):
+    return np.array_equal(np.asarray(a).view(np.uint32), np.asarray(b).view(np.uint32))
+
+
+def check_evict(c, sinks, recent, **call):
+    d = c.on_gpu()
+    dgp.dg_op_cache_evict(**d, budget=c.budget, sinks=sinks, recent=recent, **call)
+    torch.cuda.synchronize()
+    dgp.dg_op_status()
+    compare_evict(d, c.ref(sinks, recent))
+    return d
+
+
+def compare_evict(d, ref):
+    k, v, mass, lens, kept = ref
+    assert np.array_equal(d["out_lens"].cpu().numpy(), lens)
+    assert np.array_equal(d["kept"].cpu().numpy(), kept)
+    assert np.array_equal(pool_view(d["k_pool"]), k) and np.array_equal(pool_view(d["v_pool"]), v)
+    assert same_floats(d["mass_pool"].cpu().numpy(), mass)
+
+
+@pytest.mark.parametrize("lens,hkv,hd,pg,budget,sinks,recent", [
+    ([2], 1, 64, 64, 1, 0, 0),
+    ([2, 1, 0], 2, 128, 64, 1, 1, 0),
+    ([300], 1, 128, 128, 299, 4, 64),
+    ([300, 77, 0, 301], 3, 64, 64, 300, 0, 0),
+    ([1000, 5, 999], 2, 128, 192, 100, 4, 96),
+    ([1000, 5, 999], 2, 128, 7, 100, 3, 90),
+    ([700] * 30, 2, 64, 64, 333, 1, 100),
+    ([2176], 8, 128, 128, 2048, 4, 256),
+    ([9000], 1, 128, 128, 8000, 0, 0),
+    ([40000], 2, 64, 128, 5000, 10, 1000),
+    ([70000, 33000], 1, 64, 128, 65000, 0, 300),
+    ([500], 2, 64, 64, 64, 64, 0),
+    ([500], 2, 64, 64, 64, 0, 64),
+])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict(lens, hkv, hd, pg, budget, sinks, recent, in_place):
+    rng = np.random.default_rng(len(lens) + pg)
+    check_evict(Cache(rng, lens, hkv, hd, pg, budget, in_place), sinks, recent)
+
+
+@pytest.mark.parametrize("weights", ["equal", "few", "nan", "signs", "ends"])
+@pytest.mark.parametrize("budget,sinks,recent", [(500, 0, 0), (900, 4, 77), (31, 3, 0)])
+def test_evict_weights_of_all_kinds(weights, budget, sinks, recent):
+    rng = np.random.default_rng(3)
+    kinds = dict(
+        equal=lambda s: np.zeros(s), few=lambda s: rng.integers(0, 3, s) * 0.5,
+        nan=lambda s: np.where(rng.random(s) < 0.6, np.nan, rng.standard_normal(s)),
+        signs=lambda s: np.where(rng.random(s) < 0.3, rng.choice([0.0, -0.0], s), rng.integers(-2, 3, s) * 1e-3),
+        ends=lambda s: rng.choice([np.inf, -np.inf, 3e38, -3e38, 1e-45, -1e-45, 1.0, 1.0000001], s))
+    for in_place in (False, True):
+        check_evict(Cache(rng, [1000, 1300], 2, 64, 64, budget, in_place, weights=kinds[weights]), sinks, recent)
+
+
+def test_evict_leaves_shared_pages_whole():
+    rng = np.random.default_rng(5)
+    c = Cache(rng, [800, 700, 30], 2, 64, 64, 200, shared=6)
+    before = c.table[0, :6]
+    d = check_evict(c, 2, 20)
+    for name, was in (("k_pool", c.k), ("v_pool", c.v)):
+        assert torch.equal(d[name].view(torch.int16).cpu()[before], was[before])
+
+
+def test_evict_some_in_place_and_some_elsewhere():
+    rng = np.random.default_rng(6)
+    c = Cache(rng, [800, 90, 1000, 40], 2, 128, 64, 200)
+    for b in (0, 3):
+        m = -(-min(c.lens[b], 200) // 64)
+        c.out[b, :m] = c.table[b, :m]
+    check_evict(c, 2, 20)
+
+
+def test_evict_without_kept_repeats_and_is_captured():
+    rng = np.random.default_rng(7)
+    c = Cache(rng, [5000, 3000, 12], 4, 128, 128, 1500)
+    ref = c.ref(4, 300)
+    d = c.on_gpu()
+    d2 = dict(d, kept=None)
+    dgp.dg_op_cache_evict(**d2, budget=1500, sinks=4, recent=300)
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        dgp.dg_op_cache_evict(**d, budget=1500, sinks=4, recent=300, stream=st)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    compare_evict(d, ref)
+    # other lengths and weights in the same tensors: the captured call takes them
+    e = Cache(rng, [4000, 100, 1800], 4, 128, 128, 1500)
+    e.table, e.out, e.n_pages = c.table, c.out, c.n_pages
+    e.k, e.v, e.mass = e.k.new_zeros(c.k.shape), e.v.new_zeros(c.v.shape), rng.random(c.mass.shape).astype(np.float32)
+    e.lens = [4000, 100, 12]
+    for name, x in e.on_gpu().items():
+        d[name].copy_(x)
+    g.replay()
+    torch.cuda.synchronize()
+    compare_evict(d, e.ref(4, 300))
+
+
+def test_evict_reports_bad_sequences_and_pages():
+    rng = np.random.default_rng(8)
+    for change, words in ((dict(lens=-1), "sequence"), (dict(lens=10 ** 6), "sequence"), (dict(lens=2 ** 31 - 1), "sequence"),
+                          (dict(table=-1), "page"), (dict(table="n"), "page"), (dict(out="n"), "page")):
+        c = Cache(rng, [500, 400, 300], 2, 64, 64, 200)
+        good = Cache.ref(c, 2, 20)
+        d = c.on_gpu()
+        for what, value in change.items():
+            if what == "lens":
+                d["lens"][1] = value
+            else:
+                d["page_tables" if what == "table" else "out_tables"][1, 2] = c.n_pages if value == "n" else value
+        dgp.dg_op_cache_evict(**d, budget=200, sinks=2, recent=20)
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert e.value.code == dgp.DG_EINVAL and words in str(e.value)
+        # the sequence is left as it is, the others are moved
+        assert d["out_lens"].tolist() == [200, -1, 200] and (d["kept"][1] == -1).all()
+        left = c.out[1, :4]
+        for name, was, want in (("k_pool", c.k, good[0]), ("v_pool", c.v, good[1])):
+            assert torch.equal(d[name].view(torch.int16).cpu()[left], was[left])
+            got = pool_view(d[name])
+            assert np.array_equal(got[c.out[0, :4]], want[c.out[0, :4]]) and np.array_equal(got[c.out[2, :4]], want[c.out[2, :4]])
+
+
+def test_evict_of_more_slots_than_are_taken_is_reported():
+    rng = np.random.default_rng(9)
+    n = 262144 + 64
+    c = Cache(rng, [64, 64], 1, 64, 64, 10)
+    d = c.on_gpu()
+    d["lens"][0] = n
+    d["page_tables"] = i32(np.tile(c.table[:, :1], (1, n // 64)))
+    dgp.dg_op_cache_evict(**d, budget=10)
+    with pytest.raises(dgp.DgError) as e:
+        dgp.dg_op_status()
+    assert "sequence" in str(e.value) and d["out_lens"].tolist() == [-1, 10]
