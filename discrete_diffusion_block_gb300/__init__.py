@@ -178,6 +178,8 @@ _SIGS = {
                                     _P, _P, _SZ, _P]),
     "dg_op_tree_attention": (_I, [_P, _I64, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
                                   _I64, _P, _SZ, _P]),
+    "dg_op_key_mass_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "dg_op_key_mass": (_I, [_P, _I64, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P]),
     "dg_op_cache_evict": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "dg_op_token_logprobs": (_I, [_P, _I, _I64, _I, _I, _F, _P, _I, _P, _P, _P, _I, _P, _P, _P]),
     "dg_op_packed": (_I, [_I, ctypes.c_char_p]),
@@ -624,7 +626,8 @@ _PACK_ATTEND = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqq").pack
 _PACK_LOGPROBS = struct.Struct("=qqqqqdqqqqqqqqq").pack
 _PACK_WINDOW = struct.Struct("=qqqqqqqqqqqqqqqqqdqqqqqq").pack
 _PACK_EVICT = struct.Struct("=qqqqqqqqqqqqqqqqqqq").pack
-DG_CALL_WINDOW_ATTENTION, DG_CALL_CACHE_EVICT = 8, 10
+_PACK_MASS = struct.Struct("=qqqqqqqqqqqqqqqqqqqdqqq").pack
+DG_CALL_WINDOW_ATTENTION, DG_CALL_KEY_MASS, DG_CALL_CACHE_EVICT = 8, 9, 10
 DG_CALL_QK_NORM_ROPE, DG_CALL_ROPE_KV_APPEND, DG_CALL_TREE_ATTENTION, DG_CALL_TOKEN_LOGPROBS = range(4)
 
 
@@ -843,6 +846,25 @@ def dg_op_window_attention(q, k_pool, v_pool, page_tables, prefix_lens, offsets,
         _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev), window, sinks, B, T, hq,
         hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, op, os_, _dense(lse, "lse", _F32, T * hq, dev),
         *_scratch(workspace, dev), _stream_on(stream, dev)))
+
+
+def dg_op_key_mass_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd):
+    return load().dg_op_key_mass_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd)
+
+
+def dg_op_key_mass(q, lse, k_pool, mass_pool, page_tables, prefix_lens, offsets, workspace, window=0, sinks=0, observe=0, scale=None,
+                   stream=None):
+    """q: [T][Hq][hd] bf16 (rows may be strided); lse fp32 [T][Hq]; mass_pool fp32
+    [n_pages][Hkv][page_size]; window 0: all keys; observe 0: all rows count;
+    workspace: a contiguous tensor; scale None: 1 / sqrt(hd); stream None: torch's current one."""
+    dev, (n_pages, hkv, pg, hd), (B, max_pages), qp, qs = _batch(q, k_pool, page_tables)
+    T, hq, _ = q.shape
+    n = n_pages * hkv * pg
+    _call(DG_CALL_KEY_MASS, _PACK_MASS(
+        qp, qs, _dense(lse, "lse", _F32, T * hq, dev), _dense(k_pool, "k_pool", _BF16, n * hd, dev),
+        _dense(mass_pool, "mass_pool", _F32, n, dev), _dense(page_tables, "page_tables", _I32T, B * max_pages, dev), max_pages,
+        _dense(prefix_lens, "prefix_lens", _I32T, B, dev), _dense(offsets, "offsets", _I32T, B + 1, dev), window, sinks, observe, B, T,
+        hq, hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, *_scratch(workspace, dev), _stream_on(stream, dev)))
 
 
 def dg_op_cache_evict(k_pool, v_pool, mass_pool, page_tables, out_tables, lens, out_lens, budget, sinks=0, recent=0, kept=None,

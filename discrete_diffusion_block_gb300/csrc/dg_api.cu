@@ -1818,6 +1818,39 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
   return DG_OK;
 }
 
+size_t dg_op_key_mass_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
+                                      int32_t head_dim) {
+  if (n_tok < 0 || n_seqs < 0 || n_kv_heads < 1 || n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return dg::key_mass_workspace_bytes();
+}
+
+int dg_op_key_mass(const uint16_t *q, int64_t q_stride, const float *lse, const uint16_t *k_pool, float *mass_pool,
+                   const int32_t *page_tables, int32_t max_pages, const int32_t *prefix_lens, const int32_t *offsets,
+                   int32_t window, int32_t sinks, int32_t observe, int32_t n_seqs, int32_t n_tok, int32_t n_q_heads,
+                   int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages, float scale,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+  CKR(check_attended(n_tok, n_q_heads, n_kv_heads, head_dim, page_size, scale));
+  if (window < 0 || sinks < 0 || observe < 0) return fail(DG_EINVAL, "window, sinks and observe must not be negative");
+  CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, k_pool, n_pages));
+  if (!mass_pool) return fail(DG_EINVAL, "null mass_pool");
+  if ((uintptr_t)mass_pool % 4 || (uintptr_t)lse % 4) return fail(DG_EINVAL, "mass_pool or lse is not aligned to its elements");
+  CKR(check_rows("q", q, q_stride, n_tok, n_q_heads, head_dim, 8));
+  if (n_tok == 0 || n_seqs == 0) return DG_OK;
+  if (!lse) return fail(DG_EINVAL, "null lse");
+  if (q_stride >= (int64_t)1 << 38) return fail(DG_EINVAL, "q: row stride %lld is too large", (long long)q_stride);
+  CKR(check_span(max_pages, page_size, n_tok, n_seqs, n_q_heads, n_kv_heads));
+  CKR(check_workspace(workspace, workspace_bytes,
+                      dg_op_key_mass_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim)));
+  int *status = nullptr;
+  CKR(op_status_ptr(&status));
+  dg::KeyMass a{(const bf16 *)q, q_stride, lse, (const bf16 *)k_pool, mass_pool, page_tables, max_pages, prefix_lens,
+                offsets, window ? window : INT32_MAX, window ? std::min(sinks, (int32_t)0x7fffff00) : 0, observe, n_seqs,
+                n_tok, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, scale};
+  CK(dg::key_mass(a, workspace, status, (cudaStream_t)stream));
+  return DG_OK;
+}
+
 int dg_op_cache_evict(uint16_t *k_pool, uint16_t *v_pool, float *mass_pool, const int32_t *page_tables, int32_t max_pages,
                       const int32_t *out_tables, int32_t out_max_pages, const int32_t *lens, int32_t n_seqs,
                       int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages, int32_t budget,
@@ -1942,6 +1975,16 @@ extern "C" int dg_op_packed(int32_t call, const void *args) {
       if (!a.fits || c.wn < 0) break;
       return dg_op_window_attention(c.q, c.qs, c.kp, c.vp, c.tab, c.mp, c.pre, c.off, c.win, c.sinks, c.b, c.n, c.hq, c.hkv, c.hd,
                                     c.pg, c.np, c.scale, c.out, c.os, c.lse, c.ws, (size_t)c.wn, c.st);
+    }
+    case DG_CALL_KEY_MASS: {
+      struct { const uint16_t *q; int64_t qs; const float *lse; const uint16_t *kp; float *mass; const int32_t *tab; int32_t mp;
+               const int32_t *pre, *off; int32_t win, sinks, obs, b, n, hq, hkv, hd, pg, np; float scale; void *ws; int64_t wn; void *st; }
+      c{a.ptr<const uint16_t>(), a.i64(), a.ptr<const float>(), a.ptr<const uint16_t>(), a.ptr<float>(), a.ptr<const int32_t>(),
+        a.i32(), a.ptr<const int32_t>(), a.ptr<const int32_t>(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(), a.i32(),
+        a.i32(), a.i32(), a.i32(), a.f(), a.ptr<void>(), a.i64(), a.ptr<void>()};
+      if (!a.fits || c.wn < 0) break;
+      return dg_op_key_mass(c.q, c.qs, c.lse, c.kp, c.mass, c.tab, c.mp, c.pre, c.off, c.win, c.sinks, c.obs, c.b, c.n, c.hq, c.hkv,
+                            c.hd, c.pg, c.np, c.scale, c.ws, (size_t)c.wn, c.st);
     }
     case DG_CALL_CACHE_EVICT: {
       struct { uint16_t *kp, *vp; float *mass; const int32_t *tab; int32_t mp; const int32_t *ot; int32_t omp; const int32_t *lens;

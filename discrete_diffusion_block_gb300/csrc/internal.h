@@ -1,5 +1,6 @@
 // Host-side launchers shared between the translation units of libdg.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -306,7 +307,30 @@ struct TokenLogprobs {
 };
 cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st);
 
-// ---- bounded caches (kernels_tree.cu: windowed attention; kernels_evict.cu) ----
+// ---- bounded caches (kernels_tree.cu: windowed attention; kernels_mass.cu, kernels_evict.cu) ----
+// A number that no other call has: a word of a workspace whose contents are
+// arbitrary does not equal it.
+unsigned long long new_ticket();
+
+// Tensor map of bf16 rows [n_tok][Hq][hd], `stride` elements apart, for tiles of
+// 64 elements x G heads x T tokens in the operand order (kernels_attn.cu).
+cudaError_t rows_map(CUtensorMap *map, const bf16 *rows, long long stride, int n_tok, int Hq, int hd, int G, int T);
+
+struct KeyMass {
+  const bf16 *q;
+  long long q_stride;
+  const float *lse;  // [n_tok][Hq]
+  const bf16 *k_pool;
+  float *mass;  // [n_pages][Hkv][pg]
+  const int *page_tables;
+  int max_pages;
+  const int *prefix_lens, *offsets;
+  int window, sinks, observe, n_seqs, n_tok, Hq, Hkv, hd, pg, n_pages;
+  float scale;
+};
+size_t key_mass_workspace_bytes();
+cudaError_t key_mass(const KeyMass &a, void *ws, int *err, cudaStream_t st);
+
 struct CacheEvict {
   bf16 *k_pool, *v_pool;
   float *mass;  // [n_pages][Hkv][pg]

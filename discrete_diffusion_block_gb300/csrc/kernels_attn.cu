@@ -632,6 +632,22 @@ PFN_cuTensorMapEncodeTiled_v12000 attn_encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+cudaError_t rows_map(CUtensorMap *map, const bf16 *rows, long long stride, int n_tok, int Hq, int hd, int G, int T) {
+  auto fn = attn_encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)Hq, (cuuint64_t)n_tok};
+  const cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)(n_tok > 1 ? stride : (long long)Hq * hd) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)T}, step[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(rows), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+
 struct AttnMapKey {
   const void *ptr;
   uint64_t d0, d1, d2, d3;

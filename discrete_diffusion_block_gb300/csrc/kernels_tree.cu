@@ -1159,8 +1159,8 @@ TreeWorkspace tree_workspace(int hd) {
   return w;
 }
 
-// A number that no other call has: a flag word of a workspace whose contents
-// are arbitrary does not equal it.
+}  // namespace
+
 unsigned long long new_ticket() {
   static std::atomic<unsigned long long> count{(unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count()};
   unsigned long long x = count.fetch_add(1) * 0x9E3779B97F4A7C15ull;  // mixed as in splitmix64 (Steele et al., 2014)
@@ -1169,6 +1169,8 @@ unsigned long long new_ticket() {
   x ^= x >> 31;
   return x ? x : 1;
 }
+
+namespace {
 
 // Blocks of a launch on the current device (all of them run together), asked
 // once; 0: the kernel does not run there.

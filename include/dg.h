@@ -710,6 +710,31 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
                            float scale, uint16_t *out, int64_t out_stride, float *lse,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* Attention weight that each key gathers: with lse as dg_op_window_attention left
+ * it for these rows (device fp32 [n_tok][n_q_heads]), for every KV head and key
+ * slot j of a sequence
+ *   mass[j] <- m_j + sum e^{x_j - lse},  m_j = mass[j] for a cached key (j <
+ *   prefix_lens[b]), 0 for a new token's own,
+ * over the rows (t, h) of its query heads whose token counts and sees j (window
+ * and sinks as there).  All new tokens count, or with observe > 0 the sequence's
+ * last `observe`.  Cached keys that no such row sees are left as they are, and
+ * their pages are not touched, nor their entries of the table.  fp32 throughout,
+ * one order of addition: results repeat bit for bit.  Rows whose lse is -inf (they
+ * saw no key) add nothing; a NaN spreads to the keys that its row sees.
+ *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size], of the cache's pages
+ *               (two sequences of a call must not share a page that is written)
+ * Other arguments, conditions and reports as dg_op_window_attention; keys of a page
+ * outside the pools are skipped.  The workspace of one call must not be used by
+ * another at the same time.  Blocks do not wait for one another. */
+size_t dg_op_key_mass_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
+                                      int32_t n_kv_heads, int32_t head_dim);
+int dg_op_key_mass(const uint16_t *q, int64_t q_stride, const float *lse, const uint16_t *k_pool,
+                   float *mass_pool, const int32_t *page_tables, int32_t max_pages,
+                   const int32_t *prefix_lens, const int32_t *offsets, int32_t window, int32_t sinks,
+                   int32_t observe, int32_t n_seqs, int32_t n_tok, int32_t n_q_heads,
+                   int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages,
+                   float scale, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Eviction by accumulated weight.  Sequence b has lens[b] cached tokens (device
  * int32); every KV head of a longer one than `budget` keeps its first `sinks`
  * slots, its last `recent`, and of those between them the budget - sinks - recent
@@ -747,7 +772,7 @@ int dg_op_cache_evict(uint16_t *k_pool, uint16_t *v_pool, float *mass_pool,
 enum {
     DG_CALL_QK_NORM_ROPE = 0, DG_CALL_ROPE_KV_APPEND = 1, DG_CALL_TREE_ATTENTION = 2,
     DG_CALL_TOKEN_LOGPROBS = 3, DG_CALL_WINDOW_ATTENTION = 8,
-  DG_CALL_CACHE_EVICT = 10
+  DG_CALL_KEY_MASS = 9, DG_CALL_CACHE_EVICT = 10
 };
 int dg_op_packed(int32_t call, const void *args);
 

@@ -81,6 +81,10 @@ def lse_tol(lse, top, hd, tiles):
     return U32 * ((hd + 8) * top + 8 * np.abs(lse) + 64 + tiles + 32)
 
 
+def same_floats(a, b):
+    return np.array_equal(np.asarray(a).view(np.uint32), np.asarray(b).view(np.uint32))
+
+
 # ---- windowed attention ------------------------------------------------------------------
 
 def window_workspace(T, B, hq, hkv, hd, fill=0xFF):
@@ -254,6 +258,258 @@ def test_window_of_a_query_that_is_not_a_number_stays_apart(pre, new, window, va
     assert (np.abs(got_z[:n] - z[:n]) <= lse_tol(z[:n], top[:n], 64, (pre[0] + new[0]) / 128 + 2)).all()
 
 
+# ---- weight that keys gather ------------------------------------------------------------
+
+def mass_ref(q, lse, bt, mass, window, sinks, observe, scale, shared=()):
+    """The weights after the call, how far fp32 may be off, and which slots must
+    keep their bits, in 64 bits; q, lse, mass as the call gets them."""
+    hq = q.shape[1]
+    G = hq // bt.hkv
+    out = mass.astype(np.float64)
+    tol, still = np.zeros(out.shape), np.ones(out.shape, bool)
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        if n == 0:
+            continue
+        first = max(0, n - observe) if observe else 0
+        see = visible(p, n, window, sinks)[first:]
+        j = np.nonzero(see.any(0) | (np.arange(p + n) >= p))[0]
+        page, slot = bt.table[b, j // bt.pg], j % bt.pg
+        rows = slice(bt.off[b] + first, bt.off[b] + n)
+        for g in range(bt.hkv):
+            total, err = np.where(j < p, out[page, g, slot], 0.0), np.zeros(len(j))
+            for h in range(g * G, (g + 1) * G):
+                x, k = q[rows, h], np.where(see.any(0)[j][:, None], bt.keys[b][j, g], 0.0)
+                z = lse[rows, h].astype(np.float64)[:, None]
+                e = np.where(see[:, j], np.exp(np.where(see[:, j], x @ k.T * scale - z, 0.0)), 0.0)
+                e = np.where(z == -np.inf, 0.0, e)
+                total += e.sum(0)
+                # scores as in lse_tol, the exponent's own roundings, sums over 128 rows and then tile by tile
+                with np.errstate(invalid="ignore"):
+                    err += (e * ((bt.hd + 8) * (np.abs(x) @ np.abs(k).T * scale) + 8 * np.where(np.isfinite(z), np.abs(z), 0) + 100 + n * G / 64)).sum(0)
+            out[page, g, slot] = total
+            tol[page, g, slot] = U32 * (err + 2 * np.abs(total))
+            still[page, g, slot] = False
+    return out, tol, still
+
+
+def mass_workspace(T, B, hq, hkv, hd, fill=0xFF):
+    return torch.full((dgp.dg_op_key_mass_workspace_bytes(T, B, hq, hkv, hd),), fill, dtype=torch.uint8, device=dev())
+
+
+def run_mass(bt, q, lse, mass, window=0, sinks=0, observe=0, scale=None, stream=None, workspace=None):
+    ws = mass_workspace(q.shape[0], len(bt.pre), q.shape[1], bt.hkv, bt.hd) if workspace is None else workspace
+    dgp.dg_op_key_mass(q, lse, bt.k_pool, mass, **bt.d, workspace=ws, window=window, sinks=sinks, observe=observe, scale=scale, stream=stream)
+
+
+def row_lse(q, bt, window, sinks, scale):
+    out = np.zeros(q.shape[:2])
+    G = q.shape[1] // bt.hkv
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        see = visible(p, n, window, sinks)
+        rows = slice(bt.off[b], bt.off[b] + n)
+        for h in range(q.shape[1]):
+            s = np.where(see, q[rows, h] @ np.nan_to_num(bt.keys[b][:, h // G]).T * scale, -np.inf)
+            m = s.max(1, keepdims=True) if n else s[:, :1]
+            out[rows, h] = m[:, 0] + np.log(np.exp(s - m).sum(1))
+    return out.astype(np.float32)
+
+
+def mass_case(rng, bt, hq, window, sinks, scale, strided=False):
+    q = randn(rng, bt.T, hq + 3, bt.hd).to(dev())[:, 1:1 + hq] if strided else randn(rng, bt.T, hq, bt.hd).to(dev())
+    lse = row_lse(f64(q), bt, window, sinks, scale)
+    lse[int(bt.off[-1]):] = np.nan                              # rows that belong to nobody
+    mass = rng.exponential(1.0, (bt.n_pages, bt.hkv, bt.pg)).astype(np.float32)
+    mass[rng.random(mass.shape) < 0.02] = np.nan
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):            # what new slots held does not matter, what cached keys hold does
+        j = np.arange(p)
+        mass[bt.table[b, j // bt.pg], :, j % bt.pg] = rng.exponential(1.0, (p, bt.hkv))
+        j = np.arange(p, p + n)
+        mass[bt.table[b, j // bt.pg], :, j % bt.pg] = np.nan
+    return q, lse, mass
+
+
+def compare_mass(got, ref, tol, still, before):
+    got = got.cpu().numpy()
+    assert np.array_equal(got.view(np.uint32)[still], before.view(np.uint32)[still])
+    with np.errstate(invalid="ignore"):
+        assert (np.abs(got - ref) <= tol)[~still].all(), np.nanmax((np.abs(got - ref) - tol)[~still])
+
+
+def check_mass(bt, hq, window, sinks, observe, rng, scale=None, strided=False):
+    factor = bt.hd ** -0.5 if scale is None else scale
+    q, lse, before = mass_case(rng, bt, hq, window, sinks, factor, strided)
+    first = observe if observe else max(bt.new)
+    hide_keys(bt, window, sinks, first)
+    mass, z = torch.from_numpy(before).to(dev()), torch.from_numpy(lse).to(dev())
+    run_mass(bt, q, z, mass, window, sinks, observe, scale)
+    dgp.dg_op_status()
+    compare_mass(mass, *mass_ref(f64(q), lse, bt, before, window, sinks, observe, factor), before)
+    return q, z, before, mass
+
+
+def hide_keys(bt, window, sinks, observe):
+    """NaN into the keys that no counted row sees; pages of which none is seen and that hold no new slot leave the table."""
+    pool = bt.k_pool.cpu()
+    for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        if n == 0:
+            continue
+        seen = visible(p, n, window, sinks)[max(0, n - observe):].any(0)
+        gone = np.nonzero(~seen)[0]
+        place(pool, bt.table[b], gone, torch.full((len(gone), bt.hkv, bt.hd), float("nan"), dtype=torch.bfloat16))
+        seen[p:] = True
+        for j in range(-(-(p + n) // bt.pg)):
+            if not seen[j * bt.pg:(j + 1) * bt.pg].any():
+                bt.table[b, j] = bt.n_pages + 9
+    bt.k_pool.copy_(pool)
+    bt.d["page_tables"].copy_(i32(bt.table))
+
+
+@pytest.mark.parametrize("hq,hkv,hd", HEADS)
+@pytest.mark.parametrize("pre,window,sinks,pg", [
+    (0, 0, 0, 128), (1, 1, 1, 64), (63, 64, 0, 64), (255, 0, 0, 128), (256, 0, 0, 192), (300, 128, 4, 64), (1000, 200, 65, 64), (1000, 200, 130, 192),
+    (1999, 600, 300, 128), (1999, 2 ** 31 - 1, 2 ** 31 - 1, 128),
+])
+def test_mass_of_single_tokens(hq, hkv, hd, pre, window, sinks, pg):
+    rng = np.random.default_rng(pre + window % 1000)
+    check_mass(Batch(rng, [pre], [1], hkv, hd, pg), hq, window, sinks, 0, rng)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,pg,pre,new", [
+    (16, 8, 128, 128, [300], [17]),
+    (16, 8, 128, 128, [0, 2000, 130], [64, 3, 0]),
+    (12, 4, 64, 64, [100, 0, 5, 640, 0], [5, 1, 0, 133, 2]),
+    (32, 1, 64, 64, [70], [90]),
+    (6, 2, 64, 128, [0], [500]),
+    (16, 8, 128, 128, [0], [700]),
+    (7, 1, 128, 64, [11] * 40, [j % 5 for j in range(40)]),
+    (4, 2, 64, 64, [j * 7 for j in range(200)], [1] * 200),
+    (128, 1, 64, 64, [20, 64], [30, 1]),
+    (3, 1, 64, 64, [1000, 3], [333, 257]),
+    (16, 4, 128, 192, [3000, 0], [40, 1100]),
+])
+@pytest.mark.parametrize("window,sinks,observe", [(0, 0, 0), (0, 0, 1), (0, 0, 50), (1, 0, 0), (1, 3, 7), (100, 0, 0), (129, 130, 30), (333, 70, 0),
+                                                  (50, 0, 1)])
+def test_mass_of_batches(hq, hkv, hd, pg, pre, new, window, sinks, observe):
+    rng = np.random.default_rng(len(pre) + hq)
+    bt = Batch(rng, pre, new, hkv, hd, pg)
+    check_mass(bt, hq, window, sinks, observe, rng, strided=window % 2 == 1)
+
+
+def test_mass_with_a_scale_and_rows_that_saw_nothing_or_nan():
+    rng = np.random.default_rng(21)
+    bt = Batch(rng, [700, 300], [5, 2], 2, 64, 64)
+    q, lse, before = mass_case(rng, bt, 4, 0, 0, 0.3)
+    lse[1] = -np.inf
+    z, mass = torch.from_numpy(lse).to(dev()), torch.from_numpy(before).to(dev())
+    run_mass(bt, q, z, mass, scale=0.3)
+    compare_mass(mass, *mass_ref(f64(q), lse, bt, before, 0, 0, 0, 0.3), before)
+    lse[6, 2] = np.nan                                  # the second sequence's last token, KV head 1
+    z, mass = torch.from_numpy(lse).to(dev()), torch.from_numpy(before).to(dev())
+    run_mass(bt, q, z, mass, scale=0.3)
+    got = mass.cpu().numpy()
+    j = np.arange(302)
+    assert np.isnan(got[bt.table[1, j // 64], 1, j % 64]).all()
+    ref, tol, still = mass_ref(f64(q), np.where(np.isnan(lse), 0, lse), bt, before, 0, 0, 0, 0.3)
+    still[bt.table[1, j // 64], 1, j % 64] = True
+    assert (np.abs(got - ref) <= tol)[~still].all()
+
+
+@pytest.mark.parametrize("hq,hkv,hd,pre,new,window,sinks,observe", [
+    (16, 8, 128, [3000, 10, 777], [20, 1, 8], 0, 0, 0),
+    (8, 2, 128, [0], [3000], 500, 4, 0),                # the first tokens' keys are seen by all rows: many pieces
+    (4, 1, 64, [20000], [600], 0, 0, 0),
+    (12, 4, 64, [100 + 37 * j for j in range(40)], [1 + j % 5 for j in range(40)], 0, 0, 0),
+])
+def test_mass_repeats_bit_for_bit(hq, hkv, hd, pre, new, window, sinks, observe):
+    rng = np.random.default_rng(22)
+    bt = Batch(rng, pre, new, hkv, hd, 128)
+    q, z, before, first = check_mass(bt, hq, window, sinks, observe, rng)
+    ws = mass_workspace(bt.T, len(pre), hq, hkv, hd)
+    old, mass = torch.from_numpy(before).to(dev()), torch.empty_like(first)
+    bits = lambda t: t.view(torch.int32)  # noqa: E731
+    for fill in (0, 0x7F, 0xFF, None, None):
+        if fill is not None:
+            ws.fill_(fill)
+        mass.copy_(old)
+        run_mass(bt, q, z, mass, window, sinks, observe, workspace=ws)
+        assert torch.equal(bits(mass), bits(first))
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        mass.copy_(old)
+        run_mass(bt, q, z, mass, window, sinks, observe, workspace=ws, stream=st)
+    for _ in range(30):
+        mass.zero_()
+        g.replay()
+        assert torch.equal(bits(mass), bits(first))
+    # the second step adds to the first's
+    run_mass(bt, q, z, mass, window, sinks, observe, workspace=ws)
+    after = first.cpu().numpy()
+    compare_mass(mass, *mass_ref(f64(q), z.cpu().numpy(), bt, after, window, sinks, observe, hd ** -0.5), after)
+
+
+def test_mass_reports_bad_pages_and_bad_sequences():
+    rng = np.random.default_rng(23)
+    bt = Batch(rng, [200, 50], [2, 3], 2, 64, 64)
+    q, lse, before = mass_case(rng, bt, 4, 0, 0, 0.125)
+    z, good = torch.from_numpy(lse).to(dev()), torch.from_numpy(before).to(dev())
+    run_mass(bt, q, z, good)
+    good = good.cpu().numpy()
+    for value in (bt.n_pages, -1):
+        bad = bt.table.copy()
+        page, bad[0, 1] = bad[0, 1], value
+        mass = torch.from_numpy(before).to(dev())
+        keep, bt.d = bt.d, dict(bt.d, page_tables=i32(bad))
+        run_mass(bt, q, z, mass)
+        bt.d = keep
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert e.value.code == dgp.DG_EINVAL and "page" in str(e.value)
+        want = good.copy()
+        want[page] = before[page]
+        assert same_floats(mass.cpu().numpy(), want)
+    for change in (dict(prefix_lens=i32([10 ** 6, 50])), dict(prefix_lens=i32([-1, 50])), dict(prefix_lens=i32([2 ** 31 - 1, 50]))):
+        mass = torch.from_numpy(before).to(dev())
+        keep, bt.d = bt.d, dict(bt.d, **change)
+        run_mass(bt, q, z, mass)
+        bt.d = keep
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert "sequence" in str(e.value)
+        want = good.copy()
+        pages = bt.table[0, :4]
+        want[pages] = before[pages]
+        assert same_floats(mass.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("hq,hkv,hd,pre,new", [(8, 2, 128, [0], [3000]), (4, 1, 64, [20000], [600])])
+def test_a_captured_mass_recovers_from_a_failure(hq, hkv, hd, pre, new):
+    # a launch that finds an earlier failure gives up and may leave counts of arrivals behind
+    rng = np.random.default_rng(24)
+    bt = Batch(rng, pre, new, hkv, hd, 128)
+    q, z, before, first = check_mass(bt, hq, 0, 0, 0, rng)
+    ws, old, mass = mass_workspace(bt.T, 1, hq, hkv, hd), torch.from_numpy(before).to(dev()), torch.empty_like(first)
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        run_mass(bt, q, z, mass, workspace=ws, stream=st)
+    for turn in range(8):
+        dgp.dg_op_wait_selftest(20_000)
+        g.replay()
+        torch.cuda.synchronize()
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert e.value.code == dgp.DG_ETIMEOUT
+        dgp.dg_op_status()                                  # cleared
+        for _ in range(3):
+            mass.copy_(old)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            dgp.dg_op_status()
+            assert torch.equal(mass.view(torch.int32), first.view(torch.int32)), turn
+
+
 # ---- eviction ----------------------------------------------------------------------------
 
 class Cache:
@@ -312,10 +568,6 @@ def pool_view(pool):
     """The pool's bits in slot order: [n_pages][pg][heads][hd] int16."""
     from test_gpu_draft_ops import pool_rows
     return pool_rows(pool.view(torch.int16) if isinstance(pool, torch.Tensor) else pool)
-
-
-def same_floats(a, b):
-    return np.array_equal(np.asarray(a).view(np.uint32), np.asarray(b).view(np.uint32))
 
 
 def check_evict(c, sinks, recent, **call):
