@@ -10,18 +10,20 @@
 //
 // The scores are computed transposed, S^T = K Q^T, so that a key is a lane of the
 // tensor memory and a thread adds up its key's weights over the rows without any
-// exchange: a unit is 256 keys of a (sequence, KV head), two tiles of 128 with a warp
-// group each, which stay in shared memory while the tiles of up to 128 rows (tokens x
-// heads of the group, staged by one TMA copy) that see any of them go by.  Each row
-// tile read from L2 serves both key tiles.  With one row tile, the keys stream
-// and the rows stay in L2.  All blocks take equal ranges of the batch's (unit, row
-// tile) pairs, found on the device as in the tree attention; a unit that spans
-// several blocks leaves a partial sum per block in the workspace, and the block whose
-// sum arrives last adds them up in order: no block waits, results repeat bit for bit.
+// exchange.  A unit is 1 or 4 tiles of 128 keys of a (sequence, KV head): they stay in
+// shared memory while the tiles of up to 128 rows (tokens x heads of the group, staged
+// by one TMA copy) that see any of them go by.  With many row tiles a unit has 4 key
+// tiles, which share each row tile read from L2; with one, 1: the keys stream through
+// the ring, the row tile stays, and ranges come out even.  All blocks take equal ranges
+// of the batch's (unit, row tile) pairs, found on the device as in the tree attention;
+// a unit that spans several blocks leaves a partial sum per block in the workspace, and
+// the block whose sum arrives last adds them up in order: no block waits, results repeat
+// bit for bit.
 //
 // Roles of a block (384 threads): warp 0 copies keys out of the pre-swizzled pages,
-// warp 1 the row tiles and their log-sum-exps, warp 2 issues the products from one
-// thread, warps 4-7 and 8-11 take the exponentials of the first and second 128 keys.
+// warp 1 the row tiles and their log-sum-exps; of every other key tile warps 2 and 3
+// each issue the products from one thread and warps 4-7 and 8-11 take the
+// exponentials, through two buffers of tensor memory a group.
 #include <atomic>
 
 #include "attn_tc.cuh"
@@ -34,18 +36,20 @@ namespace {
 
 constexpr int kMassThreads = 384;
 constexpr int kMassCtas = 152;       // most blocks: one per SM
-constexpr int kMassKeys = 256;       // keys of a unit
+constexpr int kMassTiles = 4;        // most key tiles of a unit
+constexpr int kMassFew = 3;          // (key tile, row tile) pairs a block up to which units are single tiles
 constexpr int kMassUnitCost = 1;     // cost of starting a unit, in row tiles
 constexpr int kMassGaveUp = 64;      // status code of a block that gave up after an earlier kernel
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct MassArgs {
-  CUtensorMap q_map;  // rows [n_tok][Hq][hd], box 64 x G x T
+  CUtensorMap q_map, few_map;  // rows [n_tok][Hq][hd], boxes 64 x G x T and 64 x G x few
   KeyMass a;
-  int G, T, ctas;     // T: tokens of a row tile
+  int G, T, few, ctas;  // T: tokens of a row tile
+  int pg_shift;         // log2 of the page size, -1 where it is no power of two
   float scale_log2;
-  float *part;                // [2 kMassCtas][kMassKeys]: block c's first piece in 2 c, its last in 2 c + 1
-  unsigned long long *count;  // [kMassCtas]: pieces that have arrived of the unit that ends in block c
+  float *part;                // [2 kMassCtas][kMassTiles * 128]: block c's first piece in 2 c, its last in 2 c + 1
+  unsigned long long *count;  // [2][kMassCtas]: pieces that have arrived of the even and odd tiles of the unit that ends in block c
   unsigned long long ticket;
   int *err;
 };
@@ -53,36 +57,45 @@ struct MassArgs {
 template <int HD>
 struct MassSmem {
   static constexpr int HB = HD / 64;
-  static constexpr int KR = HD == 128 ? 2 : 3, QR = HD == 128 ? 3 : 4;  // ring depths
-  static constexpr int LR = QR + 2;  // log-sum-exps: those of pair i are written once the products of pair i - QR are
-                                     // done, which began when the exponentials of pair i - QR - 2 had been taken
-  static constexpr size_t tile = (size_t)HB * 16384;  // 128 keys or rows
+  static constexpr int KR = HD == 128 ? 4 : 8, QR = HD == 128 ? 3 : 4;  // ring depths, in tiles
+  static constexpr size_t tile = (size_t)HB * 16384;                    // 128 keys or rows
   static constexpr size_t kring = 0;
-  static constexpr size_t qring = kring + 2 * KR * tile;
+  static constexpr size_t qring = kring + KR * tile;
   static constexpr size_t lse = qring + QR * tile;
-  static constexpr size_t bars = lse + LR * 512;
-  static constexpr int n_bars = 2 * KR + 2 * QR + 4 + 1;  // full and empty of K, Q, S; drained
+  static constexpr size_t bars = lse + QR * 512;
+  static constexpr int n_bars = 2 * KR + 2 * QR + 8 + 2;  // full and empty of K, Q, S (2 buffers of each group); drained
   static constexpr size_t slot = bars + n_bars * 8;
   static constexpr size_t bytes = slot + 32;
 };
 
+// n = 0: nothing to do, or rows or slots outside the call's arrays.  Of its units of
+// `keys` keys those below `sink` and from `low` on hold a key which some token sees,
+// or a new key (it is set to 0 otherwise).
 struct MassSeq {
-  int row0, n, pre, tf, row_tiles, units;  // tf: the first token that counts
+  int row0, n, pre, tf, row_tiles, sink, low, units;  // tf: the first token that counts
   bool bad;
+  __device__ __forceinline__ int visits() const { return sink + units - low; }
+  __device__ __forceinline__ int unit(int i) const { return i < sink ? i : i - sink + low; }  // the i-th visited
 };
 
-__device__ __forceinline__ MassSeq load_seq(const MassArgs &p, int b) {
+__device__ __forceinline__ MassSeq load_seq(const MassArgs &p, int b, int keys) {
   MassSeq s;
   const int o0 = p.a.offsets[b], o1 = p.a.offsets[b + 1];
   s.row0 = o0;
   s.pre = p.a.prefix_lens[b];
-  const long long n = (long long)o1 - o0, keys = (long long)s.pre + n;
+  const long long n = (long long)o1 - o0, end = (long long)s.pre + n;
   const long long room = min((long long)p.a.max_pages * p.a.pg, (long long)0x7fffff00);
-  s.bad = n != 0 && (o0 < 0 || n < 0 || o1 > p.a.n_tok || s.pre < 0 || keys > room);
+  s.bad = n != 0 && (o0 < 0 || n < 0 || o1 > p.a.n_tok || s.pre < 0 || end > room);
   s.n = s.bad ? 0 : (int)n;
   s.tf = p.a.observe ? max(0, s.n - p.a.observe) : 0;
-  s.row_tiles = ceil_div(s.n - s.tf, p.T);
-  s.units = s.n ? (int)((keys + kMassKeys - 1) / kMassKeys) : 0;
+  s.row_tiles = s.n - s.tf <= p.T ? 1 : ceil_div(s.n - s.tf, p.T);
+  s.sink = s.low = s.units = 0;
+  if (s.n) {  // (keys: a power of two)
+    const int shift = 31 - __clz(keys);
+    s.units = (int)(((unsigned)s.pre + s.n + keys - 1) >> shift);
+    s.low = min(max(0, s.pre + s.tf - p.a.window + 1), s.pre) >> shift;
+    s.sink = min((int)(((unsigned)p.a.sinks + keys - 1) >> shift), s.low);
+  }
   return s;
 }
 
@@ -92,147 +105,209 @@ struct Tokens {
 };
 __device__ __forceinline__ Tokens seen_by(const MassArgs &p, const MassSeq &s, int j0, int j1) {
   Tokens t;
+  const int last = j1 - 1 - s.pre;  // (last + window where it is below n)
   t.t0 = max(s.tf, j0 - s.pre);
-  t.t1 = j0 < p.a.sinks ? s.n : (int)min((long long)s.n, (long long)j1 - 1 + p.a.window - s.pre);
+  t.t1 = j0 < p.a.sinks || last >= s.n - p.a.window ? s.n : last + p.a.window;
   return t;
 }
 
-// The row tiles of a unit: [first, first + count).  A unit with new keys that no
-// token sees takes a tile too: its new keys are set to 0.
+// The row tiles of a unit: [first, first + count), one at least.
 struct Rows {
   int first, count;
 };
-__device__ __forceinline__ Rows unit_rows(const MassArgs &p, const MassSeq &s, int u) {
-  const int j0 = u * kMassKeys, j1 = min(j0 + kMassKeys, s.pre + s.n);
-  const Tokens t = seen_by(p, s, j0, j1);
+__device__ __forceinline__ Rows unit_rows(const MassArgs &p, const MassSeq &s, int u, int keys) {
   Rows r;
-  r.first = r.count = 0;
-  if (t.t0 < t.t1) {
-    r.first = (t.t0 - s.tf) / p.T;
-    r.count = ceil_div(t.t1 - s.tf, p.T) - r.first;
-  } else if (j1 > s.pre) {
-    r.count = 1;
+  r.first = 0;
+  r.count = 1;
+  if (s.row_tiles > 1) {
+    const int j0 = u * keys;
+    const Tokens t = seen_by(p, s, j0, min(j0 + keys, s.pre + s.n));
+    if (t.t0 < t.t1) {
+      r.first = (t.t0 - s.tf) / p.T;
+      r.count = ceil_div(t.t1 - s.tf, p.T) - r.first;
+    }
   }
   return r;
 }
 
-// The next unit from u on that a token sees or that holds new keys: between the first
-// tokens and the first window there is none.
-__device__ __forceinline__ int next_unit(const MassArgs &p, const MassSeq &s, int u, Rows &r) {
-  r = unit_rows(p, s, u);
-  if (r.count == 0 && u < s.units) {
-    u = max(u, min(max(0, s.pre + s.tf - p.a.window + 1), s.pre) / kMassKeys);
-    r = unit_rows(p, s, u);
-  }
-  return u;
-}
+constexpr unsigned kMassMost = 1u << 30;  // more than an ascending batch's cost: offsets that overlap stop here
 
-// Cost of the units of one KV head.
-__device__ __forceinline__ int head_cost(const MassArgs &p, const MassSeq &s) {
+// Cost of the units of one KV head; run by the whole warp for one sequence.
+__device__ __forceinline__ int head_cost(const MassArgs &p, const MassSeq &s, int keys, int lane) {
+  const int n = s.visits();
+  if (s.row_tiles <= 1) return n * (1 + kMassUnitCost);
   int sum = 0;
-  Rows r;
 #pragma unroll 1
-  for (int u = next_unit(p, s, 0, r); u < s.units; u = next_unit(p, s, u + 1, r)) sum += r.count + kMassUnitCost;
-  return sum;
+  for (int i = lane; i < n; i += 32) sum += unit_rows(p, s, s.unit(i), keys).count + kMassUnitCost;
+  return (int)min(__reduce_add_sync(0xffffffffu, (unsigned)min(sum, 1 << 26)), kMassMost);
 }
 
-// The pieces of a block's range: row tiles [q0, q1) of unit (b, g, u).
+// A block's share: `count` cost units from unit `at` of sequence b on, of the equal
+// ranges of `per`; `tiles` key tiles of `keys` keys a unit.  Found by every warp for
+// itself, 32 sequences at a time, in three rounds: how much there is (units of one
+// tile where that is little, so that all blocks have some), its cost, and the
+// sequence in which the range begins.
+struct MassRange {
+  int b, at, count, per, tiles, keys;
+};
+__device__ __forceinline__ MassRange block_range(const MassArgs &p, int lane) {
+  MassRange r;
+  r.tiles = 1;
+  r.keys = 128;
+  r.b = r.at = r.count = r.per = 0;
+  unsigned first = 0;
+#pragma unroll 1
+  for (int round = 0; round < 3; ++round) {
+    unsigned total = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
+      MassSeq s = load_seq(p, min(b0 + lane, p.a.n_seqs - 1), r.keys);
+      if (b0 + lane >= p.a.n_seqs) s.n = s.units = s.low = s.sink = 0;
+      long long c = (long long)s.visits() * (1 + kMassUnitCost);
+      if (round == 0) {
+        c = (long long)s.visits() * s.row_tiles;
+        if (s.bad && blockIdx.x == 0 && threadIdx.x < 32 && p.err) atomicExch(p.err + 1, kBadSequence);
+      } else {
+#pragma unroll 1
+        for (unsigned many = __ballot_sync(0xffffffffu, s.n && s.row_tiles > 1); many; many &= many - 1) {
+          const int l = __ffs(many) - 1, h = head_cost(p, load_seq(p, b0 + l, r.keys), r.keys, lane);
+          if (lane == l) c = h;
+        }
+      }
+      const unsigned cost = (unsigned)min(c * p.a.Hkv, (long long)kMassMost);
+      unsigned incl = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl = min(incl + v, kMassMost);
+      }
+      if (round == 2) {
+        const unsigned end = min(total + incl, kMassMost), begin = end - min(cost, end);
+        const unsigned here = __ballot_sync(0xffffffffu, first >= begin && first < end);
+        if (here) {
+          const int l = __ffs(here) - 1;
+          r.b = b0 + l;
+          r.at = __shfl_sync(0xffffffffu, (int)(first - begin), l);
+          return r;
+        }
+      }
+      total = min(total + __shfl_sync(0xffffffffu, incl, 31), kMassMost);
+    }
+    if (round == 0) {
+      if (total > (unsigned)(kMassFew * p.ctas)) {
+        r.tiles = kMassTiles;
+        r.keys = 128 * kMassTiles;
+      }
+    } else if (round == 1) {
+      r.per = (int)((total + p.ctas - 1) / p.ctas);
+      const long long at = (long long)r.per * blockIdx.x;
+      if (at >= total) return r;
+      first = (unsigned)at;
+      r.count = (int)min((unsigned)r.per, total - first);
+    }
+  }
+  r.count = 0;
+  return r;
+}
+
+// The pieces of a block's range: row tiles [q0, q1) of unit u of (b, g), the i-th of
+// its sequence.  at: where the unit begins, relative to the range; left: what the
+// range holds behind the piece.
 struct MassWalk {
   MassSeq s;
   Rows r;
-  int b, g, u, q0, q1, at, left;
+  int keys, b, g, i, u, q0, q1, at, left;
   __device__ __forceinline__ void clip(int from, int n) {
     const int end = min(r.count + kMassUnitCost, from + n);
     q0 = max(0, from - kMassUnitCost);
     q1 = max(0, end - kMassUnitCost);
     left = n - (end - from);
   }
-  __device__ __forceinline__ bool begin(const MassArgs &p, int b_, int from, int n) {
-    b = b_;
-    s = load_seq(p, b);
-    const int head = head_cost(p, s);
-    g = from / head;
-    at = g * head - from;
-    u = next_unit(p, s, 0, r);
+  __device__ __forceinline__ void visit(const MassArgs &p) {
+    u = s.unit(i);
+    r = unit_rows(p, s, u, keys);
+  }
+  // Run by a whole warp.  false: the range holds no row tile.
+  __device__ __forceinline__ bool begin(const MassArgs &p, const MassRange &range, int lane) {
+    b = range.b;
+    keys = range.keys;
+    s = load_seq(p, b, keys);
+    const int head = head_cost(p, s, keys, lane), visits = s.visits();
+    g = range.at / head;
+    const int rem = range.at - g * head;
+    if (s.row_tiles <= 1) {
+      i = rem / (1 + kMassUnitCost);
+      at = i * (1 + kMassUnitCost) - rem;
+    } else {  // 32 units at a time
+      int before = 0;
+      i = visits - 1;
+      at = 0;
 #pragma unroll 1
-    while (at + r.count + kMassUnitCost <= 0) {  // (the head's last unit ends behind `from`)
-      at += r.count + kMassUnitCost;
-      u = next_unit(p, s, u + 1, r);
+      for (int k0 = 0; k0 < visits; k0 += 32) {
+        const int cost = k0 + lane < visits ? unit_rows(p, s, s.unit(k0 + lane), keys).count + kMassUnitCost : 0;
+        int incl = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, rem < before + incl);
+        if (here) {
+          const int l = __ffs(here) - 1;
+          i = k0 + l;
+          at = __shfl_sync(0xffffffffu, before + incl - cost - rem, l);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
     }
-    clip(-at, n);
+    visit(p);
+    clip(-at, range.count);
     return q0 < q1 || next(p);
   }
   __device__ __forceinline__ bool next(const MassArgs &p) {
     do {
       if (left <= 0) return false;
       at += r.count + kMassUnitCost;
-      u = next_unit(p, s, u + 1, r);
-      if (u >= s.units) {
+      if (++i == s.visits()) {
+        i = 0;
         if (++g == p.a.Hkv) {
           g = 0;
           do {
             if (++b >= p.a.n_seqs) return false;
-            s = load_seq(p, b);
+            s = load_seq(p, b, keys);
           } while (s.n == 0);
         }
-        u = next_unit(p, s, 0, r);
       }
+      visit(p);
       clip(0, left);
     } while (q0 == q1);
     return true;
   }
+  // Row tile q of the piece: its first token, its columns (rows).
+  __device__ __forceinline__ int token(const MassArgs &p, int q) const { return s.tf + (r.first + q) * p.T; }
+  __device__ __forceinline__ int columns(const MassArgs &p, int t0) const { return min(p.T, s.n - t0) * p.G; }
+  // Bit k: some key of the unit's tile k is seen by a token of [t0, t1) that counts.  Run by a whole warp.
+  __device__ __forceinline__ unsigned seen_tiles(const MassArgs &p, int t0, int t1, int lane) const {
+    const int j0 = u * keys + 128 * lane, end = s.pre + s.n;
+    bool sees = false;
+    if (128 * lane < keys && j0 < end) {
+      const Tokens t = seen_by(p, s, j0, min(j0 + 128, end));
+      sees = max(t.t0, t0) < min(t.t1, t1);
+    }
+    return __ballot_sync(0xffffffffu, sees);
+  }
+  __device__ __forceinline__ bool same_rows(const MassWalk &o, int q, int oq) const {
+    return b == o.b && g == o.g && r.first + q == o.r.first + oq;
+  }
 };
 
-// A block's share: `count` cost units from unit `at` of sequence b on, of the equal
-// ranges of `per`.  Found by every warp for itself.
-struct MassRange {
-  int b, at, count, per;
-};
-__device__ __forceinline__ MassRange block_range(const MassArgs &p, int lane) {
-  const int run = ceil_div(p.a.n_seqs, 32), lo = min(p.a.n_seqs, lane * run), hi = min(p.a.n_seqs, lo + run);
-  constexpr unsigned kMost = 1 << 30;  // more than an ascending batch's sum
-  unsigned mine = 0;
-#pragma unroll 1
-  for (int b = lo; b < hi; ++b) {
-    const MassSeq s = load_seq(p, b);
-    if (s.n) mine = min(mine + (unsigned)(p.a.Hkv * head_cost(p, s)), kMost);
-    if (s.bad && blockIdx.x == 0 && threadIdx.x < 32 && p.err) atomicExch(p.err + 1, kBadSequence);
-  }
-  unsigned incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl = min(incl + v, kMost);
-  }
-  const int total = (int)__shfl_sync(0xffffffffu, incl, 31);
-  MassRange r;
-  r.per = (int)(((unsigned)total + (unsigned)p.ctas - 1) / (unsigned)p.ctas);
-  const long long first = (long long)r.per * blockIdx.x;
-  r.count = (int)min((long long)r.per, total - first);
-  r.b = -1;
-  r.at = 0;
-  const int start = (int)min(first, (long long)total);
-  int at = (int)__shfl_up_sync(0xffffffffu, incl, 1);
-  if (lane == 0) at = 0;
-  const bool here = start >= at && start < (int)incl;
-  if (here) {
-#pragma unroll 1
-    for (int b = lo; b < hi; ++b) {
-      const MassSeq s = load_seq(p, b);
-      const int n = s.n ? p.a.Hkv * head_cost(p, s) : 0;
-      if (start < at + n) {
-        r.b = b;
-        r.at = start - at;
-        break;
-      }
-      at += n;
-    }
-  }
-  const int src = max(0, __ffs(__ballot_sync(0xffffffffu, here)) - 1);
-  r.b = __shfl_sync(0xffffffffu, r.b, src);
-  r.at = __shfl_sync(0xffffffffu, r.at, src);
-  if (r.b < 0) r.count = 0;
-  return r;
+// The entry of the page table for slot j of sequence b; slot: j's place in the page.
+__device__ __forceinline__ int page_entry(const MassArgs &p, int b, int j) {
+  return p.a.page_tables[(size_t)b * p.a.max_pages + (p.pg_shift >= 0 ? j >> p.pg_shift : j / p.a.pg)];
+}
+__device__ __forceinline__ int page_slot(const MassArgs &p, int j) {
+  return p.pg_shift >= 0 ? j & (p.a.pg - 1) : j % p.a.pg;
 }
 
 // A piece's arrival: true in the block whose piece is the unit's last to arrive.
@@ -255,7 +330,30 @@ __device__ __forceinline__ bool mass_wait(uint64_t *b, uint32_t parity, int *err
   return tc::mbar_try_wait(b, parity) || tc::mbar_wait(b, parity, err, code, abort);
 }
 
-__device__ __forceinline__ void mass_sync() { asm volatile("barrier.sync 6, 256;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t *r) {  // ties the loaded registers to the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+// tc::mma_bf16 with the low halves of the operands' descriptors: the high ones are
+// those of every K-major tile.
+__device__ __forceinline__ void mma_low(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accum) {
+  const uint64_t high = tc::sw128_desc(0) & 0xffffffff00000000ull;
+  tc::mma_bf16(d_tmem, high | a, high | b, idesc, accum);
+}
+
+// The four warps of a group meet.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("barrier.sync %0, 128;\n" ::"r"(1 + group) : "memory"); }
 
 template <int HD>
 __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_constant__ MassArgs p) {
@@ -264,9 +362,9 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
   extern __shared__ __align__(1024) unsigned char base[];
   uint64_t *k_full = (uint64_t *)(base + S::bars), *k_empty = k_full + KR;
   uint64_t *q_full = k_empty + KR, *q_empty = q_full + QR;
-  uint64_t *s_full = q_empty + QR, *s_empty = s_full + 2, *drained = s_empty + 2;
+  uint64_t *s_full = q_empty + QR, *s_empty = s_full + 4, *drained = s_empty + 4;
   uint32_t *tmem_slot = (uint32_t *)(base + S::slot);
-  volatile int *abort = (volatile int *)(tmem_slot + 1), *last = abort + 1;
+  volatile int *abort = (volatile int *)(tmem_slot + 1), *last = abort + 1;  // last: [2]
   float *lse2 = (float *)(base + S::lse);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (tc::smem_u32(base) & 1023u) {  // the operand tiles' swizzle needs it: the same in every block
@@ -281,65 +379,77 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     }
     for (int i = 0; i < QR; ++i) {
       tc::mbar_init(q_full + i, 1);
-      tc::mbar_init(q_empty + i, 1);
+      tc::mbar_init(q_empty + i, 10);  // the products of both groups, and the eight warps that read the log-sum-exps
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(s_full + i, 1);
-      tc::mbar_init(s_empty + i, 8);  // one arrival per warp
+      tc::mbar_init(s_empty + i, 4);  // one arrival per warp of the group
     }
     tc::mbar_init(drained, 1);
+    tc::mbar_init(drained + 1, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
   const MassRange range = block_range(p, lane);  // the same in every warp
   MassWalk w;
-  if (range.count <= 0 || !w.begin(p, range.b, range.at, range.count)) return;
+  if (range.count <= 0 || !w.begin(p, range, lane)) return;
+  const int tiles = range.tiles;
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(tc::smem_u32(tmem_slot)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
   unsigned long long status = 0;
-  if (warp == 4) {
+  if (warp == 4 || warp == 8)
     if (p.err) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];\n" : "=l"(status) : "l"(p.err - 1) : "memory");
-  }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (status >> 32) *abort = 1;  // an earlier kernel gave up
-  const uint32_t tmem = *tmem_slot;  // S^T of key tile k, buffer b: columns 128 (2 b + k)
+  const uint32_t tmem = *tmem_slot;  // S^T of group g, buffer b: columns 128 (2 g + b)
 
+  // Key tiles are numbered through the block's pieces: tile o = tiles x piece + k is
+  // taken by group o & 1.  The steps (row tile, key tile) of a group take its buffers
+  // in turn; steps in which no row sees a key are left out, everywhere alike.  A row
+  // tile that the next piece begins with again stays in its slot.
   if (warp == 0) {
-    // ---- keys: lane (half, hd block) copies 64 keys of 64 elements -----------------
+    // ---- keys: lane (tile, half, hd block) copies 64 keys of 64 elements -------------
     int slot = 0, phase = 0, issued = 0;
     bool ok = true, more = true;
+    const int k_lane = lane / (2 * HB), half = lane / HB & 1, blk = lane % HB;
+    // the half's entry of the page table; -2: not seen by any row (its page is not touched)
+    auto entry_of = [&](const MassWalk &x) {
+      const int j0 = x.u * x.keys + 128 * k_lane + 64 * half, end = x.s.pre + x.s.n;
+      if (k_lane >= tiles || j0 >= end) return -2;
+      const Tokens t = seen_by(p, x.s, j0, min(j0 + 64, end));
+      return t.t0 < t.t1 ? page_entry(p, x.b, j0) : -2;
+    };
+    int page = entry_of(w);
     while (ok && more) {
-      if (lane == 0) {
-        if (issued >= KR) ok = mass_wait(k_empty + slot, phase ^ 1, p.err, 65, abort);
-        if (*abort) ok = false;
-        if (ok) tc::mbar_expect_tx(k_full + slot, (uint32_t)(2 * S::tile));
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      if (lane < 4 * HB) {
-        const int half = lane / HB, blk = lane % HB, j0 = w.u * kMassKeys + 64 * half, end = w.s.pre + w.s.n;
-        unsigned char *d = base + S::kring + (size_t)slot * 2 * S::tile + (half >> 1) * S::tile + (size_t)blk * 16384 + (half & 1) * kAttnSlotHalfBytes;
-        const bf16 *src = nullptr;
-        if (j0 < end) {
-          const Tokens t = seen_by(p, w.s, j0, min(j0 + 64, end));
-          if (t.t0 < t.t1) {  // pages that hold no such key are not touched
-            const int page = p.a.page_tables[(size_t)w.b * p.a.max_pages + j0 / p.a.pg];
-            if (page >= 0 && page < p.a.n_pages)
-              src = p.a.k_pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)blk * p.a.pg * 64 + (size_t)(j0 % p.a.pg) * 64;
-          }
-        }
-        tc::bulk_load(d, src ? (const void *)src : (const void *)g_zero_half, kAttnSlotHalfBytes, k_full + slot);
-      }
-      ++issued;
-      if (++slot == KR) {
-        slot = 0;
-        phase ^= 1;
-      }
+      const void *src = g_zero_half;
+      if (page >= 0 && page < p.a.n_pages)
+        src = p.a.k_pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)blk * p.a.pg * 64 +
+              (size_t)page_slot(p, w.u * w.keys + 128 * k_lane + 64 * half) * 64;
+      unsigned used = w.seen_tiles(p, 0, w.s.n, lane);
       more = w.next(p);
+      if (more) page = entry_of(w);
+      for (; used; used &= used - 1) {
+        if (lane == 0) {
+          if (issued >= KR) ok = mass_wait(k_empty + slot, phase ^ 1, p.err, 65, abort);
+          if (*abort) ok = false;
+          if (ok) tc::mbar_expect_tx(k_full + slot, (uint32_t)S::tile);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (k_lane == __ffs(used) - 1)
+          tc::bulk_load(base + S::kring + (size_t)slot * S::tile + (size_t)blk * 16384 + half * kAttnSlotHalfBytes, src, kAttnSlotHalfBytes,
+                        k_full + slot);
+        __syncwarp();
+        ++issued;
+        if (++slot == KR) {
+          slot = 0;
+          phase ^= 1;
+        }
+      }
     }
     if (!ok && lane == 0) {  // gave up: wait (bounded) for the copies in flight
       for (int i = issued - 1; i >= 0 && i >= issued - KR; --i) {
@@ -350,47 +460,54 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     }
   } else if (warp == 1) {
     // ---- row tiles and their log-sum-exps ------------------------------------------
-    int slot = 0, phase = 0, issued = 0, entry = 0;
+    int slot = 0, phase = 0, issued = 0, q = w.q0;
     bool ok = true, more = true;
-    while (ok && more) {
-      for (int q = w.q0; ok && q < w.q1; ++q) {
-        const int t0 = w.s.tf + (w.r.first + q) * p.T, cols = min(p.T, w.s.n - t0) * p.G;
-        // column c: token t0 + c / G, head g G + c % G; rows without a key (-inf) weigh nothing
-        float v[4];
+    while (more) {
+      const int t0 = w.token(p, q), cols = w.columns(p, t0);
+      // column c: token t0 + c / G, head g G + c % G; kept negative, in units of log2;
+      // rows without a key (-inf) weigh nothing
+      float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int c = lane + 32 * k, t = c / p.G;
-          v[k] = 0.0f;
-          if (c < cols) {
-            v[k] = p.a.lse[(size_t)(w.s.row0 + t0 + t) * p.a.Hq + w.g * p.G + c - t * p.G] * kLog2e;
-            if (v[k] == __int_as_float(0xff800000)) v[k] = __int_as_float(0x7f800000);
-          }
+      for (int k = 0; k < 4; ++k) {
+        const int c = lane + 32 * k;
+        v[k] = 0.0f;
+        if (c < cols) {
+          const int t = c / p.G;
+          v[k] = p.a.lse[(size_t)(w.s.row0 + t0 + t) * p.a.Hq + w.g * p.G + c - t * p.G] * -kLog2e;
+          if (v[k] == __int_as_float(0x7f800000)) v[k] = -v[k];
         }
-        if (lane == 0) {
-          if (issued >= QR) ok = mass_wait(q_empty + slot, phase ^ 1, p.err, 66, abort);
-          if (*abort) ok = false;
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) lse2[128 * entry + lane + 32 * k] = v[k];
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t box = 128u * p.T * p.G;
-          tc::mbar_expect_tx(q_full + slot, HB * box);
-#pragma unroll
-          for (int blk = 0; blk < HB; ++blk)
-            tc::tma_load_3d(base + S::qring + (size_t)slot * S::tile + (size_t)blk * 16384, &p.q_map, 64 * blk, w.g * p.G, w.s.row0 + t0,
-                            q_full + slot);
-        }
-        ++issued;
-        if (++slot == QR) {
-          slot = 0;
-          phase ^= 1;
-        }
-        if (++entry == S::LR) entry = 0;
       }
-      more = ok && w.next(p);
+      if (lane == 0) {
+        if (issued >= QR) ok = mass_wait(q_empty + slot, phase ^ 1, p.err, 66, abort);
+        if (*abort) ok = false;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lse2[128 * slot + lane + 32 * k] = v[k];
+      __syncwarp();
+      if (lane == 0) {
+        const bool few = cols <= p.few * p.G;
+        const CUtensorMap *map = few ? &p.few_map : &p.q_map;
+        tc::mbar_expect_tx(q_full + slot, HB * 128u * (few ? p.few : p.T) * p.G);
+#pragma unroll
+        for (int blk = 0; blk < HB; ++blk)
+          tc::tma_load_3d(base + S::qring + (size_t)slot * S::tile + (size_t)blk * 16384, map, 64 * blk, w.g * p.G, w.s.row0 + t0, q_full + slot);
+      }
+      ++issued;
+      if (++slot == QR) {
+        slot = 0;
+        phase ^= 1;
+      }
+      // the next row tile that is another one
+      const MassWalk was = w;
+      const int was_q = q;
+      do {
+        if (++q >= w.q1) {
+          more = w.next(p);
+          q = w.q0;
+        }
+      } while (more && w.same_rows(was, q, was_q));
     }
     if (!ok && lane == 0) {
       for (int i = issued - 1; i >= 0 && i >= issued - QR; --i) {
@@ -399,121 +516,149 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         }
       }
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
     // ---- S^T = K Q^T -----------------------------------------------------------------
-    if (lane == 0) {
-      bool ok = true, more = true;
-      int ks = 0, kphase = 0, qs = 0, qphase = 0, i = 0;
-      while (ok && more) {
-        ok = mass_wait(k_full + ks, kphase, p.err, 67, abort);
-        for (int q = w.q0; ok && q < w.q1; ++q, ++i) {
-          const int buf = i & 1, t0 = w.s.tf + (w.r.first + q) * p.T, cols = min(p.T, w.s.n - t0) * p.G;
-          if (i >= 2) ok = mass_wait(s_empty + buf, ((i >> 1) - 1) & 1, p.err, 68, abort);
-          ok = ok && mass_wait(q_full + qs, qphase, p.err, 69, abort);
-          if (!ok) break;
-          tc::fence_after();
-          const uint32_t idesc = tc::idesc_bf16(128, (cols + 15) & ~15);
+    bool ok = true, more = true, fresh = true;
+    const int g = warp - 2;
+    int ks = 0, kphase = 0, qs = 0, qphase = 0, order = 0, step = 0;
+    const uint32_t kdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::kring)), qdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::qring));
+    while (ok && more) {
+      const MassWalk was = w;
+      more = w.next(p);
+      const unsigned used = was.seen_tiles(p, 0, was.s.n, lane);
+      const int n_used = __popc(used);
+      int ring = 0;  // key tiles of the unit that have arrived, from slot ks on
+      auto arrived = [&]() {
+        const int slot = ks + ring;
+        ++ring;
+        return mass_wait(k_full + (slot < KR ? slot : slot - KR), slot < KR ? kphase : kphase ^ 1, p.err, 67, abort);
+      };
+      for (int q = was.q0; ok && q < was.q1; ++q) {
+        const int t0 = was.token(p, q), cols = was.columns(p, t0);
+        // the group's: every other one
+        unsigned live = was.seen_tiles(p, t0, t0 + p.T, lane) & (0x55555555u << ((order + g) & 1));
+        if (fresh) ok = mass_wait(q_full + qs, qphase, p.err, 69, abort);
+        const uint32_t idesc = tc::idesc_bf16(128, (cols + 15) & ~15);
+        for (; ok && live; live &= live - 1) {
+          const int k = __ffs(live) - 1, at = __popc(used & ((1u << k) - 1));
+          while (ok && ring <= at) ok = arrived();
+          int slot = ks + at;
+          if (slot >= KR) slot -= KR;
+          const int buf = 2 * g + (step & 1);
+          if (ok && step >= 2) ok = mass_wait(s_empty + buf, ((step >> 1) - 1) & 1, p.err, 68, abort);
+          ++step;
+          __syncwarp();
+          if (ok && lane == 0) {
+            tc::fence_after();
+            const uint32_t a = kdesc + slot * (uint32_t)(S::tile >> 4), b = qdesc + qs * (uint32_t)(S::tile >> 4);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint64_t adesc = tc::sw128_desc(tc::smem_u32(base + S::kring + (size_t)(2 * ks + k) * S::tile + (size_t)(kk >> 2) * 16384)) + 2 * (kk & 3);
-              const uint64_t bdesc = tc::sw128_desc(tc::smem_u32(base + S::qring + (size_t)qs * S::tile + (size_t)(kk >> 2) * 16384)) + 2 * (kk & 3);
-              tc::mma_bf16(tmem + 128 * (2 * buf + k), adesc, bdesc, idesc, kk ? 1u : 0u);
-            }
+            for (int kk = 0; kk < HD / 16; ++kk)
+              mma_low(tmem + 128 * buf, a + (kk >> 2) * 1024 + 2 * (kk & 3), b + (kk >> 2) * 1024 + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+            tc::mma_commit(s_full + buf);
           }
-          tc::mma_commit(s_full + buf);
-          tc::mma_commit(q_empty + qs);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        // the row tile is done with unless the next piece begins with it
+        fresh = q + 1 < was.q1 || !more || !was.same_rows(w, q, w.q0);
+        if (ok && fresh) {
+          if (lane == 0) tc::mma_commit(q_empty + qs);
           if (++qs == QR) {
             qs = 0;
             qphase ^= 1;
           }
         }
-        if (!ok) break;
-        tc::mma_commit(k_empty + ks);
+      }
+      while (ok && ring < n_used) ok = arrived();
+      for (unsigned left = used; ok && left; left &= left - 1) {  // (a key tile is one group's)
+        if (lane == 0 && ((order + __ffs(left) - 1) & 1) == g) tc::mma_commit(k_empty + ks);
         if (++ks == KR) {
           ks = 0;
           kphase ^= 1;
         }
-        more = w.next(p);
       }
+      ok = __all_sync(0xffffffffu, ok);
+      order += tiles;
+    }
+    if (lane == 0) {
       if (!ok) {  // gave up: wait (bounded) for the products in flight
-        tc::mma_commit(drained);
+        tc::mma_commit(drained + g);
         const long long t0 = clock64();
-        while (!tc::mbar_try_wait(drained, 0) && clock64() - t0 < tc::kWaitCycles) {
+        while (!tc::mbar_try_wait(drained + g, 0) && clock64() - t0 < tc::kWaitCycles) {
         }
       }
     }
   } else if (warp >= 4) {
-    // ---- weights: thread = key ---------------------------------------------------------
-    const int k = (warp - 4) >> 2, tid = threadIdx.x - 128;  // tid: the key's place in the unit
+    // ---- weights: thread = key, up to two key tiles of a unit ---------------------------
+    const int g = (warp - 4) >> 2, row = (threadIdx.x - 128) & 127;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const unsigned long long up = p.ticket + (uint32_t)status;  // (thread 0 of these warps)
-    // Where the key's weight lies: < 0 where none is written (behind the sequence,
-    // not seen by any row and not new, on a bad page), and what it was.
-    auto place = [&](const MassWalk &u, float &old) {
-      const int j = u.u * kMassKeys + tid;
+    const unsigned long long up = p.ticket + (uint32_t)status;  // (the group's first warp)
+    const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
+    int order = 0, piece = 0, slot = 0, step = 0;
+    bool ok = true;
+    // The thread's keys are those of tiles k0 and k0 + 2 (where the unit has them).
+    // entry: the key's entry of the page table, -2 where no weight is written
+    // (behind the sequence, neither new nor seen by any row).
+    auto entry = [&](const MassWalk &x, int k) {
+      const int j = x.u * x.keys + 128 * k + row;
+      if (k >= tiles || j >= x.s.pre + x.s.n) return -2;
+      const Tokens t = seen_by(p, x.s, j, j + 1);
+      return j >= x.s.pre || t.t0 < t.t1 ? page_entry(p, x.b, j) : -2;
+    };
+    // where the weight lies (< 0: none is written), and what it was
+    auto place = [&](const MassWalk &x, int k, int page, float &old) {
+      const int j = x.u * x.keys + 128 * k + row;
       long long at = -1;
       old = 0.0f;
-      if (j < u.s.pre + u.s.n) {
-        const Tokens t = seen_by(p, u.s, j, j + 1);
-        if (j >= u.s.pre || t.t0 < t.t1) {
-          const int page = p.a.page_tables[(size_t)u.b * p.a.max_pages + j / p.a.pg];
-          if (page >= 0 && page < p.a.n_pages) {
-            at = ((long long)page * p.a.Hkv + u.g) * p.a.pg + j % p.a.pg;
-            if (j < u.s.pre) old = p.a.mass[at];
-          } else if (p.err) {
-            atomicExch(p.err + 1, kBadPage);
-          }
-        }
+      if (page >= 0 && page < p.a.n_pages) {
+        at = ((long long)page * p.a.Hkv + x.g) * p.a.pg + page_slot(p, j);
+        if (j < x.s.pre) old = p.a.mass[at];
+      } else if (page != -2 && p.err) {
+        atomicExch(p.err + 1, kBadPage);
       }
       return at;
     };
-    int i = 0, piece = 0, entry = 0;
-    float old;
-    long long at = place(w, old);
-    bool ok = true;
+    long long at[2];
+    float old[2];
+    int page[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) page[m] = entry(w, g + 2 * m);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) at[m] = place(w, g + 2 * m, page[m], old[m]);
     while (true) {
+      const int k0 = (order + g) & 1;  // (with one tile a unit, every other unit is the group's)
       MassWalk nx = w;
       const bool more = nx.next(p);
-      float next_old = 0.0f;
-      long long next_at = -1;
-      if (more) next_at = place(nx, next_old);
-      const int j = w.u * kMassKeys + tid;
-      float sum = 0.0f;
-      for (int q = w.q0; q < w.q1; ++q, ++i) {
-        const int buf = i & 1, t0 = w.s.tf + (w.r.first + q) * p.T, cols = min(p.T, w.s.n - t0) * p.G;
-        // the key's columns [c0, c1): tokens from its own on, up to the window's end
-        const long long far = (long long)j + p.a.window - w.s.pre - t0;
-        const int c0 = min(max(j - w.s.pre - t0, 0), 128) * p.G;
-        const int c1 = j < p.a.sinks ? cols : (int)max(0ll, min((long long)cols, far * p.G));
-        if (!mass_wait(s_full + buf, (i >> 1) & 1, p.err, 70, abort)) ok = false;
-        __syncwarp();
-        tc::fence_after();
-        const float *ls = lse2 + 128 * entry;
-        const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
-        f32x2 s0 = pair(0.0f, 0.0f), s1 = s0;
+      const int next_k0 = (order + tiles + g) & 1;
+      if (more) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) page[m] = entry(nx, next_k0 + 2 * m);
+      }
+      float sum[2] = {0.0f, 0.0f};
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t x[32];
-          tc::tmem_ld32(tmem + 128 * (2 * buf + k) + lane_off + c, x);
-          float4 l[8];
-#pragma unroll
-          for (int m = 0; m < 8; ++m) l[m] = *(const float4 *)(ls + c + 4 * m);
-          tc::tmem_ld_wait(x);
-          if (c + 32 >= cols) {  // the tile's last columns: the buffer is free for the next but one
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) attn_arrive(s_empty + buf);
-          }
-          const bool all = __all_sync(0xffffffffu, c0 <= c && c1 >= c + 32);
-#pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const float2 d = split(fma2(pair(__uint_as_float(x[4 * m]), __uint_as_float(x[4 * m + 1])), scale2, pair(-l[m].x, -l[m].y)));
-            const float2 e = split(fma2(pair(__uint_as_float(x[4 * m + 2]), __uint_as_float(x[4 * m + 3])), scale2, pair(-l[m].z, -l[m].w)));
+      for (int q = w.q0; q < w.q1; ++q) {
+        const int t0 = w.token(p, q), cols = w.columns(p, t0);
+        const unsigned live = w.seen_tiles(p, t0, t0 + p.T, lane) >> k0;
+        const float *ls = lse2 + 128 * slot;
+#pragma unroll 1
+        for (int m = 0; m < 2; ++m) {
+          if (!(live >> (2 * m) & 1)) continue;
+          const int buf = 2 * g + (step & 1), j = w.u * w.keys + 128 * (k0 + 2 * m) + row;
+          const uint32_t col = tmem + 128 * buf + lane_off;
+          // the key's columns [c0, c1): tokens from its own on, up to the window's end
+          const int away = j - w.s.pre - t0, span = min(p.T, w.s.n - t0);
+          const int c0 = min(max(away, 0), 128) * p.G;
+          const int c1 = j < p.a.sinks || away >= span - p.a.window ? cols : max(0, away + p.a.window) * p.G;
+          if (!mass_wait(s_full + buf, (step >> 1) & 1, p.err, 70, abort)) ok = false;
+          ++step;
+          __syncwarp();
+          tc::fence_after();
+          f32x2 s0 = pair(0.0f, 0.0f), s1 = s0;
+          // 2^(scale x - lse) of four columns, added up
+          auto add4 = [&](const uint32_t *y, float4 l, int cc, bool all) {
+            const float2 d = split(fma2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), scale2, pair(l.x, l.y)));
+            const float2 e = split(fma2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), scale2, pair(l.z, l.w)));
             float a0 = ex2(d.x), a1 = ex2(d.y), a2 = ex2(e.x), a3 = ex2(e.y);
             if (!all) {
-              const int cc = c + 4 * m;
               a0 = cc >= c0 && cc < c1 ? a0 : 0.0f;
               a1 = cc + 1 >= c0 && cc + 1 < c1 ? a1 : 0.0f;
               a2 = cc + 2 >= c0 && cc + 2 < c1 ? a2 : 0.0f;
@@ -521,36 +666,84 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
             }
             s0 = add2(s0, pair(a0, a1));
             s1 = add2(s1, pair(a2, a3));
+          };
+          auto release = [&]() {  // the buffer is free for the step after next
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) attn_arrive(s_empty + buf);
+          };
+          // (few instructions, run over and over: a loop that is unrolled for all
+          // columns and both forms waits for its instructions)
+          if (__all_sync(0xffffffffu, c0 == 0 && c1 == 128)) {
+            uint32_t x[2][32];
+            tc::tmem_ld32(col, x[0]);
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {
+              tc::tmem_ld_wait(x[0]);
+              tc::tmem_ld32(col + c + 32, x[1]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) add4(x[0] + 4 * i, *(const float4 *)(ls + c + 4 * i), 0, true);
+              tc::tmem_ld_wait(x[1]);
+              if (c == 0) tc::tmem_ld32(col + 64, x[0]);
+              else release();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) add4(x[1] + 4 * i, *(const float4 *)(ls + c + 32 + 4 * i), 0, true);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 16) {
+              uint32_t x[16];
+              tmem_ld16(col + c, x);
+              tmem_ld_wait16(x);
+              if (c + 16 >= cols) release();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) add4(x + 4 * i, *(const float4 *)(ls + c + 4 * i), c + 4 * i, false);
+            }
           }
+          const float2 r = split(add2(s0, s1));
+          if (m) sum[1] += r.x + r.y;
+          else sum[0] += r.x + r.y;
         }
-        const float2 r = split(add2(s0, s1));
-        sum += r.x + r.y;
-        if (++entry == S::LR) entry = 0;
+        if (q + 1 < w.q1 || !more || !w.same_rows(nx, q, nx.q0)) {  // done with the row tile's log-sum-exps
+          __syncwarp();
+          if (lane == 0) attn_arrive(q_empty + slot);
+          if (++slot == QR) slot = 0;
+        }
       }
       if (w.q0 == 0 && w.q1 == w.r.count) {
-        if (at >= 0 && ok) p.a.mass[at] = old + sum;
-      } else {
-        // a piece: cost units begin .. of the unit, relative to the first block's range
-        const int slot = 2 * blockIdx.x + (piece ? 1 : 0);
-        p.part[(size_t)slot * kMassKeys + tid] = sum;
-        const int begin = range.per * (int)blockIdx.x + w.at, tiles = begin + kMassUnitCost;
-        const int b0 = tiles / range.per, b1 = (tiles + w.r.count - 1) / range.per;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          if (at[m] >= 0 && ok) p.a.mass[at[m]] = old[m] + sum[m];
+      } else if (k0 < tiles) {
+        // a piece: the unit begins at cost unit `begin` of all ranges
+        const int to = 2 * blockIdx.x + (piece ? 1 : 0);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          if (k0 + 2 * m < tiles) p.part[((size_t)to * kMassTiles + k0 + 2 * m) * 128 + row] = sum[m];
+        const int begin = range.per * (int)blockIdx.x + w.at, first = begin + kMassUnitCost;
+        const int b0 = first / range.per, b1 = (first + w.r.count - 1) / range.per;
         const int slot0 = 2 * b0 + (begin > b0 * range.per ? 1 : 0);  // a piece of the unit before comes first there
         __threadfence();
-        mass_sync();
-        if (tid == 0) *last = !*abort && arrive_last(p.count + b1, up, b1 - b0 + 1);
-        mass_sync();
-        if (*last && at >= 0) {
+        group_sync(g);
+        if (row == 0) last[g] = !*abort && arrive_last(p.count + (size_t)k0 * kMassCtas + b1, up, b1 - b0 + 1);
+        group_sync(g);
+        if (last[g]) {
           __threadfence();
-          float total = __ldcg(p.part + (size_t)slot0 * kMassKeys + tid);
-          for (int b = b0 + 1; b <= b1; ++b) total += __ldcg(p.part + (size_t)2 * b * kMassKeys + tid);
-          p.a.mass[at] = old + total;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (at[m] < 0) continue;
+            const float *src = p.part + (size_t)(k0 + 2 * m) * 128 + row;
+            float total = __ldcg(src + (size_t)slot0 * kMassTiles * 128);
+            for (int b = b0 + 1; b <= b1; ++b) total += __ldcg(src + (size_t)2 * b * kMassTiles * 128);
+            p.a.mass[at[m]] = old[m] + total;
+          }
         }
       }
       if (!more) break;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) at[m] = place(nx, next_k0 + 2 * m, page[m], old[m]);
       w = nx;
-      at = next_at;
-      old = next_old;
+      order += tiles;
       ++piece;
     }
   }
@@ -566,8 +759,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
 
 struct MassWorkspace {
   static constexpr size_t part = 0;
-  static constexpr size_t count = part + (size_t)2 * kMassCtas * kMassKeys * 4;
-  static constexpr size_t bytes = count + (size_t)kMassCtas * 8;
+  static constexpr size_t count = part + (size_t)2 * kMassCtas * kMassTiles * 128 * 4;
+  static constexpr size_t bytes = count + (size_t)2 * kMassCtas * 8;
 };
 
 // Blocks of a launch on the current device, asked once.
@@ -614,7 +807,10 @@ cudaError_t key_mass(const KeyMass &a, void *ws, int *err, cudaStream_t st) {
   p.count = (unsigned long long *)((unsigned char *)ws + MassWorkspace::count);
   p.ticket = new_ticket();
   p.err = err;
-  const cudaError_t e = rows_map(&p.q_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.T);
+  p.few = max(1, 16 / p.G);
+  p.pg_shift = (a.pg & (a.pg - 1)) ? -1 : __builtin_ctz(a.pg);
+  cudaError_t e = rows_map(&p.q_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.T);
+  if (e == cudaSuccess) e = rows_map(&p.few_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.few);
   if (e != cudaSuccess) return e;
   return a.hd == 128 ? launch_mass<128>(p, st) : launch_mass<64>(p, st);
 }
