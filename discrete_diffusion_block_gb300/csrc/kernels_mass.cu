@@ -20,10 +20,10 @@
 // the block whose sum arrives last adds them up in order: no block waits, results repeat
 // bit for bit.
 //
-// Roles of a block (384 threads): warp 0 copies keys out of the pre-swizzled pages,
-// warp 1 the row tiles and their log-sum-exps; of every other key tile warps 2 and 3
-// each issue the products from one thread and warps 4-7 and 8-11 take the
-// exponentials, through two buffers of tensor memory a group.
+// Roles of a block (640 threads): warp 0 copies keys out of the pre-swizzled pages,
+// warp 1 the row tiles and their log-sum-exps; warps 2 and 3 issue the products of
+// every other key tile from one thread each; warps 4-19 take the exponentials, four
+// warps a key tile, four key tiles at a time.
 #include <atomic>
 
 #include "attn_tc.cuh"
@@ -34,7 +34,7 @@ namespace dg {
 
 namespace {
 
-constexpr int kMassThreads = 384;
+constexpr int kMassThreads = 640;
 constexpr int kMassCtas = 152;       // most blocks: one per SM
 constexpr int kMassTiles = 4;        // most key tiles of a unit
 constexpr int kMassFew = 3;          // (key tile, row tile) pairs a block up to which units are single tiles
@@ -49,7 +49,7 @@ struct MassArgs {
   int pg_shift;         // log2 of the page size, -1 where it is no power of two
   float scale_log2;
   float *part;                // [2 kMassCtas][kMassTiles * 128]: block c's first piece in 2 c, its last in 2 c + 1
-  unsigned long long *count;  // [2][kMassCtas]: pieces that have arrived of the even and odd tiles of the unit that ends in block c
+  unsigned long long *count;  // [kMassTiles][kMassCtas]: pieces that have arrived of tile k of the unit that ends in block c
   unsigned long long ticket;
   int *err;
 };
@@ -63,9 +63,9 @@ struct MassSmem {
   static constexpr size_t qring = kring + KR * tile;
   static constexpr size_t lse = qring + QR * tile;
   static constexpr size_t bars = lse + QR * 512;
-  static constexpr int n_bars = 2 * KR + 2 * QR + 8 + 2;  // full and empty of K, Q, S (2 buffers of each group); drained
+  static constexpr int n_bars = 2 * KR + 2 * QR + 8 + 2;  // full and empty of K, Q, S (one buffer a group); drained
   static constexpr size_t slot = bars + n_bars * 8;
-  static constexpr size_t bytes = slot + 32;
+  static constexpr size_t bytes = slot + 8 + 4 * kMassTiles;
 };
 
 // n = 0: nothing to do, or rows or slots outside the call's arrays.  Of its units of
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
   uint64_t *q_full = k_empty + KR, *q_empty = q_full + QR;
   uint64_t *s_full = q_empty + QR, *s_empty = s_full + 4, *drained = s_empty + 4;
   uint32_t *tmem_slot = (uint32_t *)(base + S::slot);
-  volatile int *abort = (volatile int *)(tmem_slot + 1), *last = abort + 1;  // last: [2]
+  volatile int *abort = (volatile int *)(tmem_slot + 1), *last = abort + 1;  // last: [kMassTiles]
   float *lse2 = (float *)(base + S::lse);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (tc::smem_u32(base) & 1023u) {  // the operand tiles' swizzle needs it: the same in every block
@@ -375,11 +375,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     *abort = 0;
     for (int i = 0; i < KR; ++i) {
       tc::mbar_init(k_full + i, 1);
-      tc::mbar_init(k_empty + i, 1);
+      tc::mbar_init(k_empty + i, 2);  // both issuing warps wait for all key tiles: none is replaced before both have
     }
     for (int i = 0; i < QR; ++i) {
       tc::mbar_init(q_full + i, 1);
-      tc::mbar_init(q_empty + i, 10);  // the products of both groups, and the eight warps that read the log-sum-exps
+      tc::mbar_init(q_empty + i, 18);  // the products of both warps, and the sixteen that read the log-sum-exps
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(s_full + i, 1);
@@ -399,18 +399,18 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
   unsigned long long status = 0;
-  if (warp == 4 || warp == 8)
+  if (warp >= 4 && !(warp & 3))
     if (p.err) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];\n" : "=l"(status) : "l"(p.err - 1) : "memory");
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   if (status >> 32) *abort = 1;  // an earlier kernel gave up
-  const uint32_t tmem = *tmem_slot;  // S^T of group g, buffer b: columns 128 (2 g + b)
+  const uint32_t tmem = *tmem_slot;  // S^T of group g: columns 128 g
 
   // Key tiles are numbered through the block's pieces: tile o = tiles x piece + k is
-  // taken by group o & 1.  The steps (row tile, key tile) of a group take its buffers
-  // in turn; steps in which no row sees a key are left out, everywhere alike.  A row
-  // tile that the next piece begins with again stays in its slot.
+  // taken by group o & 3, its products issued by warp 2 + (o & 1).  Steps (row tile,
+  // key tile) in which no row sees a key are left out, everywhere alike.  A row tile
+  // that the next piece begins with again stays in its slot.
   if (warp == 0) {
     // ---- keys: lane (tile, half, hd block) copies 64 keys of 64 elements -------------
     int slot = 0, phase = 0, issued = 0;
@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
   } else if (warp < 4) {
     // ---- S^T = K Q^T -----------------------------------------------------------------
     bool ok = true, more = true, fresh = true;
-    const int g = warp - 2;
-    int ks = 0, kphase = 0, qs = 0, qphase = 0, order = 0, step = 0;
+    const int half = warp - 2;
+    int ks = 0, kphase = 0, qs = 0, qphase = 0, order = 0, step0 = 0, step1 = 0;  // steps of groups half, half + 2
     const uint32_t kdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::kring)), qdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::qring));
     while (ok && more) {
       const MassWalk was = w;
@@ -535,8 +535,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       };
       for (int q = was.q0; ok && q < was.q1; ++q) {
         const int t0 = was.token(p, q), cols = was.columns(p, t0);
-        // the group's: every other one
-        unsigned live = was.seen_tiles(p, t0, t0 + p.T, lane) & (0x55555555u << ((order + g) & 1));
+        unsigned live = was.seen_tiles(p, t0, t0 + p.T, lane) & (0x55555555u << ((order + half) & 1));  // this warp's
         if (fresh) ok = mass_wait(q_full + qs, qphase, p.err, 69, abort);
         const uint32_t idesc = tc::idesc_bf16(128, (cols + 15) & ~15);
         for (; ok && live; live &= live - 1) {
@@ -544,17 +543,16 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
           while (ok && ring <= at) ok = arrived();
           int slot = ks + at;
           if (slot >= KR) slot -= KR;
-          const int buf = 2 * g + (step & 1);
-          if (ok && step >= 2) ok = mass_wait(s_empty + buf, ((step >> 1) - 1) & 1, p.err, 68, abort);
-          ++step;
+          const int g = (order + k) & 3, step = g >= 2 ? step1++ : step0++;
+          if (ok && step) ok = mass_wait(s_empty + g, (step - 1) & 1, p.err, 68, abort);
           __syncwarp();
           if (ok && lane == 0) {
             tc::fence_after();
             const uint32_t a = kdesc + slot * (uint32_t)(S::tile >> 4), b = qdesc + qs * (uint32_t)(S::tile >> 4);
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk)
-              mma_low(tmem + 128 * buf, a + (kk >> 2) * 1024 + 2 * (kk & 3), b + (kk >> 2) * 1024 + 2 * (kk & 3), idesc, kk ? 1u : 0u);
-            tc::mma_commit(s_full + buf);
+              mma_low(tmem + 128 * g, a + (kk >> 2) * 1024 + 2 * (kk & 3), b + (kk >> 2) * 1024 + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+            tc::mma_commit(s_full + g);
           }
           ok = __all_sync(0xffffffffu, ok);
         }
@@ -569,8 +567,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         }
       }
       while (ok && ring < n_used) ok = arrived();
-      for (unsigned left = used; ok && left; left &= left - 1) {  // (a key tile is one group's)
-        if (lane == 0 && ((order + __ffs(left) - 1) & 1) == g) tc::mma_commit(k_empty + ks);
+      for (unsigned left = used; ok && left; left &= left - 1) {
+        if (lane == 0) {
+          if (((order + __ffs(left) - 1) & 1) == half) tc::mma_commit(k_empty + ks);
+          else attn_arrive(k_empty + ks);
+        }
         if (++ks == KR) {
           ks = 0;
           kphase ^= 1;
@@ -581,74 +582,63 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     }
     if (lane == 0) {
       if (!ok) {  // gave up: wait (bounded) for the products in flight
-        tc::mma_commit(drained + g);
+        tc::mma_commit(drained + half);
         const long long t0 = clock64();
-        while (!tc::mbar_try_wait(drained + g, 0) && clock64() - t0 < tc::kWaitCycles) {
+        while (!tc::mbar_try_wait(drained + half, 0) && clock64() - t0 < tc::kWaitCycles) {
         }
       }
     }
   } else if (warp >= 4) {
-    // ---- weights: thread = key, up to two key tiles of a unit ---------------------------
-    const int g = (warp - 4) >> 2, row = (threadIdx.x - 128) & 127;
-    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const unsigned long long up = p.ticket + (uint32_t)status;  // (the group's first warp)
+    // ---- weights: thread = key of tile k of the unit ------------------------------------
+    const int g = (warp - 4) >> 2, row = threadIdx.x & 127;
+    const uint32_t col = tmem + 128 * g + ((uint32_t)(32 * (warp & 3)) << 16);
     const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
-    int order = 0, piece = 0, slot = 0, step = 0;
-    bool ok = true;
-    // The thread's keys are those of tiles k0 and k0 + 2 (where the unit has them).
-    // entry: the key's entry of the page table, -2 where no weight is written
-    // (behind the sequence, neither new nor seen by any row).
-    auto entry = [&](const MassWalk &x, int k) {
-      const int j = x.u * x.keys + 128 * k + row;
-      if (k >= tiles || j >= x.s.pre + x.s.n) return -2;
-      const Tokens t = seen_by(p, x.s, j, j + 1);
-      return j >= x.s.pre || t.t0 < t.t1 ? page_entry(p, x.b, j) : -2;
+    int order = 0, piece = 0, slot = 0, phase = 0, step = 0;
+    bool ok = true, more = true, fresh = true;
+    // The key's entry of the page table: -2 where no weight is written (another
+    // group's, behind the sequence, neither new nor seen by any row).
+    auto entry = [&]() {
+      const int k = (g - order) & 3, j = w.u * w.keys + 128 * k + row;
+      if (k >= tiles || j >= w.s.pre + w.s.n) return -2;
+      const Tokens t = seen_by(p, w.s, j, j + 1);
+      return j >= w.s.pre || t.t0 < t.t1 ? page_entry(p, w.b, j) : -2;
     };
-    // where the weight lies (< 0: none is written), and what it was
-    auto place = [&](const MassWalk &x, int k, int page, float &old) {
-      const int j = x.u * x.keys + 128 * k + row;
+    int page = entry();
+    while (more) {
+      const int k = (g - order) & 3;
+      const bool mine = k < tiles;
+      // where the weight lies (< 0: none is written), and what it was
+      const int j = w.u * w.keys + 128 * k + row;
       long long at = -1;
-      old = 0.0f;
+      float old = 0.0f, sum = 0.0f;
       if (page >= 0 && page < p.a.n_pages) {
-        at = ((long long)page * p.a.Hkv + x.g) * p.a.pg + page_slot(p, j);
-        if (j < x.s.pre) old = p.a.mass[at];
+        at = ((long long)page * p.a.Hkv + w.g) * p.a.pg + page_slot(p, j);
+        if (j < w.s.pre) old = p.a.mass[at];
       } else if (page != -2 && p.err) {
         atomicExch(p.err + 1, kBadPage);
       }
-      return at;
-    };
-    long long at[2];
-    float old[2];
-    int page[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) page[m] = entry(w, g + 2 * m);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) at[m] = place(w, g + 2 * m, page[m], old[m]);
-    while (true) {
-      const int k0 = (order + g) & 1;  // (with one tile a unit, every other unit is the group's)
-      MassWalk nx = w;
-      const bool more = nx.next(p);
-      const int next_k0 = (order + tiles + g) & 1;
-      if (more) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m) page[m] = entry(nx, next_k0 + 2 * m);
-      }
-      float sum[2] = {0.0f, 0.0f};
+      // the piece, and the next one: its entry of the page table is on its way meanwhile
+      const int pre = w.s.pre, n = w.s.n, q0 = w.q0, q1 = w.q1, count = w.r.count, tile = w.r.first, begin = range.per * (int)blockIdx.x + w.at;
+      const int t_first = w.token(p, q0), b = w.b, h = w.g;
+      const bool end = pre + n <= j - row;  // no key of the tile is the sequence's
+      const Tokens seen = seen_by(p, w.s, j - row, min(j - row + 128, pre + n));
+      more = w.next(p);
+      order += tiles;
+      if (more) page = entry();
+      const bool stays = more && w.b == b && w.g == h && w.r.first + w.q0 == tile + q1 - 1;  // the last row tile
+      int t0 = t_first;
 #pragma unroll 1
-      for (int q = w.q0; q < w.q1; ++q) {
-        const int t0 = w.token(p, q), cols = w.columns(p, t0);
-        const unsigned live = w.seen_tiles(p, t0, t0 + p.T, lane) >> k0;
-        const float *ls = lse2 + 128 * slot;
-#pragma unroll 1
-        for (int m = 0; m < 2; ++m) {
-          if (!(live >> (2 * m) & 1)) continue;
-          const int buf = 2 * g + (step & 1), j = w.u * w.keys + 128 * (k0 + 2 * m) + row;
-          const uint32_t col = tmem + 128 * buf + lane_off;
+      for (int q = q0; q < q1; ++q, t0 += p.T) {
+        // (waited for by groups without a step too: none gives the slot back twice)
+        if (fresh && !mass_wait(q_full + slot, phase, p.err, 71, abort)) ok = false;
+        if (mine && !end && max(seen.t0, t0) < min(seen.t1, t0 + p.T)) {
+          const int span = min(p.T, n - t0), cols = span * p.G;
+          const float *ls = lse2 + 128 * slot;
           // the key's columns [c0, c1): tokens from its own on, up to the window's end
-          const int away = j - w.s.pre - t0, span = min(p.T, w.s.n - t0);
+          const int away = j - pre - t0;
           const int c0 = min(max(away, 0), 128) * p.G;
           const int c1 = j < p.a.sinks || away >= span - p.a.window ? cols : max(0, away + p.a.window) * p.G;
-          if (!mass_wait(s_full + buf, (step >> 1) & 1, p.err, 70, abort)) ok = false;
+          if (!mass_wait(s_full + g, step & 1, p.err, 70, abort)) ok = false;
           ++step;
           __syncwarp();
           tc::fence_after();
@@ -667,27 +657,27 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
             s0 = add2(s0, pair(a0, a1));
             s1 = add2(s1, pair(a2, a3));
           };
-          auto release = [&]() {  // the buffer is free for the step after next
+          auto release = [&]() {  // the buffer is free for the group's next step
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) attn_arrive(s_empty + buf);
+            if (lane == 0) attn_arrive(s_empty + g);
           };
           // (few instructions, run over and over: a loop that is unrolled for all
           // columns and both forms waits for its instructions)
           if (__all_sync(0xffffffffu, c0 == 0 && c1 == 128)) {
-            uint32_t x[2][32];
-            tc::tmem_ld32(col, x[0]);
+            uint32_t x[2][16];
+            tmem_ld16(col, x[0]);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {
-              tc::tmem_ld_wait(x[0]);
-              tc::tmem_ld32(col + c + 32, x[1]);
+            for (int c = 0; c < 128; c += 32) {
+              tmem_ld_wait16(x[0]);
+              tmem_ld16(col + c + 16, x[1]);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) add4(x[0] + 4 * i, *(const float4 *)(ls + c + 4 * i), 0, true);
-              tc::tmem_ld_wait(x[1]);
-              if (c == 0) tc::tmem_ld32(col + 64, x[0]);
+              for (int i = 0; i < 4; ++i) add4(x[0] + 4 * i, *(const float4 *)(ls + c + 4 * i), 0, true);
+              tmem_ld_wait16(x[1]);
+              if (c < 96) tmem_ld16(col + c + 32, x[0]);
               else release();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) add4(x[1] + 4 * i, *(const float4 *)(ls + c + 32 + 4 * i), 0, true);
+              for (int i = 0; i < 4; ++i) add4(x[1] + 4 * i, *(const float4 *)(ls + c + 16 + 4 * i), 0, true);
             }
           } else {
 #pragma unroll 1
@@ -701,49 +691,38 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
             }
           }
           const float2 r = split(add2(s0, s1));
-          if (m) sum[1] += r.x + r.y;
-          else sum[0] += r.x + r.y;
+          sum += r.x + r.y;
         }
-        if (q + 1 < w.q1 || !more || !w.same_rows(nx, q, nx.q0)) {  // done with the row tile's log-sum-exps
+        fresh = q + 1 < q1 || !stays;
+        if (fresh) {  // done with the row tile's log-sum-exps
           __syncwarp();
           if (lane == 0) attn_arrive(q_empty + slot);
-          if (++slot == QR) slot = 0;
-        }
-      }
-      if (w.q0 == 0 && w.q1 == w.r.count) {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          if (at[m] >= 0 && ok) p.a.mass[at[m]] = old[m] + sum[m];
-      } else if (k0 < tiles) {
-        // a piece: the unit begins at cost unit `begin` of all ranges
-        const int to = 2 * blockIdx.x + (piece ? 1 : 0);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          if (k0 + 2 * m < tiles) p.part[((size_t)to * kMassTiles + k0 + 2 * m) * 128 + row] = sum[m];
-        const int begin = range.per * (int)blockIdx.x + w.at, first = begin + kMassUnitCost;
-        const int b0 = first / range.per, b1 = (first + w.r.count - 1) / range.per;
-        const int slot0 = 2 * b0 + (begin > b0 * range.per ? 1 : 0);  // a piece of the unit before comes first there
-        __threadfence();
-        group_sync(g);
-        if (row == 0) last[g] = !*abort && arrive_last(p.count + (size_t)k0 * kMassCtas + b1, up, b1 - b0 + 1);
-        group_sync(g);
-        if (last[g]) {
-          __threadfence();
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (at[m] < 0) continue;
-            const float *src = p.part + (size_t)(k0 + 2 * m) * 128 + row;
-            float total = __ldcg(src + (size_t)slot0 * kMassTiles * 128);
-            for (int b = b0 + 1; b <= b1; ++b) total += __ldcg(src + (size_t)2 * b * kMassTiles * 128);
-            p.a.mass[at[m]] = old[m] + total;
+          if (++slot == QR) {
+            slot = 0;
+            phase ^= 1;
           }
         }
       }
-      if (!more) break;
-#pragma unroll
-      for (int m = 0; m < 2; ++m) at[m] = place(nx, next_k0 + 2 * m, page[m], old[m]);
-      w = nx;
-      order += tiles;
+      if (q0 == 0 && q1 == count) {
+        if (at >= 0 && ok) p.a.mass[at] = old + sum;
+      } else if (mine) {
+        // a piece: the unit begins at cost unit `begin` of all ranges
+        const int to = 2 * blockIdx.x + (piece ? 1 : 0);
+        p.part[((size_t)to * kMassTiles + k) * 128 + row] = sum;
+        const int first = begin + kMassUnitCost, b0 = first / range.per, b1 = (first + count - 1) / range.per;
+        const int slot0 = 2 * b0 + (begin > b0 * range.per ? 1 : 0);  // a piece of the unit before comes first there
+        __threadfence();
+        group_sync(g);
+        if (row == 0) last[g] = !*abort && arrive_last(p.count + (size_t)k * kMassCtas + b1, p.ticket + (uint32_t)status, b1 - b0 + 1);
+        group_sync(g);
+        if (last[g] && at >= 0) {
+          __threadfence();
+          const float *src = p.part + (size_t)k * 128 + row;
+          float total = __ldcg(src + (size_t)slot0 * kMassTiles * 128);
+          for (int c = b0 + 1; c <= b1; ++c) total += __ldcg(src + (size_t)2 * c * kMassTiles * 128);
+          p.a.mass[at] = old + total;
+        }
+      }
       ++piece;
     }
   }
@@ -760,7 +739,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
 struct MassWorkspace {
   static constexpr size_t part = 0;
   static constexpr size_t count = part + (size_t)2 * kMassCtas * kMassTiles * 128 * 4;
-  static constexpr size_t bytes = count + (size_t)2 * kMassCtas * 8;
+  static constexpr size_t bytes = count + (size_t)kMassTiles * kMassCtas * 8;
 };
 
 // Blocks of a launch on the current device, asked once.
