@@ -1831,6 +1831,7 @@ int dg_op_key_mass(const uint16_t *q, int64_t q_stride, const float *lse, const 
                    int32_t n_kv_heads, int32_t head_dim, int32_t page_size, int32_t n_pages, float scale,
                    void *workspace, size_t workspace_bytes, void *stream) {
   CKR(check_attended(n_tok, n_q_heads, n_kv_heads, head_dim, page_size, scale));
+  if (scale < 1e-30f) return fail(DG_EINVAL, "scale must be at least 1e-30");  // lse / scale has to be finite
   if (window < 0 || sinks < 0 || observe < 0) return fail(DG_EINVAL, "window, sinks and observe must not be negative");
   CKR(check_batch(prefix_lens, offsets, page_tables, max_pages, n_seqs, k_pool, k_pool, n_pages));
   if (!mass_pool) return fail(DG_EINVAL, "null mass_pool");

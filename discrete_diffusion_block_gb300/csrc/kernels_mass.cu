@@ -10,7 +10,11 @@
 //
 // The scores are computed transposed, S^T = K Q^T, so that a key is a lane of the
 // tensor memory and a thread adds up its key's weights over the rows without any
-// exchange.  A unit is 1 or 4 tiles of 128 keys of a (sequence, KV head): they stay in
+// exchange.  A row's -lse / scale comes in as 16 more columns of its operand (three
+// bf16 numbers whose sum is the fp32 one; the keys have ones there): added up by the
+// tensor core it costs an eighth of the products, read from shared memory by every
+// thread it cost as much of that memory's bandwidth as the products themselves
+// (8192 rows: 141 us).  A unit is 1 or 4 tiles of 128 keys of a (sequence, KV head): they stay in
 // shared memory while the tiles of up to 128 rows (tokens x heads of the group, staged
 // by one TMA copy) that see any of them go by.  With many row tiles a unit has 4 key
 // tiles, which share each row tile read from L2; with one, 1: the keys stream through
@@ -40,14 +44,13 @@ constexpr int kMassTiles = 4;        // most key tiles of a unit
 constexpr int kMassFew = 3;          // (key tile, row tile) pairs a block up to which units are single tiles
 constexpr int kMassUnitCost = 1;     // cost of starting a unit, in row tiles
 constexpr int kMassGaveUp = 64;      // status code of a block that gave up after an earlier kernel
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct MassArgs {
   CUtensorMap q_map, few_map;  // rows [n_tok][Hq][hd], boxes 64 x G x T and 64 x G x few
   KeyMass a;
   int G, T, few, ctas;  // T: tokens of a row tile
   int pg_shift;         // log2 of the page size, -1 where it is no power of two
-  float scale_log2;
+  float scale_log2, inv_scale;
   float *part;                // [2 kMassCtas][kMassTiles * 128]: block c's first piece in 2 c, its last in 2 c + 1
   unsigned long long *count;  // [kMassTiles][kMassCtas]: pieces that have arrived of tile k of the unit that ends in block c
   unsigned long long ticket;
@@ -57,12 +60,13 @@ struct MassArgs {
 template <int HD>
 struct MassSmem {
   static constexpr int HB = HD / 64;
-  static constexpr int KR = HD == 128 ? 4 : 8, QR = HD == 128 ? 3 : 4;  // ring depths, in tiles
+  static constexpr int KR = HD == 128 ? 4 : 8, QR = HD == 128 ? 2 : 4;  // ring depths, in tiles
   static constexpr size_t tile = (size_t)HB * 16384;                    // 128 keys or rows
   static constexpr size_t kring = 0;
   static constexpr size_t qring = kring + KR * tile;
-  static constexpr size_t lse = qring + QR * tile;
-  static constexpr size_t bars = lse + QR * 512;
+  static constexpr size_t ones = qring + QR * tile;  // 16 columns of 128 keys: 1 in the first three
+  static constexpr size_t lse = ones + 4096;         // [QR] 16 columns of 128 rows
+  static constexpr size_t bars = lse + QR * 4096;
   static constexpr int n_bars = 2 * KR + 2 * QR + 8 + 2;  // full and empty of K, Q, S (one buffer a group); drained
   static constexpr size_t slot = bars + n_bars * 8;
   static constexpr size_t bytes = slot + 8 + 4 * kMassTiles;
@@ -287,15 +291,13 @@ struct MassWalk {
   // Row tile q of the piece: its first token, its columns (rows).
   __device__ __forceinline__ int token(const MassArgs &p, int q) const { return s.tf + (r.first + q) * p.T; }
   __device__ __forceinline__ int columns(const MassArgs &p, int t0) const { return min(p.T, s.n - t0) * p.G; }
-  // Bit k: some key of the unit's tile k is seen by a token of [t0, t1) that counts.  Run by a whole warp.
-  __device__ __forceinline__ unsigned seen_tiles(const MassArgs &p, int t0, int t1, int lane) const {
-    const int j0 = u * keys + 128 * lane, end = s.pre + s.n;
-    bool sees = false;
-    if (128 * lane < keys && j0 < end) {
-      const Tokens t = seen_by(p, s, j0, min(j0 + 128, end));
-      sees = max(t.t0, t0) < min(t.t1, t1);
-    }
-    return __ballot_sync(0xffffffffu, sees);
+  // The tokens that count and see a key of the unit's tile k (none: t0 >= t1).
+  __device__ __forceinline__ Tokens tile_tokens(const MassArgs &p, int k) const {
+    const int j0 = u * keys + 128 * k, end = s.pre + s.n;
+    Tokens t;
+    t.t0 = t.t1 = 0;
+    if (128 * k < keys && j0 < end) t = seen_by(p, s, j0, min(j0 + 128, end));
+    return t;
   }
   __device__ __forceinline__ bool same_rows(const MassWalk &o, int q, int oq) const {
     return b == o.b && g == o.g && r.first + q == o.r.first + oq;
@@ -326,23 +328,13 @@ __device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned l
   return true;
 }
 
+// A bounded wait that costs one test when the phase is over already; the loop is not
+// inlined: the roles' code has to stay short.
+__device__ __noinline__ bool mass_wait_on(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
+  return tc::mbar_wait(b, parity, err, code, abort);
+}
 __device__ __forceinline__ bool mass_wait(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
-  return tc::mbar_try_wait(b, parity) || tc::mbar_wait(b, parity, err, code, abort);
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t *r) {  // ties the loaded registers to the wait
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
-                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
+  return tc::mbar_try_wait(b, parity) || mass_wait_on(b, parity, err, code, abort);
 }
 
 // tc::mma_bf16 with the low halves of the operands' descriptors: the high ones are
@@ -350,6 +342,16 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t *r) {  // ties the loade
 __device__ __forceinline__ void mma_low(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accum) {
   const uint64_t high = tc::sw128_desc(0) & 0xffffffff00000000ull;
   tc::mma_bf16(d_tmem, high | a, high | b, idesc, accum);
+}
+
+// Shared-memory descriptor of 16 columns without swizzle: 8 x 8 element blocks of
+// 128 bytes, the next 8 columns 128 bytes on, the next 8 rows 256.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(128 >> 4) << 16;
+  d |= (uint64_t)(256 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
 }
 
 // The four warps of a group meet.
@@ -365,7 +367,6 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
   uint64_t *s_full = q_empty + QR, *s_empty = s_full + 4, *drained = s_empty + 4;
   uint32_t *tmem_slot = (uint32_t *)(base + S::slot);
   volatile int *abort = (volatile int *)(tmem_slot + 1), *last = abort + 1;  // last: [kMassTiles]
-  float *lse2 = (float *)(base + S::lse);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (tc::smem_u32(base) & 1023u) {  // the operand tiles' swizzle needs it: the same in every block
     if (threadIdx.x == 0 && p.err) atomicExch(p.err, kShapeErrorBase + 6);
@@ -378,8 +379,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       tc::mbar_init(k_empty + i, 2);  // both issuing warps wait for all key tiles: none is replaced before both have
     }
     for (int i = 0; i < QR; ++i) {
-      tc::mbar_init(q_full + i, 1);
-      tc::mbar_init(q_empty + i, 18);  // the products of both warps, and the sixteen that read the log-sum-exps
+      tc::mbar_init(q_full + i, 2);  // the copies, and the log-sum-exps
+      tc::mbar_init(q_empty + i, 2);  // the products of both warps
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(s_full + i, 1);
@@ -390,6 +391,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
+  // The operands' further columns: 16-byte chunk c of row r at chunk position
+  // 16 (r / 8) + 8 c + r % 8.
+  for (int i = threadIdx.x; i < (1 + QR) * 256; i += kMassThreads)
+    *(uint4 *)(base + S::ones + 16 * i) = i < 256 && !(i & 8) ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   const MassRange range = block_range(p, lane);  // the same in every warp
   MassWalk w;
   if (range.count <= 0 || !w.begin(p, range, lane)) return;
@@ -429,7 +435,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       if (page >= 0 && page < p.a.n_pages)
         src = p.a.k_pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)blk * p.a.pg * 64 +
               (size_t)page_slot(p, w.u * w.keys + 128 * k_lane + 64 * half) * 64;
-      unsigned used = w.seen_tiles(p, 0, w.s.n, lane);
+      const Tokens t = w.tile_tokens(p, lane);
+      unsigned used = __ballot_sync(0xffffffffu, t.t0 < t.t1);
       more = w.next(p);
       if (more) page = entry_of(w);
       for (; used; used &= used - 1) {
@@ -460,40 +467,49 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     }
   } else if (warp == 1) {
     // ---- row tiles and their log-sum-exps ------------------------------------------
-    int slot = 0, phase = 0, issued = 0, q = w.q0;
+    int slot = 0, phase = 0, issued = 0, q = w.q0, t0 = w.token(p, q), cols = w.columns(p, t0);
     bool ok = true, more = true;
-    while (more) {
-      const int t0 = w.token(p, q), cols = w.columns(p, t0);
-      // column c: token t0 + c / G, head g G + c % G; kept negative, in units of log2;
-      // rows without a key (-inf) weigh nothing
-      float v[4];
+    // row c of the tile: token t0 + c / G, head g G + c % G
+    int off[4];
+    float v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k;
-        v[k] = 0.0f;
-        if (c < cols) {
-          const int t = c / p.G;
-          v[k] = p.a.lse[(size_t)(w.s.row0 + t0 + t) * p.a.Hq + w.g * p.G + c - t * p.G] * -kLog2e;
-          if (v[k] == __int_as_float(0x7f800000)) v[k] = -v[k];
-        }
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int c = lane + 32 * k, t = c / p.G;
+      off[k] = t * p.a.Hq + c - t * p.G;
+    }
+    auto load = [&]() {
+      const float *src = p.a.lse + (size_t)(w.s.row0 + t0) * p.a.Hq + w.g * p.G;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < cols ? src[off[k]] : 0.0f;
+    };
+    load();
+    while (more) {
       if (lane == 0) {
         if (issued >= QR) ok = mass_wait(q_empty + slot, phase ^ 1, p.err, 66, abort);
         if (*abort) ok = false;
+        if (ok) {
+          const bool few = cols <= p.few * p.G;
+          const CUtensorMap *map = few ? &p.few_map : &p.q_map;
+          tc::mbar_expect_tx(q_full + slot, HB * 128u * (few ? p.few : p.T) * p.G);
+#pragma unroll
+          for (int blk = 0; blk < HB; ++blk)
+            tc::tma_load_3d(base + S::qring + (size_t)slot * S::tile + (size_t)blk * 16384, map, 64 * blk, w.g * p.G, w.s.row0 + t0, q_full + slot);
+        }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) lse2[128 * slot + lane + 32 * k] = v[k];
-      __syncwarp();
-      if (lane == 0) {
-        const bool few = cols <= p.few * p.G;
-        const CUtensorMap *map = few ? &p.few_map : &p.q_map;
-        tc::mbar_expect_tx(q_full + slot, HB * 128u * (few ? p.few : p.T) * p.G);
-#pragma unroll
-        for (int blk = 0; blk < HB; ++blk)
-          tc::tma_load_3d(base + S::qring + (size_t)slot * S::tile + (size_t)blk * 16384, map, 64 * blk, w.g * p.G, w.s.row0 + t0, q_full + slot);
+      for (int k = 0; k < 4; ++k) {
+        const int c = lane + 32 * k;
+        float x = v[k] * -p.inv_scale;
+        if (x == __int_as_float(0x7f800000)) x = -x;  // rows without a key (lse -inf) weigh nothing
+        const float a = __bfloat162float(__float2bfloat16_rn(x)), rest = isfinite(a) ? x - a : 0.0f;
+        const float b = __bfloat162float(__float2bfloat16_rn(rest));
+        *(uint2 *)(base + S::lse + 4096 * slot + 256 * (c >> 3) + 16 * (c & 7)) = make_uint2(pack_bf16(a, b), pack_bf16(rest - b, 0.0f));
       }
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      __syncwarp();
+      if (lane == 0) attn_arrive(q_full + slot);
       ++issued;
       if (++slot == QR) {
         slot = 0;
@@ -508,6 +524,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
           q = w.q0;
         }
       } while (more && w.same_rows(was, q, was_q));
+      if (more) {
+        t0 = w.token(p, q);
+        cols = w.columns(p, t0);
+        load();
+      }
     }
     if (!ok && lane == 0) {
       for (int i = issued - 1; i >= 0 && i >= issued - QR; --i) {
@@ -523,9 +544,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     int ks = 0, kphase = 0, qs = 0, qphase = 0, order = 0, step0 = 0, step1 = 0;  // steps of groups half, half + 2
     const uint32_t kdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::kring)), qdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::qring));
     while (ok && more) {
-      const MassWalk was = w;
+      const Tokens mine = w.tile_tokens(p, lane);  // of tile `lane`
+      const unsigned used = __ballot_sync(0xffffffffu, mine.t0 < mine.t1);
+      const int q0 = w.q0, q1 = w.q1, n = w.s.n, b = w.b, h = w.g, last_tile = w.r.first + q1 - 1;
+      int t0 = w.token(p, q0);
       more = w.next(p);
-      const unsigned used = was.seen_tiles(p, 0, was.s.n, lane);
+      const bool stays = more && w.b == b && w.g == h && w.r.first + w.q0 == last_tile;  // the next piece begins with the row tile
       const int n_used = __popc(used);
       int ring = 0;  // key tiles of the unit that have arrived, from slot ks on
       auto arrived = [&]() {
@@ -533,9 +557,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         ++ring;
         return mass_wait(k_full + (slot < KR ? slot : slot - KR), slot < KR ? kphase : kphase ^ 1, p.err, 67, abort);
       };
-      for (int q = was.q0; ok && q < was.q1; ++q) {
-        const int t0 = was.token(p, q), cols = was.columns(p, t0);
-        unsigned live = was.seen_tiles(p, t0, t0 + p.T, lane) & (0x55555555u << ((order + half) & 1));  // this warp's
+      const unsigned turn = 0x55555555u << ((order + half) & 1);  // this warp's tiles
+#pragma unroll 1
+      for (int q = q0; ok && q < q1; ++q, t0 += p.T) {
+        const int cols = min(p.T, n - t0) * p.G;
+        unsigned live = __ballot_sync(0xffffffffu, max(mine.t0, t0) < min(mine.t1, t0 + p.T)) & turn;
         if (fresh) ok = mass_wait(q_full + qs, qphase, p.err, 69, abort);
         const uint32_t idesc = tc::idesc_bf16(128, (cols + 15) & ~15);
         for (; ok && live; live &= live - 1) {
@@ -552,12 +578,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk)
               mma_low(tmem + 128 * g, a + (kk >> 2) * 1024 + 2 * (kk & 3), b + (kk >> 2) * 1024 + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+            tc::mma_bf16(tmem + 128 * g, plain_desc(tc::smem_u32(base + S::ones)), plain_desc(tc::smem_u32(base + S::lse + 4096 * qs)), idesc, 1u);
             tc::mma_commit(s_full + g);
           }
           ok = __all_sync(0xffffffffu, ok);
         }
-        // the row tile is done with unless the next piece begins with it
-        fresh = q + 1 < was.q1 || !more || !was.same_rows(w, q, w.q0);
+        fresh = q + 1 < q1 || !stays;
         if (ok && fresh) {
           if (lane == 0) tc::mma_commit(q_empty + qs);
           if (++qs == QR) {
@@ -593,8 +619,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     const int g = (warp - 4) >> 2, row = threadIdx.x & 127;
     const uint32_t col = tmem + 128 * g + ((uint32_t)(32 * (warp & 3)) << 16);
     const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
-    int order = 0, piece = 0, slot = 0, phase = 0, step = 0;
-    bool ok = true, more = true, fresh = true;
+    int order = 0, piece = 0, step = 0;
+    bool ok = true, more = true;
     // The key's entry of the page table: -2 where no weight is written (another
     // group's, behind the sequence, neither new nor seen by any row).
     auto entry = [&]() {
@@ -618,22 +644,16 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         atomicExch(p.err + 1, kBadPage);
       }
       // the piece, and the next one: its entry of the page table is on its way meanwhile
-      const int pre = w.s.pre, n = w.s.n, q0 = w.q0, q1 = w.q1, count = w.r.count, tile = w.r.first, begin = range.per * (int)blockIdx.x + w.at;
-      const int t_first = w.token(p, q0), b = w.b, h = w.g;
-      const bool end = pre + n <= j - row;  // no key of the tile is the sequence's
-      const Tokens seen = seen_by(p, w.s, j - row, min(j - row + 128, pre + n));
+      const int pre = w.s.pre, n = w.s.n, q0 = w.q0, q1 = w.q1, count = w.r.count, begin = range.per * (int)blockIdx.x + w.at;
+      int t0 = w.token(p, q0);
+      const Tokens seen = w.tile_tokens(p, k);
       more = w.next(p);
       order += tiles;
       if (more) page = entry();
-      const bool stays = more && w.b == b && w.g == h && w.r.first + w.q0 == tile + q1 - 1;  // the last row tile
-      int t0 = t_first;
 #pragma unroll 1
       for (int q = q0; q < q1; ++q, t0 += p.T) {
-        // (waited for by groups without a step too: none gives the slot back twice)
-        if (fresh && !mass_wait(q_full + slot, phase, p.err, 71, abort)) ok = false;
-        if (mine && !end && max(seen.t0, t0) < min(seen.t1, t0 + p.T)) {
+        if (max(seen.t0, t0) < min(seen.t1, t0 + p.T)) {
           const int span = min(p.T, n - t0), cols = span * p.G;
-          const float *ls = lse2 + 128 * slot;
           // the key's columns [c0, c1): tokens from its own on, up to the window's end
           const int away = j - pre - t0;
           const int c0 = min(max(away, 0), 128) * p.G;
@@ -643,10 +663,10 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
           __syncwarp();
           tc::fence_after();
           f32x2 s0 = pair(0.0f, 0.0f), s1 = s0;
-          // 2^(scale x - lse) of four columns, added up
-          auto add4 = [&](const uint32_t *y, float4 l, int cc, bool all) {
-            const float2 d = split(fma2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), scale2, pair(l.x, l.y)));
-            const float2 e = split(fma2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), scale2, pair(l.z, l.w)));
+          // 2^(scale (x - lse / scale)) of four columns, added up
+          auto add4 = [&](const uint32_t *y, int cc, bool all) {
+            const float2 d = split(mul2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), scale2));
+            const float2 e = split(mul2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), scale2));
             float a0 = ex2(d.x), a1 = ex2(d.y), a2 = ex2(e.x), a3 = ex2(e.y);
             if (!all) {
               a0 = cc >= c0 && cc < c1 ? a0 : 0.0f;
@@ -672,12 +692,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
               tmem_ld_wait16(x[0]);
               tmem_ld16(col + c + 16, x[1]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) add4(x[0] + 4 * i, *(const float4 *)(ls + c + 4 * i), 0, true);
+              for (int i = 0; i < 4; ++i) add4(x[0] + 4 * i, 0, true);
               tmem_ld_wait16(x[1]);
               if (c < 96) tmem_ld16(col + c + 32, x[0]);
               else release();
 #pragma unroll
-              for (int i = 0; i < 4; ++i) add4(x[1] + 4 * i, *(const float4 *)(ls + c + 16 + 4 * i), 0, true);
+              for (int i = 0; i < 4; ++i) add4(x[1] + 4 * i, 0, true);
             }
           } else {
 #pragma unroll 1
@@ -687,20 +707,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
               tmem_ld_wait16(x);
               if (c + 16 >= cols) release();
 #pragma unroll
-              for (int i = 0; i < 4; ++i) add4(x + 4 * i, *(const float4 *)(ls + c + 4 * i), c + 4 * i, false);
+              for (int i = 0; i < 4; ++i) add4(x + 4 * i, c + 4 * i, false);
             }
           }
           const float2 r = split(add2(s0, s1));
           sum += r.x + r.y;
-        }
-        fresh = q + 1 < q1 || !stays;
-        if (fresh) {  // done with the row tile's log-sum-exps
-          __syncwarp();
-          if (lane == 0) attn_arrive(q_empty + slot);
-          if (++slot == QR) {
-            slot = 0;
-            phase ^= 1;
-          }
         }
       }
       if (q0 == 0 && q1 == count) {
@@ -782,6 +793,7 @@ cudaError_t key_mass(const KeyMass &a, void *ws, int *err, cudaStream_t st) {
   p.G = a.Hq / a.Hkv;
   p.T = 128 / p.G;
   p.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
+  p.inv_scale = (float)(1.0 / (double)a.scale);
   p.part = (float *)((unsigned char *)ws + MassWorkspace::part);
   p.count = (unsigned long long *)((unsigned char *)ws + MassWorkspace::count);
   p.ticket = new_ticket();

@@ -723,8 +723,8 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
  * saw no key) add nothing; a NaN spreads to the keys that its row sees.
  *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size], of the cache's pages
  *               (two sequences of a call must not share a page that is written)
- * Other arguments, conditions and reports as dg_op_window_attention; keys of a page
- * outside the pools are skipped.  The workspace of one call must not be used by
+ * Other arguments, conditions and reports as dg_op_window_attention (but scale >=
+ * 1e-30); keys of a page outside the pools are skipped.  The workspace of one call must not be used by
  * another at the same time.  Blocks do not wait for one another. */
 size_t dg_op_key_mass_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
                                       int32_t n_kv_heads, int32_t head_dim);

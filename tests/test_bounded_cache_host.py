@@ -39,7 +39,7 @@ KM = dict(q=A, qs=2048, lse=A, k_pool=A, mass=A, tables=A, max_pages=4, prefix=A
     dict(q=None), dict(lse=None), dict(k_pool=None), dict(mass=None), dict(q=A + 8), dict(lse=A + 2), dict(mass=A + 1), dict(k_pool=A + 8),
     dict(qs=2047), dict(qs=1024), dict(tables=None), dict(prefix=None), dict(offsets=None), dict(window=-1), dict(sinks=-1), dict(observe=-1),
     dict(n_seqs=-1), dict(n_tok=-1), dict(hq=15), dict(hkv=0), dict(hq=1032), dict(hd=256), dict(pg=32), dict(pg=100), dict(n_pages=0),
-    dict(scale=0.0), dict(scale=INF), dict(scale=float("nan")), dict(max_pages=-1), dict(n_tok=1 << 28), dict(qs=1 << 40),
+    dict(scale=0.0), dict(scale=INF), dict(scale=float("nan")), dict(max_pages=-1), dict(n_tok=1 << 28), dict(qs=1 << 40), dict(scale=1e-31),
 ])
 def test_key_mass_refuses(L, change):  # noqa: F811
     assert call(L.dg_op_key_mass, KM, **change) == dgp.DG_EINVAL
