@@ -1787,7 +1787,9 @@ int dg_op_tree_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_
 
 size_t dg_op_window_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
                                               int32_t head_dim) {
-  return dg_op_tree_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);
+  if (n_tok < 0 || n_seqs < 0 || n_kv_heads < 1 || n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
+    return 0;
+  return dg::window_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim);
 }
 
 int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool, const uint16_t *v_pool,
@@ -1804,6 +1806,7 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
   if ((uintptr_t)lse % 4) return fail(DG_EINVAL, "lse is not aligned to its elements");
   if (n_tok == 0 || n_seqs == 0) return DG_OK;
   if (q == out) return fail(DG_EINVAL, "out must not be q");
+  if (q_stride >= (int64_t)1 << 38) return fail(DG_EINVAL, "q: row stride %lld is too large", (long long)q_stride);
   CKR(check_span(max_pages, page_size, n_tok, n_seqs, n_q_heads, n_kv_heads));
   CKR(check_workspace(workspace, workspace_bytes,
                       dg_op_window_attention_workspace_bytes(n_tok, n_seqs, n_q_heads, n_kv_heads, head_dim)));
@@ -1814,7 +1817,7 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
                       prefix_lens, offsets, nullptr, 0, n_seqs, n_tok, n_q_heads, n_kv_heads, head_dim, page_size,
                       n_pages, scale, (bf16 *)out, out_stride, window ? window : INT32_MAX,
                       window ? std::min(sinks, (int32_t)0x7fffff00) : 0, lse};
-  CK(dg::tree_attention(a, workspace, status, (cudaStream_t)stream));
+  CK(dg::window_attention(a, workspace, status, (cudaStream_t)stream));
   return DG_OK;
 }
 

@@ -307,7 +307,11 @@ struct TokenLogprobs {
 };
 cudaError_t token_logprobs(const TokenLogprobs &a, int *err, cudaStream_t st);
 
-// ---- bounded caches (kernels_tree.cu: windowed attention; kernels_mass.cu, kernels_evict.cu) ----
+// ---- bounded caches (kernels_chunk.cu, kernels_mass.cu, kernels_evict.cu) ----
+// The attention with a.window > 0, by the tree attention's kernel or one for many rows.
+size_t window_attention_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int hd);
+cudaError_t window_attention(const TreeAttention &a, void *ws, int *err, cudaStream_t st);
+
 // A number that no other call has: a word of a workspace whose contents are
 // arbitrary does not equal it.
 unsigned long long new_ticket();

@@ -51,12 +51,12 @@
 #include "attn_tc.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
+#include "window.cuh"
 
 namespace dg {
 
 namespace {
 
-constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kTreeThreads = 384;
 constexpr int kTreePvWarp = 11;
 constexpr int kTreeCtas = 152;      // most blocks: one per SM
@@ -351,15 +351,6 @@ __device__ __forceinline__ bool tree_wait(uint64_t *b, uint32_t parity, int *err
 __device__ __forceinline__ void warp_wait(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
   tree_wait(b, parity, err, code, abort);
   __syncwarp();
-}
-
-// The 64 keys from slot key0 on that a row at slot `at` sees through its window.
-__device__ __forceinline__ unsigned long long window_bits(const TreeArgs &p, int at, int key0) {
-  const int up = at + 1 - key0, low = max(0, at - p.a.window + 1) - key0, sink = p.a.sinks - key0;
-  if (up <= 0) return 0ull;
-  unsigned long long v = low <= 0 ? ~0ull : low >= 64 ? 0ull : ~0ull << low;
-  if (sink > 0) v |= sink >= 64 ? ~0ull : (1ull << sink) - 1;
-  return up >= 64 ? v : v & ((1ull << up) - 1);
 }
 
 // 64 mask bits of a row from drafted key d0 on (d0 may be negative: prefix
@@ -979,7 +970,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
                               : key_base + 64 > w.s.pre;
         if (some || bad) {
           unsigned long long see = (bad >> half) & 1 ? 0ull
-                                   : WIN             ? window_bits(p, w.s.pre + t, key_base)
+                                   : WIN             ? window_bits(w.s.pre + t, key_base, p.a.window, p.a.sinks)
                                                      : row_bits(p, w.s, t, key_base - w.s.pre);
           if (row >= rows) see = 0ull;
           const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
