@@ -867,11 +867,10 @@ def dg_op_key_mass(q, lse, k_pool, mass_pool, page_tables, prefix_lens, offsets,
         hq, hkv, hd, pg, n_pages, hd ** -0.5 if scale is None else scale, *_scratch(workspace, dev), _stream_on(stream, dev)))
 
 
-def dg_op_cache_evict(k_pool, v_pool, mass_pool, page_tables, out_tables, lens, out_lens, budget, sinks=0, recent=0, kept=None,
-                      stream=None):
+def dg_op_cache_evict(k_pool, v_pool, mass_pool, page_tables, out_tables, lens, out_lens, budget, kept, sinks=0, recent=0, stream=None):
     """mass_pool fp32 [n_pages][Hkv][page_size]; page_tables and out_tables int32
     [B][pages] (the same tensor: in place); lens, out_lens int32 [B]; kept int32
-    [B][Hkv][budget] or None; stream None: torch's current one."""
+    [B][Hkv][budget]; stream None: torch's current one."""
     dev = _device(k_pool)
     pool, table, out_table = k_pool.shape, page_tables.shape, out_tables.shape
     if len(pool) != 4 or len(table) != 2 or len(out_table) != 2 or out_table[0] != table[0]:

@@ -1870,7 +1870,7 @@ int dg_op_cache_evict(uint16_t *k_pool, uint16_t *v_pool, float *mass_pool, cons
   if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
     return fail(DG_EINVAL, "budget >= 1, sinks, recent >= 0 and sinks + recent <= budget required");
   if (n_seqs == 0) return DG_OK;
-  if (!lens || !out_lens || (max_pages && !page_tables) || (out_max_pages && !out_tables)) return fail(DG_EINVAL, "null pointer");
+  if (!lens || !out_lens || !kept || (max_pages && !page_tables) || (out_max_pages && !out_tables)) return fail(DG_EINVAL, "null pointer");
   if (lens == out_lens) return fail(DG_EINVAL, "out_lens must not be lens");
   int *status = nullptr;
   CKR(op_status_ptr(&status));

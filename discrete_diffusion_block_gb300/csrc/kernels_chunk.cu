@@ -548,39 +548,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
       __threadfence();
       float top = NEG, L = 0.0f;
       for (int b = blocks.first; b <= blocks.last; ++b) top = fmaxf(top, __ldcg(&p.state[(size_t)(2 * blocks.slot(b) + t) * 128 + row].x));
+      float4 acc[HD / 4];
+#pragma unroll
+      for (int j = 0; j < HD / 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-      for (int c = 0; c < HD; c += 32) {
-        float4 acc[8];
+      for (int b = blocks.first; b <= blocks.last; ++b) {
+        const size_t piece_at = (size_t)(2 * blocks.slot(b) + t);
+        const float2 ml = __ldcg(p.state + piece_at * 128 + row);
+        const float f = ml.x == NEG ? 0.0f : ex2(ml.x - top);
+        if (f == 0.0f) continue;  // (a tile that saw none of the piece's keys has left no sums)
+        L += f * ml.y;
+        const float4 *src = p.part + piece_at * (HD / 4) * 128 + row;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        L = 0.0f;
-#pragma unroll 1
-        for (int b = blocks.first; b <= blocks.last; ++b) {
-          const size_t piece_at = (size_t)(2 * blocks.slot(b) + t);
-          const float2 ml = __ldcg(p.state + piece_at * 128 + row);
-          const float f = ml.x == NEG ? 0.0f : ex2(ml.x - top);
-          if (f == 0.0f) continue;  // (a tile that saw none of the piece's keys has left no sums)
-          L += f * ml.y;
-          const float4 *src = p.part + (piece_at * (HD / 4) + c / 4) * 128 + row;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 v = __ldcg(src + (size_t)j * 128);
-            acc[j].x += f * v.x;
-            acc[j].y += f * v.y;
-            acc[j].z += f * v.z;
-            acc[j].w += f * v.w;
-          }
+        for (int j = 0; j < HD / 4; ++j) {
+          const float4 v = __ldcg(src + (size_t)j * 128);
+          acc[j].x += f * v.x;
+          acc[j].y += f * v.y;
+          acc[j].z += f * v.z;
+          acc[j].w += f * v.w;
         }
-        const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+      }
+      const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          uint4 o;
-          o.x = pack_bf16(acc[j].x * inv, acc[j].y * inv);
-          o.y = pack_bf16(acc[j].z * inv, acc[j].w * inv);
-          o.z = pack_bf16(acc[j + 1].x * inv, acc[j + 1].y * inv);
-          o.w = pack_bf16(acc[j + 1].z * inv, acc[j + 1].w * inv);
-          *(uint4 *)(dst + c + 4 * j) = o;
-        }
+      for (int j = 0; j < HD / 4; j += 2) {
+        uint4 o;
+        o.x = pack_bf16(acc[j].x * inv, acc[j].y * inv);
+        o.y = pack_bf16(acc[j].z * inv, acc[j].w * inv);
+        o.z = pack_bf16(acc[j + 1].x * inv, acc[j + 1].y * inv);
+        o.w = pack_bf16(acc[j + 1].z * inv, acc[j + 1].w * inv);
+        *(uint4 *)(dst + 4 * j) = o;
       }
       if (lse) *lse = fmaf(top, kLn2, logf(L));
     } while (w.next(list, p.a.n_seqs, p.a.Hkv));
@@ -638,10 +634,16 @@ cudaError_t launch_chunk(ChunkArgs &p, cudaStream_t st) {
 
 }  // namespace
 
-// Which kernel: with more than one tile of rows a sequence on the average, the one of
-// this file.
+// Which kernel: this file's takes pairs of row tiles, and is ahead where every block
+// has one or nearly (units: pairs of 128 rows of a sequence and KV head, if they were
+// full) and sequences fill a tile.  Measured, this kernel and the tree attention's
+// (16 and 8 heads of 128): one of 2048 tokens, windows of 1024 (128 units) 47 and 67
+// us; one of 4096, all keys (256) 86 and 134; 8 of 512 over 2k (256) 102 and 125; 64 of
+// 100, windows of 1024 (400) 162 and 173.  One of 1024 tokens (64 units), windows of 1024
+// 37 and 26, over 16k keys 135 and 146; 21 of up to 201, 12 and 4 heads of 64 (103) 38
+// and 29; 32 of 64 tokens over 2k (128 units, one tile of rows each) 101 and 76.
 static bool many_rows(int n_tok, int n_seqs, int Hq, int Hkv) {
-  return n_seqs > 0 && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;
+  return (long long)n_tok * Hq >= 120 * 256 && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;
 }
 
 size_t window_attention_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int hd) {

@@ -8,14 +8,15 @@
 // and V read and written once (8 hd bytes a row): the memory's bandwidth, for few
 // sequences the latency of the chain weights -> choice -> rows.
 //
-// A cluster of 1 to 8 blocks takes one KV head of one sequence.  Each of its blocks
-// makes the whole choice for itself (reading L weights from L2 costs less than
-// passing counts between blocks): a radix select, 11, 11 and 10 bits at a time over
-// histograms in shared memory, gives the smallest kept weight and how many of its
-// equals stay; then a bit per slot says what is kept, and a running count per word
-// of bits finds the d-th kept slot by bisection.  The blocks take turns of
-// kEvictTurn rows each; a warp moves K and V of its rows through registers (the
-// 16-byte chunks of a row change places with slot % 8), all loads before all stores.
+// Two launches.  The choice, a block per KV head and sequence: a radix select, 11, 11
+// and 10 bits at a time over histograms in shared memory, gives the smallest kept weight
+// and how many of its equals stay; then a bit per slot says what is kept, and running
+// counts of the bits give every kept slot its place in the list.  The move, a cluster
+// of up to 8 blocks per KV head and sequence: the blocks take turns of kMoveTurn rows each;
+// a warp moves K and V of its rows through registers (the 16-byte chunks of a row change
+// places with slot % 8), all loads before all stores.  (In one launch, with every block
+// of a cluster making the choice for itself: 12 sequences of up to 32k to 8k 137 us, 29
+// of up to 2900 to 1111 26 us.)
 //
 // In place (out_tables holds the sequence's own pages) this order is what makes it
 // safe: the d-th kept slot is never before d, so the rows that a turn reads lie
@@ -30,27 +31,32 @@ namespace dg {
 
 namespace {
 
-constexpr int kEvictThreads = 512;
-constexpr int kEvictRows = 16;                               // rows of a warp in a turn
-constexpr int kEvictTurn = kEvictThreads / 32 * kEvictRows;  // of a block
-constexpr int kEvictKeys = 32768;                            // weights kept in shared memory; later ones are read again
+constexpr int kEvictThreads = 1024;  // of the choice
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 16;                              // rows of a warp in a turn
+constexpr int kMoveTurn = kMoveThreads / 32 * kMoveRows;   // of a block
+constexpr int kEvictKeys = 32768;    // weights kept in shared memory; later ones are read again
 constexpr int kEvictBins = 2048;
+constexpr int kEvictPages = 1024;    // entries of the page table kept in shared memory
 
 struct EvictArgs {
   CacheEvict a;
   int words;  // words of bits that the shared memory holds: a sequence may have 32 times as many slots
   int keys;   // weights that it holds
+  int pg_shift, vec;  // log2 of the page size (-1: no power of two); weights can be loaded four at a time
   int *err;
 };
 
-// A weight as an integer of the same order: NaN below all, -0 as 0.
+// A weight as an integer of the same order: NaN below all (1), -0 as 0.  kStays: above
+// all; 0: no slot of the sequence.
+constexpr uint32_t kStays = 0xffffffffu;
 __device__ __forceinline__ uint32_t order_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
-  if (w != w) return 0u;
+  if (w != w) return 1u;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sum of v over the threads before this one; total: over all.  scratch: 17 ints.
+// Sum of v over the threads before this one; total: over all.  scratch: 32 ints.
 __device__ __forceinline__ int block_scan(int v, int *scratch, int *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
@@ -92,168 +98,197 @@ __device__ __forceinline__ int nth_bit(uint32_t w, int n) {
   return at;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kEvictThreads, 1) cache_evict_kernel(const __grid_constant__ EvictArgs p) {
+__global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __grid_constant__ EvictArgs p) {
   extern __shared__ uint32_t smem[];
-  __shared__ int scan[20], hist[kEvictBins], found[2], flags;
+  __shared__ int scan[32], hist[kEvictBins], found[2], flags, entries[kEvictPages];
   uint32_t *bits = smem, *equal = bits + p.words, *keys = equal + p.words;
-  int *before = (int *)equal;  // kept slots before a word (once `equal` is done with)
   const CacheEvict &a = p.a;
-  const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C;
-  const int b = unit / a.Hkv, g = unit - b * a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / a.Hkv, g = blockIdx.x - b * a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = a.lens[b], n_out = min(L, a.budget);
   const int *table = a.page_tables + (size_t)b * a.max_pages, *out_table = a.out_tables + (size_t)b * a.out_max_pages;
-  int *kept = a.kept ? a.kept + ((size_t)b * a.Hkv + g) * a.budget : nullptr;
+  int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
 
   // Sequences that the call cannot move are left alone; the same in all blocks.
   if (tid == 0) flags = 0;
   __syncthreads();
   const bool bad_length = L < 0 || (long long)L > (long long)a.max_pages * a.pg || (L + 31) / 32 > p.words ||
                           (long long)n_out > (long long)a.out_max_pages * a.pg;
+  const int n_pages = bad_length ? 0 : ceil_div(L, a.pg);
   if (!bad_length) {
-    int f = 0;
-    const int n_pages = ceil_div(L, a.pg), n_out_pages = ceil_div(n_out, a.pg);
+    bool f = false;
+    const int n_out_pages = ceil_div(n_out, a.pg);
     for (int i = tid; i < n_pages; i += kEvictThreads) {
-      const int src = table[i], dst = i < n_out_pages ? out_table[i] : -1;
-      if (src < 0 || src >= a.n_pages || (i < n_out_pages && (dst < 0 || dst >= a.n_pages))) f |= 1;
-      if (src == dst) f |= 2;  // in place
+      const int src = table[i], dst = i < n_out_pages ? out_table[i] : 0;
+      if (i < kEvictPages) entries[i] = src;
+      f |= src < 0 || src >= a.n_pages || dst < 0 || dst >= a.n_pages;
     }
-    if (f) atomicOr(&flags, f);
+    if (f) flags = 1;
   }
   __syncthreads();
-  const bool bad = bad_length || (flags & 1), in_place = flags & 2;
+  const bool bad = bad_length || flags;
   if (bad) {
     if (tid == 0 && p.err) atomicExch(p.err + 1, bad_length ? kBadSequence : kBadPage);
-    if (tid == 0 && rank == 0 && g == 0) a.out_lens[b] = -1;
-    if (kept && rank == 0)
-      for (int d = tid; d < a.budget; d += kEvictThreads) kept[d] = -1;
+    if (tid == 0 && g == 0) a.out_lens[b] = -1;
+    for (int d = tid; d < a.budget; d += kEvictThreads) kept[d] = -1;
     return;
   }
-  if (tid == 0 && rank == 0 && g == 0) a.out_lens[b] = n_out;
+  if (tid == 0 && g == 0) a.out_lens[b] = n_out;
+  for (int d = n_out + tid; d < a.budget; d += kEvictThreads) kept[d] = -1;
+  if (L <= a.budget) {
+    for (int d = tid; d < L; d += kEvictThreads) kept[d] = d;
+    return;
+  }
   const int words = (L + 31) / 32;
 
-  // ---- the choice
-  if (L > a.budget) {
-    auto weight = [&](int j) { return order_key(__ldcg(a.mass + ((size_t)table[j / a.pg] * a.Hkv + g) * a.pg + j % a.pg)); };
-    const int lo = a.sinks, hi = L - a.recent;
-    const int cached = min(L, p.keys);
-    for (int j = tid; j < cached; j += kEvictThreads) keys[j] = weight(j);
-    auto key = [&](int j) { return j < cached ? keys[j] : weight(j); };
-    uint32_t least = 0xffffffffu, mask = 0;
-    int left = a.budget - a.sinks - a.recent;  // equals of `least` that stay
-    if (left > 0) {
-      least = 0;
-#pragma unroll 1
-      for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-        for (int i = tid; i < bins; i += kEvictThreads) hist[i] = 0;
-        __syncthreads();
-        for (int j0 = lo + 32 * warp; j0 < hi; j0 += kEvictThreads) {
-          const int j = j0 + lane;
-          const uint32_t k = j < hi ? key(j) : 0;
-          const bool in = j < hi && (k & mask) == least;
-          const int bin = (k >> shift) & (bins - 1);
-          // (weights that nothing looked at are all 0: one addition for a warp of equals)
-          int same;
-          __match_all_sync(0xffffffffu, in ? bin : -1, &same);
-          if (same) {
-            if (lane == 0 && in) atomicAdd(&hist[bin], 32);
-          } else if (in) {
-            atomicAdd(&hist[bin], 1);
-          }
-        }
-        __syncthreads();
-        // from the top: the bin in which the count reaches `left`
-        const int per = bins / kEvictThreads, top = bins - 1 - tid * per;
-        int n = 0, total;
-        for (int i = 0; i < per; ++i) n += hist[top - i];
-        int above = block_scan(n, scan, &total);
-        if (above < left && above + n >= left) {
-          int bin = top;
-          while (above + hist[bin] < left) above += hist[bin--];
-          found[0] = bin;
-          found[1] = left - above;
-        }
-        __syncthreads();
-        least |= (uint32_t)found[0] << shift;
-        left = found[1];
-        mask |= (uint32_t)(bins - 1) << shift;
-        __syncthreads();
-      }
+  const int *pages = n_pages <= kEvictPages ? entries : table;
+  auto place = [&](int j) {
+    const int page = p.pg_shift >= 0 ? j >> p.pg_shift : j / a.pg;
+    return a.mass + ((size_t)pages[page] * a.Hkv + g) * a.pg + (j - page * a.pg);
+  };
+  auto key_of = [&](int j, float w) { return j >= L ? 0u : j < a.sinks || j >= L - a.recent ? kStays : order_key(w); };
+  // four slots, from a multiple of four on
+  auto load4 = [&](int j) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.vec) {  // (the fours behind the last slot lie in its page)
+      v = __ldcg((const float4 *)place(j));
     } else {
-      __syncthreads();
+      v.x = __ldcg(place(j));
+      if (j + 1 < L) v.y = __ldcg(place(j + 1));
+      if (j + 2 < L) v.z = __ldcg(place(j + 2));
+      if (j + 3 < L) v.w = __ldcg(place(j + 3));
     }
-    // bits of the slots that stay whatever their equals do, and of the equals
-    for (int w = warp; w < words; w += kEvictThreads / 32) {
-      const int j = 32 * w + lane;
-      const bool there = j < L, always = there && (j < lo || j >= hi);
-      const uint32_t k = there ? key(j) : 0;
-      const uint32_t more = __ballot_sync(0xffffffffu, always || (there && k > least));
-      const uint32_t same = __ballot_sync(0xffffffffu, there && !always && k == least);
-      if (lane == 0) {
-        bits[w] = more;
-        equal[w] = same;
+    return make_uint4(key_of(j, v.x), key_of(j + 1, v.y), key_of(j + 2, v.z), key_of(j + 3, v.w));
+  };
+  const int cached = min(128 * ceil_div(L, 128), p.keys);
+#pragma unroll 8
+  for (int j = 4 * tid; j < cached; j += 4 * kEvictThreads) *(uint4 *)(keys + j) = j < L ? load4(j) : make_uint4(0u, 0u, 0u, 0u);
+  auto key4 = [&](int j) { return j < cached ? *(const uint4 *)(keys + j) : j < L ? load4(j) : make_uint4(0u, 0u, 0u, 0u); };
+  // the budget's largest, those that stay in any case among them: the least of them, and
+  // how many of its equals stay (`left`)
+  uint32_t least = 0, mask = 0;
+  int left = a.budget;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int i = tid; i < bins; i += kEvictThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int j0 = 128 * warp; j0 < L; j0 += 4 * kEvictThreads) {
+      const uint4 k = key4(j0 + 4 * lane);
+      const bool in[4] = {(k.x & mask) == least && k.x, (k.y & mask) == least && k.y, (k.z & mask) == least && k.z, (k.w & mask) == least && k.w};
+      if (!__any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) continue;
+      const int bin[4] = {(int)(k.x >> shift) & (bins - 1), (int)(k.y >> shift) & (bins - 1), (int)(k.z >> shift) & (bins - 1),
+                          (int)(k.w >> shift) & (bins - 1)};
+      // (weights that nothing looked at are all 0, and many stay: one addition for a warp of equals)
+      const bool equal4 = in[0] && in[1] && in[2] && in[3] && bin[0] == bin[1] && bin[0] == bin[2] && bin[0] == bin[3];
+      const int bin0 = __shfl_sync(0xffffffffu, bin[0], 0);
+      if (__all_sync(0xffffffffu, equal4 && bin[0] == bin0)) {
+        if (lane == 0) atomicAdd(&hist[bin[0]], 128);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (in[i]) atomicAdd(&hist[bin[i]], 1);
       }
     }
     __syncthreads();
-    // of the equals the first `left`
-    const int per = ceil_div(words, kEvictThreads), w0 = min(words, tid * per), w1 = min(words, w0 + per);
+    // from the top: the bin in which the count reaches `left`
+    const int per = bins / kEvictThreads, top = bins - 1 - tid * per;
     int n = 0, total;
-    for (int w = w0; w < w1; ++w) n += __popc(equal[w]);
-    int at = block_scan(n, scan, &total);
-    for (int w = w0; w < w1 && at < left; ++w) {
-      const uint32_t e = equal[w];
-      const int c = __popc(e);
-      bits[w] |= at + c <= left ? e : e & ((1u << nth_bit(e, left - at)) - 1);
-      at += c;
+    for (int i = 0; i < per; ++i) n += hist[top - i];
+    int above = block_scan(n, scan, &total);
+    if (above < left && above + n >= left) {
+      int bin = top;
+      while (above + hist[bin] < left) above += hist[bin--];
+      found[0] = bin;
+      found[1] = left - above;
     }
     __syncthreads();
-    n = 0;
-    for (int w = w0; w < w1; ++w) n += __popc(bits[w]);
-    at = block_scan(n, scan, &total);
-    for (int w = w0; w < w1; ++w) {
-      before[w] = at;
-      at += __popc(bits[w]);
-    }
-    __syncthreads();
+    least |= (uint32_t)found[0] << shift;
+    left = found[1];
+    mask |= (uint32_t)(bins - 1) << shift;
   }
+  // bits of the slots above it, and of its equals: a lane has four slots, eight lanes a word
+#pragma unroll 1
+  for (int j0 = 128 * warp; j0 < L; j0 += 4 * kEvictThreads) {
+    const uint4 k = key4(j0 + 4 * lane);
+    const int at = 4 * (lane & 7);
+    uint32_t more = ((k.x > least ? 1u : 0u) | (k.y > least ? 2u : 0u) | (k.z > least ? 4u : 0u) | (k.w > least ? 8u : 0u)) << at;
+    uint32_t same = ((k.x == least ? 1u : 0u) | (k.y == least ? 2u : 0u) | (k.z == least ? 4u : 0u) | (k.w == least ? 8u : 0u)) << at;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      more |= __shfl_xor_sync(0xffffffffu, more, o);
+      same |= __shfl_xor_sync(0xffffffffu, same, o);
+    }
+    if ((lane & 7) == 0) {
+      bits[j0 / 32 + lane / 8] = more;
+      equal[j0 / 32 + lane / 8] = same;
+    }
+  }
+  __syncthreads();
+  // of the equals the first `left`
+  const int per = ceil_div(words, kEvictThreads), w0 = min(words, tid * per), w1 = min(words, w0 + per);
+  int n = 0, total;
+  for (int w = w0; w < w1; ++w) n += __popc(equal[w]);
+  int at = block_scan(n, scan, &total);
+  for (int w = w0; w < w1 && at < left; ++w) {
+    const uint32_t e = equal[w];
+    const int c = __popc(e);
+    bits[w] |= at + c <= left ? e : e & ((1u << nth_bit(e, left - at)) - 1);
+    at += c;
+  }
+  __syncthreads();
+  // kept slots before each word, then the list
+  n = 0;
+  for (int w = w0; w < w1; ++w) n += __popc(bits[w]);
+  at = block_scan(n, scan, &total);
+  int *before = (int *)equal;  // (done with)
+  for (int w = w0; w < w1; ++w) {
+    before[w] = at;
+    at += __popc(bits[w]);
+  }
+  __syncthreads();
+  for (int w = warp; w < words; w += kEvictThreads / 32) {
+    const uint32_t e = bits[w];
+    if (e >> lane & 1) kept[before[w] + __popc(e & ((1u << lane) - 1))] = 32 * w + lane;
+  }
+}
 
-  // ---- the move
+// Moves the rows of the choice's lists, K, V and weights.
+template <int HD>
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictArgs p) {
+  const CacheEvict &a = p.a;
+  const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C;
+  const int b = unit / a.Hkv, g = unit - b * a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n_out = a.out_lens[b];
+  if (n_out <= 0) return;  // (the same in all blocks of a cluster)
+  const int *table = a.page_tables + (size_t)b * a.max_pages, *out_table = a.out_tables + (size_t)b * a.out_max_pages;
+  const int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
+  const bool in_place = table[0] == out_table[0];
   constexpr int kLanes = HD / 8;        // lanes of a row of K, and of V
   constexpr int kSide = 32 / (2 * kLanes);  // rows of K and V that the warp moves at once
   const int half = lane & (2 * kLanes - 1), v_side = half / kLanes, c = half % kLanes;
   const bf16 *pool = v_side ? a.v_pool : a.k_pool;
   bf16 *out = v_side ? a.v_pool : a.k_pool;
   const size_t sub = (size_t)(c >> 3) * a.pg * 64;
-  for (int d0 = 0; d0 < n_out; d0 += C * kEvictTurn) {
-    const int first = d0 + (rank * (kEvictThreads / 32) + warp) * kEvictRows;
+  for (int d0 = 0; d0 < n_out; d0 += C * kMoveTurn) {
+    const int first = d0 + (rank * (kMoveThreads / 32) + warp) * kMoveRows;
     // row `first + lane` of the warp's: where it lies and where it goes
     int src = -1, src_slot = 0, dst_slot = 0;
     size_t src_at = 0, dst_at = 0;
     float w = 0.0f;
-    if (lane < kEvictRows && first + lane < n_out) {
+    if (lane < kMoveRows && first + lane < n_out) {
       const int d = first + lane;
-      src = d;
-      if (L > a.budget) {
-        int l = 0, r = words - 1;  // the last word with before <= d
-        while (l < r) {
-          const int m = (l + r + 1) >> 1;
-          if (before[m] <= d) l = m;
-          else r = m - 1;
-        }
-        src = 32 * l + nth_bit(bits[l], d - before[l]);
-      }
+      src = kept[d];
       const int sp = src / a.pg, dp = d / a.pg;
       src_slot = src - sp * a.pg;
       dst_slot = d - dp * a.pg;
       src_at = ((size_t)table[sp] * a.Hkv + g) * a.pg;
       dst_at = ((size_t)out_table[dp] * a.Hkv + g) * a.pg;
       w = __ldcg(a.mass + src_at + src_slot);
-      if (kept) kept[d] = src;
     }
-    uint4 row[kEvictRows / kSide];
+    uint4 row[kMoveRows / kSide];
 #pragma unroll
-    for (int i = 0; i < kEvictRows / kSide; ++i) {
+    for (int i = 0; i < kMoveRows / kSide; ++i) {
       const int from = i * kSide + lane / (2 * kLanes);
       const int s = __shfl_sync(0xffffffffu, src_slot, from);
       const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)src_at, from);
@@ -264,7 +299,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) cache_evict_kernel(const __g
       else __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < kEvictRows / kSide; ++i) {
+    for (int i = 0; i < kMoveRows / kSide; ++i) {
       const int from = i * kSide + lane / (2 * kLanes);
       const int s = __shfl_sync(0xffffffffu, dst_slot, from);
       const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)dst_at, from);
@@ -273,18 +308,13 @@ __global__ void __launch_bounds__(kEvictThreads, 1) cache_evict_kernel(const __g
     }
     if (src >= 0) a.mass[dst_at + dst_slot] = w;
   }
-  if (kept && rank == 0)
-    for (int d = n_out + tid; d < a.budget; d += kEvictThreads) kept[d] = -1;
 }
 
 template <int HD>
-cudaError_t launch_evict(const EvictArgs &p, int cluster, size_t smem, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(cache_evict_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_move(const EvictArgs &p, int cluster, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.a.n_seqs * p.a.Hkv * cluster);
-  cfg.blockDim = dim3(kEvictThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -292,7 +322,7 @@ cudaError_t launch_evict(const EvictArgs &p, int cluster, size_t smem, cudaStrea
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_evict_kernel<HD>, p);
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel<HD>, p);
 }
 
 }  // namespace
@@ -303,14 +333,19 @@ cudaError_t cache_evict(const CacheEvict &a, int *err, cudaStream_t st) {
   p.a = a;
   p.err = err;
   const int slots = (int)(std::min)((long long)a.max_pages * a.pg, (long long)kEvictMostSlots);
-  p.words = ceil_div(slots, 32);
-  p.keys = (std::min)(slots, kEvictKeys);
-  // Blocks for all SMs where there are few heads of few sequences, as far as the
-  // kept rows give each block of a cluster a turn.
-  int cluster = 1;
-  while (cluster < 8 && a.n_seqs * a.Hkv * cluster < 152 && cluster * kEvictTurn < a.budget) cluster *= 2;
+  p.words = 4 * ceil_div(slots, 128);  // (whole groups of 128 slots)
+  p.keys = (std::min)(32 * p.words, kEvictKeys);
+  p.pg_shift = (a.pg & (a.pg - 1)) ? -1 : __builtin_ctz(a.pg);
+  p.vec = a.pg % 4 == 0 && (uintptr_t)a.mass % 16 == 0;
   const size_t smem = ((size_t)2 * p.words + p.keys) * 4;
-  return a.hd == 128 ? launch_evict<128>(p, cluster, smem, st) : launch_evict<64>(p, cluster, smem, st);
+  cudaError_t e = cudaFuncSetAttribute(evict_choice_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  evict_choice_kernel<<<a.n_seqs * a.Hkv, kEvictThreads, smem, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  int cluster = 1;  // as many blocks as the kept rows have turns for
+  while (cluster < 8 && cluster * kMoveTurn < a.budget) cluster *= 2;
+  return a.hd == 128 ? launch_move<128>(p, cluster, st) : launch_move<64>(p, cluster, st);
 }
 
 }  // namespace dg

@@ -750,7 +750,7 @@ int dg_op_key_mass(const uint16_t *q, int64_t q_stride, const float *lse, const 
  *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size]: the weights
  *   out_lens    device int32 [n_seqs]: min(lens[b], budget); must not overlap lens
  *   kept        device int32 [n_seqs][n_kv_heads][budget]: the slot that each kept
- *               token had, -1 behind the last (may be NULL)
+ *               token had, -1 behind the last
  * Heads keep different tokens: from then on a slot is not a position (rotate and
  * append new tokens with positions of their own).  A sequence of a negative length,
  * of more than 262144 slots, or whose slots or kept ones lie outside the tables, and

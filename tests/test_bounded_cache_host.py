@@ -61,7 +61,7 @@ EV = dict(k_pool=A, v_pool=A, mass=A, tables=A, max_pages=4, out_tables=2 * A, o
 
 @pytest.mark.parametrize("change", [
     dict(k_pool=None), dict(v_pool=None), dict(mass=None), dict(k_pool=A + 8), dict(mass=A + 2), dict(tables=None), dict(out_tables=None),
-    dict(lens=None), dict(out_lens=None), dict(out_lens=A), dict(max_pages=-1), dict(out_max=-1), dict(n_seqs=-1), dict(hkv=0), dict(hd=96),
+    dict(lens=None), dict(out_lens=None), dict(out_lens=A), dict(kept=None), dict(max_pages=-1), dict(out_max=-1), dict(n_seqs=-1), dict(hkv=0), dict(hd=96),
     dict(hd=256), dict(pg=0), dict(n_pages=0), dict(budget=0), dict(sinks=-1), dict(recent=-1), dict(sinks=100, recent=101),
     dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), dict(n_seqs=1 << 30),
 ])
@@ -93,7 +93,7 @@ def test_binding_refuses_tensors_that_are_not_on_the_device():
     pool = torch.zeros(2, 4, 64, 64, dtype=torch.bfloat16)
     calls = [lambda: dgp.dg_op_window_attention(t, pool, pool, i[:, None], i, torch.zeros(3, dtype=torch.int32), t.clone(), None),
              lambda: dgp.dg_op_key_mass(t, torch.zeros(2, 4), pool, torch.zeros(2, 4, 64), i[:, None], i, torch.zeros(3, dtype=torch.int32), None),
-             lambda: dgp.dg_op_cache_evict(pool, pool, torch.zeros(2, 4, 64), i[:, None], i[:, None], i, i.clone(), 5)]
+             lambda: dgp.dg_op_cache_evict(pool, pool, torch.zeros(2, 4, 64), i[:, None], i[:, None], i, i.clone(), 5, torch.zeros(2, 4, 5, dtype=torch.int32))]
     for c in calls:
         with pytest.raises(dgp.DgError) as e:
             c()

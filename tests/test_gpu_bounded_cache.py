@@ -639,13 +639,12 @@ def test_evict_some_in_place_and_some_elsewhere():
     check_evict(c, 2, 20)
 
 
-def test_evict_without_kept_repeats_and_is_captured():
+def test_evict_repeats_and_is_captured():
     rng = np.random.default_rng(7)
     c = Cache(rng, [5000, 3000, 12], 4, 128, 128, 1500)
     ref = c.ref(4, 300)
     d = c.on_gpu()
-    d2 = dict(d, kept=None)
-    dgp.dg_op_cache_evict(**d2, budget=1500, sinks=4, recent=300)
+    dgp.dg_op_cache_evict(**d, budget=1500, sinks=4, recent=300)
     g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.graph(g, stream=st):
