@@ -14,12 +14,14 @@
 // bf16 numbers whose sum is the fp32 one; the keys have ones there): added up by the
 // tensor core it costs an eighth of the products, read from shared memory by every
 // thread it cost as much of that memory's bandwidth as the products themselves
-// (8192 rows: 141 us).  A unit is 1 or 4 tiles of 128 keys of a (sequence, KV head): they stay in
-// shared memory while the tiles of up to 128 rows (tokens x heads of the group, staged
-// by one TMA copy) that see any of them go by.  With many row tiles a unit has 4 key
-// tiles, which share each row tile read from L2; with one, 1: the keys stream through
-// the ring, the row tile stays, and ranges come out even.  All blocks take equal ranges
-// of the batch's (unit, row tile) pairs, found on the device as in the tree attention;
+// (8192 rows: 141 us).  A unit is 1, 2 or 4 tiles of 128 keys of a (sequence, KV head):
+// they stay in shared memory while the tiles of up to 128 rows (tokens x heads of the
+// group, staged by one TMA copy) that see any of them go by.  With many row tiles a unit
+// has 4 key tiles, which share each row tile read from L2; with one row tile, which stays
+// while the keys stream by, 2 (48 sequences of one token over up to 16k keys: 170 us with 1,
+// 128 with 2, 151 with 4, which leave the ring no room for the next unit); where there is
+// little to do, what gives each block one unit.  All blocks take equal ranges
+// of the batch's (unit, row tile) pairs (ranges.cuh);
 // a unit that spans several blocks leaves a partial sum per block in the workspace, and
 // the block whose sum arrives last adds them up in order: no block waits, results repeat
 // bit for bit.
@@ -33,6 +35,7 @@
 #include "attn_tc.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
+#include "ranges.cuh"
 
 namespace dg {
 
@@ -41,15 +44,14 @@ namespace {
 constexpr int kMassThreads = 640;
 constexpr int kMassCtas = 152;       // most blocks: one per SM
 constexpr int kMassTiles = 4;        // most key tiles of a unit
-constexpr int kMassFew = 3;          // (key tile, row tile) pairs a block up to which units are single tiles
-constexpr int kMassUnitCost = 1;     // cost of starting a unit, in row tiles
 constexpr int kMassGaveUp = 64;      // status code of a block that gave up after an earlier kernel
 
 struct MassArgs {
   CUtensorMap q_map, few_map;  // rows [n_tok][Hq][hd], boxes 64 x G x T and 64 x G x few
   KeyMass a;
   int G, T, few, ctas;  // T: tokens of a row tile
-  int pg_shift;         // log2 of the page size, -1 where it is no power of two
+  int pg_shift, t_shift;  // log2 of the page size and of T, -1 where they are no powers of two
+  int many;               // sequences have more than two row tiles on the average
   float scale_log2, inv_scale;
   float *part;                // [2 kMassCtas][kMassTiles * 128]: block c's first piece in 2 c, its last in 2 c + 1
   unsigned long long *count;  // [kMassTiles][kMassCtas]: pieces that have arrived of tile k of the unit that ends in block c
@@ -72,36 +74,15 @@ struct MassSmem {
   static constexpr size_t bytes = slot + 8 + 4 * kMassTiles;
 };
 
-// n = 0: nothing to do, or rows or slots outside the call's arrays.  Of its units of
-// `keys` keys those below `sink` and from `low` on hold a key which some token sees,
-// or a new key (it is set to 0 otherwise).
+// n = 0: nothing to do, or rows or slots outside the call's arrays.  Of its units
+// those below `sink` and from `low` on hold a key which some token sees, or a new key
+// (it is set to 0 otherwise).
 struct MassSeq {
   int row0, n, pre, tf, row_tiles, sink, low, units;  // tf: the first token that counts
   bool bad;
   __device__ __forceinline__ int visits() const { return sink + units - low; }
   __device__ __forceinline__ int unit(int i) const { return i < sink ? i : i - sink + low; }  // the i-th visited
 };
-
-__device__ __forceinline__ MassSeq load_seq(const MassArgs &p, int b, int keys) {
-  MassSeq s;
-  const int o0 = p.a.offsets[b], o1 = p.a.offsets[b + 1];
-  s.row0 = o0;
-  s.pre = p.a.prefix_lens[b];
-  const long long n = (long long)o1 - o0, end = (long long)s.pre + n;
-  const long long room = min((long long)p.a.max_pages * p.a.pg, (long long)0x7fffff00);
-  s.bad = n != 0 && (o0 < 0 || n < 0 || o1 > p.a.n_tok || s.pre < 0 || end > room);
-  s.n = s.bad ? 0 : (int)n;
-  s.tf = p.a.observe ? max(0, s.n - p.a.observe) : 0;
-  s.row_tiles = s.n - s.tf <= p.T ? 1 : ceil_div(s.n - s.tf, p.T);
-  s.sink = s.low = s.units = 0;
-  if (s.n) {  // (keys: a power of two)
-    const int shift = 31 - __clz(keys);
-    s.units = (int)(((unsigned)s.pre + s.n + keys - 1) >> shift);
-    s.low = min(max(0, s.pre + s.tf - p.a.window + 1), s.pre) >> shift;
-    s.sink = min((int)(((unsigned)p.a.sinks + keys - 1) >> shift), s.low);
-  }
-  return s;
-}
 
 // Tokens [t0, t1) that count and see a key of [j0, j1) (j1 - 1 a slot of the sequence).
 struct Tokens {
@@ -115,192 +96,92 @@ __device__ __forceinline__ Tokens seen_by(const MassArgs &p, const MassSeq &s, i
   return t;
 }
 
-// The row tiles of a unit: [first, first + count), one at least.
-struct Rows {
-  int first, count;
-};
-__device__ __forceinline__ Rows unit_rows(const MassArgs &p, const MassSeq &s, int u, int keys) {
-  Rows r;
-  r.first = 0;
-  r.count = 1;
-  if (s.row_tiles > 1) {
-    const int j0 = u * keys;
+// Units of `keys` keys (a power of two), their items the row tiles that see any.
+struct MassList {
+  typedef MassSeq Seq;
+  static constexpr int kUnitCost = 1;
+  const MassArgs &p;
+  int keys;
+  __device__ __forceinline__ int row_tile(int t) const { return p.t_shift >= 0 ? t >> p.t_shift : t / p.T; }
+  __device__ __forceinline__ Seq load(int b) const {
+    Seq s;
+    const int o0 = p.a.offsets[b], o1 = p.a.offsets[b + 1];
+    s.row0 = o0;
+    s.pre = p.a.prefix_lens[b];
+    const long long n = (long long)o1 - o0, end = (long long)s.pre + n;
+    const long long room = min((long long)p.a.max_pages * p.a.pg, (long long)0x7fffff00);
+    s.bad = n != 0 && (o0 < 0 || n < 0 || o1 > p.a.n_tok || s.pre < 0 || end > room);
+    s.n = s.bad ? 0 : (int)n;
+    s.tf = p.a.observe ? max(0, s.n - p.a.observe) : 0;
+    s.row_tiles = row_tile(s.n - s.tf + p.T - 1);
+    s.sink = s.low = s.units = 0;
+    if (s.n) {
+      const int shift = 31 - __clz(keys);
+      s.units = (int)(((unsigned)s.pre + s.n + keys - 1) >> shift);
+      s.low = min(max(0, s.pre + s.tf - p.a.window + 1), s.pre) >> shift;
+      s.sink = min((int)(((unsigned)p.a.sinks + keys - 1) >> shift), s.low);
+    }
+    return s;
+  }
+  __device__ __forceinline__ bool even(const Seq &s) const { return s.row_tiles <= 1; }
+  // The row tiles of the i-th unit: [first, first + count), one at least.
+  __device__ __forceinline__ int rows(const Seq &s, int i, int &first) const {
+    first = 0;
+    if (s.row_tiles <= 1) return 1;
+    const int j0 = s.unit(i) * keys;
     const Tokens t = seen_by(p, s, j0, min(j0 + keys, s.pre + s.n));
-    if (t.t0 < t.t1) {
-      r.first = (t.t0 - s.tf) / p.T;
-      r.count = ceil_div(t.t1 - s.tf, p.T) - r.first;
-    }
+    if (t.t0 >= t.t1) return 1;
+    first = row_tile(t.t0 - s.tf);
+    return row_tile(t.t1 - s.tf + p.T - 1) - first;
   }
-  return r;
-}
-
-constexpr unsigned kMassMost = 1u << 30;  // more than an ascending batch's cost: offsets that overlap stop here
-
-// Cost of the units of one KV head; run by the whole warp for one sequence.
-__device__ __forceinline__ int head_cost(const MassArgs &p, const MassSeq &s, int keys, int lane) {
-  const int n = s.visits();
-  if (s.row_tiles <= 1) return n * (1 + kMassUnitCost);
-  int sum = 0;
-#pragma unroll 1
-  for (int i = lane; i < n; i += 32) sum += unit_rows(p, s, s.unit(i), keys).count + kMassUnitCost;
-  return (int)min(__reduce_add_sync(0xffffffffu, (unsigned)min(sum, 1 << 26)), kMassMost);
-}
-
-// A block's share: `count` cost units from unit `at` of sequence b on, of the equal
-// ranges of `per`; `tiles` key tiles of `keys` keys a unit.  Found by every warp for
-// itself, 32 sequences at a time, in three rounds: how much there is (units of one
-// tile where that is little, so that all blocks have some), its cost, and the
-// sequence in which the range begins.
-struct MassRange {
-  int b, at, count, per, tiles, keys;
+  __device__ __forceinline__ int items(const Seq &s, int i) const {
+    int first;
+    return rows(s, i, first);
+  }
 };
-__device__ __forceinline__ MassRange block_range(const MassArgs &p, int lane) {
-  MassRange r;
-  r.tiles = 1;
-  r.keys = 128;
-  r.b = r.at = r.count = r.per = 0;
-  unsigned first = 0;
+
+// The units' key tiles: as many as give every block one unit where there is that
+// little to do; 4 for many row tiles, 2 for one or two (see above).
+__device__ __forceinline__ int unit_tiles(const MassArgs &p, int lane) {
+  const MassList list{p, 128};
+  unsigned total = 0;
 #pragma unroll 1
-  for (int round = 0; round < 3; ++round) {
-    unsigned total = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
-      MassSeq s = load_seq(p, min(b0 + lane, p.a.n_seqs - 1), r.keys);
-      if (b0 + lane >= p.a.n_seqs) s.n = s.units = s.low = s.sink = 0;
-      long long c = (long long)s.visits() * (1 + kMassUnitCost);
-      if (round == 0) {
-        c = (long long)s.visits() * s.row_tiles;
-        if (s.bad && blockIdx.x == 0 && threadIdx.x < 32 && p.err) atomicExch(p.err + 1, kBadSequence);
-      } else {
-#pragma unroll 1
-        for (unsigned many = __ballot_sync(0xffffffffu, s.n && s.row_tiles > 1); many; many &= many - 1) {
-          const int l = __ffs(many) - 1, h = head_cost(p, load_seq(p, b0 + l, r.keys), r.keys, lane);
-          if (lane == l) c = h;
-        }
-      }
-      const unsigned cost = (unsigned)min(c * p.a.Hkv, (long long)kMassMost);
-      unsigned incl = cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl = min(incl + v, kMassMost);
-      }
-      if (round == 2) {
-        const unsigned end = min(total + incl, kMassMost), begin = end - min(cost, end);
-        const unsigned here = __ballot_sync(0xffffffffu, first >= begin && first < end);
-        if (here) {
-          const int l = __ffs(here) - 1;
-          r.b = b0 + l;
-          r.at = __shfl_sync(0xffffffffu, (int)(first - begin), l);
-          return r;
-        }
-      }
-      total = min(total + __shfl_sync(0xffffffffu, incl, 31), kMassMost);
-    }
-    if (round == 0) {
-      if (total > (unsigned)(kMassFew * p.ctas)) {
-        r.tiles = kMassTiles;
-        r.keys = 128 * kMassTiles;
-      }
-    } else if (round == 1) {
-      r.per = (int)((total + p.ctas - 1) / p.ctas);
-      const long long at = (long long)r.per * blockIdx.x;
-      if (at >= total) return r;
-      first = (unsigned)at;
-      r.count = (int)min((unsigned)r.per, total - first);
-    }
+  for (int b0 = 0; b0 < p.a.n_seqs; b0 += 32) {
+    const MassSeq s = list.load(min(b0 + lane, p.a.n_seqs - 1));
+    const long long c = b0 + lane < p.a.n_seqs && s.n ? (long long)s.visits() * s.row_tiles * p.a.Hkv : 0;
+    total = min(total + __shfl_sync(0xffffffffu, lane_sums((unsigned)min(c, (long long)kMostCost), lane), 31), kMostCost);
   }
-  r.count = 0;
-  return r;
+  const unsigned ctas = (unsigned)p.ctas;
+  return total <= ctas ? 1 : total <= 2 * ctas ? 2 : total <= 4 * ctas || p.many ? 4 : 2;
 }
 
-// The pieces of a block's range: row tiles [q0, q1) of unit u of (b, g), the i-th of
-// its sequence.  at: where the unit begins, relative to the range; left: what the
-// range holds behind the piece.
-struct MassWalk {
-  MassSeq s;
-  Rows r;
-  int keys, b, g, i, u, q0, q1, at, left;
-  __device__ __forceinline__ void clip(int from, int n) {
-    const int end = min(r.count + kMassUnitCost, from + n);
-    q0 = max(0, from - kMassUnitCost);
-    q1 = max(0, end - kMassUnitCost);
-    left = n - (end - from);
+// The walk over a block's pieces, with the unit's first key and first row tile.
+struct MassWalk : RangeWalk<MassList> {
+  int key0, tile0;
+  __device__ __forceinline__ void locate(const MassList &list) {
+    key0 = s.unit(u) * list.keys;
+    list.rows(s, u, tile0);
   }
-  __device__ __forceinline__ void visit(const MassArgs &p) {
-    u = s.unit(i);
-    r = unit_rows(p, s, u, keys);
+  __device__ __forceinline__ bool begin(const MassList &list, const BlockRange &range, int lane) {
+    const bool some = RangeWalk<MassList>::begin(list, range, list.p.a.n_seqs, list.p.a.Hkv, lane);
+    if (some) locate(list);
+    return some;
   }
-  // Run by a whole warp.  false: the range holds no row tile.
-  __device__ __forceinline__ bool begin(const MassArgs &p, const MassRange &range, int lane) {
-    b = range.b;
-    keys = range.keys;
-    s = load_seq(p, b, keys);
-    const int head = head_cost(p, s, keys, lane), visits = s.visits();
-    g = range.at / head;
-    const int rem = range.at - g * head;
-    if (s.row_tiles <= 1) {
-      i = rem / (1 + kMassUnitCost);
-      at = i * (1 + kMassUnitCost) - rem;
-    } else {  // 32 units at a time
-      int before = 0;
-      i = visits - 1;
-      at = 0;
-#pragma unroll 1
-      for (int k0 = 0; k0 < visits; k0 += 32) {
-        const int cost = k0 + lane < visits ? unit_rows(p, s, s.unit(k0 + lane), keys).count + kMassUnitCost : 0;
-        int incl = cost;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        const unsigned here = __ballot_sync(0xffffffffu, rem < before + incl);
-        if (here) {
-          const int l = __ffs(here) - 1;
-          i = k0 + l;
-          at = __shfl_sync(0xffffffffu, before + incl - cost - rem, l);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
-    visit(p);
-    clip(-at, range.count);
-    return q0 < q1 || next(p);
-  }
-  __device__ __forceinline__ bool next(const MassArgs &p) {
-    do {
-      if (left <= 0) return false;
-      at += r.count + kMassUnitCost;
-      if (++i == s.visits()) {
-        i = 0;
-        if (++g == p.a.Hkv) {
-          g = 0;
-          do {
-            if (++b >= p.a.n_seqs) return false;
-            s = load_seq(p, b, keys);
-          } while (s.n == 0);
-        }
-      }
-      visit(p);
-      clip(0, left);
-    } while (q0 == q1);
-    return true;
+  __device__ __forceinline__ bool next(const MassList &list) {
+    const bool more = RangeWalk<MassList>::next(list, list.p.a.n_seqs, list.p.a.Hkv);
+    if (more) locate(list);
+    return more;
   }
   // Row tile q of the piece: its first token, its columns (rows).
-  __device__ __forceinline__ int token(const MassArgs &p, int q) const { return s.tf + (r.first + q) * p.T; }
+  __device__ __forceinline__ int token(const MassArgs &p, int q) const { return s.tf + (tile0 + q) * p.T; }
   __device__ __forceinline__ int columns(const MassArgs &p, int t0) const { return min(p.T, s.n - t0) * p.G; }
   // The tokens that count and see a key of the unit's tile k (none: t0 >= t1).
-  __device__ __forceinline__ Tokens tile_tokens(const MassArgs &p, int k) const {
-    const int j0 = u * keys + 128 * k, end = s.pre + s.n;
+  __device__ __forceinline__ Tokens tile_tokens(const MassList &list, int k) const {
+    const int j0 = key0 + 128 * k, end = s.pre + s.n;
     Tokens t;
     t.t0 = t.t1 = 0;
-    if (128 * k < keys && j0 < end) t = seen_by(p, s, j0, min(j0 + 128, end));
+    if (128 * k < list.keys && j0 < end) t = seen_by(list.p, s, j0, min(j0 + 128, end));
     return t;
-  }
-  __device__ __forceinline__ bool same_rows(const MassWalk &o, int q, int oq) const {
-    return b == o.b && g == o.g && r.first + q == o.r.first + oq;
   }
 };
 
@@ -310,22 +191,6 @@ __device__ __forceinline__ int page_entry(const MassArgs &p, int b, int j) {
 }
 __device__ __forceinline__ int page_slot(const MassArgs &p, int j) {
   return p.pg_shift >= 0 ? j & (p.a.pg - 1) : j % p.a.pg;
-}
-
-// A piece's arrival: true in the block whose piece is the unit's last to arrive.
-// The word counts arrivals of this launch (its high bits are the launch's own, see
-// the tree attention's flags), and is 0 again after the last.
-__device__ __forceinline__ bool arrive_last(unsigned long long *word, unsigned long long up, int pieces) {
-  const unsigned long long base = up & ~0xfffull;
-  unsigned long long old = *(volatile unsigned long long *)word, seen;
-  do {
-    seen = old;
-    old = atomicCAS(word, seen, (seen & ~0xfffull) == base ? seen + 1 : base + 1);
-  } while (old != seen);
-  const int n = (seen & ~0xfffull) == base ? (int)(seen & 0xfff) + 1 : 1;
-  if (n < pieces) return false;
-  *(volatile unsigned long long *)word = 0;
-  return true;
 }
 
 // A bounded wait that costs one test when the phase is over already; the loop is not
@@ -396,10 +261,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
   for (int i = threadIdx.x; i < (1 + QR) * 256; i += kMassThreads)
     *(uint4 *)(base + S::ones + 16 * i) = i < 256 && !(i & 8) ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-  const MassRange range = block_range(p, lane);  // the same in every warp
+  const int tiles = unit_tiles(p, lane);  // the same in every warp, as what follows
+  const MassList list{p, 128 * tiles};
+  const BlockRange range = block_range(list, p.a.n_seqs, p.a.Hkv, p.ctas, p.err, lane);
   MassWalk w;
-  if (range.count <= 0 || !w.begin(p, range, lane)) return;
-  const int tiles = range.tiles;
+  if (range.count <= 0 || !w.begin(list, range, lane)) return;
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(tc::smem_u32(tmem_slot)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
@@ -424,7 +290,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     const int k_lane = lane / (2 * HB), half = lane / HB & 1, blk = lane % HB;
     // the half's entry of the page table; -2: not seen by any row (its page is not touched)
     auto entry_of = [&](const MassWalk &x) {
-      const int j0 = x.u * x.keys + 128 * k_lane + 64 * half, end = x.s.pre + x.s.n;
+      const int j0 = x.key0 + 128 * k_lane + 64 * half, end = x.s.pre + x.s.n;
       if (k_lane >= tiles || j0 >= end) return -2;
       const Tokens t = seen_by(p, x.s, j0, min(j0 + 64, end));
       return t.t0 < t.t1 ? page_entry(p, x.b, j0) : -2;
@@ -434,10 +300,10 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       const void *src = g_zero_half;
       if (page >= 0 && page < p.a.n_pages)
         src = p.a.k_pool + ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)blk * p.a.pg * 64 +
-              (size_t)page_slot(p, w.u * w.keys + 128 * k_lane + 64 * half) * 64;
-      const Tokens t = w.tile_tokens(p, lane);
+              (size_t)page_slot(p, w.key0 + 128 * k_lane + 64 * half) * 64;
+      const Tokens t = w.tile_tokens(list, lane);
       unsigned used = __ballot_sync(0xffffffffu, t.t0 < t.t1);
-      more = w.next(p);
+      more = w.next(list);
       if (more) page = entry_of(w);
       for (; used; used &= used - 1) {
         if (lane == 0) {
@@ -467,7 +333,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     }
   } else if (warp == 1) {
     // ---- row tiles and their log-sum-exps ------------------------------------------
-    int slot = 0, phase = 0, issued = 0, q = w.q0, t0 = w.token(p, q), cols = w.columns(p, t0);
+    int slot = 0, phase = 0, issued = 0, q = w.i0, t0 = w.token(p, q), cols = w.columns(p, t0);
     bool ok = true, more = true;
     // row c of the tile: token t0 + c / G, head g G + c % G
     int off[4];
@@ -516,14 +382,13 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         phase ^= 1;
       }
       // the next row tile that is another one
-      const MassWalk was = w;
-      const int was_q = q;
+      const int b = w.b, g = w.g, tile = w.tile0 + q;
       do {
-        if (++q >= w.q1) {
-          more = w.next(p);
-          q = w.q0;
+        if (++q >= w.i1) {
+          more = w.next(list);
+          q = w.i0;
         }
-      } while (more && w.same_rows(was, q, was_q));
+      } while (more && w.b == b && w.g == g && w.tile0 + q == tile);
       if (more) {
         t0 = w.token(p, q);
         cols = w.columns(p, t0);
@@ -544,12 +409,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     int ks = 0, kphase = 0, qs = 0, qphase = 0, order = 0, step0 = 0, step1 = 0;  // steps of groups half, half + 2
     const uint32_t kdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::kring)), qdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::qring));
     while (ok && more) {
-      const Tokens mine = w.tile_tokens(p, lane);  // of tile `lane`
+      const Tokens mine = w.tile_tokens(list, lane);  // of tile `lane`
       const unsigned used = __ballot_sync(0xffffffffu, mine.t0 < mine.t1);
-      const int q0 = w.q0, q1 = w.q1, n = w.s.n, b = w.b, h = w.g, last_tile = w.r.first + q1 - 1;
+      const int q0 = w.i0, q1 = w.i1, n = w.s.n, b = w.b, h = w.g, last_tile = w.tile0 + q1 - 1;
       int t0 = w.token(p, q0);
-      more = w.next(p);
-      const bool stays = more && w.b == b && w.g == h && w.r.first + w.q0 == last_tile;  // the next piece begins with the row tile
+      more = w.next(list);
+      const bool stays = more && w.b == b && w.g == h && w.tile0 + w.i0 == last_tile;  // the next piece begins with the row tile
       const int n_used = __popc(used);
       int ring = 0;  // key tiles of the unit that have arrived, from slot ks on
       auto arrived = [&]() {
@@ -624,7 +489,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     // The key's entry of the page table: -2 where no weight is written (another
     // group's, behind the sequence, neither new nor seen by any row).
     auto entry = [&]() {
-      const int k = (g - order) & 3, j = w.u * w.keys + 128 * k + row;
+      const int k = (g - order) & 3, j = w.key0 + 128 * k + row;
       if (k >= tiles || j >= w.s.pre + w.s.n) return -2;
       const Tokens t = seen_by(p, w.s, j, j + 1);
       return j >= w.s.pre || t.t0 < t.t1 ? page_entry(p, w.b, j) : -2;
@@ -634,7 +499,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       const int k = (g - order) & 3;
       const bool mine = k < tiles;
       // where the weight lies (< 0: none is written), and what it was
-      const int j = w.u * w.keys + 128 * k + row;
+      const int j = w.key0 + 128 * k + row;
       long long at = -1;
       float old = 0.0f, sum = 0.0f;
       if (page >= 0 && page < p.a.n_pages) {
@@ -644,10 +509,13 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         atomicExch(p.err + 1, kBadPage);
       }
       // the piece, and the next one: its entry of the page table is on its way meanwhile
-      const int pre = w.s.pre, n = w.s.n, q0 = w.q0, q1 = w.q1, count = w.r.count, begin = range.per * (int)blockIdx.x + w.at;
+      const int pre = w.s.pre, n = w.s.n, q0 = w.i0, q1 = w.i1;
+      const bool whole = q0 == 0 && q1 == w.items;
+      UnitBlocks blocks{};
+      if (!whole) blocks = unit_blocks(w, range.per);
       int t0 = w.token(p, q0);
-      const Tokens seen = w.tile_tokens(p, k);
-      more = w.next(p);
+      const Tokens seen = w.tile_tokens(list, k);
+      more = w.next(list);
       order += tiles;
       if (more) page = entry();
 #pragma unroll 1
@@ -714,23 +582,21 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
           sum += r.x + r.y;
         }
       }
-      if (q0 == 0 && q1 == count) {
+      if (whole) {
         if (at >= 0 && ok) p.a.mass[at] = old + sum;
       } else if (mine) {
-        // a piece: the unit begins at cost unit `begin` of all ranges
         const int to = 2 * blockIdx.x + (piece ? 1 : 0);
         p.part[((size_t)to * kMassTiles + k) * 128 + row] = sum;
-        const int first = begin + kMassUnitCost, b0 = first / range.per, b1 = (first + count - 1) / range.per;
-        const int slot0 = 2 * b0 + (begin > b0 * range.per ? 1 : 0);  // a piece of the unit before comes first there
         __threadfence();
         group_sync(g);
-        if (row == 0) last[g] = !*abort && arrive_last(p.count + (size_t)k * kMassCtas + b1, p.ticket + (uint32_t)status, b1 - b0 + 1);
+        if (row == 0) last[g] = !*abort && arrive_last(p.count + (size_t)k * kMassCtas + blocks.last, p.ticket + (uint32_t)status,
+                                                           blocks.last - blocks.first + 1);
         group_sync(g);
         if (last[g] && at >= 0) {
           __threadfence();
           const float *src = p.part + (size_t)k * 128 + row;
-          float total = __ldcg(src + (size_t)slot0 * kMassTiles * 128);
-          for (int c = b0 + 1; c <= b1; ++c) total += __ldcg(src + (size_t)2 * c * kMassTiles * 128);
+          float total = 0.0f;
+          for (int c = blocks.first; c <= blocks.last; ++c) total += __ldcg(src + (size_t)blocks.slot(c) * kMassTiles * 128);
           p.a.mass[at] = old + total;
         }
       }
@@ -800,6 +666,9 @@ cudaError_t key_mass(const KeyMass &a, void *ws, int *err, cudaStream_t st) {
   p.err = err;
   p.few = max(1, 16 / p.G);
   p.pg_shift = (a.pg & (a.pg - 1)) ? -1 : __builtin_ctz(a.pg);
+  p.t_shift = (p.T & (p.T - 1)) ? -1 : __builtin_ctz(p.T);
+  const int tokens = ceil_div(a.n_tok, a.n_seqs);
+  p.many = (long long)(a.observe ? min(a.observe, tokens) : tokens) * p.G > 256;
   cudaError_t e = rows_map(&p.q_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.T);
   if (e == cudaSuccess) e = rows_map(&p.few_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.few);
   if (e != cudaSuccess) return e;

@@ -40,30 +40,43 @@ __device__ __forceinline__ unsigned lane_sums(unsigned v, int lane) {
 
 // A block's share: `count` cost units from unit `at` of sequence b on, of the equal
 // ranges of `per`.  Found by every warp for itself, 32 sequences at a time: their
-// cost, then the sequence in which the range begins.
+// cost, then the sequence in which the range begins.  Short lists are added up by the
+// sequence's lane, long ones by the warp, one after the other.
 struct BlockRange {
   int b, at, count, per;
 };
+constexpr int kShortList = 16;
 template <class L>
 __device__ __forceinline__ BlockRange block_range(const L &list, int n_seqs, int heads, int ctas, int *err, int lane) {
   BlockRange r;
   r.b = r.at = r.count = r.per = 0;
-  unsigned first = 0;
+  unsigned first = 0, cost = 0;
 #pragma unroll 1
   for (int round = 0; round < 2; ++round) {
     unsigned total = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < n_seqs; b0 += 32) {
-      const bool there = b0 + lane < n_seqs;
-      const typename L::Seq s = list.load(min(b0 + lane, n_seqs - 1));
-      long long c = there && s.n && list.even(s) ? (long long)s.visits() * (1 + L::kUnitCost) : 0;
+      if (round == 0 || n_seqs > 32) {  // (else they are still there)
+        const bool there = b0 + lane < n_seqs;
+        const typename L::Seq s = list.load(min(b0 + lane, n_seqs - 1));
+        const int visits = there && s.n ? s.visits() : 0;
+        const bool lengthy = visits > kShortList && !list.even(s);
+        long long c = 0;
+        if (visits && list.even(s)) {
+          c = (long long)visits * (1 + L::kUnitCost);
+        } else if (!lengthy) {
 #pragma unroll 1
-      for (unsigned many = __ballot_sync(0xffffffffu, there && s.n && !list.even(s)); many; many &= many - 1) {
-        const int l = __ffs(many) - 1, h = head_cost(list, list.load(b0 + l), lane);
-        if (lane == l) c = h;
+          for (int i = 0; i < visits; ++i) c += list.items(s, i) + L::kUnitCost;
+        }
+#pragma unroll 1
+        for (unsigned many = __ballot_sync(0xffffffffu, lengthy); many; many &= many - 1) {
+          const int l = __ffs(many) - 1, h = head_cost(list, list.load(b0 + l), lane);
+          if (lane == l) c = h;
+        }
+        if (there && s.bad && round == 0 && blockIdx.x == 0 && threadIdx.x < 32 && err) atomicExch(err + 1, kBadSequence);
+        cost = (unsigned)min(c * heads, (long long)kMostCost);
       }
-      if (there && s.bad && round == 0 && blockIdx.x == 0 && threadIdx.x < 32 && err) atomicExch(err + 1, kBadSequence);
-      const unsigned cost = (unsigned)min(c * heads, (long long)kMostCost), incl = lane_sums(cost, lane);
+      const unsigned incl = lane_sums(cost, lane);
       if (round) {
         const unsigned end = min(total + incl, kMostCost), begin = end - min(cost, end);
         const unsigned here = __ballot_sync(0xffffffffu, first >= begin && first < end);
