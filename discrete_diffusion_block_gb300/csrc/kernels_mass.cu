@@ -50,8 +50,9 @@ struct MassArgs {
   CUtensorMap q_map, few_map;  // rows [n_tok][Hq][hd], boxes 64 x G x T and 64 x G x few
   KeyMass a;
   int G, T, few, ctas;  // T: tokens of a row tile
-  int pg_shift, t_shift;  // log2 of the page size and of T, -1 where they are no powers of two
-  int many;               // sequences have more than two row tiles on the average
+  int pg_shift;         // log2 of the page size, -1 where it is no power of two
+  uint32_t t_magic;     // 2^32 / T, rounded up (0: divide)
+  int many;             // sequences have more than two row tiles on the average
   float scale_log2, inv_scale;
   float *part;                // [2 kMassCtas][kMassTiles * 128]: block c's first piece in 2 c, its last in 2 c + 1
   unsigned long long *count;  // [kMassTiles][kMassCtas]: pieces that have arrived of tile k of the unit that ends in block c
@@ -102,7 +103,9 @@ struct MassList {
   static constexpr int kUnitCost = 1;
   const MassArgs &p;
   int keys;
-  __device__ __forceinline__ int row_tile(int t) const { return p.t_shift >= 0 ? t >> p.t_shift : t / p.T; }
+  // t / T: t ceil(2^32 / T) / 2^32 is above t / T by less than t / 2^32, and so exact
+  // below 2^25 tokens (T <= 128).  Divisions took most of the start of a batch of prompts.
+  __device__ __forceinline__ int row_tile(int t) const { return p.t_magic ? (int)__umulhi((uint32_t)t, p.t_magic) : t / p.T; }
   __device__ __forceinline__ Seq load(int b) const {
     Seq s;
     const int o0 = p.a.offsets[b], o1 = p.a.offsets[b + 1];
@@ -666,7 +669,7 @@ cudaError_t key_mass(const KeyMass &a, void *ws, int *err, cudaStream_t st) {
   p.err = err;
   p.few = max(1, 16 / p.G);
   p.pg_shift = (a.pg & (a.pg - 1)) ? -1 : __builtin_ctz(a.pg);
-  p.t_shift = (p.T & (p.T - 1)) ? -1 : __builtin_ctz(p.T);
+  p.t_magic = p.T > 1 && a.n_tok < (1 << 25) - 256 ? (uint32_t)(((1ull << 32) + p.T - 1) / p.T) : 0;
   const int tokens = ceil_div(a.n_tok, a.n_seqs);
   p.many = (long long)(a.observe ? min(a.observe, tokens) : tokens) * p.G > 256;
   cudaError_t e = rows_map(&p.q_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.T);
