@@ -23,6 +23,7 @@
 //
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
+#include <algorithm>
 #include <atomic>
 
 #include "attn_tc.cuh"
@@ -128,13 +129,9 @@ __device__ __forceinline__ RowTile row_tile(const ChunkList &list, const ChunkWa
   return r;
 }
 
-// A bounded wait that costs one test when the phase is over already; the loop is not
-// inlined: the roles' code has to stay short.
-__device__ __forceinline__ bool chunk_wait_on(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
-  return tc::mbar_wait(b, parity, err, code, abort);
-}
+// A bounded wait that costs one test when the phase is over already.
 __device__ __forceinline__ bool chunk_wait(uint64_t *b, uint32_t parity, int *err, int code, volatile int *abort) {
-  return tc::mbar_try_wait(b, parity) || chunk_wait_on(b, parity, err, code, abort);
+  return tc::mbar_try_wait(b, parity) || tc::mbar_wait(b, parity, err, code, abort);
 }
 
 template <int HD>
@@ -642,12 +639,15 @@ cudaError_t launch_chunk(ChunkArgs &p, cudaStream_t st) {
 // 100, windows of 1024 (400) 162 and 173.  One of 1024 tokens (64 units), windows of 1024
 // 37 and 26, over 16k keys 135 and 146; 21 of up to 201, 12 and 4 heads of 64 (103) 38
 // and 29; 32 of 64 tokens over 2k (128 units, one tile of rows each) 101 and 76.
+static bool blocks_full(int n_tok, int Hq) { return (long long)n_tok * Hq >= 120 * 256; }
 static bool many_rows(int n_tok, int n_seqs, int Hq, int Hkv) {
-  return (long long)n_tok * Hq >= 120 * 256 && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;
+  return blocks_full(n_tok, Hq) && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;
 }
 
+// What is enough for n_tok rows is so for fewer, in however many sequences.
 size_t window_attention_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int hd) {
-  return many_rows(n_tok, n_seqs, Hq, Hkv) ? chunk_workspace(hd).bytes : tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd);
+  const size_t tree = tree_attention_workspace_bytes(n_tok, n_seqs, Hq, Hkv, hd);
+  return blocks_full(n_tok, Hq) ? std::max(tree, chunk_workspace(hd).bytes) : tree;
 }
 
 cudaError_t window_attention(const TreeAttention &a, void *ws, int *err, cudaStream_t st) {

@@ -696,10 +696,11 @@ int dg_op_token_logprobs(const void *logits, int32_t logits_bf16, int64_t row_st
  *   out = sum_j p_j v_j,  p = softmax_j(x_j),  x_j = scale q . k_j,
  *   lse [n_tok][n_q_heads] = log sum_j e^{x_j}   (device fp32, may be NULL).
  * Roundings as in dg_op_tree_attention, whose conditions hold too: rows, pages,
- * bad sequences and pages, shapes, scale, workspace, cooperative launch; out must
- * not be q.  Keys and values that a row of the sequence sees must be finite; all
- * else may hold anything: pages of which no row of the sequence sees a slot are not
- * read, nor their entries of the table (they may have been given back). */
+ * bad sequences and pages, shapes, scale, workspace (one for n_tok rows serves calls
+ * of fewer, and of any n_seqs); out must not be q.  With few rows the launch is
+ * cooperative, as there.  Keys and values that a row of the sequence sees must be
+ * finite; all else may hold anything: pages of which no row of the sequence sees a
+ * slot are not read, nor their entries of the table (they may have been given back). */
 size_t dg_op_window_attention_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
                                               int32_t n_kv_heads, int32_t head_dim);
 int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *k_pool,
@@ -724,8 +725,8 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
  *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size], of the cache's pages
  *               (two sequences of a call must not share a page that is written)
  * Other arguments, conditions and reports as dg_op_window_attention (but scale >=
- * 1e-30); keys of a page outside the pools are skipped.  The workspace of one call must not be used by
- * another at the same time.  Blocks do not wait for one another. */
+ * 1e-30); keys of a page outside the pools are skipped.  The workspace of one call
+ * must not be used by another at the same time.  Blocks do not wait for one another. */
 size_t dg_op_key_mass_workspace_bytes(int32_t n_tok, int32_t n_seqs, int32_t n_q_heads,
                                       int32_t n_kv_heads, int32_t head_dim);
 int dg_op_key_mass(const uint16_t *q, int64_t q_stride, const float *lse, const uint16_t *k_pool,
@@ -772,7 +773,7 @@ int dg_op_cache_evict(uint16_t *k_pool, uint16_t *v_pool, float *mass_pool,
 enum {
     DG_CALL_QK_NORM_ROPE = 0, DG_CALL_ROPE_KV_APPEND = 1, DG_CALL_TREE_ATTENTION = 2,
     DG_CALL_TOKEN_LOGPROBS = 3, DG_CALL_WINDOW_ATTENTION = 8,
-  DG_CALL_KEY_MASS = 9, DG_CALL_CACHE_EVICT = 10
+    DG_CALL_KEY_MASS = 9, DG_CALL_CACHE_EVICT = 10
 };
 int dg_op_packed(int32_t call, const void *args);
 
