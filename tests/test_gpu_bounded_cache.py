@@ -305,11 +305,13 @@ def row_lse(q, bt, window, sinks, scale):
     out = np.zeros(q.shape[:2])
     G = q.shape[1] // bt.hkv
     for b, (p, n) in enumerate(zip(bt.pre, bt.new)):
+        if n == 0:
+            continue
         see = visible(p, n, window, sinks)
         rows = slice(bt.off[b], bt.off[b] + n)
         for h in range(q.shape[1]):
             s = np.where(see, q[rows, h] @ np.nan_to_num(bt.keys[b][:, h // G]).T * scale, -np.inf)
-            m = s.max(1, keepdims=True) if n else s[:, :1]
+            m = s.max(1, keepdims=True)
             out[rows, h] = m[:, 0] + np.log(np.exp(s - m).sum(1))
     return out.astype(np.float32)
 
