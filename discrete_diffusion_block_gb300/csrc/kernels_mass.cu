@@ -16,20 +16,24 @@
 // thread it cost as much of that memory's bandwidth as the products themselves
 // (8192 rows: 141 us).  A unit is 1, 2 or 4 tiles of 128 keys of a (sequence, KV head):
 // they stay in shared memory while the tiles of up to 128 rows (tokens x heads of the
-// group, staged by one TMA copy) that see any of them go by.  With many row tiles a unit
-// has 4 key tiles, which share each row tile read from L2; with one row tile, which stays
-// while the keys stream by, 2 (48 sequences of one token over up to 16k keys: 170 us with 1,
-// 128 with 2, 151 with 4, which leave the ring no room for the next unit); where there is
-// little to do, what gives each block one unit.  All blocks take equal ranges
-// of the batch's (unit, row tile) pairs (ranges.cuh);
-// a unit that spans several blocks leaves a partial sum per block in the workspace, and
-// the block whose sum arrives last adds them up in order: no block waits, results repeat
-// bit for bit.
+// group, staged by one TMA copy) that see any of them go by.  A unit has 4 key tiles, which
+// share each row tile read from L2 and what every role does per unit (with single tokens that
+// took longer than the keys' stream: 48 sequences over up to 16k keys 207 us with 1, 142 with
+// 2, 125 with 4, at 6.1 TB/s); where there is little to do, what gives each block one unit.
+// All blocks take equal ranges of the batch's (unit, row tile) pairs (ranges.cuh); a unit that
+// spans several blocks leaves a partial sum per block in the workspace, and the block whose
+// sum arrives last adds them up in order: no block waits, results repeat bit for bit.
 //
 // Roles of a block (640 threads): warp 0 copies keys out of the pre-swizzled pages,
 // warp 1 the row tiles and their log-sum-exps; warps 2 and 3 issue the products of
-// every other key tile from one thread each; warps 4-19 take the exponentials, four
-// warps a key tile, four key tiles at a time.
+// every other key tile from one thread each, and give a key tile back with its last ones
+// (all at the unit's end: 151 us); warps 4-19 take the exponentials, four warps a key tile,
+// four key tiles at a time.
+//
+// Measured (16 query and 8 KV heads of 128): one token over 8k keys 8.3 us, latency; 8192
+// rows of a prompt 116 us, 62% of the measured product rate: a product of 128 columns takes
+// as long as its 128 x 128 exponentials on the block's special function units, and neither
+// stops for the other most of the time; 8 sequences of 512 rows over 2k keys 48.
 #include <atomic>
 
 #include "attn_tc.cuh"
@@ -52,7 +56,6 @@ struct MassArgs {
   int G, T, few, ctas;  // T: tokens of a row tile
   int pg_shift;         // log2 of the page size, -1 where it is no power of two
   uint32_t t_magic;     // 2^32 / T, rounded up (0: divide)
-  int many;             // sequences have more than two row tiles on the average
   float scale_log2, inv_scale;
   float *part;                // [2 kMassCtas][kMassTiles * 128]: block c's first piece in 2 c, its last in 2 c + 1
   unsigned long long *count;  // [kMassTiles][kMassCtas]: pieces that have arrived of tile k of the unit that ends in block c
@@ -144,7 +147,7 @@ struct MassList {
 };
 
 // The units' key tiles: as many as give every block one unit where there is that
-// little to do; 4 for many row tiles, 2 for one or two (see above).
+// little to do, or 4.
 __device__ __forceinline__ int unit_tiles(const MassArgs &p, int lane) {
   const MassList list{p, 128};
   unsigned total = 0;
@@ -155,7 +158,7 @@ __device__ __forceinline__ int unit_tiles(const MassArgs &p, int lane) {
     total = min(total + __shfl_sync(0xffffffffu, lane_sums((unsigned)min(c, (long long)kMostCost), lane), 31), kMostCost);
   }
   const unsigned ctas = (unsigned)p.ctas;
-  return total <= ctas ? 1 : total <= 2 * ctas ? 2 : total <= 4 * ctas || p.many ? 4 : 2;
+  return total <= ctas ? 1 : total <= 2 * ctas ? 2 : 4;
 }
 
 // The walk over a block's pieces, with the unit's first key and first row tile.
@@ -429,25 +432,32 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
 #pragma unroll 1
       for (int q = q0; ok && q < q1; ++q, t0 += p.T) {
         const int cols = min(p.T, n - t0) * p.G;
-        unsigned live = __ballot_sync(0xffffffffu, max(mine.t0, t0) < min(mine.t1, t0 + p.T)) & turn;
+        const unsigned live = __ballot_sync(0xffffffffu, max(mine.t0, t0) < min(mine.t1, t0 + p.T)) & turn;
+        const bool end = q + 1 == q1;  // the piece's last row tile: the key tiles go back one by one
         if (fresh) ok = mass_wait(q_full + qs, qphase, p.err, 69, abort);
         const uint32_t idesc = tc::idesc_bf16(128, (cols + 15) & ~15);
-        for (; ok && live; live &= live - 1) {
-          const int k = __ffs(live) - 1, at = __popc(used & ((1u << k) - 1));
+        for (unsigned left = end ? used : live; ok && left; left &= left - 1) {
+          const int k = __ffs(left) - 1, at = __popc(used & ((1u << k) - 1));
           while (ok && ring <= at) ok = arrived();
           int slot = ks + at;
           if (slot >= KR) slot -= KR;
-          const int g = (order + k) & 3, step = g >= 2 ? step1++ : step0++;
-          if (ok && step) ok = mass_wait(s_empty + g, (step - 1) & 1, p.err, 68, abort);
-          __syncwarp();
-          if (ok && lane == 0) {
-            tc::fence_after();
-            const uint32_t a = kdesc + slot * (uint32_t)(S::tile >> 4), b = qdesc + qs * (uint32_t)(S::tile >> 4);
+          if (ok && live >> k & 1) {
+            const int g = (order + k) & 3, step = g >= 2 ? step1++ : step0++;
+            if (step) ok = mass_wait(s_empty + g, (step - 1) & 1, p.err, 68, abort);
+            __syncwarp();
+            if (ok && lane == 0) {
+              tc::fence_after();
+              const uint32_t a = kdesc + slot * (uint32_t)(S::tile >> 4), b = qdesc + qs * (uint32_t)(S::tile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk)
-              mma_low(tmem + 128 * g, a + (kk >> 2) * 1024 + 2 * (kk & 3), b + (kk >> 2) * 1024 + 2 * (kk & 3), idesc, kk ? 1u : 0u);
-            tc::mma_bf16(tmem + 128 * g, plain_desc(tc::smem_u32(base + S::ones)), plain_desc(tc::smem_u32(base + S::lse + 4096 * qs)), idesc, 1u);
-            tc::mma_commit(s_full + g);
+              for (int kk = 0; kk < HD / 16; ++kk)
+                mma_low(tmem + 128 * g, a + (kk >> 2) * 1024 + 2 * (kk & 3), b + (kk >> 2) * 1024 + 2 * (kk & 3), idesc, kk ? 1u : 0u);
+              tc::mma_bf16(tmem + 128 * g, plain_desc(tc::smem_u32(base + S::ones)), plain_desc(tc::smem_u32(base + S::lse + 4096 * qs)), idesc, 1u);
+              tc::mma_commit(s_full + g);
+            }
+          }
+          if (end && ok && lane == 0) {
+            if (((order + k) & 1) == half) tc::mma_commit(k_empty + slot);
+            else attn_arrive(k_empty + slot);
           }
           ok = __all_sync(0xffffffffu, ok);
         }
@@ -460,18 +470,11 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
           }
         }
       }
-      while (ok && ring < n_used) ok = arrived();
-      for (unsigned left = used; ok && left; left &= left - 1) {
-        if (lane == 0) {
-          if (((order + __ffs(left) - 1) & 1) == half) tc::mma_commit(k_empty + ks);
-          else attn_arrive(k_empty + ks);
-        }
-        if (++ks == KR) {
-          ks = 0;
-          kphase ^= 1;
-        }
+      ks += n_used;
+      if (ks >= KR) {
+        ks -= KR;
+        kphase ^= 1;
       }
-      ok = __all_sync(0xffffffffu, ok);
       order += tiles;
     }
     if (lane == 0) {
@@ -670,8 +673,6 @@ cudaError_t key_mass(const KeyMass &a, void *ws, int *err, cudaStream_t st) {
   p.few = max(1, 16 / p.G);
   p.pg_shift = (a.pg & (a.pg - 1)) ? -1 : __builtin_ctz(a.pg);
   p.t_magic = p.T > 1 && a.n_tok < (1 << 25) - 256 ? (uint32_t)(((1ull << 32) + p.T - 1) / p.T) : 0;
-  const int tokens = ceil_div(a.n_tok, a.n_seqs);
-  p.many = (long long)(a.observe ? min(a.observe, tokens) : tokens) * p.G > 256;
   cudaError_t e = rows_map(&p.q_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.T);
   if (e == cudaSuccess) e = rows_map(&p.few_map, a.q, a.q_stride, a.n_tok, a.Hq, a.hd, p.G, p.few);
   if (e != cudaSuccess) return e;
