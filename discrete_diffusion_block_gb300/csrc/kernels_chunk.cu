@@ -18,8 +18,9 @@
 // each, from one thread, taking turns (what a thread does around its products costs as
 // much time as half of them; without turns both tiles' products run at once, and then
 // both softmaxes run at once and the tensor core waits); warps 4-7 and 8-11 do the
-// softmax of one row tile each (thread = row).  A row's 128 scores are loaded at once:
-// tensor memory answers late while products run.
+// softmax of one row tile each (thread = row).  A row's 128 scores are loaded at once
+// (tensor memory answers late while products run), for which the other warps give
+// registers away: with 168 for all threads 2048 tokens over 30k keys took 421 us.
 //
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
@@ -39,6 +40,10 @@ namespace {
 constexpr int kChunkThreads = 384;
 constexpr int kChunkCtas = 152;    // most blocks: one per SM
 constexpr int kChunkGaveUp = 80;   // status code of a block that gave up after an earlier kernel
+// Registers of a thread: 168 at the launch, of which the first four warps give 64 each.
+constexpr int kChunkFewRegs = 104, kChunkManyRegs = 200;
+static_assert(128 * kChunkFewRegs + 256 * kChunkManyRegs <= kChunkThreads * 168, "registers of the block");
+constexpr int kChunkKept = 80;     // bytes of a ChunkKept
 constexpr int kChunkFlags = 8;     // key tiles whose bad-page flags are kept: more than are ever in flight
 
 struct ChunkArgs {
@@ -64,7 +69,8 @@ struct ChunkSmem {
   static constexpr size_t bars = flags + kChunkFlags * 4;
   // full[KR], empty[KR]; of each row tile: q_full, q_empty, s_full, p_full, pv_done, o_empty, turn, drained
   static constexpr int n_bars = 2 * KR + 2 * 8;
-  static constexpr size_t slot = bars + n_bars * 8;
+  static constexpr size_t kept = bars + n_bars * 8;        // ChunkKept of the 8 softmax warps
+  static constexpr size_t slot = kept + 8 * kChunkKept;
   static constexpr size_t bytes = slot + 16;
 };
 
@@ -107,6 +113,16 @@ struct ChunkList {
   __device__ __forceinline__ int items(const Seq &s, int u) const { return keys(s, u).count; }
 };
 typedef RangeWalk<ChunkList> ChunkWalk;
+
+// What a softmax warp uses only at a piece's beginning and end.  Its steps take all
+// registers; left to the compiler this lies in local memory, with parts of what the steps
+// use (2048 tokens over 30k keys: 413 us instead of 402).
+struct ChunkKept {
+  ChunkWalk w;
+  int rows, t0, steps, number, piece;
+  uint32_t status;
+};
+static_assert(sizeof(ChunkKept) <= kChunkKept, "");
 
 // Row tile t of the walk's unit within its piece: tokens [t0, t0 + n), and the items
 // whose key tiles a row of it sees: below `sink` and in [lo, hi).
@@ -189,227 +205,249 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
 
   // Key tiles are numbered through the block's pieces (item number); K of tile n is the
   // ring's 2 n-th tile, V its 2 n + 1-st.
-  if (warp == 0) {
-    // ---- keys and values: lane = 64-key half of a run of up to 16 key tiles -----------
-    int slot = 0, phase = 0, issued = 0, number = 0;
-    bool ok = true, more = true;
-    ChunkList::Keys ks = list.keys(w.s, w.u);
-    auto half_key = [&](int i) {
-      const int n = i + (lane >> 1);
-      return 128 * (n < ks.sink ? n : n - ks.sink + ks.first) + 64 * (lane & 1);
-    };
-    // the half's entry of the page table; -2 where no row sees a key of it (its page is not touched)
-    auto entry_of = [&](int i) {
-      const int key = half_key(i);
-      return i + (lane >> 1) < w.i1 && key < ks.end && (key + 64 > ks.low || key < p.a.sinks)
-                 ? p.a.page_tables[(size_t)w.b * p.a.max_pages + key / p.a.pg] : -2;
-    };
-    int i = w.i0, page = entry_of(i);
-    while (ok && more) {
-      const int n = min(16, w.i1 - i), key = half_key(i);
-      const bool off = page != -2 && (page < 0 || page >= p.a.n_pages);
-      if (off && p.err) atomicExch(p.err + 1, kBadPage);
-      const unsigned bad = __ballot_sync(0xffffffffu, off);
-      // rows [0, e) of the half are keys, those in [sink, low) are not seen by any row
-      const int e = page < 0 || off ? 0 : min(64, ks.end - key);
-      const int sink = min(max(p.a.sinks - key, 0), e), low = max(sink, min(max(ks.low - key, 0), e));
-      const size_t at = e ? ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key % p.a.pg) * 64 : 0;
-      i += n;
-      if (i >= w.i1) {
-        more = w.next(list, p.a.n_seqs, p.a.Hkv);
-        if (more) {
-          ks = list.keys(w.s, w.u);
-          i = w.i0;
-        }
-      }
-      if (more) page = entry_of(i);
-#pragma unroll 1
-      for (int j = 0; ok && j < 2 * n; ++j) {
-        const bool is_v = j & 1;
-        if (lane == 0) {
-          if (issued >= KR) ok = chunk_wait(empty + slot, phase ^ 1, p.err, 81, abort);
-          if (*abort) ok = false;
-          if (ok) {
-            if (!is_v) flags[number & (kChunkFlags - 1)] = (int)(bad >> j) & 3;
-            tc::mbar_expect_tx(full + slot, (uint32_t)S::tile);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kChunkFewRegs));
+    if (warp == 0) {
+      // ---- keys and values: lane = 64-key half of a run of up to 16 key tiles -----------
+      int slot = 0, phase = 0, issued = 0, number = 0;
+      bool ok = true, more = true;
+      ChunkList::Keys ks = list.keys(w.s, w.u);
+      auto half_key = [&](int i) {
+        const int n = i + (lane >> 1);
+        return 128 * (n < ks.sink ? n : n - ks.sink + ks.first) + 64 * (lane & 1);
+      };
+      // the half's entry of the page table; -2 where no row sees a key of it (its page is not touched)
+      auto entry_of = [&](int i) {
+        const int key = half_key(i);
+        return i + (lane >> 1) < w.i1 && key < ks.end && (key + 64 > ks.low || key < p.a.sinks)
+                   ? p.a.page_tables[(size_t)w.b * p.a.max_pages + key / p.a.pg] : -2;
+      };
+      int i = w.i0, page = entry_of(i);
+      while (ok && more) {
+        const int n = min(16, w.i1 - i), key = half_key(i);
+        const bool off = page != -2 && (page < 0 || page >= p.a.n_pages);
+        if (off && p.err) atomicExch(p.err + 1, kBadPage);
+        const unsigned bad = __ballot_sync(0xffffffffu, off);
+        // rows [0, e) of the half are keys, those in [sink, low) are not seen by any row
+        const int e = page < 0 || off ? 0 : min(64, ks.end - key);
+        const int sink = min(max(p.a.sinks - key, 0), e), low = max(sink, min(max(ks.low - key, 0), e));
+        const size_t at = e ? ((size_t)page * p.a.Hkv + w.g) * p.a.pg * HD + (size_t)(key % p.a.pg) * 64 : 0;
+        i += n;
+        if (i >= w.i1) {
+          more = w.next(list, p.a.n_seqs, p.a.Hkv);
+          if (more) {
+            ks = list.keys(w.s, w.u);
+            i = w.i0;
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if ((lane >> 1) == (j >> 1)) {
-          unsigned char *d = base + S::ring + (size_t)slot * S::tile + (lane & 1) * kAttnSlotHalfBytes;
-          const bf16 *src = (is_v ? p.a.v_pool : p.a.k_pool) + at;
-          // K: the page's other slots too (their scores are masked); V: zeros in place of
-          // rows that nothing sees (0 times anything must be 0)
-          const int a = e == 0 ? 0 : is_v ? (low > sink ? sink : e) : 64, c = is_v ? low : 64, z = is_v ? e : 64;
+        if (more) page = entry_of(i);
+#pragma unroll 1
+        for (int j = 0; ok && j < 2 * n; ++j) {
+          const bool is_v = j & 1;
+          if (lane == 0) {
+            if (issued >= KR) ok = chunk_wait(empty + slot, phase ^ 1, p.err, 81, abort);
+            if (*abort) ok = false;
+            if (ok) {
+              if (!is_v) flags[number & (kChunkFlags - 1)] = (int)(bad >> j) & 3;
+              tc::mbar_expect_tx(full + slot, (uint32_t)S::tile);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if ((lane >> 1) == (j >> 1)) {
+            unsigned char *d = base + S::ring + (size_t)slot * S::tile + (lane & 1) * kAttnSlotHalfBytes;
+            const bf16 *src = (is_v ? p.a.v_pool : p.a.k_pool) + at;
+            // K: the page's other slots too (their scores are masked); V: zeros in place of
+            // rows that nothing sees (0 times anything must be 0)
+            const int a = e == 0 ? 0 : is_v ? (low > sink ? sink : e) : 64, c = is_v ? low : 64, z = is_v ? e : 64;
 #pragma unroll
-          for (int blk = 0; blk < HB; ++blk) {
-            unsigned char *db = d + (size_t)blk * 16384;
-            const bf16 *sb = src + (size_t)blk * p.a.pg * 64;
-            if (a > 0) tc::bulk_load(db, sb, 128u * a, full + slot);
-            if (a < 64) {  // (a: e, or sink with [low, e) to come)
-              const int zero_to = a < z && c > a ? c : 64;
-              tc::bulk_load(db + 128 * a, g_zero_half, 128u * (zero_to - a), full + slot);
-              if (zero_to < 64) {
-                if (z > c) tc::bulk_load(db + 128 * c, sb + 64 * c, 128u * (z - c), full + slot);
-                if (z < 64) tc::bulk_load(db + 128 * z, g_zero_half, 128u * (64 - z), full + slot);
+            for (int blk = 0; blk < HB; ++blk) {
+              unsigned char *db = d + (size_t)blk * 16384;
+              const bf16 *sb = src + (size_t)blk * p.a.pg * 64;
+              if (a > 0) tc::bulk_load(db, sb, 128u * a, full + slot);
+              if (a < 64) {  // (a: e, or sink with [low, e) to come)
+                const int zero_to = a < z && c > a ? c : 64;
+                tc::bulk_load(db + 128 * a, g_zero_half, 128u * (zero_to - a), full + slot);
+                if (zero_to < 64) {
+                  if (z > c) tc::bulk_load(db + 128 * c, sb + 64 * c, 128u * (z - c), full + slot);
+                  if (z < 64) tc::bulk_load(db + 128 * z, g_zero_half, 128u * (64 - z), full + slot);
+                }
               }
             }
           }
-        }
-        __syncwarp();
-        number += is_v;
-        ++issued;
-        if (++slot == KR) {
-          slot = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    if (!ok && lane == 0) {  // gave up: wait (bounded) for the copies in flight
-      for (int k = issued - 1; k >= 0 && k >= issued - KR; --k) {
-        const long long t0 = clock64();
-        while (!tc::mbar_try_wait(full + k % KR, (k / KR) & 1) && clock64() - t0 < tc::kWaitCycles) {
+          __syncwarp();
+          number += is_v;
+          ++issued;
+          if (++slot == KR) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
-    }
-  } else if (warp == 2) {
-    // ---- rows ------------------------------------------------------------------------
-    if (lane == 0) {
-      bool ok = true, more = true;
-      int pieces[2] = {0, 0};
-      while (ok && more) {
-        const ChunkList::Keys ks = list.keys(w.s, w.u);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const RowTile r = row_tile(list, w, ks, t);
-          if (r.steps == 0) continue;
-          uint64_t *q_full = tile_bars + 8 * t, *q_empty = q_full + 1;
-          if (pieces[t]) ok = ok && chunk_wait(q_empty, (pieces[t] - 1) & 1, p.err, 82, abort);
-          if (*abort) ok = false;
-          if (!ok) break;
-          ++pieces[t];
-          tc::mbar_expect_tx(q_full, HB * 128u * p.T * p.G);
-#pragma unroll
-          for (int blk = 0; blk < HB; ++blk)
-            tc::tma_load_3d(base + S::q + t * S::tile + (size_t)blk * 16384, &p.q_map, 64 * blk, w.g * p.G, w.s.row0 + r.t0, q_full);
-        }
-        more = ok && w.next(list, p.a.n_seqs, p.a.Hkv);
-      }
-      if (!ok) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
+      if (!ok && lane == 0) {  // gave up: wait (bounded) for the copies in flight
+        for (int k = issued - 1; k >= 0 && k >= issued - KR; --k) {
           const long long t0 = clock64();
-          while (pieces[t] && !tc::mbar_try_wait(tile_bars + 8 * t, (pieces[t] - 1) & 1) && clock64() - t0 < tc::kWaitCycles) {
+          while (!tc::mbar_try_wait(full + k % KR, (k / KR) & 1) && clock64() - t0 < tc::kWaitCycles) {
           }
         }
       }
-    }
-  } else if (warp < 4) {
-    // ---- products of row tile t: P V of its step, then S of its next -------------------
-    const int t = warp >> 1;  // warps 1 and 3
-    uint64_t *q_full = tile_bars + 8 * t, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 3, *pv_done = q_full + 4,
-             *o_empty = q_full + 5, *turn = q_full + 6, *drained = q_full + 7, *other_turn = tile_bars + 8 * (t ^ 1) + 6;
-    const uint32_t t_s = tmem + 128 * t, t_o = tmem + 256 + 128 * t;
-    if (lane == 0) {
-      bool ok = true, more = true;
-      int k_slot = 0, k_phase = 0, pieces = 0, steps = 0, turns = 0;  // (K of the next item)
-      const uint32_t a = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::q + t * S::tile));
-      const uint32_t kdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::ring)), vdesc = (uint32_t)mn_desc(tc::smem_u32(base + S::ring));
-      const uint64_t k_high = tc::sw128_desc(0) & 0xffffffff00000000ull, v_high = mn_desc(0) & 0xffffffff00000000ull;
-      auto next_slot = [&](int &slot, int &phase) {
-        if (++slot == KR) {
-          slot = 0;
-          phase ^= 1;
-        }
-      };
-      if (t == 0) attn_arrive(turn);  // the first turn
-      while (ok && more) {
-        const RowTile r = row_tile(list, w, list.keys(w.s, w.u), t);
-        const int i0 = w.i0, i1 = w.i1;
-        more = w.next(list, p.a.n_seqs, p.a.Hkv);
-        int s_left = r.steps;
-        bool had = false, pv = false;  // the piece has had a step; P V of the item before is due
-        int v_slot = 0, v_phase = 0;   // V of the item before
-#pragma unroll 1
-        for (int i = i0; i <= i1; ++i) {
-          const bool s = i < i1 && r.live(i);
-          // what the turn's products need: V of the item before, K of this one; the
-          // softmax has read S, and written P over it; the sums are free; the rows
-          ok = (i == i0 || chunk_wait(full + v_slot, v_phase, p.err, 85, abort)) && (i == i1 || chunk_wait(full + k_slot, k_phase, p.err, 84, abort)) &&
-               (!pv || (chunk_wait(p_full, steps & 1, p.err, 86, abort) && (had || !pieces || chunk_wait(o_empty, (pieces - 1) & 1, p.err, 87, abort)))) &&
-               (!s || s_left < r.steps || chunk_wait(q_full, pieces & 1, p.err, 83, abort)) && chunk_wait(turn, turns & 1, p.err, 91, abort);
-          if (!ok) break;
-          ++turns;
-          tc::fence_after();
-          if (pv) {
-            const uint32_t b = vdesc + v_slot * (uint32_t)(S::tile >> 4);
+    } else if (warp == 2) {
+      // ---- rows ------------------------------------------------------------------------
+      if (lane == 0) {
+        bool ok = true, more = true;
+        int pieces[2] = {0, 0};
+        while (ok && more) {
+          const ChunkList::Keys ks = list.keys(w.s, w.u);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 128 keys, 16 (8 columns of P) per MMA
-              mma_bf16_tmem_a(t_o, t_s + 8 * kk, v_high | (b + kk * (2048 >> 4)), tc::idesc_bf16(128, HD) | (1u << 16),
-                              had || kk ? 1u : 0u);
-            tc::mma_commit(pv_done);
-            had = true;
-            // S may be written again (and O rescaled) once P has been read
-            ok = chunk_wait(pv_done, steps & 1, p.err, 88, abort);
+          for (int t = 0; t < 2; ++t) {
+            const RowTile r = row_tile(list, w, ks, t);
+            if (r.steps == 0) continue;
+            uint64_t *q_full = tile_bars + 8 * t, *q_empty = q_full + 1;
+            if (pieces[t]) ok = ok && chunk_wait(q_empty, (pieces[t] - 1) & 1, p.err, 82, abort);
+            if (*abort) ok = false;
             if (!ok) break;
-            ++steps;
-          }
-          if (s) {
-            const uint32_t b = kdesc + k_slot * (uint32_t)(S::tile >> 4);
+            ++pieces[t];
+            tc::mbar_expect_tx(q_full, HB * 128u * p.T * p.G);
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint32_t o = (kk >> 2) * 1024 + 2 * (kk & 3);
-              tc::mma_bf16(t_s, k_high | (a + o), k_high | (b + o), tc::idesc_bf16(128, 128), kk ? 1u : 0u);
+            for (int blk = 0; blk < HB; ++blk)
+              tc::tma_load_3d(base + S::q + t * S::tile + (size_t)blk * 16384, &p.q_map, 64 * blk, w.g * p.G, w.s.row0 + r.t0, q_full);
+          }
+          more = ok && w.next(list, p.a.n_seqs, p.a.Hkv);
+        }
+        if (!ok) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const long long t0 = clock64();
+            while (pieces[t] && !tc::mbar_try_wait(tile_bars + 8 * t, (pieces[t] - 1) & 1) && clock64() - t0 < tc::kWaitCycles) {
             }
           }
-          attn_arrive(other_turn);
-          if (s) {
-            tc::mma_commit(s_full);
-            if (--s_left == 0) tc::mma_commit(q_empty);
-          }
-          if (i > i0) attn_arrive(empty + v_slot);  // (P V is done)
-          if (i < i1) {
-            if (s) tc::mma_commit(empty + k_slot);
-            else attn_arrive(empty + k_slot);
-            next_slot(k_slot, k_phase);
-            v_slot = k_slot;
-            v_phase = k_phase;
-            next_slot(k_slot, k_phase);
-          }
-          pv = s;
         }
-        if (r.steps) ++pieces;
       }
-      if (!ok) {  // gave up: wait (bounded) for the products in flight
-        tc::mma_commit(drained);
-        const long long t0 = clock64();
-        while (!tc::mbar_try_wait(drained, 0) && clock64() - t0 < tc::kWaitCycles) {
+    } else {
+      // ---- products of row tile t: P V of its step, then S of its next -------------------
+      const int t = warp >> 1;  // warps 1 and 3
+      uint64_t *q_full = tile_bars + 8 * t, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 3, *pv_done = q_full + 4,
+               *o_empty = q_full + 5, *turn = q_full + 6, *drained = q_full + 7, *other_turn = tile_bars + 8 * (t ^ 1) + 6;
+      const uint32_t t_s = tmem + 128 * t, t_o = tmem + 256 + 128 * t;
+      if (lane == 0) {
+        bool ok = true, more = true;
+        int k_slot = 0, k_phase = 0, pieces = 0, steps = 0, turns = 0;  // (K of the next item)
+        const uint32_t a = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::q + t * S::tile));
+        const uint32_t kdesc = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::ring)), vdesc = (uint32_t)mn_desc(tc::smem_u32(base + S::ring));
+        const uint64_t k_high = tc::sw128_desc(0) & 0xffffffff00000000ull, v_high = mn_desc(0) & 0xffffffff00000000ull;
+        auto next_slot = [&](int &slot, int &phase) {
+          if (++slot == KR) {
+            slot = 0;
+            phase ^= 1;
+          }
+        };
+        if (t == 0) attn_arrive(turn);  // the first turn
+        while (ok && more) {
+          const RowTile r = row_tile(list, w, list.keys(w.s, w.u), t);
+          const int i0 = w.i0, i1 = w.i1;
+          more = w.next(list, p.a.n_seqs, p.a.Hkv);
+          int s_left = r.steps;
+          bool had = false, pv = false;  // the piece has had a step; P V of the item before is due
+          int v_slot = 0, v_phase = 0;   // V of the item before
+#pragma unroll 1
+          for (int i = i0; i <= i1; ++i) {
+            const bool s = i < i1 && r.live(i);
+            // what the turn's products need: V of the item before, K of this one; the
+            // softmax has read S, and written P over it; the sums are free; the rows
+            ok = (i == i0 || chunk_wait(full + v_slot, v_phase, p.err, 85, abort)) && (i == i1 || chunk_wait(full + k_slot, k_phase, p.err, 84, abort)) &&
+                 (!pv || (chunk_wait(p_full, steps & 1, p.err, 86, abort) && (had || !pieces || chunk_wait(o_empty, (pieces - 1) & 1, p.err, 87, abort)))) &&
+                 (!s || s_left < r.steps || chunk_wait(q_full, pieces & 1, p.err, 83, abort)) && chunk_wait(turn, turns & 1, p.err, 91, abort);
+            if (!ok) break;
+            ++turns;
+            tc::fence_after();
+            if (pv) {
+              const uint32_t b = vdesc + v_slot * (uint32_t)(S::tile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)  // 128 keys, 16 (8 columns of P) per MMA
+                mma_bf16_tmem_a(t_o, t_s + 8 * kk, v_high | (b + kk * (2048 >> 4)), tc::idesc_bf16(128, HD) | (1u << 16),
+                                had || kk ? 1u : 0u);
+              tc::mma_commit(pv_done);
+              had = true;
+              // S may be written again (and O rescaled) once P has been read
+              ok = chunk_wait(pv_done, steps & 1, p.err, 88, abort);
+              if (!ok) break;
+              ++steps;
+            }
+            if (s) {
+              const uint32_t b = kdesc + k_slot * (uint32_t)(S::tile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint32_t o = (kk >> 2) * 1024 + 2 * (kk & 3);
+                tc::mma_bf16(t_s, k_high | (a + o), k_high | (b + o), tc::idesc_bf16(128, 128), kk ? 1u : 0u);
+              }
+            }
+            attn_arrive(other_turn);
+            if (s) {
+              tc::mma_commit(s_full);
+              if (--s_left == 0) tc::mma_commit(q_empty);
+            }
+            if (i > i0) attn_arrive(empty + v_slot);  // (P V is done)
+            if (i < i1) {
+              if (s) tc::mma_commit(empty + k_slot);
+              else attn_arrive(empty + k_slot);
+              next_slot(k_slot, k_phase);
+              v_slot = k_slot;
+              v_phase = k_phase;
+              next_slot(k_slot, k_phase);
+            }
+            pv = s;
+          }
+          if (r.steps) ++pieces;
+        }
+        if (!ok) {  // gave up: wait (bounded) for the products in flight
+          tc::mma_commit(drained);
+          const long long t0 = clock64();
+          while (!tc::mbar_try_wait(drained, 0) && clock64() - t0 < tc::kWaitCycles) {
+          }
         }
       }
     }
-  } else if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kChunkManyRegs));
     // ---- softmax of row tile t: thread = row -------------------------------------------
     const int t = warp >= 8, q4 = warp & 3, row = threadIdx.x & 127;
     uint64_t *s_full = tile_bars + 8 * t + 2, *p_full = s_full + 1, *pv_done = s_full + 2, *o_empty = s_full + 3;
     const float NEG = __int_as_float(0xff800000);
-    const uint32_t lane_off = (uint32_t)(32 * q4) << 16, t_s = tmem + 128 * t + lane_off, t_o = tmem + 256 + 128 * t + lane_off;
+    const uint32_t t_s = tmem + 128 * t + ((uint32_t)(32 * q4) << 16), t_o = t_s + 256;
     const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
     int step = 0, number = 0, piece = 0;
+    ChunkKept &kept = *(ChunkKept *)(base + S::kept + (warp - 4) * kChunkKept);
     do {
-      const ChunkList::Keys ks = list.keys(w.s, w.u);
-      const RowTile r = row_tile(list, w, ks, t);
-      const int rows = r.n * p.G, token = r.t0 + row / p.G, head = w.g * p.G + row % p.G;
-      const bool active = 32 * q4 < rows, whole = w.i0 == 0 && w.i1 == w.items;
-      const int at = row < rows ? w.s.pre + token : -1;  // the row's slot
-      // The piece's steps: `sinks` key tiles from key0 on, then those from key1 on.
-      const int sinks = max(0, min(w.i1, r.sink) - w.i0), item1 = max(w.i0, max(r.lo, r.sink));
-      const int key0 = 128 * w.i0, key1 = 128 * (item1 - ks.sink + ks.first - sinks), flag1 = item1 - w.i0 - sinks;
-      // masks: keys behind the first row's slot, or before the last row's window
-      const int up = w.s.pre + r.t0 - 127, low = w.s.pre + r.t0 + r.n - p.a.window;
+      int at, up, low, sinks, jump, key_base, item, skip, steps;
+      bool active;
+      {
+        const ChunkList::Keys ks = list.keys(w.s, w.u);
+        const RowTile r = row_tile(list, w, ks, t);
+        const int rows = r.n * p.G;
+        active = 32 * q4 < rows;
+        at = row < rows ? w.s.pre + r.t0 + row / p.G : -1;  // the row's slot
+        // The piece's steps: `sinks` key tiles from key_base on, then others, `jump` keys and `skip` items later.
+        const int item1 = max(w.i0, max(r.lo, r.sink));
+        sinks = max(0, min(w.i1, r.sink) - w.i0);
+        key_base = 128 * w.i0;
+        jump = 128 * (item1 - ks.sink + ks.first - sinks - w.i0);
+        skip = item1 - w.i0 - sinks;
+        item = number;
+        // masks: keys behind the slot of the warp's first row, or before its last row's window
+        up = w.s.pre + r.t0 + 32 * q4 / p.G - 127;
+        low = w.s.pre + r.t0 + min(r.n, (32 * q4 + 31) / p.G + 1) - p.a.window;
+        steps = r.steps;
+        number += w.i1 - w.i0;
+        if (lane == 0) kept = ChunkKept{w, rows, r.t0, r.steps, number, piece, (uint32_t)status};
+        __syncwarp();
+      }
       float m = NEG, l = 0.0f;
 #pragma unroll 1
-      for (int n = 0; n < r.steps; ++n, ++step) {
+      for (int n = 0; n < steps; ++n, ++step, ++item, key_base += 128) {
+        if (n == sinks) {
+          key_base += jump;
+          item += skip;
+        }
         chunk_wait(s_full, step & 1, p.err, 89, abort);
         __syncwarp();
         if (!active) {
@@ -420,19 +458,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         uint32_t x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(t_s + 32 * c, x[c]);
-        const int key_base = 128 * n + (n < sinks ? key0 : key1);
-        const int bad = flags[(number + n + (n < sinks ? 0 : flag1)) & (kChunkFlags - 1)];
+        const int bad = flags[item & (kChunkFlags - 1)];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld_wait(x[c]);  // ties every loaded register to the wait
         if (key_base > up || (key_base < low && key_base + 128 > p.a.sinks) || bad) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const unsigned long long see = (bad >> h & 1) || at < 0 ? 0ull : window_bits(at, key_base + 64 * h, p.a.window, p.a.sinks);
-            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
+            // (a warp's rows are few tokens: one or two of the four columns' ranges need masks)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (!(lo >> j & 1u)) x[2 * h][j] = 0xff800000u;
-              if (!(hi >> j & 1u)) x[2 * h + 1][j] = 0xff800000u;
+            for (int c = 2 * h; c < 2 * h + 2; ++c) {
+              const uint32_t bits = (uint32_t)(see >> 32 * (c & 1));
+              if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1u)) x[c][j] = 0xff800000u;
             }
           }
         }
@@ -489,10 +529,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         __syncwarp();
         if (lane == 0) attn_arrive(p_full);
       }
-      number += w.i1 - w.i0;
+      w = kept.w;
+      number = kept.number;
+      piece = kept.piece;
+      steps = kept.steps;
+      status = kept.status;
+      const int rows = kept.rows, token = kept.t0 + row / p.G, head = w.g * p.G + row % p.G;
+      const bool whole = w.i0 == 0 && w.i1 == w.items;
       const int slot = 2 * blockIdx.x + (piece++ ? 1 : 0);
+      __syncwarp();
       if (rows == 0) continue;
-      if (r.steps) chunk_wait(pv_done, (step - 1) & 1, p.err, 90, abort);
+      if (steps) chunk_wait(pv_done, (step - 1) & 1, p.err, 90, abort);
       __syncwarp();
       bf16 *dst = p.a.out + (size_t)(w.s.row0 + token) * p.a.out_stride + (size_t)head * HD;
       float *lse = p.a.lse ? p.a.lse + (size_t)(w.s.row0 + token) * p.a.Hq + head : nullptr;
@@ -500,7 +547,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         tc::fence_after();
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         float4 *part = p.part + (size_t)(2 * slot + t) * (HD / 4) * 128 + row;
-        if (r.steps) {
+        if (steps) {
 #pragma unroll 1
           for (int c = 0; c < HD; c += 32) {
             uint32_t v[32];
@@ -532,7 +579,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         }
       }
       __syncwarp();
-      if (r.steps && lane == 0) attn_arrive(o_empty);
+      if (steps && lane == 0) attn_arrive(o_empty);
       if (whole) continue;
       // ---- a piece: the last block to arrive joins the unit's rows of this tile
       const UnitBlocks blocks = unit_blocks(w, range.per);
@@ -543,37 +590,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
       asm volatile("barrier.sync %0, 128;\n" ::"r"(1 + t) : "memory");
       if (!last[t] || row >= rows) continue;
       __threadfence();
+      // (32 columns at a time: as one stretch of code for all, 16384 tokens of 1024 took 3% more)
       float top = NEG, L = 0.0f;
       for (int b = blocks.first; b <= blocks.last; ++b) top = fmaxf(top, __ldcg(&p.state[(size_t)(2 * blocks.slot(b) + t) * 128 + row].x));
-      float4 acc[HD / 4];
-#pragma unroll
-      for (int j = 0; j < HD / 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-      for (int b = blocks.first; b <= blocks.last; ++b) {
-        const size_t piece_at = (size_t)(2 * blocks.slot(b) + t);
-        const float2 ml = __ldcg(p.state + piece_at * 128 + row);
-        const float f = ml.x == NEG ? 0.0f : ex2(ml.x - top);
-        if (f == 0.0f) continue;  // (a tile that saw none of the piece's keys has left no sums)
-        L += f * ml.y;
-        const float4 *src = p.part + piece_at * (HD / 4) * 128 + row;
+      for (int c = 0; c < HD / 4; c += 8) {
+        float4 acc[8];
 #pragma unroll
-        for (int j = 0; j < HD / 4; ++j) {
-          const float4 v = __ldcg(src + (size_t)j * 128);
-          acc[j].x += f * v.x;
-          acc[j].y += f * v.y;
-          acc[j].z += f * v.z;
-          acc[j].w += f * v.w;
+        for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        L = 0.0f;
+#pragma unroll 1
+        for (int b = blocks.first; b <= blocks.last; ++b) {
+          const size_t piece_at = (size_t)(2 * blocks.slot(b) + t);
+          const float2 ml = __ldcg(p.state + piece_at * 128 + row);
+          const float f = ml.x == NEG ? 0.0f : ex2(ml.x - top);
+          if (f == 0.0f) continue;  // (a tile that saw none of the piece's keys has left no sums)
+          L += f * ml.y;
+          const float4 *src = p.part + (piece_at * (HD / 4) + c) * 128 + row;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 v = __ldcg(src + (size_t)j * 128);
+            acc[j].x += f * v.x;
+            acc[j].y += f * v.y;
+            acc[j].z += f * v.z;
+            acc[j].w += f * v.w;
+          }
         }
-      }
-      const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+        const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
 #pragma unroll
-      for (int j = 0; j < HD / 4; j += 2) {
-        uint4 o;
-        o.x = pack_bf16(acc[j].x * inv, acc[j].y * inv);
-        o.y = pack_bf16(acc[j].z * inv, acc[j].w * inv);
-        o.z = pack_bf16(acc[j + 1].x * inv, acc[j + 1].y * inv);
-        o.w = pack_bf16(acc[j + 1].z * inv, acc[j + 1].w * inv);
-        *(uint4 *)(dst + 4 * j) = o;
+        for (int j = 0; j < 8; j += 2) {
+          uint4 o;
+          o.x = pack_bf16(acc[j].x * inv, acc[j].y * inv);
+          o.y = pack_bf16(acc[j].z * inv, acc[j].w * inv);
+          o.z = pack_bf16(acc[j + 1].x * inv, acc[j + 1].y * inv);
+          o.w = pack_bf16(acc[j + 1].z * inv, acc[j + 1].w * inv);
+          *(uint4 *)(dst + 4 * (c + j)) = o;
+        }
       }
       if (lse) *lse = fmaf(top, kLn2, logf(L));
     } while (w.next(list, p.a.n_seqs, p.a.Hkv));

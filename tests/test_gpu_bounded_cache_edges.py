@@ -431,6 +431,20 @@ def test_workspaces_of_long_chunks_serve_all_smaller_calls(new, pre):
     assert torch.equal(outs[0][:n], outs[1][:n])
 
 
+# ---- weights of long sequences ---------------------------------------------------------
+
+@pytest.mark.parametrize("hq,hkv,hd,seqs,most,new,window,sinks", [
+    (16, 8, 128, 30, 6000, 1, 0, 0), (12, 4, 64, 40, 5000, 1, 0, 0), (16, 8, 128, 30, 5000, 2, 1500, 200), (16, 8, 64, 30, 4000, 9, 700, 0),
+    (8, 8, 128, 12, 3000, 150, 1000, 4),
+])
+def test_mass_of_many_long_sequences(hq, hkv, hd, seqs, most, new, window, sinks):
+    # many units to a block, whose last ones have one to three key tiles: every slot and
+    # buffer is used many times over, some roles have nothing to do in some units
+    rng = np.random.default_rng(seqs + hd)
+    pre = [int(x) for x in rng.integers(0, most, seqs)]
+    check_mass(Batch(rng, pre, [int(x) for x in rng.integers(1, new + 1, seqs)], hkv, hd, 64), hq, window, sinks, 0, rng)
+
+
 # ---- batches of all kinds ------------------------------------------------------------------
 
 def shifted(bt, by):
