@@ -70,6 +70,16 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *b, uint32_t bytes) {
                : "memory");
 }
 
+// True in one lane of a converged warp, the same one every time.  Code under it that
+// issues products and copies is known to run in one thread: their operands are registers
+// of the warp, and under `lane == 0` each took the longer way for code that several
+// threads may run (the windowed attention's long chunks: 404 us instead of 380).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *b, uint32_t parity) {
   uint32_t ok;
   asm volatile(

@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
       }
     } else if (warp == 2) {
       // ---- rows ------------------------------------------------------------------------
-      if (lane == 0) {
+      if (tc::elect_one()) {
         bool ok = true, more = true;
         int pieces[2] = {0, 0};
         while (ok && more) {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
       uint64_t *q_full = tile_bars + 8 * t, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 3, *pv_done = q_full + 4,
                *o_empty = q_full + 5, *turn = q_full + 6, *drained = q_full + 7, *other_turn = tile_bars + 8 * (t ^ 1) + 6;
       const uint32_t t_s = tmem + 128 * t, t_o = tmem + 256 + 128 * t;
-      if (lane == 0) {
+      if (tc::elect_one()) {
         bool ok = true, more = true;
         int k_slot = 0, k_phase = 0, pieces = 0, steps = 0, turns = 0;  // (K of the next item)
         const uint32_t a = (uint32_t)tc::sw128_desc(tc::smem_u32(base + S::q + t * S::tile));
@@ -686,11 +686,11 @@ cudaError_t launch_chunk(ChunkArgs &p, cudaStream_t st) {
 // Which kernel: this file's takes pairs of row tiles, and is ahead where every block
 // has one or nearly (units: pairs of 128 rows of a sequence and KV head, if they were
 // full) and sequences fill a tile.  Measured, this kernel and the tree attention's
-// (16 and 8 heads of 128): one of 2048 tokens, windows of 1024 (128 units) 47 and 67
-// us; one of 4096, all keys (256) 86 and 134; 8 of 512 over 2k (256) 102 and 125; 64 of
-// 100, windows of 1024 (400) 162 and 173.  One of 1024 tokens (64 units), windows of 1024
-// 37 and 26, over 16k keys 135 and 146; 21 of up to 201, 12 and 4 heads of 64 (103) 38
-// and 29; 32 of 64 tokens over 2k (128 units, one tile of rows each) 101 and 76.
+// (16 and 8 heads of 128): one of 2048 tokens, windows of 1024 (128 units) 44 and 67
+// us; one of 4096, all keys (256) 81 and 134; 8 of 512 over 2k (256) 91 and 125; 64 of
+// 100, windows of 1024 (400) 113 and 174.  One of 1024 tokens (64 units), windows of 1024
+// 34 and 27, over 16k keys 128 and 146 (the host does not know which); one of 256 over 16k
+// 64 and 51; 32 of 64 tokens over 2k (128 units, one tile of rows each) 76 and 75.
 static bool blocks_full(int n_tok, int Hq) { return (long long)n_tok * Hq >= 120 * 256; }
 static bool many_rows(int n_tok, int n_seqs, int Hq, int Hkv) {
   return blocks_full(n_tok, Hq) && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;

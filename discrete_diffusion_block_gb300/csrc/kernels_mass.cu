@@ -31,9 +31,9 @@
 // four key tiles at a time.
 //
 // Measured (16 query and 8 KV heads of 128): one token over 8k keys 8.3 us, latency; 8192
-// rows of a prompt 116 us, 62% of the measured product rate: a product of 128 columns takes
-// as long as its 128 x 128 exponentials on the block's special function units, and neither
-// stops for the other most of the time; 8 sequences of 512 rows over 2k keys 48.
+// rows of a prompt 109 us, 66% of the measured product rate (of a row tile's 9 x 64 cycles
+// on the tensor core an eighth are the log-sum-exps'; its exponentials take 512 cycles of
+// all special function units).
 #include <atomic>
 
 #include "attn_tc.cuh"
@@ -434,18 +434,19 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         const int cols = min(p.T, n - t0) * p.G;
         const unsigned live = __ballot_sync(0xffffffffu, max(mine.t0, t0) < min(mine.t1, t0 + p.T)) & turn;
         const bool end = q + 1 == q1;  // the piece's last row tile: the key tiles go back one by one
-        if (fresh) ok = mass_wait(q_full + qs, qphase, p.err, 69, abort);
+        // (all threads agree on `ok`: one is elected below)
+        if (fresh) ok = __all_sync(0xffffffffu, mass_wait(q_full + qs, qphase, p.err, 69, abort));
         const uint32_t idesc = tc::idesc_bf16(128, (cols + 15) & ~15);
         for (unsigned left = end ? used : live; ok && left; left &= left - 1) {
           const int k = __ffs(left) - 1, at = __popc(used & ((1u << k) - 1));
           while (ok && ring <= at) ok = arrived();
           int slot = ks + at;
           if (slot >= KR) slot -= KR;
-          if (ok && live >> k & 1) {
+          if (live >> k & 1) {
             const int g = (order + k) & 3, step = g >= 2 ? step1++ : step0++;
-            if (step) ok = mass_wait(s_empty + g, (step - 1) & 1, p.err, 68, abort);
+            if (ok && step) ok = mass_wait(s_empty + g, (step - 1) & 1, p.err, 68, abort);
             __syncwarp();
-            if (ok && lane == 0) {
+            if (tc::elect_one() && ok) {
               tc::fence_after();
               const uint32_t a = kdesc + slot * (uint32_t)(S::tile >> 4), b = qdesc + qs * (uint32_t)(S::tile >> 4);
 #pragma unroll
@@ -455,7 +456,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
               tc::mma_commit(s_full + g);
             }
           }
-          if (end && ok && lane == 0) {
+          __syncwarp();
+          if (end && tc::elect_one() && ok) {
             if (((order + k) & 1) == half) tc::mma_commit(k_empty + slot);
             else attn_arrive(k_empty + slot);
           }
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
         }
         fresh = q + 1 < q1 || !stays;
         if (ok && fresh) {
-          if (lane == 0) tc::mma_commit(q_empty + qs);
+          if (tc::elect_one()) tc::mma_commit(q_empty + qs);
           if (++qs == QR) {
             qs = 0;
             qphase ^= 1;
@@ -477,12 +479,10 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       }
       order += tiles;
     }
-    if (lane == 0) {
-      if (!ok) {  // gave up: wait (bounded) for the products in flight
-        tc::mma_commit(drained + half);
-        const long long t0 = clock64();
-        while (!tc::mbar_try_wait(drained + half, 0) && clock64() - t0 < tc::kWaitCycles) {
-        }
+    if (tc::elect_one() && !ok) {  // gave up: wait (bounded) for the products in flight
+      tc::mma_commit(drained + half);
+      const long long t0 = clock64();
+      while (!tc::mbar_try_wait(drained + half, 0) && clock64() - t0 < tc::kWaitCycles) {
       }
     }
   } else if (warp >= 4) {

@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
   } else if (warp == 1 || warp == kTreePvWarp) {
     set_up();
     const uint32_t tmem = *tmem_slot, t_s = tmem, t_o = tmem + 256, t_p = tmem + 384;
-    if (lane == 0) {
+    if (tc::elect_one()) {
       bool ok = true;
       int i = 0, slot = 0, phase = 0, piece = 0;
       if (warp == 1) {  // ---- S = Q K^T
