@@ -15,12 +15,16 @@
 //
 // Roles of a block (384 threads): warp 0 copies keys and values out of the
 // pre-swizzled pages, warp 2 the rows; warps 1 and 3 issue the products of one row tile
-// each, from one thread, taking turns (what a thread does around its products costs as
-// much time as half of them; without turns both tiles' products run at once, and then
-// both softmaxes run at once and the tensor core waits); warps 4-7 and 8-11 do the
+// each, from one thread, taking turns (without turns both tiles' products run at once, and
+// then both softmaxes run at once and the tensor core waits); warps 4-7 and 8-11 do the
 // softmax of one row tile each (thread = row).  A row's 128 scores are loaded at once
 // (tensor memory answers late while products run), for which the other warps give
-// registers away: with 168 for all threads 2048 tokens over 30k keys took 421 us.
+// registers away (with 168 for all threads 2048 tokens over 30k keys took 4% longer).
+//
+// Measured (16 query and 8 KV heads of 128): 2048 tokens over 30k keys 370 us, 74% of the
+// measured product rate; 16384 tokens with windows of 1024 176 us, 40%: a tenth of a row
+// tile's steps are the first tokens', two tenths half masked, and a unit's beginning and
+// end (its lengths, first scores, output) take as long as four of its ten steps.
 //
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
@@ -67,8 +71,8 @@ struct ChunkSmem {
   static constexpr size_t ring = q + 2 * tile;
   static constexpr size_t flags = ring + KR * tile;        // [kChunkFlags] bad halves of a key tile (2 bits)
   static constexpr size_t bars = flags + kChunkFlags * 4;
-  // full[KR], empty[KR]; of each row tile: q_full, q_empty, s_full, p_full, pv_done, o_empty, turn, drained
-  static constexpr int n_bars = 2 * KR + 2 * 8;
+  // full[KR], empty[KR]; of each row tile: q_full, q_empty, s_full, p_full, pv_done, o_empty, turn, drained; p_half[2]
+  static constexpr int n_bars = 2 * KR + 2 * 8 + 2;
   static constexpr size_t kept = bars + n_bars * 8;        // ChunkKept of the 8 softmax warps
   static constexpr size_t slot = kept + 8 * kChunkKept;
   static constexpr size_t bytes = slot + 16;
@@ -180,6 +184,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
       tc::mbar_init(b + 5, 4);
       tc::mbar_init(b + 6, 1);
       tc::mbar_init(b + 7, 1);
+      tc::mbar_init(tile_bars + 16 + i, 4);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
       // ---- products of row tile t: P V of its step, then S of its next -------------------
       const int t = warp >> 1;  // warps 1 and 3
       uint64_t *q_full = tile_bars + 8 * t, *q_empty = q_full + 1, *s_full = q_full + 2, *p_full = q_full + 3, *pv_done = q_full + 4,
-               *o_empty = q_full + 5, *turn = q_full + 6, *drained = q_full + 7, *other_turn = tile_bars + 8 * (t ^ 1) + 6;
+               *o_empty = q_full + 5, *turn = q_full + 6, *drained = q_full + 7, *other_turn = tile_bars + 8 * (t ^ 1) + 6, *p_half = tile_bars + 16 + t;
       const uint32_t t_s = tmem + 128 * t, t_o = tmem + 256 + 128 * t;
       if (tc::elect_one()) {
         bool ok = true, more = true;
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             // what the turn's products need: V of the item before, K of this one; the
             // softmax has read S, and written P over it; the sums are free; the rows
             ok = (i == i0 || chunk_wait(full + v_slot, v_phase, p.err, 85, abort)) && (i == i1 || chunk_wait(full + k_slot, k_phase, p.err, 84, abort)) &&
-                 (!pv || (chunk_wait(p_full, steps & 1, p.err, 86, abort) && (had || !pieces || chunk_wait(o_empty, (pieces - 1) & 1, p.err, 87, abort)))) &&
+                 (!pv || (chunk_wait(p_half, steps & 1, p.err, 92, abort) && (had || !pieces || chunk_wait(o_empty, (pieces - 1) & 1, p.err, 87, abort)))) &&
                  (!s || s_left < r.steps || chunk_wait(q_full, pieces & 1, p.err, 83, abort)) && chunk_wait(turn, turns & 1, p.err, 91, abort);
             if (!ok) break;
             ++turns;
@@ -363,9 +368,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             if (pv) {
               const uint32_t b = vdesc + v_slot * (uint32_t)(S::tile >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)  // 128 keys, 16 (8 columns of P) per MMA
-                mma_bf16_tmem_a(t_o, t_s + 8 * kk, v_high | (b + kk * (2048 >> 4)), tc::idesc_bf16(128, HD) | (1u << 16),
-                                had || kk ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)  // 128 keys, 16 (8 columns of P) per MMA; half of them
+                mma_bf16_tmem_a(t_o, t_s + 8 * kk, v_high | (b + kk * (2048 >> 4)), tc::idesc_bf16(128, HD) | (1u << 16), had || kk ? 1u : 0u);
+              ok = chunk_wait(p_full, steps & 1, p.err, 86, abort);
+              if (!ok) break;
+              tc::fence_after();
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                mma_bf16_tmem_a(t_o, t_s + 8 * kk, v_high | (b + kk * (2048 >> 4)), tc::idesc_bf16(128, HD) | (1u << 16), 1u);
               tc::mma_commit(pv_done);
               had = true;
               // S may be written again (and O rescaled) once P has been read
@@ -411,7 +421,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kChunkManyRegs));
     // ---- softmax of row tile t: thread = row -------------------------------------------
     const int t = warp >= 8, q4 = warp & 3, row = threadIdx.x & 127;
-    uint64_t *s_full = tile_bars + 8 * t + 2, *p_full = s_full + 1, *pv_done = s_full + 2, *o_empty = s_full + 3;
+    uint64_t *s_full = tile_bars + 8 * t + 2, *p_full = s_full + 1, *pv_done = s_full + 2, *o_empty = s_full + 3, *p_half = tile_bars + 16 + t;
     const float NEG = __int_as_float(0xff800000);
     const uint32_t t_s = tmem + 128 * t + ((uint32_t)(32 * q4) << 16), t_o = t_s + 256;
     const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
@@ -451,7 +461,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         chunk_wait(s_full, step & 1, p.err, 89, abort);
         __syncwarp();
         if (!active) {
-          if (lane == 0) attn_arrive(p_full);
+          if (lane == 0) {
+            attn_arrive(p_half);
+            attn_arrive(p_full);
+          }
           continue;
         }
         tc::fence_after();
@@ -493,21 +506,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         if (grow) m = m_new;
         const float nmu = m == NEG ? 0.0f : -m;
         const f32x2 nmu2 = pair(nmu, nmu);
-        f32x2 sum0 = pair(0.0f, 0.0f), sum1 = sum0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 d = split(fma2(pair(__uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1])), scale2, nmu2));
-            const float p0 = ex2(d.x), p1 = ex2(d.y);
-            pk[j >> 1] = pack_bf16(p0, p1);
-            if (j & 2) sum1 = add2(sum1, pair(p0, p1));
-            else sum0 = add2(sum0, pair(p0, p1));
-          }
-          tmem_st16(t_s + 16 * c, pk);
-        }
-        const float2 sum = split(add2(sum0, sum1));
         // rows whose maximum grew: O (and l) to the new reference, O <- O 2^(m_old - m)
         // (P V of every earlier step is done)
         float f = 1.0f;
@@ -523,6 +521,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             tmem_st32(t_o + c, o);
           }
         }
+        f32x2 sum0 = pair(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float2 d = split(fma2(pair(__uint_as_float(x[c][j]), __uint_as_float(x[c][j + 1])), scale2, nmu2));
+            const float p0 = ex2(d.x), p1 = ex2(d.y);
+            pk[j >> 1] = pack_bf16(p0, p1);
+            if (j & 2) sum1 = add2(sum1, pair(p0, p1));
+            else sum0 = add2(sum0, pair(p0, p1));
+          }
+          tmem_st16(t_s + 16 * c, pk);
+          if (c == 1) {  // P V of the first 64 keys may begin (the whole tile's at once: 16384 tokens of 1024 2.5% more)
+            asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) attn_arrive(p_half);
+          }
+        }
+        const float2 sum = split(add2(sum0, sum1));
         l = l * f + (sum.x + sum.y);
         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");  // P (and O) written before the release
         tc::fence_before();
