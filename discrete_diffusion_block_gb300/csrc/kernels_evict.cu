@@ -8,21 +8,27 @@
 // and V read and written once (8 hd bytes a row): the memory's bandwidth, for few
 // sequences the latency of the chain weights -> choice -> rows.
 //
-// Two launches.  The choice, a block per KV head and sequence: a radix select, 11, 11
-// and 10 bits at a time over histograms in shared memory, gives the smallest kept weight
-// and how many of its equals stay; then a bit per slot says what is kept, and running
-// counts of the bits give every kept slot its place in the list.  The move, a cluster
-// of up to 8 blocks per KV head and sequence: the blocks take turns of kMoveTurn rows each;
-// a warp moves K and V of its rows through registers (the 16-byte chunks of a row change
-// places with slot % 8), all loads before all stores.  (In one launch, with every block
-// of a cluster making the choice for itself: 12 sequences of up to 32k to 8k 137 us, 29
-// of up to 2900 to 1111 26 us.)
+// The choice, by a block of 1024 threads: a radix select, 11, 11 and 10 bits at a time over
+// histograms in shared memory, gives the smallest kept weight and how many of its equals
+// stay; then a bit per slot says what is kept, and running counts of the bits give every
+// kept slot its place in the list.  The move, by a cluster of up to 8 blocks: the blocks
+// take turns of some rows a warp; a warp moves K and V of its rows through registers (the
+// 16-byte chunks of a row change places with slot % 8), all loads before all stores.  Small
+// calls are one launch, in which each block makes the choice for itself, others two, the
+// choices and the moves (launch_evict has the rule and both sides' times).
+//
+// Measured (8 KV heads of 128): 12 sequences of up to 32k slots to 8k 124 us, 70% of the
+// copy bandwidth (the move alone 95 us, the choice 27); 29 of up to 2900 to 1111 (4 heads
+// of 64) 24 us; one of 2176 to 2048 13.7, a chain of latencies: launch, the lengths, tables
+// and weights, three passes, rows.  Passes that end early where all that is left of a bin
+// stays: 0.1 us less, not kept.
 //
 // In place (out_tables holds the sequence's own pages) this order is what makes it
 // safe: the d-th kept slot is never before d, so the rows that a turn reads lie
 // behind all that earlier turns wrote, and a cluster barrier between a turn's loads
 // and its stores keeps those from overtaking the loads of the same turn.
 #include <algorithm>
+#include <atomic>
 
 #include "gemm_tc.cuh"
 #include "internal.h"
@@ -35,8 +41,12 @@ constexpr int kEvictThreads = 1024;  // of the choice
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 16;                              // rows of a warp in a turn
 constexpr int kMoveTurn = kMoveThreads / 32 * kMoveRows;   // of a block
+constexpr int kBothRows = 8, kBothTurn = kEvictThreads / 32 * kBothRows;  // the same, in one launch with the choice
 constexpr int kEvictKeys = 32768;    // weights kept in shared memory; later ones are read again
 constexpr int kEvictBins = 2048;
+constexpr int kFewUnits = 152;  // (KV head, sequence) pairs of a call in one launch
+constexpr int kChoiceBytes = (2 * (kEvictMostSlots / 32) + kEvictKeys) * 4;  // most of its dynamic shared memory
+static_assert(kEvictMostSlots % 128 == 0 && kChoiceBytes <= 212992, "shared memory of the choice");
 constexpr int kEvictPages = 1024;    // entries of the page table kept in shared memory
 
 struct EvictArgs {
@@ -98,12 +108,15 @@ __device__ __forceinline__ int nth_bit(uint32_t w, int n) {
   return at;
 }
 
-__global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __grid_constant__ EvictArgs p) {
-  extern __shared__ uint32_t smem[];
+// The choice for KV head g of sequence b, by a block; `lists`: it writes the call's lists
+// and lengths.  Returns the number of slots kept, -1 where the sequence is left alone.
+// Of a sequence beyond the budget a bit per slot (bits, in shared memory) says whether it
+// is kept, and before[w] how many before word w are.
+__device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lists, uint32_t *smem) {
   __shared__ int scan[32], hist[kEvictBins], found[2], flags, entries[kEvictPages];
   uint32_t *bits = smem, *equal = bits + p.words, *keys = equal + p.words;
   const CacheEvict &a = p.a;
-  const int b = blockIdx.x / a.Hkv, g = blockIdx.x - b * a.Hkv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = a.lens[b], n_out = min(L, a.budget);
   const int *table = a.page_tables + (size_t)b * a.max_pages, *out_table = a.out_tables + (size_t)b * a.out_max_pages;
   int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
@@ -128,15 +141,15 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __
   const bool bad = bad_length || flags;
   if (bad) {
     if (tid == 0 && p.err) atomicExch(p.err + 1, bad_length ? kBadSequence : kBadPage);
-    if (tid == 0 && g == 0) a.out_lens[b] = -1;
-    for (int d = tid; d < a.budget; d += kEvictThreads) kept[d] = -1;
-    return;
+    if (tid == 0 && g == 0 && lists) a.out_lens[b] = -1;
+    for (int d = tid; d < a.budget && lists; d += kEvictThreads) kept[d] = -1;
+    return -1;
   }
-  if (tid == 0 && g == 0) a.out_lens[b] = n_out;
-  for (int d = n_out + tid; d < a.budget; d += kEvictThreads) kept[d] = -1;
+  if (tid == 0 && g == 0 && lists) a.out_lens[b] = n_out;
+  for (int d = n_out + tid; d < a.budget && lists; d += kEvictThreads) kept[d] = -1;
   if (L <= a.budget) {
-    for (int d = tid; d < L; d += kEvictThreads) kept[d] = d;
-    return;
+    for (int d = tid; d < L && lists; d += kEvictThreads) kept[d] = d;
+    return L;
   }
   const int words = (L + 31) / 32;
 
@@ -247,22 +260,26 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __
     at += __popc(bits[w]);
   }
   __syncthreads();
-  for (int w = warp; w < words; w += kEvictThreads / 32) {
+  for (int w = warp; w < words && lists; w += kEvictThreads / 32) {
     const uint32_t e = bits[w];
     if (e >> lane & 1) kept[before[w] + __popc(e & ((1u << lane) - 1))] = 32 * w + lane;
   }
+  return n_out;
 }
 
-// Moves the rows of the choice's lists, K, V and weights.
-template <int HD>
-__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictArgs p) {
+__global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __grid_constant__ EvictArgs p) {
+  extern __shared__ uint32_t smem[];
+  const int b = blockIdx.x / p.a.Hkv;
+  choose(p, b, blockIdx.x - b * p.a.Hkv, true, smem);
+}
+
+// Moves the n_out > 0 kept rows of a KV head, K, V and weights, by a cluster of C blocks of
+// WARPS warps, ROWS rows a warp in a turn; slot_of(d): the slot that the d-th had.
+template <int HD, int WARPS, int ROWS, class SlotOf>
+__device__ __forceinline__ void move_rows(const EvictArgs &p, int b, int g, int n_out, int C, int rank, SlotOf slot_of) {
   const CacheEvict &a = p.a;
-  const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C;
-  const int b = unit / a.Hkv, g = unit - b * a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n_out = a.out_lens[b];
-  if (n_out <= 0) return;  // (the same in all blocks of a cluster)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int *table = a.page_tables + (size_t)b * a.max_pages, *out_table = a.out_tables + (size_t)b * a.out_max_pages;
-  const int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
   const bool in_place = table[0] == out_table[0];
   constexpr int kLanes = HD / 8;        // lanes of a row of K, and of V
   constexpr int kSide = 32 / (2 * kLanes);  // rows of K and V that the warp moves at once
@@ -270,15 +287,15 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
   const bf16 *pool = v_side ? a.v_pool : a.k_pool;
   bf16 *out = v_side ? a.v_pool : a.k_pool;
   const size_t sub = (size_t)(c >> 3) * a.pg * 64;
-  for (int d0 = 0; d0 < n_out; d0 += C * kMoveTurn) {
-    const int first = d0 + (rank * (kMoveThreads / 32) + warp) * kMoveRows;
+  for (int d0 = 0; d0 < n_out; d0 += C * WARPS * ROWS) {
+    const int first = d0 + (rank * WARPS + warp) * ROWS;
     // row `first + lane` of the warp's: where it lies and where it goes
     int src = -1, src_slot = 0, dst_slot = 0;
     size_t src_at = 0, dst_at = 0;
     float w = 0.0f;
-    if (lane < kMoveRows && first + lane < n_out) {
+    if (lane < ROWS && first + lane < n_out) {
       const int d = first + lane;
-      src = kept[d];
+      src = slot_of(d);
       const int sp = src / a.pg, dp = d / a.pg;
       src_slot = src - sp * a.pg;
       dst_slot = d - dp * a.pg;
@@ -286,9 +303,9 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
       dst_at = ((size_t)out_table[dp] * a.Hkv + g) * a.pg;
       w = __ldcg(a.mass + src_at + src_slot);
     }
-    uint4 row[kMoveRows / kSide];
+    uint4 row[ROWS / kSide];
 #pragma unroll
-    for (int i = 0; i < kMoveRows / kSide; ++i) {
+    for (int i = 0; i < ROWS / kSide; ++i) {
       const int from = i * kSide + lane / (2 * kLanes);
       const int s = __shfl_sync(0xffffffffu, src_slot, from);
       const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)src_at, from);
@@ -299,7 +316,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
       else __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < kMoveRows / kSide; ++i) {
+    for (int i = 0; i < ROWS / kSide; ++i) {
       const int from = i * kSide + lane / (2 * kLanes);
       const int s = __shfl_sync(0xffffffffu, dst_slot, from);
       const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)dst_at, from);
@@ -311,10 +328,58 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
 }
 
 template <int HD>
-cudaError_t launch_move(const EvictArgs &p, int cluster, cudaStream_t st) {
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __grid_constant__ EvictArgs p) {
+  const CacheEvict &a = p.a;
+  const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C, b = unit / a.Hkv, g = unit - b * a.Hkv;
+  const int n_out = a.out_lens[b];
+  if (n_out <= 0) return;  // (the same in all blocks of a cluster)
+  const int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
+  move_rows<HD, kMoveThreads / 32, kMoveRows>(p, b, g, n_out, C, rank, [&](int d) { return kept[d]; });
+}
+
+// Both in one launch: every block of the cluster makes the choice for itself.
+template <int HD>
+__global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_constant__ EvictArgs p) {
+  extern __shared__ uint32_t smem[];
+  const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C, b = unit / p.a.Hkv, g = unit - b * p.a.Hkv;
+  const int n_out = choose(p, b, g, rank == 0, smem);
+  if (n_out <= 0) return;  // (the same in all blocks of a cluster)
+  const uint32_t *bits = smem;
+  const int *before = (const int *)(bits + p.words), L = p.a.lens[b], words = (L + 31) / 32;
+  __syncthreads();
+  move_rows<HD, kEvictThreads / 32, kBothRows>(p, b, g, n_out, C, rank, [&](int d) {
+    if (L <= p.a.budget) return d;
+    int l = 0, r = words - 1;  // the last word with before <= d
+    while (l < r) {
+      const int m = (l + r + 1) >> 1;
+      if (before[m] <= d) l = m;
+      else r = m - 1;
+    }
+    return 32 * l + nth_bit(bits[l], d - before[l]);
+  });
+}
+
+// Lets a kernel use as much shared memory as any call needs, once per device.
+template <void (*KERNEL)(const EvictArgs)>
+cudaError_t choice_memory() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load()) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kChoiceBytes);
+    if (e != cudaSuccess) return e;
+    done[dev].store(true);
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_clusters(void (*kernel)(const EvictArgs), const EvictArgs &p, int cluster, int threads, size_t smem, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.a.n_seqs * p.a.Hkv * cluster);
-  cfg.blockDim = dim3(kMoveThreads);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -322,7 +387,34 @@ cudaError_t launch_move(const EvictArgs &p, int cluster, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, evict_move_kernel<HD>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int HD>
+cudaError_t launch_evict(const EvictArgs &p, int slots, cudaStream_t st) {
+  const CacheEvict &a = p.a;
+  const size_t smem = ((size_t)2 * p.words + p.keys) * 4;
+  const long long units = (long long)a.n_seqs * a.Hkv;
+  int cluster = 1;  // as many blocks as the kept rows have turns for
+  // One launch while there is little to move and little to choose from: it saves a launch
+  // and a round through the lists, but every block of a cluster makes the choice, and 1024
+  // threads that hold a choice keep fewer rows on their way.  Measured, calls in a row, one
+  // launch and two (8 heads of 128 unless stated): 1 sequence of 2176 slots to 2048 16.1 and
+  // 18.6 us, of 8192 to 2048 18.6 and 21.2; 29 of 2900 to 1111, 4 heads of 64, 25.1 and 29.7;
+  // 4 of 8192 to 2048 (32 MB) 30.3 and 30.9.  1 of 8192 to 7000 39.1 and 37.1; 4 of 4096 to
+  // 4000 (62 MB) 41.7 and 38.1; 16 of 2300 to 2048 70 and 59; 12 of 32k to 8k 212 and 128.
+  if (units <= kFewUnits && slots <= 8192 && a.budget <= 4096 && units * a.budget * HD * 4 <= 32 << 20) {
+    while (cluster < 8 && 2 * units * cluster <= kFewUnits && cluster * kBothTurn < a.budget) cluster *= 2;
+    const cudaError_t e = choice_memory<evict_kernel<HD>>();
+    return e != cudaSuccess ? e : launch_clusters(evict_kernel<HD>, p, cluster, kEvictThreads, smem, st);
+  }
+  cudaError_t e = choice_memory<evict_choice_kernel>();
+  if (e != cudaSuccess) return e;
+  evict_choice_kernel<<<a.n_seqs * a.Hkv, kEvictThreads, smem, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  while (cluster < 8 && cluster * kMoveTurn < a.budget) cluster *= 2;
+  return launch_clusters(evict_move_kernel<HD>, p, cluster, kMoveThreads, 0, st);
 }
 
 }  // namespace
@@ -337,15 +429,7 @@ cudaError_t cache_evict(const CacheEvict &a, int *err, cudaStream_t st) {
   p.keys = (std::min)(32 * p.words, kEvictKeys);
   p.pg_shift = (a.pg & (a.pg - 1)) ? -1 : __builtin_ctz(a.pg);
   p.vec = a.pg % 4 == 0 && (uintptr_t)a.mass % 16 == 0;
-  const size_t smem = ((size_t)2 * p.words + p.keys) * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_choice_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  evict_choice_kernel<<<a.n_seqs * a.Hkv, kEvictThreads, smem, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  int cluster = 1;  // as many blocks as the kept rows have turns for
-  while (cluster < 8 && cluster * kMoveTurn < a.budget) cluster *= 2;
-  return a.hd == 128 ? launch_move<128>(p, cluster, st) : launch_move<64>(p, cluster, st);
+  return a.hd == 128 ? launch_evict<128>(p, slots, st) : launch_evict<64>(p, slots, st);
 }
 
 }  // namespace dg

@@ -4,6 +4,10 @@
 // its mask words (without masks: the drafted keys up to itself).
 //   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale q[t][h] . k_j)
 // over the keys it sees; a row that sees none is zero.
+// The same kernel with WIN: windowed attention of batches of few rows (kernels_chunk.cu
+// has those of many).  Token t lies at slot prefix + t and sees itself, the window - 1
+// slots before it and the first `sinks`; a unit's key tiles are those of the sinks and
+// those from its first row's window on, numbered without the gap between them.
 //
 // What bounds it: every key and value is read once for the n G rows of its
 // sequence and KV head (G = Hq / Hkv), 4 n G flops per element of K and V, so
@@ -34,7 +38,10 @@
 // heads of 64) 25.4 us; one of 61 tokens over 32k 36 us, of which the keys' stream
 // takes 19, at 7.1 TB/s, and launch (2), start (3.5), the last tile and the join (8)
 // most of the rest; one token over 2k keys 11.3 to 12.1 us (by machine), all of it
-// latency; 16 sequences of one token over 2k 28.8 us.
+// latency; 16 sequences of one token over 2k 28.8 us.  With WIN: one token of 4096 keys
+// 14.1 us, 64 sequences of one token 146 us (6.1 TB/s), 21 of up to 201 tokens, windows
+// of 333 (12 and 4 heads of 64) 28 us: 1.7 units a block, a chain of loads, products and
+// softmax for each, beside launch, start and join.
 // Slower and not kept: the pieces joined over a cluster's shared memory, or by a
 // kernel of their own; rows copied into idle quarters of a tile; no range shorter
 // than 3 tiles (one token over 2k: 0.3 us more); the join's code gone through

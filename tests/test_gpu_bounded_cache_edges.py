@@ -12,7 +12,7 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_bounded_cache import (place, check_mass, check_window, compare_mass, lse_tol, mass_ref, mass_workspace, run_mass, run_window,  # noqa: F401
+from test_gpu_bounded_cache import (Cache, check_evict, check_mass, check_window, compare_mass, lse_tol, mass_ref, mass_workspace, place, run_mass, run_window,  # noqa: F401
                                     window_ref, window_workspace)
 from test_gpu_draft_ops import (U16, Batch, _clean_status, _lib, attention_tol, f64, head_ref, head_tol, i32, pool_rows, randn)  # noqa: F401
 
@@ -443,6 +443,21 @@ def test_mass_of_many_long_sequences(hq, hkv, hd, seqs, most, new, window, sinks
     rng = np.random.default_rng(seqs + hd)
     pre = [int(x) for x in rng.integers(0, most, seqs)]
     check_mass(Batch(rng, pre, [int(x) for x in rng.integers(1, new + 1, seqs)], hkv, hd, 64), hq, window, sinks, 0, rng)
+
+
+# ---- eviction in one launch and in two -----------------------------------------------------
+
+@pytest.mark.parametrize("hkv,hd,pg,lens,budget", [
+    (8, 128, 128, [2500, 2049, 0, 2048], 2048),             # one launch, clusters
+    (4, 64, 64, [3000] * 20 + [5, 1200, 1111] * 6, 1111),   # one launch, single blocks
+    (38, 64, 64, [900, 800, 700, 901], 800),                # 152 heads: the last such call
+    (51, 64, 64, [900, 800, 700], 800),                     # 153: two launches
+    (8, 128, 100, [5000, 4097], 4097),                      # a budget beyond one launch's
+    (1, 64, 64, [8193, 300], 200),                          # slots beyond one launch's
+])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_in_one_launch_and_in_two(hkv, hd, pg, lens, budget, in_place):
+    check_evict(Cache(np.random.default_rng(hkv + budget), lens, hkv, hd, pg, budget, in_place), 3, 50)
 
 
 # ---- batches of all kinds ------------------------------------------------------------------
