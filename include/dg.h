@@ -723,7 +723,8 @@ int dg_op_window_attention(const uint16_t *q, int64_t q_stride, const uint16_t *
  * one order of addition: results repeat bit for bit.  Rows whose lse is -inf (they
  * saw no key) add nothing; a NaN spreads to the keys that its row sees.
  *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size], of the cache's pages
- *               (two sequences of a call must not share a page that is written)
+ *               (a page that is written occurs once in the call's tables: sequences
+ *               that share pages are weighed in calls one after another)
  * Other arguments, conditions and reports as dg_op_window_attention (but scale >=
  * 1e-30); keys of a page outside the pools are skipped.  The workspace of one call
  * must not be used by another at the same time.  Blocks do not wait for one another. */
@@ -745,7 +746,7 @@ int dg_op_key_mass(const uint16_t *q, int64_t q_stride, const float *lse, const 
  * int32 [n_seqs][out_max_pages]), in the order of their slots; all other slots are
  * left as they are.  A sequence's pages in out_tables are either its own, entry by
  * entry (it is compacted in place), or pages that no sequence of the call reads or
- * moves to (pages that sequences share stay whole then).
+ * moves to, each once (pages that sequences share stay whole then).
  *   k_pool,
  *   v_pool      device bf16 pools of one layer, layout of dg_op_canvas_attention
  *   mass_pool   device fp32 [n_pages][n_kv_heads][page_size]: the weights

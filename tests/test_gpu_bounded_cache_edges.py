@@ -414,7 +414,19 @@ def test_chunks_report_bad_pages_and_leave_other_sequences_alone():
     assert bool(torch.isfinite(good.float()).all())
 
 
-@pytest.mark.parametrize("new,pre", [([1], [600]), ([1000, 1], [300, 200])])
+@pytest.mark.parametrize("hq,hkv,hd,pre,new,pg", CHUNKS)
+def test_chunks_without_lse_have_the_same_output(hq, hkv, hd, pre, new, pg):
+    rng = np.random.default_rng(88)
+    bt = Batch(rng, pre, new, hkv, hd, pg)
+    q, n = randn(rng, bt.T, hq, hd).to(dev()), int(bt.off[-1])
+    want, z = torch.full((bt.T, hq, hd), 7.0, dtype=torch.bfloat16, device=dev()), torch.zeros(bt.T, hq, device=dev())
+    out = want.clone()
+    run_window(bt, q, 333, 7, want, z)
+    run_window(bt, q, 333, 7, out)
+    assert torch.equal(out, want) and (out[:n] != 7.0).any() and (out[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("new,pre", [([1], [600]), ([1000, 1], [300, 200]), ([2500, 1], [300, 200])])
 def test_workspaces_of_long_chunks_serve_all_smaller_calls(new, pre):
     rng = np.random.default_rng(87)
     most = dgp.dg_op_window_attention_workspace_bytes(3000, 1, 16, 8, 128)
@@ -458,6 +470,22 @@ def test_mass_of_many_long_sequences(hq, hkv, hd, seqs, most, new, window, sinks
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_in_one_launch_and_in_two(hkv, hd, pg, lens, budget, in_place):
     check_evict(Cache(np.random.default_rng(hkv + budget), lens, hkv, hd, pg, budget, in_place), 3, 50)
+
+
+@pytest.mark.parametrize("lens,budget", [([700, 90, 901], 300), ([20000], 9000)])
+def test_evict_with_weights_at_odd_addresses(lens, budget):
+    results = []
+    for shift in (0, 1):
+        c = Cache(np.random.default_rng(90), lens, 2, 64, 64, budget, True)
+        d = c.on_gpu()
+        store = torch.zeros(d["mass_pool"].numel() + shift, device=dev())
+        mass = store[shift:].view(d["mass_pool"].shape)
+        mass.copy_(d["mass_pool"])
+        dgp.dg_op_cache_evict(d["k_pool"], d["v_pool"], mass, d["page_tables"], d["out_tables"], d["lens"], d["out_lens"], budget, d["kept"], recent=5)
+        torch.cuda.synchronize()
+        dgp.dg_op_status()
+        results.append((d["kept"], d["out_lens"], mass, d["k_pool"].view(torch.int16), d["v_pool"].view(torch.int16)))
+    assert all(torch.equal(a, b) and a.any() for a, b in zip(*results))
 
 
 # ---- batches of all kinds ------------------------------------------------------------------
