@@ -22,7 +22,7 @@
 // registers away (with 168 for all threads 2048 tokens over 30k keys took 4% longer).
 //
 // Measured (16 query and 8 KV heads of 128): 2048 tokens over 30k keys 370 us, 74% of the
-// measured product rate; 16384 tokens with windows of 1024 176 us, 40%: a tenth of a row
+// measured product rate; 16384 tokens with windows of 1024 171 us, 41%: a tenth of a row
 // tile's steps are the first tokens', two tenths half masked, and a unit's beginning and
 // end (its lengths, first scores, output) take as long as four of its ten steps.
 //
@@ -54,6 +54,7 @@ struct ChunkArgs {
   CUtensorMap q_map;  // rows [n_tok][Hq][hd], box 64 x G x T
   TreeAttention a;
   int G, T, ctas;     // T: tokens of a row tile
+  int wide;           // rows of out begin at multiples of 32 bytes: stored 32 at a time (16384 tokens of 1024 171 us, 176 with 16)
   float scale_log2;
   float4 *part;               // [2 kChunkCtas][2 row tiles][hd / 4][128 rows]
   float2 *state;              // [2 kChunkCtas][2][128]: (m, l) of each row
@@ -575,13 +576,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             if (row >= rows) continue;
             if (whole) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                uint4 o;
-                o.x = pack_bf16(__uint_as_float(v[j]) * inv, __uint_as_float(v[j + 1]) * inv);
-                o.y = pack_bf16(__uint_as_float(v[j + 2]) * inv, __uint_as_float(v[j + 3]) * inv);
-                o.z = pack_bf16(__uint_as_float(v[j + 4]) * inv, __uint_as_float(v[j + 5]) * inv);
-                o.w = pack_bf16(__uint_as_float(v[j + 6]) * inv, __uint_as_float(v[j + 7]) * inv);
-                *(uint4 *)(dst + c + j) = o;
+              for (int j = 0; j < 32; j += 16) {
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(v[j + 2 * i]) * inv, __uint_as_float(v[j + 2 * i + 1]) * inv);
+                if (p.wide) {
+                  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + c + j), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                               "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                               : "memory");
+                } else {
+                  *(uint4 *)(dst + c + j) = make_uint4(o[0], o[1], o[2], o[3]);
+                  *(uint4 *)(dst + c + j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
               }
             } else {
 #pragma unroll
@@ -729,6 +735,7 @@ cudaError_t window_attention(const TreeAttention &a, void *ws, int *err, cudaStr
   p.a = a;
   p.G = a.Hq / a.Hkv;
   p.T = 128 / p.G;
+  p.wide = (uintptr_t)a.out % 32 == 0 && a.out_stride % 16 == 0;
   p.scale_log2 = (float)(1.4426950408889634 * (double)a.scale);
   p.part = (float4 *)((unsigned char *)ws + w.part);
   p.state = (float2 *)((unsigned char *)ws + w.state);

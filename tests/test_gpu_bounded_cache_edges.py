@@ -426,6 +426,21 @@ def test_chunks_without_lse_have_the_same_output(hq, hkv, hd, pre, new, pg):
     assert torch.equal(out, want) and (out[:n] != 7.0).any() and (out[n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("first,stride", [(0, 0), (8, 0), (0, 8), (16, 24), (8, 16)])
+def test_chunks_into_rows_at_addresses_of_16_bytes(first, stride):
+    rng = np.random.default_rng(91)
+    bt = Batch(rng, [100], [1000], 16, 64, 64)
+    q = randn(rng, bt.T, 32, 64).to(dev())
+    want = torch.full((bt.T, 32, 64), 7.0, dtype=torch.bfloat16, device=dev())
+    run_window(bt, q, 300, 4, want)
+    store = torch.full((first + bt.T * (2048 + stride),), 7.0, dtype=torch.bfloat16, device=dev())
+    out = torch.as_strided(store, (bt.T, 32, 64), (2048 + stride, 64, 1), first)
+    run_window(bt, q, 300, 4, out)
+    assert torch.equal(out, want)
+    out.fill_(7.0)
+    assert (store == 7.0).all()                                            # nothing between the rows was written
+
+
 @pytest.mark.parametrize("new,pre", [([1], [600]), ([1000, 1], [300, 200]), ([2500, 1], [300, 200])])
 def test_workspaces_of_long_chunks_serve_all_smaller_calls(new, pre):
     rng = np.random.default_rng(87)
