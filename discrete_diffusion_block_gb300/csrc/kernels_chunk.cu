@@ -708,15 +708,16 @@ cudaError_t launch_chunk(ChunkArgs &p, cudaStream_t st) {
 
 }  // namespace
 
-// Which kernel: this file's takes pairs of row tiles, and is ahead where every block
-// has one or nearly (units: pairs of 128 rows of a sequence and KV head, if they were
-// full) and sequences fill a tile.  Measured, this kernel and the tree attention's
-// (16 and 8 heads of 128): one of 2048 tokens, windows of 1024 (128 units) 44 and 67
-// us; one of 4096, all keys (256) 81 and 134; 8 of 512 over 2k (256) 91 and 125; 64 of
-// 100, windows of 1024 (400) 113 and 174.  One of 1024 tokens (64 units), windows of 1024
-// 34 and 27, over 16k keys 128 and 146 (the host does not know which); one of 256 over 16k
-// 64 and 51; 32 of 64 tokens over 2k (128 units, one tile of rows each) 76 and 75.
-static bool blocks_full(int n_tok, int Hq) { return (long long)n_tok * Hq >= 120 * 256; }
+// Which kernel: this file's takes pairs of row tiles, and is ahead where there are more
+// tiles of 128 rows than blocks (the tree attention's kernel gives each block one until
+// then) and sequences fill a tile.  Measured, this kernel and the tree attention's (16 and
+// 8 heads of 128): one of 1300 tokens, windows of 1024 (168 tiles) 36 and 45; of 2048 (256)
+// 42 and 61; one of 4096, all keys 76 and 117; 8 of 512 over 2k 84 and 103; 13 of 100,
+// windows of 512 (208) 34 and 33, 16 of 100 (256) 36 and 41; 64 of 100, windows of 1024 105
+// and 140.  One of 1024 tokens (128 tiles), windows of 1024 33 and 24, over 16k keys 118 and
+// 129 (the host does not know which); one of 256 over 16k 63 and 47; 64 of 64 tokens,
+// windows of 1024 (512, one tile to a unit) 97 and 86.
+static bool blocks_full(int n_tok, int Hq) { return (long long)n_tok * Hq > kChunkCtas * 128; }
 static bool many_rows(int n_tok, int n_seqs, int Hq, int Hkv) {
   return blocks_full(n_tok, Hq) && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;
 }

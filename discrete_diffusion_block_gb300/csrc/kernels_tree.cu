@@ -39,9 +39,8 @@
 // takes 19, at 7.1 TB/s, and launch (2), start (3.5), the last tile and the join (8)
 // most of the rest; one token over 2k keys 11.3 to 12.1 us (by machine), all of it
 // latency; 16 sequences of one token over 2k 28.8 us.  With WIN: one token of 4096 keys
-// 14.1 us, 64 sequences of one token 146 us (6.1 TB/s), 21 of up to 201 tokens, windows
-// of 333 (12 and 4 heads of 64) 28 us: 1.7 units a block, a chain of loads, products and
-// softmax for each, beside launch, start and join.
+// 14.1 us, 64 sequences of one token 146 us (6.1 TB/s), one of 1024 tokens, windows of
+// 1024, 24 us.
 // Slower and not kept: the pieces joined over a cluster's shared memory, or by a
 // kernel of their own; rows copied into idle quarters of a tile; no range shorter
 // than 3 tiles (one token over 2k: 0.3 us more); the join's code gone through
