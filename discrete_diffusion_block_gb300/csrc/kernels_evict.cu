@@ -110,9 +110,9 @@ __device__ __forceinline__ int nth_bit(uint32_t w, int n) {
 
 // The choice for KV head g of sequence b, by a block; `lists`: it writes the call's lists
 // and lengths.  Returns the number of slots kept, -1 where the sequence is left alone.
-// Of a sequence beyond the budget a bit per slot (bits, in shared memory) says whether it
-// is kept, and before[w] how many before word w are.
-__device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lists, uint32_t *smem) {
+// slots (or NULL): the slots kept of a sequence beyond the budget, once more in shared
+// memory (in place of the weights).
+__device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lists, uint32_t *smem, int *slots) {
   __shared__ int scan[32], hist[kEvictBins], found[2], flags, entries[kEvictPages];
   uint32_t *bits = smem, *equal = bits + p.words, *keys = equal + p.words;
   const CacheEvict &a = p.a;
@@ -260,9 +260,13 @@ __device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lis
     at += __popc(bits[w]);
   }
   __syncthreads();
-  for (int w = warp; w < words && lists; w += kEvictThreads / 32) {
+  for (int w = warp; w < words && (lists || slots); w += kEvictThreads / 32) {
     const uint32_t e = bits[w];
-    if (e >> lane & 1) kept[before[w] + __popc(e & ((1u << lane) - 1))] = 32 * w + lane;
+    const int d = before[w] + __popc(e & ((1u << lane) - 1));
+    if (e >> lane & 1) {
+      if (lists) kept[d] = 32 * w + lane;
+      if (slots) slots[d] = 32 * w + lane;
+    }
   }
   return n_out;
 }
@@ -270,7 +274,7 @@ __device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lis
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __grid_constant__ EvictArgs p) {
   extern __shared__ uint32_t smem[];
   const int b = blockIdx.x / p.a.Hkv;
-  choose(p, b, blockIdx.x - b * p.a.Hkv, true, smem);
+  choose(p, b, blockIdx.x - b * p.a.Hkv, true, smem, nullptr);
 }
 
 // Moves the n_out > 0 kept rows of a KV head, K, V and weights, by a cluster of C blocks of
@@ -296,7 +300,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs &p, int b, int g, int 
     if (lane < ROWS && first + lane < n_out) {
       const int d = first + lane;
       src = slot_of(d);
-      const int sp = src / a.pg, dp = d / a.pg;
+      const int sp = p.pg_shift >= 0 ? src >> p.pg_shift : src / a.pg, dp = p.pg_shift >= 0 ? d >> p.pg_shift : d / a.pg;
       src_slot = src - sp * a.pg;
       dst_slot = d - dp * a.pg;
       src_at = ((size_t)table[sp] * a.Hkv + g) * a.pg;
@@ -342,21 +346,12 @@ template <int HD>
 __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_constant__ EvictArgs p) {
   extern __shared__ uint32_t smem[];
   const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C, b = unit / p.a.Hkv, g = unit - b * p.a.Hkv;
-  const int n_out = choose(p, b, g, rank == 0, smem);
+  int *slots = (int *)(smem + 2 * p.words);
+  const int n_out = choose(p, b, g, rank == 0, smem, slots);
   if (n_out <= 0) return;  // (the same in all blocks of a cluster)
-  const uint32_t *bits = smem;
-  const int *before = (const int *)(bits + p.words), L = p.a.lens[b], words = (L + 31) / 32;
+  const bool all = p.a.lens[b] <= p.a.budget;
   __syncthreads();
-  move_rows<HD, kEvictThreads / 32, kBothRows>(p, b, g, n_out, C, rank, [&](int d) {
-    if (L <= p.a.budget) return d;
-    int l = 0, r = words - 1;  // the last word with before <= d
-    while (l < r) {
-      const int m = (l + r + 1) >> 1;
-      if (before[m] <= d) l = m;
-      else r = m - 1;
-    }
-    return 32 * l + nth_bit(bits[l], d - before[l]);
-  });
+  move_rows<HD, kEvictThreads / 32, kBothRows>(p, b, g, n_out, C, rank, [&](int d) { return all ? d : slots[d]; });
 }
 
 // Lets a kernel use as much shared memory as any call needs, once per device.
