@@ -479,8 +479,9 @@ def test_mass_of_many_long_sequences(hq, hkv, hd, seqs, most, new, window, sinks
     (4, 64, 64, [3000] * 20 + [5, 1200, 1111] * 6, 1111),   # one launch, single blocks
     (38, 64, 64, [900, 800, 700, 901], 800),                # 152 heads: the last such call
     (51, 64, 64, [900, 800, 700], 800),                     # 153: two launches
-    (8, 128, 100, [5000, 4097], 4097),                      # a budget beyond one launch's
+    (8, 128, 100, [5000, 4097], 4097),                      # one launch, lists of more than a block's threads
     (1, 64, 64, [8193, 300], 200),                          # slots beyond one launch's
+    (8, 128, 128, [2500, 2600, 2700, 2800, 2049], 2048),    # rows beyond one launch's
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_in_one_launch_and_in_two(hkv, hd, pg, lens, budget, in_place):
