@@ -716,7 +716,8 @@ cudaError_t launch_chunk(ChunkArgs &p, cudaStream_t st) {
 // windows of 512 (208) 34 and 33, 16 of 100 (256) 36 and 41; 64 of 100, windows of 1024 105
 // and 140.  One of 1024 tokens (128 tiles), windows of 1024 33 and 24, over 16k keys 118 and
 // 129 (the host does not know which); one of 256 over 16k 63 and 47; 64 of 64 tokens,
-// windows of 1024 (512, one tile to a unit) 97 and 86.
+// windows of 1024 (512, one tile to a unit) 97 and 86; one of 2048 among 64 single ones, 4k
+// keys each 276 and 245, windows of 1024 102 and 124.
 static bool blocks_full(int n_tok, int Hq) { return (long long)n_tok * Hq > kChunkCtas * 128; }
 static bool many_rows(int n_tok, int n_seqs, int Hq, int Hkv) {
   return blocks_full(n_tok, Hq) && (long long)n_tok * (Hq / Hkv) > 128ll * n_seqs;
