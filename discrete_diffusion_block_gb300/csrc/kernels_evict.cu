@@ -278,6 +278,12 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_choice_kernel(const __
   choose(p, b, blockIdx.x - b * p.a.Hkv, true, smem, nullptr);
 }
 
+// Whether sequence b, of one slot or more, stays as it is: within the budget, in place.
+__device__ __forceinline__ bool stays(const EvictArgs &p, int b) {
+  const CacheEvict &a = p.a;
+  return a.lens[b] <= a.budget && a.page_tables[(size_t)b * a.max_pages] == a.out_tables[(size_t)b * a.out_max_pages];
+}
+
 // Moves the n_out > 0 kept rows of a KV head, K, V and weights, by a cluster of C blocks of
 // WARPS warps, ROWS rows a warp in a turn; slot_of(d): the slot that the d-th had.
 template <int HD, int WARPS, int ROWS, class SlotOf>
@@ -308,13 +314,15 @@ __device__ __forceinline__ void move_rows(const EvictArgs &p, int b, int g, int 
       dst_at = ((size_t)out_table[dp] * a.Hkv + g) * a.pg;
       w = __ldcg(a.mass + src_at + src_slot);
     }
+    // (in place the rows before the first that goes stay where they are)
+    const unsigned moving = __ballot_sync(0xffffffffu, src >= 0 && (src_at != dst_at || src_slot != dst_slot));
     uint4 row[ROWS / kSide];
 #pragma unroll
     for (int i = 0; i < ROWS / kSide; ++i) {
       const int from = i * kSide + lane / (2 * kLanes);
       const int s = __shfl_sync(0xffffffffu, src_slot, from);
       const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)src_at, from);
-      if (first + from < n_out) row[i] = __ldcg((const uint4 *)(pool + at * HD + sub + (size_t)s * 64 + (((c & 7) ^ (s & 7)) << 3)));
+      if (moving >> from & 1) row[i] = __ldcg((const uint4 *)(pool + at * HD + sub + (size_t)s * 64 + (((c & 7) ^ (s & 7)) << 3)));
     }
     if (in_place) {
       if (C > 1) tc::cluster_sync();
@@ -325,10 +333,9 @@ __device__ __forceinline__ void move_rows(const EvictArgs &p, int b, int g, int 
       const int from = i * kSide + lane / (2 * kLanes);
       const int s = __shfl_sync(0xffffffffu, dst_slot, from);
       const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)dst_at, from);
-      const bool moved = __shfl_sync(0xffffffffu, (int)(src_at != dst_at || src_slot != dst_slot), from);
-      if (first + from < n_out && moved) *(uint4 *)(out + at * HD + sub + (size_t)s * 64 + (((c & 7) ^ (s & 7)) << 3)) = row[i];
+      if (moving >> from & 1) *(uint4 *)(out + at * HD + sub + (size_t)s * 64 + (((c & 7) ^ (s & 7)) << 3)) = row[i];
     }
-    if (src >= 0) a.mass[dst_at + dst_slot] = w;
+    if (moving >> lane & 1) a.mass[dst_at + dst_slot] = w;
   }
 }
 
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const __gri
   const CacheEvict &a = p.a;
   const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C, b = unit / a.Hkv, g = unit - b * a.Hkv;
   const int n_out = a.out_lens[b];
-  if (n_out <= 0) return;  // (the same in all blocks of a cluster)
+  if (n_out <= 0 || stays(p, b)) return;  // (the same in all blocks of a cluster)
   const int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
   move_rows<HD, kMoveThreads / 32, kMoveRows>(p, b, g, n_out, C, rank, [&](int d) { return kept[d]; });
 }
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) evict_kernel(const __grid_co
   const int C = cluster_ctas(), rank = blockIdx.x % C, unit = blockIdx.x / C, b = unit / p.a.Hkv, g = unit - b * p.a.Hkv;
   int *slots = (int *)(smem + 2 * p.words);
   const int n_out = choose(p, b, g, rank == 0, smem, slots);
-  if (n_out <= 0) return;  // (the same in all blocks of a cluster)
+  if (n_out <= 0 || stays(p, b)) return;  // (the same in all blocks of a cluster)
   const bool all = p.a.lens[b] <= p.a.budget;
   __syncthreads();
   move_rows<HD, kEvictThreads / 32, kBothRows>(p, b, g, n_out, C, rank, [&](int d) { return all ? d : slots[d]; });
