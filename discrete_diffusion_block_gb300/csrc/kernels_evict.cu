@@ -19,8 +19,8 @@
 //
 // Measured (8 KV heads of 128): 12 sequences of up to 32k slots to 8k 124 us, 70% of the
 // copy bandwidth (the move alone 95 us, the choice 27); 29 of up to 2900 to 1111 (4 heads
-// of 64) 21 us; one of 2176 to 2048 13.1, a chain of latencies: launch (2 us), the lengths,
-// tables and weights (2.5), three passes (4.3), bits and lists (2.3), rows (4).  Not kept:
+// of 64) 19.5 us; one of 2176 to 2048 12.8, a chain of latencies: launch (2 us), the lengths,
+// tables and weights (2.5), three passes (4.3), bits and lists (2.3), rows (3.5).  Not kept:
 // passes that end early where all that is left of a bin stays (0.1 us less); the move's
 // launch begun under the choice (0.5 us less of the small ones, 4 more of the large).
 //
@@ -403,10 +403,11 @@ cudaError_t launch_evict(const EvictArgs &p, int slots, cudaStream_t st) {
   // and a round through the lists, but every block of a cluster makes the choice, and 1024
   // threads that hold a choice keep fewer rows on their way.  Measured, calls in a row, one
   // launch and two (8 heads of 128 unless stated): 1 sequence of 2176 slots to 2048 14.5 and
-  // 18.6 us, of 8192 to 7000 (29 MB) 35.0 and 37.2; 29 of 2900 to 1111, 4 heads of 64, 22.7
-  // and 29.5; 4 of 8192 to 2048 (34 MB) 29.0 and 30.9, in a graph 27.7 and 27.3.  4 of 4096
-  // to 4000 (66 MB) 40.0 and 38.3; 16 of 2300 to 2048 66 and 59; 12 of 32k to 8k 190 and 128.
-  if (units <= kFewUnits && slots <= 8192 && units * a.budget * HD * 4 <= 32 << 20) {
+  // 18.6 us, of 8192 to 7000 (29 MB) 29.0 and 37.1; 29 of 2900 to 1111, 4 heads of 64, 20.9
+  // and 30.1; 4 of 8192 to 2048 (34 MB) 26.8 and 30.9, of 4096 to 4000 (66 MB) 35.1 and 38.5;
+  // 16 of 2300 to 2048 (134 MB) 59.4 and 59.5, in a graph 57.2 and 55.5; 19 of 4500 to 4096
+  // 120 and 117; 12 of 32k to 8k 134 and 128.
+  if (units <= kFewUnits && slots <= 8192 && units * a.budget * HD * 4 <= 96 << 20) {
     while (cluster < 8 && 2 * units * cluster <= kFewUnits && cluster * kBothTurn < a.budget) cluster *= 2;
     const cudaError_t e = choice_memory<evict_kernel<HD>>();
     return e != cudaSuccess ? e : launch_clusters(evict_kernel<HD>, p, cluster, kEvictThreads, smem, st);

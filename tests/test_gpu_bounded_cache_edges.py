@@ -481,7 +481,7 @@ def test_mass_of_many_long_sequences(hq, hkv, hd, seqs, most, new, window, sinks
     (51, 64, 64, [900, 800, 700], 800),                     # 153: two launches
     (8, 128, 100, [5000, 4097], 4097),                      # one launch, lists of more than a block's threads
     (1, 64, 64, [8193, 300], 200),                          # slots beyond one launch's
-    (8, 128, 128, [2500, 2600, 2700, 2800, 2049], 2048),    # rows beyond one launch's
+    (8, 128, 128, [2500, 2600, 2700, 2800, 2049] + [2100] * 8, 2048),   # rows beyond one launch's
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_in_one_launch_and_in_two(hkv, hd, pg, lens, budget, in_place):
