@@ -60,6 +60,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
       : "memory");
 }
 
+// Entry i of a page table, all negative ones as -1: what a table holds is then never
+// kNotRead, which the kernels that copy keys keep in place of entries that they skip.
+constexpr int kNotRead = -2;
+__device__ __forceinline__ int table_entry(const int *table, size_t i) { return max(table[i], -1); }
+
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"

@@ -222,16 +222,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
         const int n = i + (lane >> 1);
         return 128 * (n < ks.sink ? n : n - ks.sink + ks.first) + 64 * (lane & 1);
       };
-      // the half's entry of the page table; -2 where no row sees a key of it (its page is not touched)
+      // the half's entry of the page table; kNotRead where no row sees a key of it (its page is not touched)
       auto entry_of = [&](int i) {
         const int key = half_key(i);
         return i + (lane >> 1) < w.i1 && key < ks.end && (key + 64 > ks.low || key < p.a.sinks)
-                   ? p.a.page_tables[(size_t)w.b * p.a.max_pages + key / p.a.pg] : -2;
+                   ? table_entry(p.a.page_tables, (size_t)w.b * p.a.max_pages + key / p.a.pg) : kNotRead;
       };
       int i = w.i0, page = entry_of(i);
       while (ok && more) {
         const int n = min(16, w.i1 - i), key = half_key(i);
-        const bool off = page != -2 && (page < 0 || page >= p.a.n_pages);
+        const bool off = page != kNotRead && (page < 0 || page >= p.a.n_pages);
         if (off && p.err) atomicExch(p.err + 1, kBadPage);
         const unsigned bad = __ballot_sync(0xffffffffu, off);
         // rows [0, e) of the half are keys, those in [sink, low) are not seen by any row

@@ -1,0 +1,72 @@
+"""The operators over the paged cache with table entries, lengths and positions at
+the ends of their types: whatever a table holds outside the pools is skipped and
+reported, and what is too long is refused on the device."""
+import contextlib
+
+import numpy as np
+import pytest
+import torch
+
+import discrete_diffusion_block_gb300 as dgp
+from gpu_util import dev
+from test_gpu_bounded_cache import lse_tol, run_window, visible
+from test_gpu_draft_ops import Batch, _clean_status, _lib, attention_tol, f64, i32, randn  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+OUTSIDE = [-1, -2, -3, -2 ** 31 + 1, -2 ** 31, 2 ** 31 - 1]       # entries outside any pool
+
+
+# ---- pages outside the pools -------------------------------------------------------------
+
+@contextlib.contextmanager
+def entry(bt, b, at, value):
+    """The batch with another entry in its page table; what the call reports is checked."""
+    table = bt.table.copy()
+    table[b, at] = value
+    keep, bt.d = bt.d, dict(bt.d, page_tables=i32(table))
+    yield
+    bt.d = keep
+    with pytest.raises(dgp.DgError) as e:
+        dgp.dg_op_status()
+    assert e.value.code == dgp.DG_EINVAL and "page" in str(e.value)
+
+
+def without_page(q, bt, at, window, sinks, head):
+    """out, sum_j p_j |v_j|, lse and the largest sum of |products| of the first
+    sequence's rows, in 64 bits, without the keys of its page `at`."""
+    p, n, G = bt.pre[0], bt.new[0], q.shape[1] // bt.hkv
+    see = visible(p, n, window, sinks) & (np.arange(p + n)[None] // bt.pg != at)
+    k, v, x, scale = bt.keys[0][:, head // G], bt.vals[0][:, head // G], q[:n, head], bt.hd ** -0.5
+    s = np.where(see, x @ k.T * scale, -np.inf)
+    m = s.max(1, keepdims=True)
+    e = np.exp(s - m)
+    z = m[:, 0] + np.log(e.sum(1))
+    e /= e.sum(1, keepdims=True)
+    return e @ v, e @ np.abs(v), z, (np.where(see, np.abs(x) @ np.abs(k).T * scale, 0)).max(1)
+
+
+def check_without_page(bt, q, out, lse, at, window, sinks, heads):
+    n, tiles = bt.new[0], (bt.pre[0] + bt.new[0]) / 128 + 2
+    for h in heads:
+        ref, mag, z, top = without_page(f64(q), bt, at, window, sinks, h)
+        assert (np.abs(f64(out)[:n, h] - ref) <= attention_tol(ref, mag)).all(), (at, h)
+        assert (np.abs(f64(lse)[:n, h] - z) <= lse_tol(z, top, bt.hd, tiles)).all(), (at, h)
+
+
+CHUNK = ([500, 100], [1000, 950], 8, 128, 128)
+
+
+@pytest.mark.parametrize("value", OUTSIDE)
+@pytest.mark.parametrize("window,sinks", [(300, 4), (0, 0)])
+def test_chunks_skip_pages_outside_the_pools(value, window, sinks):
+    rng = np.random.default_rng(101)
+    bt = Batch(rng, *CHUNK)
+    q = randn(rng, bt.T, 16, 128).to(dev())
+    good, lse = torch.zeros_like(q), torch.zeros(bt.T, 16, device=dev())
+    run_window(bt, q, window, sinks, good, lse)
+    for at in (0, 2, 6):
+        out, z = torch.zeros_like(q), torch.zeros_like(lse)
+        with entry(bt, 0, at, value):
+            run_window(bt, q, window, sinks, out, z)
+        check_without_page(bt, q, out, z, at, window, sinks, (0, 15))
+        assert torch.equal(out[1000:1950], good[1000:1950]) and torch.equal(z[1000:1950], lse[1000:1950])
