@@ -193,7 +193,7 @@ struct MassWalk : RangeWalk<MassList> {
 
 // The entry of the page table for slot j of sequence b; slot: j's place in the page.
 __device__ __forceinline__ int page_entry(const MassArgs &p, int b, int j) {
-  return p.a.page_tables[(size_t)b * p.a.max_pages + (p.pg_shift >= 0 ? j >> p.pg_shift : j / p.a.pg)];
+  return table_entry(p.a.page_tables, (size_t)b * p.a.max_pages + (p.pg_shift >= 0 ? j >> p.pg_shift : j / p.a.pg));
 }
 __device__ __forceinline__ int page_slot(const MassArgs &p, int j) {
   return p.pg_shift >= 0 ? j & (p.a.pg - 1) : j % p.a.pg;
@@ -294,12 +294,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     int slot = 0, phase = 0, issued = 0;
     bool ok = true, more = true;
     const int k_lane = lane / (2 * HB), half = lane / HB & 1, blk = lane % HB;
-    // the half's entry of the page table; -2: not seen by any row (its page is not touched)
+    // the half's entry of the page table; kNotRead: not seen by any row (its page is not touched)
     auto entry_of = [&](const MassWalk &x) {
       const int j0 = x.key0 + 128 * k_lane + 64 * half, end = x.s.pre + x.s.n;
-      if (k_lane >= tiles || j0 >= end) return -2;
+      if (k_lane >= tiles || j0 >= end) return kNotRead;
       const Tokens t = seen_by(p, x.s, j0, min(j0 + 64, end));
-      return t.t0 < t.t1 ? page_entry(p, x.b, j0) : -2;
+      return t.t0 < t.t1 ? page_entry(p, x.b, j0) : kNotRead;
     };
     int page = entry_of(w);
     while (ok && more) {
@@ -492,13 +492,13 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     const f32x2 scale2 = pair(p.scale_log2, p.scale_log2);
     int order = 0, piece = 0, step = 0;
     bool ok = true, more = true;
-    // The key's entry of the page table: -2 where no weight is written (another
+    // The key's entry of the page table: kNotRead where no weight is written (another
     // group's, behind the sequence, neither new nor seen by any row).
     auto entry = [&]() {
       const int k = (g - order) & 3, j = w.key0 + 128 * k + row;
-      if (k >= tiles || j >= w.s.pre + w.s.n) return -2;
+      if (k >= tiles || j >= w.s.pre + w.s.n) return kNotRead;
       const Tokens t = seen_by(p, w.s, j, j + 1);
-      return j >= w.s.pre || t.t0 < t.t1 ? page_entry(p, w.b, j) : -2;
+      return j >= w.s.pre || t.t0 < t.t1 ? page_entry(p, w.b, j) : kNotRead;
     };
     int page = entry();
     while (more) {
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
       if (page >= 0 && page < p.a.n_pages) {
         at = ((long long)page * p.a.Hkv + w.g) * p.a.pg + page_slot(p, j);
         if (j < w.s.pre) old = p.a.mass[at];
-      } else if (page != -2 && p.err) {
+      } else if (page != kNotRead && p.err) {
         atomicExch(p.err + 1, kBadPage);
       }
       // the piece, and the next one: its entry of the page table is on its way meanwhile

@@ -9,7 +9,7 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_bounded_cache import lse_tol, run_window, visible
+from test_gpu_bounded_cache import lse_tol, mass_case, run_mass, run_window, same_floats, visible
 from test_gpu_draft_ops import Batch, _clean_status, _lib, attention_tol, f64, i32, randn  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +70,21 @@ def test_chunks_skip_pages_outside_the_pools(value, window, sinks):
             run_window(bt, q, window, sinks, out, z)
         check_without_page(bt, q, out, z, at, window, sinks, (0, 15))
         assert torch.equal(out[1000:1950], good[1000:1950]) and torch.equal(z[1000:1950], lse[1000:1950])
+
+
+@pytest.mark.parametrize("value", OUTSIDE)
+@pytest.mark.parametrize("pre,new,window", [([700, 50], [2, 3], 0), ([700, 50], [2, 3], 600), ([700, 50], [400, 3], 0)])
+def test_mass_skips_and_reports_pages_outside_the_pools(value, pre, new, window):
+    rng = np.random.default_rng(102)
+    bt = Batch(rng, pre, new, 2, 64, 64)
+    q, lse, before = mass_case(rng, bt, 4, window, 4, 0.125)
+    z, good = torch.from_numpy(lse).to(dev()), torch.from_numpy(before).to(dev())
+    run_mass(bt, q, z, good, window, 4)
+    dgp.dg_op_status()
+    for at in (0, 5, (pre[0] + new[0] - 1) // 64):         # first tokens, cached keys, new keys
+        mass = torch.from_numpy(before).to(dev())
+        with entry(bt, 0, at, value):
+            run_mass(bt, q, z, mass, window, 4)
+        want, page = good.cpu().numpy(), bt.table[0, at]
+        want[page] = before[page]
+        assert same_floats(mass.cpu().numpy(), want)
