@@ -48,8 +48,6 @@
 //
 // Roundings: P is rounded to bf16 for the second product (the row sum adds the
 // unrounded values); scores, sums, accumulators and partial sums are fp32.
-#include <limits.h>
-
 #include <atomic>
 #include <chrono>
 #include <mutex>
@@ -728,8 +726,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
     } else {
       set_up();
     }
-    // Of a run of up to 16 tiles each lane holds one 64-key half: its logical
-    // page, -1 past the last key.  The next run's entries of the page table (and
+    // Of a run of up to 16 tiles each lane holds one 64-key half: its page,
+    // kNotRead past the last key.  The next run's entries of the page table (and
     // the next unit's lengths) are loaded while this one's tiles are copied.
     auto half_key = [&](const Walk<WIN> &u, int kt) {
       return WIN ? 128 * u.key_tile(kt + (lane >> 1)) + 64 * (lane & 1) : 128 * kt + 64 * lane;
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       const int key = half_key(u, kt);
       // (halves that no row sees are not read, nor their entries of the table)
       return kt + (lane >> 1) < u.kt1 && key < u.end() && (!WIN || key + 64 > u.keys.low || key < p.a.sinks)
-                 ? p.a.page_tables[(size_t)u.b * p.a.max_pages + key / p.a.pg] : INT_MIN;
+                 ? table_entry(p.a.page_tables, (size_t)u.b * p.a.max_pages + key / p.a.pg) : kNotRead;
     };
     int kt = w.kt0, page = pages_of(w, kt);
     bool more = true;
@@ -748,8 +746,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
       // masked); V: the sequence's own rows only (0 times anything must be 0), with a
       // window those up to row `sink` and from row `low` on.
       const int n = min(16, w.kt1 - kt), key = half_key(w, kt);
-      const bool off = page != INT_MIN && (page < 0 || page >= p.a.n_pages);
-      const int rows = page == INT_MIN || off ? 0 : is_k ? 64 : min(64, w.end() - key);
+      const bool off = page != kNotRead && (page < 0 || page >= p.a.n_pages);
+      const int rows = page == kNotRead || off ? 0 : is_k ? 64 : min(64, w.end() - key);
       int sink = 0, low = 0;
       if (WIN && !is_k) {
         sink = min(max(p.a.sinks - key, 0), rows);

@@ -10,7 +10,7 @@ import torch
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
 from test_gpu_bounded_cache import lse_tol, mass_case, run_mass, run_window, same_floats, visible
-from test_gpu_draft_ops import Batch, _clean_status, _lib, attention_tol, f64, i32, randn  # noqa: F401  (fixtures)
+from test_gpu_draft_ops import Batch, _clean_status, _lib, attention_tol, f64, i32, randn, run_attention  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
 OUTSIDE = [-1, -2, -3, -2 ** 31 + 1, -2 ** 31, 2 ** 31 - 1]       # entries outside any pool
@@ -88,3 +88,39 @@ def test_mass_skips_and_reports_pages_outside_the_pools(value, pre, new, window)
         want, page = good.cpu().numpy(), bt.table[0, at]
         want[page] = before[page]
         assert same_floats(mass.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("value", OUTSIDE)
+@pytest.mark.parametrize("window,sinks", [(300, 4), (0, 0)])
+@pytest.mark.parametrize("pre,new", [([500, 50], [3, 2]), ([500, 50], [200, 3])])
+def test_few_rows_skip_pages_outside_the_pools(value, window, sinks, pre, new):
+    rng = np.random.default_rng(103)
+    bt = Batch(rng, pre, new, 2, 64, 64)
+    q = randn(rng, bt.T, 4, 64).to(dev())
+    good, lse = torch.zeros_like(q), torch.zeros(bt.T, 4, device=dev())
+    run_window(bt, q, window, sinks, good, lse)
+    a, b = new[0], sum(new)
+    for at in (0, 4, 7):
+        out, z = torch.zeros_like(q), torch.zeros_like(lse)
+        with entry(bt, 0, at, value):
+            run_window(bt, q, window, sinks, out, z)
+        check_without_page(bt, q, out, z, at, window, sinks, (0, 3))
+        assert torch.equal(out[a:b], good[a:b]) and torch.equal(z[a:b], lse[a:b])
+
+
+@pytest.mark.parametrize("value", OUTSIDE)
+@pytest.mark.parametrize("pre,new", [([500, 50], [3, 2]), ([500, 50], [200, 3])])
+def test_drafted_tokens_skip_pages_outside_the_pools(value, pre, new):
+    rng = np.random.default_rng(104)
+    bt = Batch(rng, pre, new, 2, 64, 64)
+    q = randn(rng, bt.T, 4, 64).to(dev())
+    good, a, b = torch.zeros_like(q), new[0], sum(new)
+    run_attention(bt, q, None, good)
+    for at in (0, 4, 7):
+        out = torch.zeros_like(q)
+        with entry(bt, 0, at, value):
+            run_attention(bt, q, None, out)
+        for h in (0, 3):
+            ref, mag, _, _ = without_page(f64(q), bt, at, 0, 0, h)
+            assert (np.abs(f64(out)[:a, h] - ref) <= attention_tol(ref, mag)).all()
+        assert torch.equal(out[a:b], good[a:b])
