@@ -125,12 +125,14 @@ __device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lis
   // Sequences that the call cannot move are left alone; the same in all blocks.
   if (tid == 0) flags = 0;
   __syncthreads();
-  const bool bad_length = L < 0 || (long long)L > (long long)a.max_pages * a.pg || (L + 31) / 32 > p.words ||
+  // (lengths and page sizes go up to 2^31 - 1: nothing is added to them)
+  const bool bad_length = L < 0 || L > 32 * p.words || (long long)L > (long long)a.max_pages * a.pg ||
                           (long long)n_out > (long long)a.out_max_pages * a.pg;
-  const int n_pages = bad_length ? 0 : ceil_div(L, a.pg);
+  auto pages_for = [&](int n) { return n / a.pg + (n % a.pg != 0); };
+  const int n_pages = bad_length ? 0 : pages_for(L);
   if (!bad_length) {
     bool f = false;
-    const int n_out_pages = ceil_div(n_out, a.pg);
+    const int n_out_pages = pages_for(n_out);
     for (int i = tid; i < n_pages; i += kEvictThreads) {
       const int src = table[i], dst = i < n_out_pages ? out_table[i] : 0;
       if (i < kEvictPages) entries[i] = src;

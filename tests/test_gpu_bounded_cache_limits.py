@@ -124,3 +124,31 @@ def test_drafted_tokens_skip_pages_outside_the_pools(value, pre, new):
             ref, mag, _, _ = without_page(f64(q), bt, at, 0, 0, h)
             assert (np.abs(f64(out)[:a, h] - ref) <= attention_tol(ref, mag)).all()
         assert torch.equal(out[a:b], good[a:b])
+
+
+# ---- sequences beyond what the eviction takes --------------------------------------------
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 31, 2 ** 31 - 32, 262144 + 1])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_leaves_sequences_of_too_many_slots_alone(length, in_place):
+    # the table covers the length: one page of many slots, over and over
+    pg, budget = 65536, 200
+    rng = np.random.default_rng(105)
+    table = np.zeros((3, 2 ** 31 // pg), np.int32)
+    table[1, :1], table[2, :1] = 1, 2
+    out = np.array([[0], [1], [2]] if in_place else [[3], [4], [5]], np.int32)
+    k, v = (torch.from_numpy(rng.integers(0, 2 ** 16, (6, 1, pg, 64), dtype=np.uint16).view(np.int16)) for _ in range(2))
+    mass = rng.exponential(1.0, (6, 1, pg)).astype(np.float32)
+    d = [x.to(dev()).view(torch.bfloat16) for x in (k, v)] + [torch.from_numpy(mass).to(dev())]
+    lens, out_lens, kept = i32([300, length, 100]), i32([7, 7, 7]), torch.full((3, 1, budget), 7, dtype=torch.int32, device=dev())
+    dgp.dg_op_cache_evict(*d, i32(table), i32(out), lens, out_lens, budget, kept, sinks=2, recent=20)
+    with pytest.raises(dgp.DgError) as e:
+        dgp.dg_op_status()
+    assert e.value.code == dgp.DG_EINVAL and "sequence" in str(e.value)
+    assert out_lens.tolist() == [200, -1, 100] and (kept[1] == -1).all()
+    j = kept[0, 0].cpu().numpy()
+    assert (np.diff(j) > 0).all() and j[-1] == 299
+    (to0, left, to2), got = out[:, 0], [x.view(torch.int16).cpu() if x.dtype == torch.bfloat16 else x.cpu() for x in d]
+    for x, was in zip(got, (k, v, torch.from_numpy(mass))):
+        assert torch.equal(x[left], was[left]) and torch.equal(x[1], was[1])
+    assert np.array_equal(got[2][to0, 0, :200].numpy(), mass[0, 0, j]) and np.array_equal(got[2][to2, 0, :100].numpy(), mass[2, 0, :100])
