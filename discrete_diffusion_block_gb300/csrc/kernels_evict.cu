@@ -121,6 +121,10 @@ __device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lis
   const int L = a.lens[b], n_out = min(L, a.budget);
   const int *table = a.page_tables + (size_t)b * a.max_pages, *out_table = a.out_tables + (size_t)b * a.out_max_pages;
   int *kept = a.kept + ((size_t)b * a.Hkv + g) * a.budget;
+  // -1 behind the last kept slot (budgets go up to 2^31 - 1: unsigned, so that the last step does not wrap)
+  auto fill = [&](int from) {
+    for (unsigned d = from + tid; lists && d < (unsigned)a.budget; d += kEvictThreads) kept[d] = -1;
+  };
 
   // Sequences that the call cannot move are left alone; the same in all blocks.
   if (tid == 0) flags = 0;
@@ -145,11 +149,11 @@ __device__ __forceinline__ int choose(const EvictArgs &p, int b, int g, bool lis
   if (bad) {
     if (tid == 0 && p.err) atomicExch(p.err + 1, bad_length ? kBadSequence : kBadPage);
     if (tid == 0 && g == 0 && lists) a.out_lens[b] = -1;
-    for (int d = tid; d < a.budget && lists; d += kEvictThreads) kept[d] = -1;
+    fill(0);
     return -1;
   }
   if (tid == 0 && g == 0 && lists) a.out_lens[b] = n_out;
-  for (int d = n_out + tid; d < a.budget && lists; d += kEvictThreads) kept[d] = -1;
+  fill(n_out);
   if (L <= a.budget) {
     for (int d = tid; d < L && lists; d += kEvictThreads) kept[d] = d;
     return L;

@@ -152,3 +152,28 @@ def test_evict_leaves_sequences_of_too_many_slots_alone(length, in_place):
     for x, was in zip(got, (k, v, torch.from_numpy(mass))):
         assert torch.equal(x[left], was[left]) and torch.equal(x[1], was[1])
     assert np.array_equal(got[2][to0, 0, :200].numpy(), mass[0, 0, j]) and np.array_equal(got[2][to2, 0, :100].numpy(), mass[2, 0, :100])
+
+
+@pytest.mark.parametrize("length", [300, -1])
+def test_evict_to_the_largest_budget(length):
+    # the lists of kept slots are as long as the budget
+    rng, budget = np.random.default_rng(106), 2 ** 31 - 1
+    k, v, mass = randn(rng, 10, 1, 64, 64).to(dev()), randn(rng, 10, 1, 64, 64).to(dev()), torch.rand(10, 1, 64, device=dev())
+    was = [x.clone() for x in (k, v, mass)]
+    kept = torch.full((1, 1, budget), 7, dtype=torch.int32, device=dev())
+    out_lens = i32([7])
+    dgp.dg_op_cache_evict(k, v, mass, i32([range(5)]), i32([range(5, 10)]), i32([length]), out_lens, budget, kept, sinks=2 ** 30, recent=2 ** 30 - 1)
+    if length < 0:
+        with pytest.raises(dgp.DgError):
+            dgp.dg_op_status()
+    dgp.dg_op_status()
+    n = max(length, 0)
+    assert out_lens.item() == length and torch.equal(kept[0, 0, :n], torch.arange(n, dtype=torch.int32, device=dev()))
+    for part in kept[0, 0, n:].split(2 ** 28):
+        assert bool((part == -1).all())
+    for x, w in zip((k, v, mass), was):
+        flat, old = x.view(10, 1, 64, -1), w.view(10, 1, 64, -1)
+        assert torch.equal(flat[:5], old[:5])
+        for d in range(5):
+            m = min(64, max(0, n - 64 * d))
+            assert torch.equal(flat[5 + d, :, :m], old[d, :, :m]) and torch.equal(flat[5 + d, :, m:], old[5 + d, :, m:])
