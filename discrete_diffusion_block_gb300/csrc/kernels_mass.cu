@@ -135,7 +135,7 @@ struct MassList {
     first = 0;
     if (s.row_tiles <= 1) return 1;
     const int j0 = s.unit(i) * keys;
-    const Tokens t = seen_by(p, s, j0, min(j0 + keys, s.pre + s.n));
+    const Tokens t = seen_by(p, s, j0, j0 + min(keys, s.pre + s.n - j0));  // (slots go up to 2^31: j0 + keys may pass it)
     if (t.t0 >= t.t1) return 1;
     first = row_tile(t.t0 - s.tf);
     return row_tile(t.t1 - s.tf + p.T - 1) - first;
@@ -183,10 +183,10 @@ struct MassWalk : RangeWalk<MassList> {
   __device__ __forceinline__ int columns(const MassArgs &p, int t0) const { return min(p.T, s.n - t0) * p.G; }
   // The tokens that count and see a key of the unit's tile k (none: t0 >= t1).
   __device__ __forceinline__ Tokens tile_tokens(const MassList &list, int k) const {
-    const int j0 = key0 + 128 * k, end = s.pre + s.n;
+    const int left = s.pre + s.n - key0 - 128 * k;  // of the sequence, from the tile on
     Tokens t;
     t.t0 = t.t1 = 0;
-    if (128 * k < list.keys && j0 < end) t = seen_by(list.p, s, j0, min(j0 + 128, end));
+    if (128 * k < list.keys && left > 0) t = seen_by(list.p, s, key0 + 128 * k, key0 + 128 * k + min(128, left));
     return t;
   }
 };
@@ -296,9 +296,10 @@ __global__ void __launch_bounds__(kMassThreads, 1) key_mass_kernel(const __grid_
     const int k_lane = lane / (2 * HB), half = lane / HB & 1, blk = lane % HB;
     // the half's entry of the page table; kNotRead: not seen by any row (its page is not touched)
     auto entry_of = [&](const MassWalk &x) {
-      const int j0 = x.key0 + 128 * k_lane + 64 * half, end = x.s.pre + x.s.n;
-      if (k_lane >= tiles || j0 >= end) return kNotRead;
-      const Tokens t = seen_by(p, x.s, j0, min(j0 + 64, end));
+      const int left = x.s.pre + x.s.n - x.key0 - 128 * k_lane - 64 * half;  // of the sequence, from the half on
+      if (k_lane >= tiles || left <= 0) return kNotRead;
+      const int j0 = x.key0 + 128 * k_lane + 64 * half;
+      const Tokens t = seen_by(p, x.s, j0, j0 + min(64, left));
       return t.t0 < t.t1 ? page_entry(p, x.b, j0) : kNotRead;
     };
     int page = entry_of(w);

@@ -9,8 +9,8 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_bounded_cache import lse_tol, mass_case, run_mass, run_window, same_floats, visible
-from test_gpu_draft_ops import Batch, _clean_status, _lib, attention_tol, f64, i32, randn, run_attention  # noqa: F401  (fixtures)
+from test_gpu_bounded_cache import lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_workspace
+from test_gpu_draft_ops import U32, Batch, _clean_status, _lib, attention_tol, f64, i32, randn, run_attention  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
 OUTSIDE = [-1, -2, -3, -2 ** 31 + 1, -2 ** 31, 2 ** 31 - 1]       # entries outside any pool
@@ -177,3 +177,101 @@ def test_evict_to_the_largest_budget(length):
         for d in range(5):
             m = min(64, max(0, n - 64 * d))
             assert torch.equal(flat[5 + d, :, :m], old[d, :, :m]) and torch.equal(flat[5 + d, :, m:], old[5 + d, :, m:])
+
+
+# ---- positions next to 2^31 ----------------------------------------------------------------
+
+LAST = 2 ** 31 - 256        # a sequence ends at or before this slot
+
+
+class Far:
+    """One sequence whose new tokens end at slot `end`: of its table only the pages
+    of the first tokens and of the last window are there, the rest names none."""
+    HQ, HKV, HD, PG, WINDOW, SINKS = 32, 8, 64, 65536, 8000, 4
+
+    def __init__(self, rng, end, n, most=2 ** 31):
+        self.n, self.pre = n, end - n
+        first = max(self.pre - self.WINDOW + 1, self.SINKS)
+        self.slots = np.concatenate([np.arange(self.SINKS), np.arange(first, end)])
+        table = np.full((1, most // self.PG), -9, np.int32)
+        there = np.unique(self.slots // self.PG)
+        table[0, there] = np.arange(len(there))
+        self.table, shape = table, (len(there), self.HKV, self.PG, self.HD)
+        k, v = randn(rng, len(self.slots), self.HKV, self.HD), randn(rng, len(self.slots), self.HKV, self.HD)
+        self.pools = []
+        for x in (k, v):
+            pool = torch.full(shape, float("nan"), dtype=torch.bfloat16)
+            place(pool, table[0], self.slots, x)
+            self.pools.append(pool.to(dev()))
+        self.k, self.v = f64(k), f64(v)
+        self.q = randn(rng, n, self.HQ, self.HD)
+        self.d = dict(page_tables=i32(table), prefix_lens=i32([self.pre]), offsets=i32([0, n]))
+        self.out, self.lse = torch.full((n, self.HQ, self.HD), 7.0, dtype=torch.bfloat16, device=dev()), torch.full((n, self.HQ), 7.0, device=dev())
+
+    def attend(self):
+        ws = window_workspace(self.n, 1, self.HQ, self.HKV, self.HD)
+        dgp.dg_op_window_attention(self.q.to(dev()), *self.pools, **self.d, out=self.out, workspace=ws, window=self.WINDOW, sinks=self.SINKS,
+                                   lse=self.lse)
+
+    def weigh(self, mass, observe=0):
+        dgp.dg_op_key_mass(self.q.to(dev()), self.lse, self.pools[0], mass, **self.d,
+                           workspace=mass_workspace(self.n, 1, self.HQ, self.HKV, self.HD), window=self.WINDOW, sinks=self.SINKS, observe=observe)
+
+    def scores(self, h):
+        s = self.pre + np.arange(self.n)[:, None]
+        see = (self.slots <= s) & ((self.slots > s - self.WINDOW) | (self.slots < self.SINKS))
+        k, x = self.k[:, h // 4], f64(self.q)[:, h]
+        return np.where(see, x @ k.T * self.HD ** -0.5, -np.inf), (np.abs(x) @ np.abs(k).T * self.HD ** -0.5) * see
+
+
+@pytest.mark.parametrize("end,n,most", [(LAST - d, n, 2 ** 31) for d in (0, 100, 255, 256, 65000) for n in (1, 3, 200)] +
+                         [(2 ** 29 - d, 700, 2 ** 29) for d in (0, 200)])        # 700 rows: the kernel for chunks
+def test_far_positions(end, n, most):
+    far = Far(np.random.default_rng(107), end, n, most)
+    far.attend()
+    dgp.dg_op_status()
+    for h in (0, 3, 28) if n > 3 else range(far.HQ):
+        s, mag = far.scores(h)
+        m = s.max(1, keepdims=True)
+        e = np.exp(s - m)
+        z = m[:, 0] + np.log(e.sum(1))
+        e /= e.sum(1, keepdims=True)
+        ref = e @ far.v[:, h // 4]
+        assert (np.abs(f64(far.out)[:, h] - ref) <= attention_tol(ref, e @ np.abs(far.v[:, h // 4]))).all()
+        assert (np.abs(f64(far.lse)[:, h] - z) <= lse_tol(z, mag.max(1), far.HD, 80)).all()
+    page, slot = far.table[0, far.slots // far.PG], far.slots % far.PG
+    for observe in (0, 1):
+        before = np.random.default_rng(108).exponential(1.0, (len(far.pools[0]), far.HKV, far.PG)).astype(np.float32)
+        mass = torch.from_numpy(before).to(dev())
+        far.weigh(mass, observe)
+        dgp.dg_op_status()
+        got, rows = mass.cpu().numpy(), slice(n - observe if observe else 0, n)
+        still = np.ones(got.shape, bool)
+        for g in range(far.HKV):
+            seen = np.isfinite(far.scores(4 * g)[0][rows]).any(0) | (far.slots >= far.pre)
+            still[page[seen], g, slot[seen]] = False
+            if g not in (0, 7):
+                continue
+            total, err = np.where(far.slots < far.pre, before[page, g, slot].astype(np.float64), 0.0), np.zeros(len(far.slots))
+            for h in range(4 * g, 4 * g + 4):
+                s, mag = far.scores(h)
+                z = f64(far.lse)[rows, h][:, None]
+                e = np.exp(s[rows] - z)
+                total += e.sum(0)
+                err += (e * ((far.HD + 8) * mag[rows] + 8 * np.abs(z) + 100 + n * 4 / 64)).sum(0)   # as for the other batches
+            assert (np.abs(got[page, g, slot] - total) <= U32 * (err + 2 * np.abs(total)))[seen].all()
+        assert np.array_equal(got.view(np.uint32)[still], before.view(np.uint32)[still])
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_sequences_that_end_behind_the_last_position_are_reported(n):
+    far = Far(np.random.default_rng(109), LAST, n)
+    mass = torch.ones(len(far.pools[0]), far.HKV, far.PG, device=dev())
+    far.d["prefix_lens"] += 1
+    far.lse.fill_(1.0)
+    for call in (far.attend, lambda: far.weigh(mass)):
+        call()
+        with pytest.raises(dgp.DgError) as e:
+            dgp.dg_op_status()
+        assert "sequence" in str(e.value)
+    assert (far.out == 7.0).all() and (far.lse == 1.0).all() and (mass == 1.0).all()
