@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             tc::fence_before();
             __syncwarp();
             if (lane == 0) attn_arrive(p_half);
+            __syncwarp();  // (the next store takes all lanes together)
           }
         }
         const float2 sum = split(add2(sum0, sum1));
@@ -573,8 +574,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
             uint32_t v[32];
             tc::tmem_ld32(t_o + c, v);
             tc::tmem_ld_wait(v);
-            if (row >= rows) continue;
-            if (whole) {
+            if (row < rows && whole) {
 #pragma unroll
               for (int j = 0; j < 32; j += 16) {
                 uint32_t o[8];
@@ -589,12 +589,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_attn_kernel(const __gr
                   *(uint4 *)(dst + c + j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
               }
-            } else {
+            } else if (row < rows) {
 #pragma unroll
               for (int j = 0; j < 32; j += 4)
                 part[(size_t)((c + j) >> 2) * 128] = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
                                                                  __uint_as_float(v[j + 3]));
             }
+            __syncwarp();  // (the next load takes all lanes together)
           }
           tc::fence_before();
         }

@@ -9,7 +9,7 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_bounded_cache import lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_workspace
+from test_gpu_bounded_cache import check_window, lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_workspace
 from test_gpu_draft_ops import U32, Batch, _clean_status, _lib, attention_tol, f64, i32, randn, run_attention  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -124,6 +124,16 @@ def test_drafted_tokens_skip_pages_outside_the_pools(value, pre, new):
             ref, mag, _, _ = without_page(f64(q), bt, at, 0, 0, h)
             assert (np.abs(f64(out)[:a, h] - ref) <= attention_tol(ref, mag)).all()
         assert torch.equal(out[a:b], good[a:b])
+
+
+# ---- warps with rows of nobody's ------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 31, 33, 64, 95, 97, 127])
+@pytest.mark.parametrize("pre,window", [(0, 200), (2000, 0)])
+def test_chunks_with_any_number_of_rows_in_the_last_tile(rows, pre, window):
+    # one row a token: the last tile's warps are full, empty, and in between
+    rng = np.random.default_rng(110 + rows)
+    check_window(Batch(rng, [pre], [10 * 128 + rows], 16, 64, 64), 16, window, 2, rng)
 
 
 # ---- sequences beyond what the eviction takes --------------------------------------------
