@@ -9,7 +9,8 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_bounded_cache import check_window, lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_workspace
+from test_gpu_bounded_cache import (check_window, lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_ref,
+                                    window_workspace)
 from test_gpu_draft_ops import U32, Batch, _clean_status, _lib, attention_tol, f64, i32, randn, run_attention  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -134,6 +135,38 @@ def test_chunks_with_any_number_of_rows_in_the_last_tile(rows, pre, window):
     # one row a token: the last tile's warps are full, empty, and in between
     rng = np.random.default_rng(110 + rows)
     check_window(Batch(rng, [pre], [10 * 128 + rows], 16, 64, 64), 16, window, 2, rng)
+
+
+# ---- scores that lie far apart -----------------------------------------------------------------
+
+@pytest.mark.parametrize("new,hq,hkv", [([4, 2], 2, 1), ([1000, 700], 48, 24)])
+@pytest.mark.parametrize("size", [30.0, 3000.0])
+def test_rows_whose_scores_lie_far_apart(new, hq, hkv, size):
+    # Keys of one number each in all 64 elements, queries likewise: a score is 64 equal
+    # products of two bf16 numbers, exact in fp32 in any order, and what the exponents
+    # add to it (one rounding of the factor, one of the maximum, the same for all keys of a
+    # row) moves weights against each other by 2^-24 of their distance in the exponent. So
+    # these rows have the tolerance of any other, and their log-sum-exps one that
+    # counts the roundings of factor, ln 2 and result.
+    rng = np.random.default_rng(120)
+    bt = Batch(rng, [900] * len(new), new, hkv, 64, 64)
+    n = 900 + max(new)
+    up = (torch.linspace(-1, 1, n)[:, None, None] * 2.0).expand(n, hkv, 64).to(torch.bfloat16)
+    pool = torch.full(bt.k_pool.shape, float("nan"), dtype=torch.bfloat16)
+    for b, m in enumerate(new):
+        place(pool, bt.table[b], np.arange(900 + m), up[:900 + m].contiguous())
+        bt.keys[b] = f64(up[:900 + m])
+    bt.k_pool = pool.to(dev())
+    q = randn(rng, bt.T, hq, 64)
+    up_rows, down_rows = bt.off[:-1].tolist(), (bt.off[:-1] + 1).tolist()
+    q[up_rows], q[down_rows] = size, -size
+    out, lse = torch.zeros(bt.T, hq, 64, dtype=torch.bfloat16, device=dev()), torch.zeros(bt.T, hq, device=dev())
+    run_window(bt, q.to(dev()), 0, 0, out, lse)
+    dgp.dg_op_status()
+    ref, mag, z, _ = window_ref(f64(q), bt, 0, 0, 0.125)
+    rows = up_rows + down_rows
+    assert (np.abs(f64(out) - ref) <= attention_tol(ref, mag))[rows].all(), np.abs(f64(out) - ref)[rows].max()
+    assert (np.abs(f64(lse) - z) <= U32 * (4 * np.abs(z) + 128))[rows].all()
 
 
 # ---- sequences beyond what the eviction takes --------------------------------------------
