@@ -9,7 +9,7 @@ import torch
 
 import discrete_diffusion_block_gb300 as dgp
 from gpu_util import dev
-from test_gpu_bounded_cache import (check_window, lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_ref,
+from test_gpu_bounded_cache import (Cache, check_evict, check_window, lse_tol, mass_case, mass_workspace, place, run_mass, run_window, same_floats, visible, window_ref,
                                     window_workspace)
 from test_gpu_draft_ops import U32, Batch, _clean_status, _lib, attention_tol, f64, i32, randn, run_attention  # noqa: F401  (fixtures)
 
@@ -318,3 +318,29 @@ def test_sequences_that_end_behind_the_last_position_are_reported(n):
             dgp.dg_op_status()
         assert "sequence" in str(e.value)
     assert (far.out == 7.0).all() and (far.lse == 1.0).all() and (mass == 1.0).all()
+
+
+# ---- evictions with pages of few slots, and tables that are too short -------------------------
+
+@pytest.mark.parametrize("pg", [1, 2, 3, 12])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_with_small_pages(pg, in_place):
+    check_evict(Cache(np.random.default_rng(111), [500, 90, 1300], 3, 64, pg, 150, in_place), 4, 30)
+
+
+@pytest.mark.parametrize("short", ["page_tables", "out_tables"])
+def test_evict_leaves_sequences_that_tables_do_not_hold_alone(short):
+    c = Cache(np.random.default_rng(112), [500, 90, 470], 2, 128, 64, 200)
+    d, ref = c.on_gpu(), c.ref(2, 20)
+    d[short] = d[short][:, :3 if short == "out_tables" else 7].contiguous()       # 192 slots of 200; 448 of 500 and of 470
+    dgp.dg_op_cache_evict(**d, budget=200, sinks=2, recent=20)
+    with pytest.raises(dgp.DgError) as e:
+        dgp.dg_op_status()
+    assert e.value.code == dgp.DG_EINVAL and "sequence" in str(e.value)
+    assert d["out_lens"].tolist() == [-1, 90, -1] and (d["kept"][0] == -1).all() and (d["kept"][2] == -1).all()
+    assert np.array_equal(d["kept"][1].cpu().numpy(), ref[4][1])
+    moved = np.zeros(c.n_pages, bool)
+    moved[c.out[1, :2]] = True
+    for x, was in ((d["k_pool"], c.k), (d["v_pool"], c.v)):
+        assert torch.equal(x.view(torch.int16).cpu()[~moved], was[~moved])
+    assert np.array_equal(d["mass_pool"].cpu().numpy()[~moved], c.mass[~moved]) and same_floats(d["mass_pool"].cpu().numpy()[moved], ref[2][moved])
