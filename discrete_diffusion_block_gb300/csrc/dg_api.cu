@@ -1675,7 +1675,11 @@ int check_attended(int32_t n_tok, int32_t n_q_heads, int32_t n_kv_heads, int32_t
   return DG_OK;
 }
 
-// The batch's key tiles, over all tiles of rows, fit the kernels' 32-bit sums.
+// The batch's key tiles, over all tiles of rows, fit the kernels' 32-bit sums: the tree
+// attention's over tiles of 128 rows of heads.  The other kernels' sums are no larger,
+// although their row tiles hold whole tokens, 65 to 128 rows of heads: the chunk attention
+// counts them in pairs, the key weights four key tiles at a time (single ones only where there
+// are no more than two pairs of a key tile and a row tile for each SM).
 int check_span(int32_t max_pages, int32_t page_size, int32_t n_tok, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads) {
   const int64_t key_tiles = ((int64_t)max_pages * page_size + 127) / 128 + dg::kTreeUnitCost;
   const int64_t row_tiles = (int64_t)n_tok * (n_q_heads / n_kv_heads) / 128 + n_seqs;

@@ -21,13 +21,16 @@
 // (tensor memory answers late while products run), for which the other warps give
 // registers away (with 168 for all threads 2048 tokens over 30k keys took 4% longer).
 //
-// Measured (16 query and 8 KV heads of 128): 2048 tokens over 30k keys 370 us, 74% of the
-// measured product rate; 16384 tokens with windows of 1024 171 us, 41%: a tenth of a row
+// Measured (16 query and 8 KV heads of 128): 2048 tokens over 30k keys 370 to 402 us, by
+// machine, 68 to 74% of the measured product rate; 16384 tokens with windows of 1024 172 to
+// 176 us, 41%: a tenth of a row
 // tile's steps are the first tokens', two tenths half masked, and a unit's beginning and
 // end (its lengths, first scores, output) take as long as four of its ten steps.
 //
-// Roundings: P is rounded to bf16 for the second product (the row sum adds the
-// unrounded values); scores, sums, accumulators and partial sums are fp32.
+// Roundings: P is rounded to bf16 for the second product, whose operands are bf16 as V is
+// (the row sum adds the unrounded values; against 64 bits the output, bf16 too, is off by
+// 2.0e-3 of its norm, by 1.7e-3 with everything in fp32 up to its own rounding); scores, sums,
+// accumulators and partial sums are fp32.
 #include <algorithm>
 #include <atomic>
 

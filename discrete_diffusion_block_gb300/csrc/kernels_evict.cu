@@ -17,10 +17,13 @@
 // calls are one launch, in which each block makes the choice for itself, others two, the
 // choices and the moves (launch_evict has the rule and both sides' times).
 //
-// Measured (8 KV heads of 128): 12 sequences of up to 32k slots to 8k 124 us, 70% of the
-// copy bandwidth (the move alone 95 us, the choice 27); 29 of up to 2900 to 1111 (4 heads
-// of 64) 19.5 us; one of 2176 to 2048 12.8, a chain of latencies: launch (2 us), the lengths,
-// tables and weights (2.5), three passes (4.3), bits and lists (2.3), rows (3.5).  Not kept:
+// Measured in captured graphs (8 KV heads of 128): 12 sequences of up to 32k slots to 8k 124
+// us, 70% of the copy bandwidth (the move alone 95 us, the choice 27); 29 of up to 2900 to
+// 1111 (4 heads of 64) 19.5 us, the choice 8.5 and the rows 9 of a block; one of 2176 to 2048
+// 12.6, a chain of latencies: lengths and tables 1.1 us, weights 0.8, three passes 3.5, bits
+// and lists 2.0, rows 3.6, launch and end 1.6 (clock stamps of a block).  In place the small
+// ones take as long, the large one 111 where it takes 133 (calls one by one, caches cold):
+// its rows before the first that goes are not moved.  Not kept:
 // passes that end early where all that is left of a bin stays (0.1 us less); the move's
 // launch begun under the choice (0.5 us less of the small ones, 4 more of the large).
 //

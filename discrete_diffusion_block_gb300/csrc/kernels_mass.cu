@@ -31,9 +31,9 @@
 // four key tiles at a time.
 //
 // Measured (16 query and 8 KV heads of 128): one token over 8k keys 8.3 us, latency; 8192
-// rows of a prompt 110 us, 66% of the measured product rate (of a row tile's 9 x 64 cycles
-// on the tensor core an eighth are the log-sum-exps'; its exponentials take 512 cycles of
-// all special function units).
+// rows of a prompt 110 to 115 us, by machine, 63 to 66% of the measured product rate (of a
+// row tile's 9 x 64 cycles on the tensor core a ninth are the log-sum-exps'; its exponentials
+// take 512 cycles of all special function units).
 #include <atomic>
 
 #include "attn_tc.cuh"
