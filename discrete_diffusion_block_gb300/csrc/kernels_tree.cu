@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_attn_kernel(const __grid
 #pragma unroll 1
         for (int c = half * (HD / 64); c < (half + 1) * (HD / 64); ++c) {
           uint32_t v[32];
-          __syncwarp();  // the load takes all lanes together (rows of nobody's leave the round before early)
+          __syncwarp();  // the load takes all lanes together (rows of nobody's leave the loop's last turn early)
           tc::tmem_ld32(t_o + lane_off + 32 * c, v);
           tc::tmem_ld_wait(v);
           if (row >= rows) continue;

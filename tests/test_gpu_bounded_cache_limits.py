@@ -344,3 +344,32 @@ def test_evict_leaves_sequences_that_tables_do_not_hold_alone(short):
     for x, was in ((d["k_pool"], c.k), (d["v_pool"], c.v)):
         assert torch.equal(x.view(torch.int16).cpu()[~moved], was[~moved])
     assert np.array_equal(d["mass_pool"].cpu().numpy()[~moved], c.mass[~moved]) and same_floats(d["mass_pool"].cpu().numpy()[moved], ref[2][moved])
+
+
+# ---- sequences whose rows lie outside the call's ------------------------------------------------
+
+@pytest.mark.parametrize("pre,new,hkv", [([300, 40, 90], [5, 3, 2], 2), ([300, 40, 90], [900, 400, 70], 16)])     # few rows, chunks
+@pytest.mark.parametrize("offsets", ["behind", "before", "descending"])
+def test_rows_outside_the_call_are_reported_and_left_alone(pre, new, hkv, offsets):
+    rng = np.random.default_rng(113)
+    bt = Batch(rng, pre, new, hkv, 64, 64)
+    q = randn(rng, bt.T, 2 * hkv, 64).to(dev())
+    a, b, c = new[0], new[0] + new[1], sum(new)
+    # one sequence's rows outside the call's; and a batch in which it has none, whose work is shared out alike
+    off, left = dict(behind=([0, a, b, bt.T + 1], [0, a, b, b]), before=([-1, a, b, c], [a, a, b, c]), descending=([0, a, b, 0], [0, a, b, b]))[offsets]
+    before, results = torch.rand(bt.n_pages, hkv, 64, device=dev()), []
+    lse = torch.full((bt.T, 2 * hkv), 3.0, device=dev())
+    for rows in (left, off):
+        out, z, mass = torch.full_like(q, 7.0), torch.full_like(lse, 7.0), before.clone()
+        bt.d["offsets"] = i32(rows)
+        for call in (lambda: run_window(bt, q, 200, 4, out, z), lambda: run_mass(bt, q, lse, mass, 200, 4)):
+            call()
+            if rows is off:
+                with pytest.raises(dgp.DgError) as e:
+                    dgp.dg_op_status()
+                assert e.value.code == dgp.DG_EINVAL and "sequence" in str(e.value)
+        dgp.dg_op_status()
+        results.append((out, z, mass))
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+    nobodys = slice(0, a) if offsets == "before" else slice(b, None)
+    assert (out[nobodys] == 7.0).all() and (z[nobodys] == 7.0).all() and (out[a:b] != 7.0).any() and not torch.equal(mass, before)
